@@ -1,0 +1,264 @@
+"""ctypes binding of the draft layer's attention (include/draftlayer.h), same names as the C ABI.
+
+As in `_binding`: argument marshalling only, torch for device memory and
+streams, outputs allocated where the caller passes none, errors as ValueError
+(an argument) or DraftHeadError (the runtime).  Shapes, types and devices of the
+tensors are checked here, since the library sees only pointers.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+import re
+
+import numpy as np
+
+from . import _binding as B
+
+_HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "draftlayer.h")
+PAGES = (32, 64, 128, 256)     # tokens a page may hold
+HEAD_DIMS = (64, 128, 256)
+
+_lib = None
+
+
+def _load():
+    global _lib
+    if _lib is None:
+        lib = B.load_library()
+        P, i32, i64, f32, f64, sz = (ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
+                                     ctypes.c_size_t)
+        for name, types in (
+                ("draft_layer_rope_table", [i32, i32, f64, f64, i32, f64, f64, f64, P]),
+                ("draft_layer_append", [P, i64, P, i64, P, i64, P, i32, i32, i32, P, P, P, P, i32, i32, P, P, P, i32, i32,
+                                        i32, i32, i32, i32, P, P]),
+                ("draft_layer_read", [P, P, P, P, i32, i32, P, P, P, i32, i32, i32, i32, i32, P, P, P]),
+                ("draft_layer_workspace_bytes", [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]),
+                ("draft_layer_attend", [P, i64, P, P, P, P, i32, i32, P, P, P, i32, i32, i32, i32, i32, i32, f32, i32, i32, P,
+                                        P, P, sz, P])):
+            f = getattr(lib, name)
+            f.restype, f.argtypes = i32, types
+        _lib = lib
+    return _lib
+
+
+def layer_header_functions() -> list[str]:
+    """Names of the functions include/draftlayer.h declares."""
+    with open(_HEADER) as f:
+        return re.findall(r"^int (draft_layer_\w+)\s*\(", f.read(), flags=re.M)
+
+
+# ------------------------------------------------------------------ host side
+def draft_layer_rope_table(positions: int, rot: int, base: float = 10000.0, factor: float = 1.0, original: int = 0,
+                           beta_fast: float = 32.0, beta_slow: float = 1.0, mscale: float | None = None) -> np.ndarray:
+    """(cos, sin) of the rotary angles, fp32 [positions][rot/2][2].
+
+    factor > 1 stretches them for contexts longer than the trained one: all
+    alike (original = 0), or by YaRN's ramp for a model trained on `original`
+    positions.  mscale: the factor on both (None: 1, and YaRN's
+    0.1 ln(factor) + 1 where its ramp is used)."""
+    lib = _load()
+    if mscale is None:
+        mscale = 0.1 * math.log(factor) + 1.0 if original > 0 and factor > 1.0 else 1.0
+    out = np.empty((max(positions, 0), max(rot // 2, 0), 2), dtype=np.float32)
+    B._check(lib.draft_layer_rope_table(positions, rot, base, factor, original, beta_fast, beta_slow, mscale, B._ptr(out)))
+    return out
+
+
+# ------------------------------------------------------------------ device side
+def _need(ok, text):
+    if not ok:
+        raise ValueError(text)
+
+
+def _rows3(name, t, dev):
+    """A bf16 [T][heads][D] tensor whose rows may have gaps; its row stride."""
+    import torch
+    _need(t.dtype == torch.bfloat16 and t.dim() == 3, f"{name} must be a bf16 tensor [T][heads][D]")
+    _need(t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
+    if t.shape[0] == 0:
+        return t.shape[1] * t.shape[2]
+    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]), f"{name}'s heads must be contiguous in a row")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _whole(name, t, dtype, shape, dev):
+    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
+          f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
+    _need(t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
+
+
+def _cache(k_codes, v_codes, k_scale, v_scale):
+    """Checks a cache's four tensors; (device, pages, kv heads, page, D)."""
+    import torch
+    _need(k_codes.dim() == 4, "k_codes must be [pages][heads][page][D]")
+    dev, shape = k_codes.device, k_codes.shape
+    _need(dev.type == "cuda" and dev.index == torch.cuda.current_device(), f"the cache must be on the current GPU, not on {dev}")
+    _whole("k_codes", k_codes, torch.uint8, shape, dev)
+    _whole("v_codes", v_codes, torch.uint8, shape, dev)
+    _whole("k_scale", k_scale, torch.float32, shape[:2], dev)
+    _whole("v_scale", v_scale, torch.float32, shape[:2], dev)
+    return dev, *shape
+
+
+def _batch(q_start, kv_len, table, dev):
+    """Checks a batch's tensors; (sequences, pages a sequence)."""
+    import torch
+    _need(kv_len.dim() == 1 and table.dim() == 2, "kv_len must be [sequences] and table [sequences][pages]")
+    n = kv_len.shape[0]
+    _whole("kv_len", kv_len, torch.int32, (n,), dev)
+    _whole("q_start", q_start, torch.int32, (n + 1,), dev)
+    _whole("table", table, torch.int32, (n, table.shape[1]), dev)
+    return n, table.shape[1]
+
+
+def _out(given, name, shape, dtype, dev, stream):
+    """The caller's tensor, checked, or a new one (kept for `stream`, if that is not the current one)."""
+    import torch
+    if given is not None:
+        _whole(name, given, dtype, shape, dev)
+        return given
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    _keep_for(t, stream)
+    return t
+
+
+def _keep_for(t, stream):
+    """Tells torch's allocator that `t`, made on the current stream, is used on `stream` too."""
+    import torch
+    if stream is None:
+        return
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
+    if stream.cuda_stream != torch.cuda.current_stream(t.device).cuda_stream:
+        stream.wait_stream(torch.cuda.current_stream(t.device))   # the memory may still be in use there
+        t.record_stream(stream)
+
+
+def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, interleaved: bool = False,
+                       q_out=None, stream=None):
+    """Rotate q and k by their positions and write k and v to the cache in 8 bits.
+
+    q: CUDA bf16 [T][hq][D] (or None: keys and values only), k, v: bf16
+    [T][hkv][D], rows with gaps allowed (slices of one projection); rope: fp32
+    [positions][rot/2][2] (None: no rotation); the cache and the batch as
+    include/draftlayer.h has them.  Returns the rotated q, bf16 [T][hq][D]
+    (q_out may be q itself where q has no gaps)."""
+    import torch
+    lib = _load()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    ldk, ldv = _rows3("k", k, dev), _rows3("v", v, dev)
+    rows = k.shape[0]
+    _need(tuple(k.shape) == (rows, hkv, d) and tuple(v.shape) == (rows, hkv, d), f"k and v must be [T][{hkv}][{d}]")
+    hq, ldq = hkv, 0
+    if q is None:
+        _need(q_out is None, "q_out needs q")
+    else:
+        ldq, hq = _rows3("q", q, dev), q.shape[1]
+        _need(q.shape[0] == rows and q.shape[2] == d, f"q must be [{rows}][heads][{d}]")
+        q_out = _out(q_out, "q_out", (rows, hq, d), torch.bfloat16, dev, stream)
+    positions = rot = 0
+    if rope is not None:
+        _need(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [positions][rot/2][2]")
+        _whole("rope", rope, torch.float32, rope.shape, dev)
+        positions, rot = rope.shape[0], rope.shape[1] * 2
+    B._check(lib.draft_layer_append(
+        None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, None if rope is None else rope.data_ptr(),
+        positions, rot, 1 if interleaved else 0, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+        n_pages, page, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
+        None if q is None else q_out.data_ptr(), B._stream(stream)))
+    return q_out
+
+
+def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, rows: int, k_out=None, v_out=None, stream=None):
+    """The last tokens of each sequence out of the cache: sequence s's
+    q_start[s+1] - q_start[s] last ones, `rows` in all.  Returns (k, v), bf16
+    [rows][hkv][D]."""
+    import torch
+    lib = _load()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    shape = (max(rows, 0), hkv, d)
+    k_out = _out(k_out, "k_out", shape, torch.bfloat16, dev, stream)
+    v_out = _out(v_out, "v_out", shape, torch.bfloat16, dev, stream)
+    B._check(lib.draft_layer_read(
+        k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page, q_start.data_ptr(),
+        kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hkv, d, k_out.data_ptr(), v_out.data_ptr(),
+        B._stream(stream)))
+    return k_out, v_out
+
+
+def draft_layer_workspace_bytes(rows: int, n_seq: int, hq: int, hkv: int, d: int) -> int:
+    """Device workspace bytes draft_layer_attend needs for `rows` rows of n_seq sequences."""
+    lib = _load()
+    out = ctypes.c_size_t()
+    B._check(lib.draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d, ctypes.byref(out)))
+    return out.value
+
+
+def draft_layer_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: int, device):
+    """A device workspace for draft_layer_attend (zero-filled once; the library
+    keeps the part that must start at zero at zero)."""
+    import torch
+    return torch.zeros(draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d), dtype=torch.uint8, device=device)
+
+
+def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, scale: float | None = None, window: int = 0,
+                       sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """Attention of the rows over the cache.
+
+    q: CUDA bf16 [T][hq][D], rows with gaps allowed; scale: None for
+    1/sqrt(D); window > 0: a row sees the last `window` tokens up to its own and
+    the first `sinks`; workspace: from draft_layer_workspace (allocated when
+    None).  Returns (out bf16 [T][hq][D], lse fp32 [T][hq])."""
+    import torch
+    lib = _load()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    ldq = _rows3("q", q, dev)
+    rows, hq = q.shape[0], q.shape[1]
+    _need(q.shape[2] == d, f"q must be [T][heads][{d}]")
+    out = _out(out, "out", (rows, hq, d), torch.bfloat16, dev, stream)
+    lse = _out(lse, "lse", (rows, hq), torch.float32, dev, stream)
+    if workspace is None:
+        workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
+        _keep_for(workspace, stream)
+    _need(workspace.device == dev and workspace.is_contiguous(), f"the workspace must be contiguous on {dev}")
+    B._check(lib.draft_layer_attend(
+        q.data_ptr(), ldq, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page,
+        q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
+        1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), B._stream(stream)))
+    return out, lse
+
+
+class DraftCache:
+    """A paged cache in 8 bits: codes and scales of `n_pages` pages of `page`
+    tokens for one layer.  Which page belongs to which sequence is the caller's
+    to say, in each call's table."""
+
+    def __init__(self, n_pages: int, hkv: int, d: int, page: int = 64, device="cuda"):
+        import torch
+        _need(page in PAGES, f"page must be one of {PAGES}")
+        _need(d in HEAD_DIMS, f"d must be one of {HEAD_DIMS}")
+        _need(n_pages > 0 and hkv > 0, "n_pages and hkv must be positive")
+        self.n_pages, self.hkv, self.d, self.page = n_pages, hkv, d, page
+        self.k_codes, self.v_codes = (torch.full((n_pages, hkv, page, d), 128, dtype=torch.uint8, device=device) for _ in range(2))
+        self.k_scale, self.v_scale = (torch.ones((n_pages, hkv), dtype=torch.float32, device=device) for _ in range(2))
+
+    @property
+    def tensors(self):
+        return self.k_codes, self.v_codes, self.k_scale, self.v_scale
+
+    def append(self, q, k, v, rope, q_start, kv_len, table, interleaved=False, q_out=None, stream=None):
+        return draft_layer_append(q, k, v, rope, *self.tensors, q_start, kv_len, table, interleaved=interleaved, q_out=q_out,
+                                  stream=stream)
+
+    def read(self, q_start, kv_len, table, rows, stream=None):
+        return draft_layer_read(*self.tensors, q_start, kv_len, table, rows, stream=stream)
+
+    def attend(self, q, q_start, kv_len, table, scale=None, window=0, sinks=0, out=None, lse=None, workspace=None, stream=None):
+        return draft_layer_attend(q, *self.tensors, q_start, kv_len, table, scale=scale, window=window, sinks=sinks, out=out,
+                                  lse=lse, workspace=workspace, stream=stream)

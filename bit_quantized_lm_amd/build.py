@@ -1,8 +1,8 @@
 """Build the draft-head shared library in-tree: bit_quantized_lm_amd/libdrafthead.so.
 
-The host translation unit (quantiser, tiler, error state) is compiled with
-g++ and -ffp-contract=off; the device translation unit (HIP kernels for
-gfx950 and their entry points) with hipcc.  Usage: python -m bit_quantized_lm_amd.build
+The host translation units (quantiser, tiler, error state, rotary table) are
+compiled with g++ and -ffp-contract=off; the device translation units (HIP
+kernels for gfx950 and their entry points) with hipcc, side by side.  Usage: python -m bit_quantized_lm_amd.build
 """
 from __future__ import annotations
 
@@ -11,10 +11,13 @@ import shutil
 import subprocess
 import sys
 import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdrafthead.so")
+HOST = ("host.cpp", "layer_host.cpp")
+DEVICE = ("device.hip", "layer_attend.hip", "layer_cache.hip")
 ARCH = os.environ.get("DRAFTHEAD_OFFLOAD_ARCH", "gfx950")
 
 
@@ -38,17 +41,25 @@ def build(verbose: bool = False) -> str:
     """Compile and link libdrafthead.so; returns its path."""
     hipcc = _hipcc()
     with tempfile.TemporaryDirectory() as tmp:
-        host_o = os.path.join(tmp, "host.o")
-        dev_o = os.path.join(tmp, "device.o")
-        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wextra",
-              "-c", os.path.join(CSRC, "host.cpp"), "-o", host_o])
-        _run([hipcc, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
-              # packed fp32 instructions are kept out of the device code
-              "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-              "-c", os.path.join(CSRC, "device.hip"), "-o", dev_o])
+        def host(src):
+            obj = os.path.join(tmp, src + ".o")
+            _run(["g++", "-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-Wextra",
+                  "-c", os.path.join(CSRC, src), "-o", obj])
+            return obj
+
+        def device(src):
+            obj = os.path.join(tmp, src + ".o")
+            _run([hipcc, f"--offload-arch={ARCH}", "-O3", "-std=c++17", "-fPIC", "-Wall",
+                  # packed fp32 instructions are kept out of the device code
+                  "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
+                  "-c", os.path.join(CSRC, src), "-o", obj])
+            return obj
+
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            objs = list(pool.map(lambda job: job[0](job[1]),
+                                 [(device, s) for s in DEVICE] + [(host, s) for s in HOST]))
         tmp_lib = LIB + ".tmp"
-        _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", host_o, dev_o,
-              "-o", tmp_lib, "-lpthread"])
+        _run([hipcc, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp_lib, "-lpthread"])
         os.replace(tmp_lib, LIB)
     if verbose:
         print(f"built {LIB}")

@@ -1,0 +1,486 @@
+// The draft layer's attention over the 8-bit cache on gfx950
+// (draft_layer_attend).
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "layer.h"
+
+namespace {
+
+using namespace dl;
+
+typedef _Float16 half8 __attribute__((ext_vector_type(8)));
+typedef _Float16 half2v __attribute__((ext_vector_type(2)));
+
+struct AttendArgs {
+  Batch b;
+  Cache c;
+  const uint16_t* q;
+  int64_t ldq;
+  int hq, group;           // group = hq / hkv
+  float scale_log2;        // scale * log2(e)
+  int window, sinks;
+  uint16_t* out;
+  float* lse;
+  int target;              // work items per head that fill the card
+  uint32_t* arrived;       // [kMaxSlots] zero between calls
+  float* part;             // [slot] partial results
+};
+
+// ------------------------------------------------------------------ the work
+// A sequence's rows for one kv head are its query heads' rows, token after
+// token: row x = (x / group)-th new token, head x % group of the kv head's.
+// Tiles of R such rows share each key and value that they load.  A tile's
+// visible tokens, as groups of 32, are cut into `splits` parts where the batch
+// has too few tiles to fill the card, each part a workgroup.
+constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kTargetBlocks = 1024;     // workgroups that fill the card
+constexpr int kMinSplitGroups = 4;      // least groups of 32 tokens a workgroup is split down to
+constexpr int kMaxSlots = 2 * (kTargetBlocks + DL_MAX_HEADS);
+constexpr size_t kArrivedBytes = (kMaxSlots * sizeof(uint32_t) + 255) / 256 * 256;
+
+struct Range {   // groups of 32 tokens a tile sees: first `ns` groups, then g0 .. g0 + n - ns - 1
+  int ns, g0, n;
+};
+
+__device__ __forceinline__ Range visible(const AttendArgs& A, int p_first, int p_last) {
+  Range r{0, 0, 0};
+  const int cap = A.b.max_pages << A.c.page_shift;
+  const int hi = (min(p_last + 1, cap) + 31) >> 5;   // groups up to the last visible token
+  if (p_last < 0) return r;
+  if (A.window > 0) {
+    const int low = p_first - A.window + 1;
+    if (low > 0) r.g0 = min(low >> 5, hi);
+    r.ns = min((min(A.sinks, cap) + 31) >> 5, r.g0);
+  }
+  r.n = r.ns + hi - r.g0;
+  return r;
+}
+
+struct Item {
+  int seq, tile, split, splits;
+  int slot;   // partial slot of split 0 (splits > 1)
+};
+
+// The batch's plan, computed by every wave from the lengths alone: parts of
+// `chunk` groups such that about A.target items per head come out.
+template <int R>
+__device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w) {
+  const int lane = threadIdx.x & 63;
+  auto tiles_of = [&](const Seq& q) { return (int)(((int64_t)q.n * A.group + R - 1) / R); };
+  auto groups_of = [&](const Seq& q) {   // of the tile that sees most
+    if (q.n == 0) return 0;
+    const int tokens = min(q.n, R / A.group + 2);
+    return visible(A, q.len - tokens, q.len - 1).n;
+  };
+  double sum = 0.0;
+  for (int s = lane; s < A.b.n_seq; s += 64) {
+    const Seq q = load_seq(A.b, s);
+    sum += (double)tiles_of(q) * groups_of(q);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
+  const int chunk = max(kMinSplitGroups, (int)fmin(ceil(sum / A.target), 1e9));
+  int slot0 = 0;
+  for (int base = 0; base < A.b.n_seq; base += 64) {
+    const int s = base + lane;
+    int tiles = 0, splits = 1;
+    if (s < A.b.n_seq) {
+      const Seq q = load_seq(A.b, s);
+      tiles = tiles_of(q);
+      splits = max(1, (groups_of(q) + chunk - 1) / chunk);
+    }
+    const int items = tiles * splits, slots = splits > 1 ? items : 0;
+    const int isum = wave_inclusive_sum(items), ssum = wave_inclusive_sum(slots);
+    const int total = __builtin_amdgcn_readlane(isum, 63);
+    if (item < total) {
+      const int at = __builtin_ctzll(__ballot(isum > item));
+      w.seq = base + at;
+      w.splits = __builtin_amdgcn_readlane(splits, at);
+      const int rest = item - (__builtin_amdgcn_readlane(isum, at) - __builtin_amdgcn_readlane(items, at));
+      w.tile = rest / w.splits;
+      w.split = rest % w.splits;
+      w.slot = slot0 + __builtin_amdgcn_readlane(ssum, at) - __builtin_amdgcn_readlane(slots, at) + rest - w.split;
+      return true;
+    }
+    item -= total;
+    slot0 += __builtin_amdgcn_readlane(ssum, 63);
+  }
+  return false;
+}
+
+// --------------------------------------------------------------- conversions
+// Eight code bytes (value + 128) as fp16: 0x6400 | u is 1024 + u, and
+// subtracting 1152 leaves the signed code exactly.
+__device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
+  const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
+  u32x4 w;
+  const uint32_t src[2] = {a, b};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, src[i], 0x04010400u)) - off);
+    w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, src[i], 0x04030402u)) - off);
+  }
+  return __builtin_bit_cast(half8, w);
+}
+
+__device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// A row's query fragments, lane (hi, lo) holding elements 64 f + 16 hi ..
+// + 15 of the tile's row lo, as fp16 scaled by 2^-e so that the row's largest
+// element is in [2^14, 2^15).  Returns scale_log2 * 2^e.  A zero row keeps 1;
+// an infinite or NaN element makes its own row NaN and no other.
+template <int D>
+__device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bool valid, float scale_log2, half8 (&frag)[D / 32]) {
+  const int hi = (threadIdx.x & 63) >> 4;
+  u32x4 raw[D / 32];
+  uint32_t top = 0;
+#pragma unroll
+  for (int f = 0; f < D / 32; ++f) {
+    raw[f] = valid ? *reinterpret_cast<const u32x4*>(row + f / 2 * 64 + hi * 16 + (f & 1) * 8) : u32x4{0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) top = max(top, max(raw[f][i] & 0x7FFFu, (raw[f][i] >> 16) & 0x7FFFu));
+  }
+  top = max(top, __shfl_xor(top, 16));
+  top = max(top, __shfl_xor(top, 32));
+  const int e = max((int)(top >> 7) - 127, -100) - 14;   // a row below 2^-100 stays below 2^14
+  const float up = __builtin_ldexpf(1.0f, -e);
+#pragma unroll
+  for (int f = 0; f < D / 32; ++f)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      frag[f][2 * i] = (_Float16)(bf16_lo(raw[f][i]) * up);
+      frag[f][2 * i + 1] = (_Float16)(bf16_hi(raw[f][i]) * up);
+    }
+  return __builtin_ldexpf(scale_log2, e);
+}
+
+// Online softmax of one row: weights are 2^(x - m) with x = z log2(e) +
+// log2(value scale), so that a weight times a value code is the value's whole
+// share, whatever its page's scale, and m near the running maximum of x; l sums
+// the weights over the value scales again.  m is set kHead below the maximum and
+// moves only when some x exceeds it by more than kHead + kSlack: the sums need
+// no rescaling in most steps, weights stay below 2^15 (fp16's largest is just
+// under 2^16), and one keeps its 11 bits down to 2^-21 of the largest.
+constexpr float kHead = 7.0f, kSlack = 8.0f;
+constexpr float kLowest = -1e30f;   // m before the first visible token; finite, so no inf - inf arises
+
+// ------------------------------------------------------- few rows: streaming
+// R = 16 MT rows against a stream of groups of 32 tokens.  Each wave takes
+// every kWaves-th group of its workgroup's part, straight from global memory
+// into the fragments (each load instruction 1 KiB without gaps), so nothing is
+// shared until the waves' results are joined.  S^T = K Q^T puts a row's
+// weights into the lanes and order that the next product takes its columns in
+// (O^T = V^T P^T), so they never leave their registers.
+template <int D, int MT>
+__global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
+  constexpr int R = 16 * MT, F = D / 32, C = D / 16;
+  constexpr int kRow = D + 4;
+  __shared__ __align__(16) float o_lds[kWaves][16][kRow];
+  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+  __shared__ int last_lds;
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
+  const int head = blockIdx.x % A.c.hkv;
+  Item w;
+  if (!find_work<R>(A, blockIdx.x / A.c.hkv, w)) return;
+  const Seq q = load_seq(A.b, w.seq);
+  const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
+  const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+
+  half8 qf[MT][F];
+  float qs[MT], m[MT], l[MT];
+  int pos[MT];
+  f32x4 o[MT][C];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) {
+    const int x = x0 + t * 16 + lo;
+    const bool valid = t * 16 + lo < rows;
+    pos[t] = valid ? q.begin + x / A.group : -1;
+    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
+    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
+    m[t] = kLowest;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const Range see = visible(A, p_first, p_last);
+  const int from = (int)((int64_t)see.n * w.split / w.splits), to = (int)((int64_t)see.n * (w.split + 1) / w.splits);
+  const size_t page_bytes = (size_t)D << A.c.page_shift;
+  for (int base = from + wave; base < to; base += 64 * kWaves) {
+    // lane i: page and scales of the wave's i-th group from here
+    const int n_mine = base + lane * kWaves, g_mine = n_mine < see.ns ? n_mine : n_mine - see.ns + see.g0;
+    const int id_mine = n_mine < to ? page_id(A.b, A.c.n_pages, w.seq, g_mine >> (A.c.page_shift - 5)) : -1;
+    const size_t at_mine = (size_t)max(id_mine, 0) * A.c.hkv + head;
+    const float ks_mine = A.c.ks[at_mine], vs_mine = fmaxf(A.c.vs[at_mine], kMinScale);
+    const int count = min(64, (to - base + kWaves - 1) / kWaves);
+    for (int i = 0; i < count; ++i) {
+      const int n = base + i * kWaves, g = n < see.ns ? n : n - see.ns + see.g0;
+      const int id = __builtin_amdgcn_readlane(id_mine, i);
+      if (id < 0) continue;
+      const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i));
+      const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_mine), i));
+      const size_t off = ((size_t)id * A.c.hkv + head) * page_bytes + (size_t)(g & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
+      const u32x4* kc = reinterpret_cast<const u32x4*>(A.c.k + off) + lane;
+      const u32x4* vc = reinterpret_cast<const u32x4*>(A.c.v + off) + lane;
+      u32x4 kw[F], vw[F];
+#pragma unroll
+      for (int f = 0; f < F; ++f) kw[f] = kc[f * 64];
+#pragma unroll
+      for (int f = 0; f < F; ++f) vw[f] = vc[f * 64];
+      f32x4 s[MT][2];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const half8 a = codes_to_half(kw[f][0], kw[f][1]), b = codes_to_half(kw[f][2], kw[f][3]);
+        const int tt = f / (D / 64), c = f % (D / 64);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          s[t][tt] = mfma(a, qf[t][2 * c], s[t][tt]);
+          s[t][tt] = mfma(b, qf[t][2 * c + 1], s[t][tt]);
+        }
+      }
+      const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
+      const int tok = g * 32 + hi * 4;
+      const bool edge = g * 32 + 31 > p_first || (A.window > 0 && g * 32 <= p_last - A.window && g * 32 + 31 >= A.sinks);
+      half8 pf[MT];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const float c = ks * qs[t];
+        float x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = s[t][j >> 2][j & 3] * c;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int at = tok + (j >> 2) * 16 + (j & 3);
+            const bool seen = at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
+            x[j] = seen ? x[j] : -INFINITY;
+          }
+        }
+        float top = x[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+        top += lv;
+        if (__any(top > m[t] + (kHead + kSlack))) {
+          top = fmaxf(top, __shfl_xor(top, 16));
+          top = fmaxf(top, __shfl_xor(top, 32));
+          const float next = fmaxf(m[t], top - kHead), down = __builtin_amdgcn_exp2f(m[t] - next);
+          m[t] = next;
+          l[t] *= down;
+#pragma unroll
+          for (int cc = 0; cc < C; ++cc) o[t][cc] *= down;
+        }
+        const float shift = lv - m[t];
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float p = __builtin_amdgcn_exp2f(x[j] + shift);
+          sum += p;
+          pf[t][j] = (_Float16)p;
+        }
+        l[t] = fmaf(sum, rv, l[t]);
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f) {
+        const half8 a = codes_to_half(vw[f][0], vw[f][1]), b = codes_to_half(vw[f][2], vw[f][3]);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          o[t][2 * f] = mfma(a, pf[t], o[t][2 * f]);
+          o[t][2 * f + 1] = mfma(b, pf[t], o[t][2 * f + 1]);
+        }
+      }
+    }
+  }
+
+  // Join the waves, 16 rows at a time, then either the result or this part's
+  // share of it.
+  float* slot = A.part + (size_t)(w.slot * A.c.hkv + head) * (R * (D + 2));   // this tile's parts: slot + split * hkv
+  const size_t slot_step = (size_t)A.c.hkv * (R * (D + 2));
+  for (int t = 0; t < MT; ++t) {
+    if (t * 16 >= rows) break;
+    if (t) __syncthreads();
+#pragma unroll
+    for (int tt = 0; tt < MT; ++tt)
+      if (tt == t) {
+        float sum = l[tt];
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (hi == 0) {
+          m_lds[wave][lo] = m[tt];
+          l_lds[wave][lo] = sum;
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&o_lds[wave][lo][c * 16 + hi * 4]) = o[tt][c];
+      }
+    __syncthreads();
+    const int r = tid >> 4, x = x0 + t * 16 + r;
+    if (t * 16 + r < rows) {
+      float top = m_lds[0][r], sum = 0.0f, share[kWaves];
+#pragma unroll
+      for (int v = 1; v < kWaves; ++v) top = fmaxf(top, m_lds[v][r]);
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        share[v] = __builtin_amdgcn_exp2f(m_lds[v][r] - top);
+        sum += l_lds[v][r] * share[v];
+      }
+      const bool none = sum == 0.0f;
+      const float inv = none ? 0.0f : 1.0f / sum;
+      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+#pragma unroll
+      for (int e = (tid & 15) * 4; e < D; e += 64) {
+        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&o_lds[v][r][e]);
+        if (w.splits == 1) {
+          y *= inv;
+          *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+        } else {
+          float* at = slot + w.split * slot_step + (t * 16 + r) * D + e;
+          *reinterpret_cast<u32x2*>(at) = __builtin_bit_cast(u32x4, y).xy;
+          *reinterpret_cast<u32x2*>(at + 2) = __builtin_bit_cast(u32x4, y).zw;
+        }
+      }
+      if ((tid & 15) == 0) {
+        if (w.splits > 1) {
+          float* at = slot + w.split * slot_step + R * D + (t * 16 + r) * 2;
+          at[0] = top;
+          at[1] = sum;
+        } else if (A.lse) {
+          A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+        }
+      }
+    }
+  }
+  if (w.splits == 1) return;
+
+  // The last part to arrive joins them all, in the parts' order, so the
+  // result does not depend on which one that is.
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");   // each wave's own stores, before the count
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t* count = A.arrived + w.slot * A.c.hkv + head;
+    const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last_lds = before == (uint32_t)w.splits - 1;
+    if (last_lds) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last_lds) return;
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+  for (int i = tid; i < rows * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), e = i % (D / 4) * 4, x = x0 + r;
+    float top = kLowest;
+    for (int v = 0; v < w.splits; ++v) top = fmaxf(top, slot[v * slot_step + R * D + r * 2]);
+    float sum = 0.0f;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int v = 0; v < w.splits; ++v) {
+      const float* at = slot + v * slot_step;
+      const float share = __builtin_amdgcn_exp2f(at[R * D + r * 2] - top);
+      sum += at[R * D + r * 2 + 1] * share;
+      const u32x2 a = *reinterpret_cast<const u32x2*>(at + r * D + e), b = *reinterpret_cast<const u32x2*>(at + r * D + e + 2);
+      y += share * __builtin_bit_cast(f32x4, u32x4{a[0], a[1], b[0], b[1]});
+    }
+    const bool none = sum == 0.0f;
+    y *= none ? 0.0f : 1.0f / sum;
+    const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+    *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+    if (e == 0 && A.lse) A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+  }
+}
+
+// ------------------------------------------------------------------- launch
+// Rows a tile of the launch holds: as many 16s as an average sequence's rows
+// for one kv head need, up to 64 (32 at D = 256, whose sums fill the
+// registers at 64).
+int tile_rows(int T, int n_seq, int hq, int hkv, int D) {
+  const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
+  return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+}
+
+int target_items(int hkv) { return std::max(1, kTargetBlocks / hkv); }
+
+size_t workspace_bytes(int T, int n_seq, int hq, int hkv, int D) {
+  const size_t slots = 2 * (size_t)target_items(hkv) * hkv;
+  return kArrivedBytes + slots * tile_rows(T, n_seq, hq, hkv, D) * (D + 2) * sizeof(float);
+}
+
+template <int D>
+int launch(const AttendArgs& A, int R, hipStream_t s) {
+  const int64_t rows = (int64_t)A.b.T * A.group;
+  // tiles: sum over the sequences of ceil(rows / R), each with a row of its own
+  const int64_t tiles = std::min<int64_t>((rows + (int64_t)A.b.n_seq * (R - 1)) / R, rows);
+  const int64_t grid = (tiles + A.target) * A.c.hkv;
+  if (grid > 0x7FFFFFFF) return dh::fail(DH_EUNSUP, "attend: too many rows for one launch");
+  const dim3 g((unsigned)grid), b(kThreads);
+  if (R == 16)
+    hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, b, 0, s, A);
+  else if (R == 32)
+    hipLaunchKernelGGL((attend_stream_kernel<D, 2>), g, b, 0, s, A);
+  else if constexpr (D < 256)
+    hipLaunchKernelGGL((attend_stream_kernel<D, 4>), g, b, 0, s, A);
+  return launched("attend_stream_kernel");
+}
+
+}  // namespace
+
+extern "C" {
+
+int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t* bytes) {
+  if (!bytes) return dh::fail(DH_EINVAL, "workspace_bytes: null pointer");
+  int rc = check_heads("workspace_bytes", hq, hkv, D);
+  if (rc) return rc;
+  if ((rc = check_rows("workspace_bytes", T, n_seq))) return rc;
+  *bytes = workspace_bytes(T, n_seq, hq, hkv, D);
+  return dh::ok();
+}
+
+int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const uint8_t* v_codes,
+                       const float* k_scale, const float* v_scale, int n_pages, int page, const int32_t* q_start,
+                       const int32_t* kv_len, const int32_t* table, int n_seq, int max_pages, int T, int hq,
+                       int hkv, int D, float scale, int window, int sinks, void* out, float* lse, void* workspace,
+                       size_t workspace_bytes_given, void* stream) {
+  const char* who = "attend";
+  int rc = check_heads(who, hq, hkv, D);
+  if (rc) return rc;
+  if ((rc = check_rows(who, T, n_seq))) return rc;
+  AttendArgs A{};
+  A.b = Batch{q_start, kv_len, table, n_seq, max_pages, T};
+  A.c = Cache{const_cast<uint8_t*>(k_codes), const_cast<uint8_t*>(v_codes), const_cast<float*>(k_scale),
+              const_cast<float*>(v_scale), n_pages, page_shift_of(page), hkv};
+  if ((rc = check_cache(who, A.c, page, A.b))) return rc;
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return dh::fail(DH_EINVAL, "attend: scale must be finite and > 0");
+  if (window < 0 || sinks < 0) return dh::fail(DH_EINVAL, "attend: window and sinks must be >= 0 (got %d, %d)", window, sinks);
+  if (T == 0) return dh::ok();
+  if ((rc = check_stride(who, "q", q, ldq, (int64_t)hq * D))) return rc;
+  if (!out || !aligned(out, 16)) return dh::fail(DH_EINVAL, "attend: out must be a 16-byte aligned pointer");
+  if (lse && !aligned(lse, 4)) return dh::fail(DH_EINVAL, "attend: lse must be 4-byte aligned");
+  if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "attend: workspace must be a 16-byte aligned pointer");
+  const size_t need = workspace_bytes(T, n_seq, hq, hkv, D);
+  if (workspace_bytes_given < need)
+    return dh::fail(DH_EINVAL, "attend: workspace of %zu bytes is below the %zu needed", workspace_bytes_given, need);
+  A.q = static_cast<const uint16_t*>(q);
+  A.ldq = ldq;
+  A.hq = hq;
+  A.group = hq / hkv;
+  A.scale_log2 = scale * 1.44269504088896f;
+  A.window = window < DL_MAX_POSITIONS ? window : 0;   // past every position: no window
+  A.sinks = std::min(sinks, DL_MAX_POSITIONS);
+  A.out = static_cast<uint16_t*>(out);
+  A.lse = lse;
+  A.target = target_items(hkv);
+  A.arrived = static_cast<uint32_t*>(workspace);
+  A.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kArrivedBytes);
+  const int R = tile_rows(T, n_seq, hq, hkv, D);
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  switch (D) {
+    case 64: return launch<64>(A, R, st);
+    case 128: return launch<128>(A, R, st);
+    default: return launch<256>(A, R, st);
+  }
+}
+
+}  // extern "C"
