@@ -67,72 +67,77 @@ def draft_layer_rope_table(positions: int, rot: int, base: float = 10000.0, fact
 
 
 # ------------------------------------------------------------------ device side
+# The checks run before every launch, so each is one expression that formats
+# nothing unless it fails.
 def _need(ok, text):
     if not ok:
         raise ValueError(text)
 
 
-def _rows3(name, t, dev):
-    """A bf16 [T][heads][D] tensor whose rows may have gaps; its row stride."""
-    import torch
-    _need(t.dtype == torch.bfloat16 and t.dim() == 3, f"{name} must be a bf16 tensor [T][heads][D]")
-    _need(t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
-    if t.shape[0] == 0:
-        return t.shape[1] * t.shape[2]
-    _need(t.stride(2) == 1 and (t.shape[1] == 1 or t.stride(1) == t.shape[2]), f"{name}'s heads must be contiguous in a row")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _wrong(name, t, dtype, shape, dev):
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {dev} "
+                     f"(the current one), not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _whole(name, t, dtype, shape, dev):
-    _need(t.dtype == dtype and tuple(t.shape) == tuple(shape) and t.is_contiguous(),
-          f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} {tuple(t.shape)}")
-    _need(t.device == dev, f"{name} is on {t.device}, the cache on {dev}")
+def _rows3(name, t, dev, heads, d, torch):
+    """Row stride of a bf16 [T][heads][D] tensor whose rows may have gaps (heads None: any number)."""
+    shape = t.shape
+    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or t.get_device() != dev:
+        _wrong(name, t, torch.bfloat16, ("T", "heads" if heads is None else heads, d), dev)
+    if shape[0] == 0:
+        return shape[1] * d
+    row, head, one = t.stride()
+    if one != 1 or (head != d and shape[1] != 1):
+        raise ValueError(f"{name}'s heads must be contiguous in a row")
+    return row if shape[0] > 1 else shape[1] * d
 
 
-def _cache(k_codes, v_codes, k_scale, v_scale):
-    """Checks a cache's four tensors; (device, pages, kv heads, page, D)."""
-    import torch
-    _need(k_codes.dim() == 4, "k_codes must be [pages][heads][page][D]")
-    dev, shape = k_codes.device, k_codes.shape
-    _need(dev.type == "cuda" and dev.index == torch.cuda.current_device(), f"the cache must be on the current GPU, not on {dev}")
-    _whole("k_codes", k_codes, torch.uint8, shape, dev)
-    _whole("v_codes", v_codes, torch.uint8, shape, dev)
-    _whole("k_scale", k_scale, torch.float32, shape[:2], dev)
-    _whole("v_scale", v_scale, torch.float32, shape[:2], dev)
+def _cache(k_codes, v_codes, k_scale, v_scale, torch):
+    """Checks a cache's four tensors; (GPU index, pages, kv heads, page, D)."""
+    dev, shape = torch.cuda.current_device(), k_codes.shape
+    if len(shape) != 4:
+        raise ValueError("k_codes must be [pages][heads][page][D]")
+    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
+        if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+            _wrong(name, t, torch.uint8, shape, dev)
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t.dtype is not torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or t.get_device() != dev:
+            _wrong(name, t, torch.float32, shape[:2], dev)
     return dev, *shape
 
 
-def _batch(q_start, kv_len, table, dev):
+def _batch(q_start, kv_len, table, dev, torch):
     """Checks a batch's tensors; (sequences, pages a sequence)."""
-    import torch
-    _need(kv_len.dim() == 1 and table.dim() == 2, "kv_len must be [sequences] and table [sequences][pages]")
-    n = kv_len.shape[0]
-    _whole("kv_len", kv_len, torch.int32, (n,), dev)
-    _whole("q_start", q_start, torch.int32, (n + 1,), dev)
-    _whole("table", table, torch.int32, (n, table.shape[1]), dev)
-    return n, table.shape[1]
+    if kv_len.dim() != 1 or table.dim() != 2:
+        raise ValueError("kv_len must be [sequences] and table [sequences][pages]")
+    n, m = table.shape
+    for name, t, size in (("kv_len", kv_len, n), ("q_start", q_start, n + 1), ("table", table, n)):
+        if t.dtype is not torch.int32 or t.shape[0] != size or not t.is_contiguous() or t.get_device() != dev:
+            _wrong(name, t, torch.int32, (size, m) if name == "table" else (size,), dev)
+    if q_start.dim() != 1:
+        _wrong("q_start", q_start, torch.int32, (n + 1,), dev)
+    return n, m
 
 
-def _out(given, name, shape, dtype, dev, stream):
+def _out(given, name, shape, dtype, dev, stream, torch):
     """The caller's tensor, checked, or a new one (kept for `stream`, if that is not the current one)."""
-    import torch
     if given is not None:
-        _whole(name, given, dtype, shape, dev)
+        if given.dtype is not dtype or given.shape != shape or not given.is_contiguous() or given.get_device() != dev:
+            _wrong(name, given, dtype, shape, dev)
         return given
     t = torch.empty(shape, dtype=dtype, device=dev)
-    _keep_for(t, stream)
+    if stream is not None:
+        _keep_for(t, stream, torch)
     return t
 
 
-def _keep_for(t, stream):
+def _keep_for(t, stream, torch):
     """Tells torch's allocator that `t`, made on the current stream, is used on `stream` too."""
-    import torch
-    if stream is None:
-        return
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
-    if stream.cuda_stream != torch.cuda.current_stream(t.device).cuda_stream:
-        stream.wait_stream(torch.cuda.current_stream(t.device))   # the memory may still be in use there
+    here = torch.cuda.current_stream(t.device)
+    if stream.cuda_stream != here.cuda_stream:
+        stream.wait_stream(here)   # the memory's last use there comes first
         t.record_stream(stream)
 
 
@@ -147,22 +152,22 @@ def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_star
     (q_out may be q itself where q has no gaps)."""
     import torch
     lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
-    ldk, ldv = _rows3("k", k, dev), _rows3("v", v, dev)
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
+    ldk, ldv = _rows3("k", k, dev, hkv, d, torch), _rows3("v", v, dev, hkv, d, torch)
     rows = k.shape[0]
-    _need(tuple(k.shape) == (rows, hkv, d) and tuple(v.shape) == (rows, hkv, d), f"k and v must be [T][{hkv}][{d}]")
+    _need(v.shape[0] == rows, "k and v must have as many rows")
     hq, ldq = hkv, 0
     if q is None:
         _need(q_out is None, "q_out needs q")
     else:
-        ldq, hq = _rows3("q", q, dev), q.shape[1]
-        _need(q.shape[0] == rows and q.shape[2] == d, f"q must be [{rows}][heads][{d}]")
-        q_out = _out(q_out, "q_out", (rows, hq, d), torch.bfloat16, dev, stream)
+        ldq, hq = _rows3("q", q, dev, None, d, torch), q.shape[1]
+        _need(q.shape[0] == rows, "q and k must have as many rows")
+        q_out = _out(q_out, "q_out", (rows, hq, d), torch.bfloat16, dev, stream, torch)
     positions = rot = 0
     if rope is not None:
-        _need(rope.dim() == 3 and rope.shape[2] == 2, "rope must be [positions][rot/2][2]")
-        _whole("rope", rope, torch.float32, rope.shape, dev)
+        if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() or rope.get_device() != dev:
+            _wrong("rope", rope, torch.float32, ("positions", "rot/2", 2), dev)
         positions, rot = rope.shape[0], rope.shape[1] * 2
     B._check(lib.draft_layer_append(
         None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, None if rope is None else rope.data_ptr(),
@@ -178,11 +183,11 @@ def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table,
     [rows][hkv][D]."""
     import torch
     lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
     shape = (max(rows, 0), hkv, d)
-    k_out = _out(k_out, "k_out", shape, torch.bfloat16, dev, stream)
-    v_out = _out(v_out, "v_out", shape, torch.bfloat16, dev, stream)
+    k_out = _out(k_out, "k_out", shape, torch.bfloat16, dev, stream, torch)
+    v_out = _out(v_out, "v_out", shape, torch.bfloat16, dev, stream, torch)
     B._check(lib.draft_layer_read(
         k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page, q_start.data_ptr(),
         kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hkv, d, k_out.data_ptr(), v_out.data_ptr(),
@@ -215,17 +220,18 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     None).  Returns (out bf16 [T][hq][D], lse fp32 [T][hq])."""
     import torch
     lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
-    ldq = _rows3("q", q, dev)
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
+    ldq = _rows3("q", q, dev, None, d, torch)
     rows, hq = q.shape[0], q.shape[1]
-    _need(q.shape[2] == d, f"q must be [T][heads][{d}]")
-    out = _out(out, "out", (rows, hq, d), torch.bfloat16, dev, stream)
-    lse = _out(lse, "lse", (rows, hq), torch.float32, dev, stream)
+    out = _out(out, "out", (rows, hq, d), torch.bfloat16, dev, stream, torch)
+    lse = _out(lse, "lse", (rows, hq), torch.float32, dev, stream, torch)
     if workspace is None:
         workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
-        _keep_for(workspace, stream)
-    _need(workspace.device == dev and workspace.is_contiguous(), f"the workspace must be contiguous on {dev}")
+        if stream is not None:
+            _keep_for(workspace, stream, torch)
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be a contiguous tensor on GPU {dev}")
     B._check(lib.draft_layer_attend(
         q.data_ptr(), ldq, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page,
         q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,

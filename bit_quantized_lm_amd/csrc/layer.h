@@ -49,14 +49,35 @@ __device__ __forceinline__ Seq load_seq(const Batch& b, int s) {
   return q;
 }
 
+// One step of a scan over the wave's lanes: `x` moved by the DPP control, 0
+// where no lane stands there.
+template <int kControl, int kRows>
+__device__ __forceinline__ int moved(int x) {
+  return __builtin_amdgcn_update_dpp(0, x, kControl, kRows, 0xf, false);
+}
+
+// Inclusive sums over the lanes: within rows of 16 (shifts by 1, 2, 4, 8), then
+// row 0's and 2's last lane to the rows after them, then the lower half's.
 __device__ __forceinline__ int wave_inclusive_sum(int x) {
-  const int lane = threadIdx.x & 63;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int y = __shfl_up(x, d);
-    if (lane >= d) x += y;
-  }
+  x += moved<0x111, 0xf>(x);
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  x += moved<0x118, 0xf>(x);
+  x += moved<0x142, 0xa>(x);
+  x += moved<0x143, 0xc>(x);
   return x;
+}
+
+// The wave's sum, in every lane.
+__device__ __forceinline__ float wave_sum(float x) {
+  auto add = [&](auto step) { x += __uint_as_float((uint32_t)step((int)__float_as_uint(x))); };
+  add([](int v) { return moved<0x111, 0xf>(v); });
+  add([](int v) { return moved<0x112, 0xf>(v); });
+  add([](int v) { return moved<0x114, 0xf>(v); });
+  add([](int v) { return moved<0x118, 0xf>(v); });
+  add([](int v) { return moved<0x142, 0xa>(v); });
+  add([](int v) { return moved<0x143, 0xc>(v); });
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
 }
 
 // Work items are numbered over the sequences in order, count(sequence) each.

@@ -35,7 +35,7 @@ struct AttendArgs {
 // visible tokens, as groups of 32, are cut into `splits` parts where the batch
 // has too few tiles to fill the card, each part a workgroup.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kTargetBlocks = 1024;     // workgroups that fill the card
+constexpr int kTargetBlocks = 512;      // workgroups that fill the card
 constexpr int kMinSplitGroups = 4;      // least groups of 32 tokens a workgroup is split down to
 constexpr int kMaxSlots = 2 * (kTargetBlocks + DL_MAX_HEADS);
 constexpr size_t kArrivedBytes = (kMaxSlots * sizeof(uint32_t) + 255) / 256 * 256;
@@ -64,7 +64,8 @@ struct Item {
 };
 
 // The batch's plan, computed by every wave from the lengths alone: parts of
-// `chunk` groups such that about A.target items per head come out.
+// `chunk` groups such that about A.target items per head come out (at most that
+// and one a tile).
 template <int R>
 __device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w) {
   const int lane = threadIdx.x & 63;
@@ -74,14 +75,14 @@ __device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w
     const int tokens = min(q.n, R / A.group + 2);
     return visible(A, q.len - tokens, q.len - 1).n;
   };
-  double sum = 0.0;
+  float sum = 0.0f;
   for (int s = lane; s < A.b.n_seq; s += 64) {
     const Seq q = load_seq(A.b, s);
-    sum += (double)tiles_of(q) * groups_of(q);
+    sum += (float)tiles_of(q) * (float)groups_of(q);
   }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
-  const int chunk = max(kMinSplitGroups, (int)fmin(ceil(sum / A.target), 1e9));
+  // 0.1% more than the sum, so that no rounding of it can bring more items than A.target and a tile each
+  sum = wave_sum(sum) * 1.001f;
+  const int chunk = max(kMinSplitGroups, (int)fminf(ceilf(sum / (float)A.target), 1e9f));
   int slot0 = 0;
   for (int base = 0; base < A.b.n_seq; base += 64) {
     const int s = base + lane;
@@ -168,6 +169,100 @@ __device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bo
 constexpr float kHead = 7.0f, kSlack = 8.0f;
 constexpr float kLowest = -1e30f;   // m before the first visible token; finite, so no inf - inf arises
 
+// --------------------------------------------------------------- split parts
+// Partial results pass between workgroups, perhaps on different XCDs, through
+// memory written and read with agent-scope accesses: written through to where
+// every XCD sees it and read past stale copies, without flushing a cache (an
+// agent-scope release fence, which writes the XCD's L2 back, cost 200 us a call
+// at 1024 workgroups).
+__device__ __forceinline__ void publish(float* at, float a, float b) {
+  __hip_atomic_store(reinterpret_cast<unsigned long long*>(at),
+                     (unsigned long long)__float_as_uint(a) | (unsigned long long)__float_as_uint(b) << 32, __ATOMIC_RELAXED,
+                     __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ float2 published(const float* at) {
+  const unsigned long long x =
+      __hip_atomic_load(reinterpret_cast<const unsigned long long*>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return float2{__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))};
+}
+
+// The last of a tile's parts to arrive joins them all, in the parts' order, so
+// the result does not depend on which one that is.  A part is rows x D sums and
+// rows x (reference, sum of weights).  Every part's stores have reached memory
+// (vmcnt 0 in each wave, then the barrier) before its workgroup is counted.
+template <int D, int R>
+__device__ __forceinline__ void join_parts(const AttendArgs& A, const Item& w, const Seq& q, int x0, int rows, int head,
+                                           const float* slot, size_t slot_step, float* lds) {
+  __shared__ int last;
+  __shared__ float top_lds[R], inv_lds[R];
+  const int tid = threadIdx.x, lane = tid & 63;
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t* count = A.arrived + w.slot * A.c.hkv + head;
+    const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    last = before == (uint32_t)w.splits - 1;
+    if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  __syncthreads();
+  if (!last) return;
+  // a wave a row: the joint reference and the sum of weights, a lane a part
+  for (int r = tid >> 6; r < rows; r += kWaves) {
+    float top = kLowest, sum = 0.0f;
+    for (int v = lane; v < w.splits; v += 64) {
+      const float2 s = published(slot + v * slot_step + R * D + r * 2);
+      const float next = fmaxf(top, s.x);
+      sum = sum * __builtin_amdgcn_exp2f(top - next) + s.y * __builtin_amdgcn_exp2f(s.x - next);
+      top = next;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const float other = __shfl_xor(top, d), weight = __shfl_xor(sum, d), next = fmaxf(top, other);
+      sum = sum * __builtin_amdgcn_exp2f(top - next) + weight * __builtin_amdgcn_exp2f(other - next);
+      top = next;
+    }
+    if (lane == 0) {
+      const int x = x0 + r;
+      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+      const bool none = sum == 0.0f;
+      top_lds[r] = top;
+      inv_lds[r] = none ? 0.0f : 1.0f / sum;
+      if (A.lse) A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+    }
+  }
+  __syncthreads();
+  // four elements a thread; where the rows leave threads over, they take turns at the parts
+  const int items = rows * (D / 4), shares = max(1, kThreads / items);
+  for (int i0 = 0; i0 < items; i0 += kThreads) {
+    const int i = i0 + (shares > 1 ? tid % items : tid), mine = shares > 1 ? tid / items : 0;
+    const bool busy = i < items && mine < shares;
+    const int r = i / (D / 4), e = i % (D / 4) * 4;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (busy) {
+      const float top = top_lds[r];
+#pragma unroll 8
+      for (int v = mine; v < w.splits; v += shares) {
+        const float* at = slot + v * slot_step;
+        const float share = __builtin_amdgcn_exp2f(published(at + R * D + r * 2).x - top);
+        const float2 a = published(at + r * D + e), b = published(at + r * D + e + 2);
+        y += share * f32x4{a.x, a.y, b.x, b.y};
+      }
+    }
+    if (shares > 1) {
+      if (busy) *reinterpret_cast<f32x4*>(lds + (mine * items + i) * 4) = y;
+      __syncthreads();
+      if (busy && mine == 0)
+        for (int v = 1; v < shares; ++v) y += *reinterpret_cast<const f32x4*>(lds + (v * items + i) * 4);
+    }
+    if (busy && mine == 0) {
+      y *= inv_lds[r];
+      const int x = x0 + r;
+      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+      *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+    }
+  }
+}
+
 // ------------------------------------------------------- few rows: streaming
 // R = 16 MT rows against a stream of groups of 32 tokens.  Each wave takes
 // every kWaves-th group of its workgroup's part, straight from global memory
@@ -175,13 +270,18 @@ constexpr float kLowest = -1e30f;   // m before the first visible token; finite,
 // shared until the waves' results are joined.  S^T = K Q^T puts a row's
 // weights into the lanes and order that the next product takes its columns in
 // (O^T = V^T P^T), so they never leave their registers.
+template <int F>
+struct Bytes {   // a lane's codes of one group
+  u32x4 k[F], v[F];
+};
+
 template <int D, int MT>
 __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
   constexpr int R = 16 * MT, F = D / 32, C = D / 16;
   constexpr int kRow = D + 4;
+  constexpr bool kAhead = D * MT <= 256;   // beyond, a second group's bytes do not fit the registers
   __shared__ __align__(16) float o_lds[kWaves][16][kRow];
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
-  __shared__ int last_lds;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
   Item w;
@@ -217,26 +317,30 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
     const size_t at_mine = (size_t)max(id_mine, 0) * A.c.hkv + head;
     const float ks_mine = A.c.ks[at_mine], vs_mine = fmaxf(A.c.vs[at_mine], kMinScale);
     const int count = min(64, (to - base + kWaves - 1) / kWaves);
-    for (int i = 0; i < count; ++i) {
-      const int n = base + i * kWaves, g = n < see.ns ? n : n - see.ns + see.g0;
-      const int id = __builtin_amdgcn_readlane(id_mine, i);
-      if (id < 0) continue;
-      const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i));
-      const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_mine), i));
-      const size_t off = ((size_t)id * A.c.hkv + head) * page_bytes + (size_t)(g & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
+    auto group_at = [&](int i) {
+      const int n = base + i * kWaves;
+      return n < see.ns ? n : n - see.ns + see.g0;
+    };
+    auto load = [&](int i, Bytes<F>& w) {   // a page that is not there: page 0's bytes, which step() hides
+      const size_t off = ((size_t)max(__builtin_amdgcn_readlane(id_mine, i), 0) * A.c.hkv + head) * page_bytes +
+                         (size_t)(group_at(i) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
       const u32x4* kc = reinterpret_cast<const u32x4*>(A.c.k + off) + lane;
       const u32x4* vc = reinterpret_cast<const u32x4*>(A.c.v + off) + lane;
-      u32x4 kw[F], vw[F];
 #pragma unroll
-      for (int f = 0; f < F; ++f) kw[f] = kc[f * 64];
+      for (int f = 0; f < F; ++f) w.k[f] = __builtin_nontemporal_load(kc + f * 64);
 #pragma unroll
-      for (int f = 0; f < F; ++f) vw[f] = vc[f * 64];
+      for (int f = 0; f < F; ++f) w.v[f] = __builtin_nontemporal_load(vc + f * 64);
+    };
+    auto step = [&](int i, const Bytes<F>& w) {
+      const int g = group_at(i), id = __builtin_amdgcn_readlane(id_mine, i);
+      const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i));
+      const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_mine), i));
       f32x4 s[MT][2];
 #pragma unroll
       for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const half8 a = codes_to_half(kw[f][0], kw[f][1]), b = codes_to_half(kw[f][2], kw[f][3]);
+        const half8 a = codes_to_half(w.k[f][0], w.k[f][1]), b = codes_to_half(w.k[f][2], w.k[f][3]);
         const int tt = f / (D / 64), c = f % (D / 64);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
@@ -246,7 +350,8 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
       }
       const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
       const int tok = g * 32 + hi * 4;
-      const bool edge = g * 32 + 31 > p_first || (A.window > 0 && g * 32 <= p_last - A.window && g * 32 + 31 >= A.sinks);
+      const bool edge = id < 0 || g * 32 + 31 > p_first ||
+                        (A.window > 0 && g * 32 <= p_last - A.window && g * 32 + 31 >= A.sinks);
       half8 pf[MT];
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -258,7 +363,7 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int at = tok + (j >> 2) * 16 + (j & 3);
-            const bool seen = at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
+            const bool seen = id >= 0 && at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
             x[j] = seen ? x[j] : -INFINITY;
           }
         }
@@ -287,12 +392,30 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
       }
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const half8 a = codes_to_half(vw[f][0], vw[f][1]), b = codes_to_half(vw[f][2], vw[f][3]);
+        const half8 a = codes_to_half(w.v[f][0], w.v[f][1]), b = codes_to_half(w.v[f][2], w.v[f][3]);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           o[t][2 * f] = mfma(a, pf[t], o[t][2 * f]);
           o[t][2 * f + 1] = mfma(b, pf[t], o[t][2 * f + 1]);
         }
+      }
+    };
+    if constexpr (kAhead) {
+      // one group's loads are under way while the one before is worked on
+      Bytes<F> even, odd;
+      load(0, even);
+      for (int i = 0; i < count; i += 2) {
+        if (i + 1 < count) load(i + 1, odd);
+        step(i, even);
+        if (i + 1 >= count) break;
+        if (i + 2 < count) load(i + 2, even);
+        step(i + 1, odd);
+      }
+    } else {
+      for (int i = 0; i < count; ++i) {
+        Bytes<F> w;
+        load(i, w);
+        step(i, w);
       }
     }
   }
@@ -340,16 +463,13 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
           y *= inv;
           *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
         } else {
-          float* at = slot + w.split * slot_step + (t * 16 + r) * D + e;
-          *reinterpret_cast<u32x2*>(at) = __builtin_bit_cast(u32x4, y).xy;
-          *reinterpret_cast<u32x2*>(at + 2) = __builtin_bit_cast(u32x4, y).zw;
+          publish(slot + w.split * slot_step + (t * 16 + r) * D + e, y[0], y[1]);
+          publish(slot + w.split * slot_step + (t * 16 + r) * D + e + 2, y[2], y[3]);
         }
       }
       if ((tid & 15) == 0) {
         if (w.splits > 1) {
-          float* at = slot + w.split * slot_step + R * D + (t * 16 + r) * 2;
-          at[0] = top;
-          at[1] = sum;
+          publish(slot + w.split * slot_step + R * D + (t * 16 + r) * 2, top, sum);
         } else if (A.lse) {
           A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
         }
@@ -358,38 +478,7 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
   }
   if (w.splits == 1) return;
 
-  // The last part to arrive joins them all, in the parts' order, so the
-  // result does not depend on which one that is.
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");   // each wave's own stores, before the count
-  __syncthreads();
-  if (tid == 0) {
-    uint32_t* count = A.arrived + w.slot * A.c.hkv + head;
-    const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last_lds = before == (uint32_t)w.splits - 1;
-    if (last_lds) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
-  __syncthreads();
-  if (!last_lds) return;
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  for (int i = tid; i < rows * (D / 4); i += kThreads) {
-    const int r = i / (D / 4), e = i % (D / 4) * 4, x = x0 + r;
-    float top = kLowest;
-    for (int v = 0; v < w.splits; ++v) top = fmaxf(top, slot[v * slot_step + R * D + r * 2]);
-    float sum = 0.0f;
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int v = 0; v < w.splits; ++v) {
-      const float* at = slot + v * slot_step;
-      const float share = __builtin_amdgcn_exp2f(at[R * D + r * 2] - top);
-      sum += at[R * D + r * 2 + 1] * share;
-      const u32x2 a = *reinterpret_cast<const u32x2*>(at + r * D + e), b = *reinterpret_cast<const u32x2*>(at + r * D + e + 2);
-      y += share * __builtin_bit_cast(f32x4, u32x4{a[0], a[1], b[0], b[1]});
-    }
-    const bool none = sum == 0.0f;
-    y *= none ? 0.0f : 1.0f / sum;
-    const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
-    *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
-    if (e == 0 && A.lse) A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
-  }
+  join_parts<D, R>(A, w, q, x0, rows, head, slot, slot_step, &o_lds[0][0][0]);
 }
 
 // ------------------------------------------------------------------- launch
@@ -398,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
 // registers at 64).
 int tile_rows(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : 64;
+  return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : rows <= 48 ? 48 : 64;
 }
 
 int target_items(int hkv) { return std::max(1, kTargetBlocks / hkv); }
@@ -420,8 +509,12 @@ int launch(const AttendArgs& A, int R, hipStream_t s) {
     hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, b, 0, s, A);
   else if (R == 32)
     hipLaunchKernelGGL((attend_stream_kernel<D, 2>), g, b, 0, s, A);
-  else if constexpr (D < 256)
-    hipLaunchKernelGGL((attend_stream_kernel<D, 4>), g, b, 0, s, A);
+  else if constexpr (D < 256) {
+    if (R == 48)
+      hipLaunchKernelGGL((attend_stream_kernel<D, 3>), g, b, 0, s, A);
+    else
+      hipLaunchKernelGGL((attend_stream_kernel<D, 4>), g, b, 0, s, A);
+  }
   return launched("attend_stream_kernel");
 }
 
