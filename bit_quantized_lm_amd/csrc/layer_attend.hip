@@ -38,6 +38,9 @@ constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kTargetBlocks = 512;      // workgroups that fill the card
 constexpr int kMinSplitGroups = 4;      // least groups of 32 tokens a workgroup is split down to
 constexpr int kMaxSlots = 2 * (kTargetBlocks + DL_MAX_HEADS);
+constexpr int kJoinFloats = 8192;       // scratch of a tile's joining: a weight for each of its rows and parts
+template <int R>
+constexpr int kMaxSplits = kJoinFloats / R;
 constexpr size_t kArrivedBytes = (kMaxSlots * sizeof(uint32_t) + 255) / 256 * 256;
 
 struct Range {   // groups of 32 tokens a tile sees: first `ns` groups, then g0 .. g0 + n - ns - 1
@@ -64,8 +67,8 @@ struct Item {
 };
 
 // The batch's plan, computed by every wave from the lengths alone: parts of
-// `chunk` groups such that about A.target items per head come out (at most that
-// and one a tile).
+// `chunk` groups such that the items per head come near A.target, which fills
+// the card once (one a tile, and at most A.target more).
 template <int R>
 __device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w) {
   const int lane = threadIdx.x & 63;
@@ -75,14 +78,17 @@ __device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w
     const int tokens = min(q.n, R / A.group + 2);
     return visible(A, q.len - tokens, q.len - 1).n;
   };
-  float sum = 0.0f;
+  float sum = 0.0f, all = 0.0f;
   for (int s = lane; s < A.b.n_seq; s += 64) {
     const Seq q = load_seq(A.b, s);
     sum += (float)tiles_of(q) * (float)groups_of(q);
+    all += (float)tiles_of(q);
   }
   // 0.1% more than the sum, so that no rounding of it can bring more items than A.target and a tile each
   sum = wave_sum(sum) * 1.001f;
-  const int chunk = max(kMinSplitGroups, (int)fminf(ceilf(sum / (float)A.target), 1e9f));
+  all = wave_sum(all);
+  const float spare = fmaxf((float)A.target - all, 0.125f * (float)A.target);
+  const int chunk = max(kMinSplitGroups, (int)fminf(ceilf(sum / spare), 1e9f));
   int slot0 = 0;
   for (int base = 0; base < A.b.n_seq; base += 64) {
     const int s = base + lane;
@@ -90,7 +96,7 @@ __device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w
     if (s < A.b.n_seq) {
       const Seq q = load_seq(A.b, s);
       tiles = tiles_of(q);
-      splits = max(1, (groups_of(q) + chunk - 1) / chunk);
+      splits = min(max(1, (groups_of(q) + chunk - 1) / chunk), kMaxSplits<R>);
     }
     const int items = tiles * splits, slots = splits > 1 ? items : 0;
     const int isum = wave_inclusive_sum(items), ssum = wave_inclusive_sum(slots);
@@ -171,30 +177,45 @@ constexpr float kLowest = -1e30f;   // m before the first visible token; finite,
 
 // --------------------------------------------------------------- split parts
 // Partial results pass between workgroups, perhaps on different XCDs, through
-// memory written and read with agent-scope accesses: written through to where
-// every XCD sees it and read past stale copies, without flushing a cache (an
-// agent-scope release fence, which writes the XCD's L2 back, cost 200 us a call
-// at 1024 workgroups).
-__device__ __forceinline__ void publish(float* at, float a, float b) {
-  __hip_atomic_store(reinterpret_cast<unsigned long long*>(at),
-                     (unsigned long long)__float_as_uint(a) | (unsigned long long)__float_as_uint(b) << 32, __ATOMIC_RELAXED,
-                     __HIP_MEMORY_SCOPE_AGENT);
+// memory written and read with agent-scope accesses (sc1): written through to where
+// every XCD sees it and read past stale copies, without flushing a cache (with an
+// agent-scope release fence, which writes the XCD's L2 back, one row over
+// 131,072 tokens took 108 us instead of 58, a windowed batch of 32 199 instead of 63).
+constexpr int kAgentScope = 16;   // sc1
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t part_buffer(const void* p) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, 0x7FFFFFFF, 0x00027000);
 }
-__device__ __forceinline__ float2 published(const float* at) {
-  const unsigned long long x =
-      __hip_atomic_load(reinterpret_cast<const unsigned long long*>(at), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  return float2{__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32))};
+__device__ __forceinline__ void publish4(__amdgpu_buffer_rsrc_t b, int at, f32x4 x) {
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, x), b, at * 4, 0, kAgentScope);
+}
+__device__ __forceinline__ void publish2(__amdgpu_buffer_rsrc_t b, int at, float x, float y) {
+  __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(x), __float_as_uint(y)}, b, at * 4, 0, kAgentScope);
+}
+__device__ __forceinline__ f32x4 published4(__amdgpu_buffer_rsrc_t b, int at) {
+  return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, at * 4, 0, kAgentScope));
+}
+__device__ __forceinline__ float2 published2(__amdgpu_buffer_rsrc_t b, int at) {
+  const u32x2 x = __builtin_amdgcn_raw_buffer_load_b64(b, at * 4, 0, kAgentScope);
+  return float2{__uint_as_float(x[0]), __uint_as_float(x[1])};
+}
+
+// A part is R x D sums and R x (reference, sum of weights).
+template <int D, int R>
+constexpr int kPartFloats = R * (D + 2);
+
+__device__ __forceinline__ void write_lse(const AttendArgs& A, size_t row, float ref, float sum) {
+  if (A.lse) A.lse[row] = sum == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
 }
 
 // The last of a tile's parts to arrive joins them all, in the parts' order, so
-// the result does not depend on which one that is.  A part is rows x D sums and
-// rows x (reference, sum of weights).  Every part's stores have reached memory
-// (vmcnt 0 in each wave, then the barrier) before its workgroup is counted.
-template <int D, int R>
+// the result does not depend on which one that is.  Every part's stores have
+// reached memory (vmcnt 0 in each wave, then the barrier) before its workgroup
+// is counted.  `parts`: part 0 of this tile and head; part v is at v * step
+// floats.  `lds`: kJoinFloats and four a thread.
+template <int D, int R, int kThreads>
 __device__ __forceinline__ void join_parts(const AttendArgs& A, const Item& w, const Seq& q, int x0, int rows, int head,
-                                           const float* slot, size_t slot_step, float* lds) {
+                                           __amdgpu_buffer_rsrc_t parts, int step, float* lds) {
   __shared__ int last;
-  __shared__ float top_lds[R], inv_lds[R];
   const int tid = threadIdx.x, lane = tid & 63;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -206,60 +227,53 @@ __device__ __forceinline__ void join_parts(const AttendArgs& A, const Item& w, c
   }
   __syncthreads();
   if (!last) return;
-  // a wave a row: the joint reference and the sum of weights, a lane a part
-  for (int r = tid >> 6; r < rows; r += kWaves) {
-    float top = kLowest, sum = 0.0f;
+  auto row_of = [&](int r) {
+    const int x = x0 + r;
+    return (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+  };
+  // a wave a row, a lane a part: the parts' shares of the row
+  for (int r = tid >> 6; r < rows; r += kThreads / 64) {
+    float top = kLowest;
     for (int v = lane; v < w.splits; v += 64) {
-      const float2 s = published(slot + v * slot_step + R * D + r * 2);
-      const float next = fmaxf(top, s.x);
-      sum = sum * __builtin_amdgcn_exp2f(top - next) + s.y * __builtin_amdgcn_exp2f(s.x - next);
-      top = next;
+      const float2 s = published2(parts, v * step + R * D + r * 2);
+      top = fmaxf(top, s.x);
+      lds[r * w.splits + v] = s.x;
     }
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const float other = __shfl_xor(top, d), weight = __shfl_xor(sum, d), next = fmaxf(top, other);
-      sum = sum * __builtin_amdgcn_exp2f(top - next) + weight * __builtin_amdgcn_exp2f(other - next);
-      top = next;
+    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    float sum = 0.0f;
+    for (int v = lane; v < w.splits; v += 64) {
+      const float share = __builtin_amdgcn_exp2f(lds[r * w.splits + v] - top);
+      sum += share * published2(parts, v * step + R * D + r * 2).y;
+      lds[r * w.splits + v] = share;
     }
-    if (lane == 0) {
-      const int x = x0 + r;
-      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
-      const bool none = sum == 0.0f;
-      top_lds[r] = top;
-      inv_lds[r] = none ? 0.0f : 1.0f / sum;
-      if (A.lse) A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
-    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    for (int v = lane; v < w.splits; v += 64) lds[r * w.splits + v] *= inv;
+    if (lane == 0) write_lse(A, row_of(r), top, sum);
   }
   __syncthreads();
-  // four elements a thread; where the rows leave threads over, they take turns at the parts
-  const int items = rows * (D / 4), shares = max(1, kThreads / items);
+  // four elements of a row a thread; threads that are left over take turns at the parts
+  const int items = rows * (D / 4), turns = max(1, kThreads / items);
+  float* turned = lds + kJoinFloats;
   for (int i0 = 0; i0 < items; i0 += kThreads) {
-    const int i = i0 + (shares > 1 ? tid % items : tid), mine = shares > 1 ? tid / items : 0;
-    const bool busy = i < items && mine < shares;
-    const int r = i / (D / 4), e = i % (D / 4) * 4;
+    const int i = turns > 1 ? tid % items : i0 + tid, turn = turns > 1 ? tid / items : 0;
+    const bool busy = i < items && turn < turns;
+    const int r = i / (D / 4), at = r * D + i % (D / 4) * 4;
     f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
     if (busy) {
-      const float top = top_lds[r];
 #pragma unroll 8
-      for (int v = mine; v < w.splits; v += shares) {
-        const float* at = slot + v * slot_step;
-        const float share = __builtin_amdgcn_exp2f(published(at + R * D + r * 2).x - top);
-        const float2 a = published(at + r * D + e), b = published(at + r * D + e + 2);
-        y += share * f32x4{a.x, a.y, b.x, b.y};
-      }
+      for (int v = turn; v < w.splits; v += turns) y += lds[r * w.splits + v] * published4(parts, v * step + at);
     }
-    if (shares > 1) {
-      if (busy) *reinterpret_cast<f32x4*>(lds + (mine * items + i) * 4) = y;
+    if (turns > 1) {
+      if (busy && turn > 0) *reinterpret_cast<f32x4*>(turned + tid * 4) = y;
       __syncthreads();
-      if (busy && mine == 0)
-        for (int v = 1; v < shares; ++v) y += *reinterpret_cast<const f32x4*>(lds + (v * items + i) * 4);
+      if (busy && turn == 0)
+        for (int k = 1; k < turns; ++k) y += *reinterpret_cast<const f32x4*>(turned + (tid + k * items) * 4);
     }
-    if (busy && mine == 0) {
-      y *= inv_lds[r];
-      const int x = x0 + r;
-      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
-      *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
-    }
+    if (busy && turn == 0)
+      *reinterpret_cast<u32x2*>(A.out + row_of(r) * D + i % (D / 4) * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
   }
 }
 
@@ -276,11 +290,14 @@ struct Bytes {   // a lane's codes of one group
 };
 
 template <int D, int MT>
-__global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 3) void attend_stream_kernel(AttendArgs A) {
   constexpr int R = 16 * MT, F = D / 32, C = D / 16;
   constexpr int kRow = D + 4;
   constexpr bool kAhead = D * MT <= 256;   // beyond, a second group's bytes do not fit the registers
-  __shared__ __align__(16) float o_lds[kWaves][16][kRow];
+  __shared__ __align__(16) union {
+    float o[kWaves][16][kRow];
+    float join[kJoinFloats + 4 * kThreads];
+  } lds;
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
@@ -422,8 +439,8 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
 
   // Join the waves, 16 rows at a time, then either the result or this part's
   // share of it.
-  float* slot = A.part + (size_t)(w.slot * A.c.hkv + head) * (R * (D + 2));   // this tile's parts: slot + split * hkv
-  const size_t slot_step = (size_t)A.c.hkv * (R * (D + 2));
+  const __amdgpu_buffer_rsrc_t parts = part_buffer(A.part + (size_t)(w.slot * A.c.hkv + head) * kPartFloats<D, R>);
+  const int step = A.c.hkv * kPartFloats<D, R>, mine = w.split * step;
   for (int t = 0; t < MT; ++t) {
     if (t * 16 >= rows) break;
     if (t) __syncthreads();
@@ -438,7 +455,7 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
           l_lds[wave][lo] = sum;
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&o_lds[wave][lo][c * 16 + hi * 4]) = o[tt][c];
+        for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&lds.o[wave][lo][c * 16 + hi * 4]) = o[tt][c];
       }
     __syncthreads();
     const int r = tid >> 4, x = x0 + t * 16 + r;
@@ -451,71 +468,294 @@ __global__ __launch_bounds__(kThreads) void attend_stream_kernel(AttendArgs A) {
         share[v] = __builtin_amdgcn_exp2f(m_lds[v][r] - top);
         sum += l_lds[v][r] * share[v];
       }
-      const bool none = sum == 0.0f;
-      const float inv = none ? 0.0f : 1.0f / sum;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
 #pragma unroll
       for (int e = (tid & 15) * 4; e < D; e += 64) {
         f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&o_lds[v][r][e]);
+        for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&lds.o[v][r][e]);
         if (w.splits == 1) {
           y *= inv;
           *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
         } else {
-          publish(slot + w.split * slot_step + (t * 16 + r) * D + e, y[0], y[1]);
-          publish(slot + w.split * slot_step + (t * 16 + r) * D + e + 2, y[2], y[3]);
+          publish4(parts, mine + (t * 16 + r) * D + e, y);
         }
       }
       if ((tid & 15) == 0) {
-        if (w.splits > 1) {
-          publish(slot + w.split * slot_step + R * D + (t * 16 + r) * 2, top, sum);
-        } else if (A.lse) {
-          A.lse[to_row] = none ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
-        }
+        if (w.splits > 1)
+          publish2(parts, mine + R * D + (t * 16 + r) * 2, top, sum);
+        else
+          write_lse(A, to_row, top, sum);
       }
     }
   }
   if (w.splits == 1) return;
 
-  join_parts<D, R>(A, w, q, x0, rows, head, slot, slot_step, &o_lds[0][0][0]);
+  __syncthreads();   // lds becomes join_parts' scratch
+  join_parts<D, R, kThreads>(A, w, q, x0, rows, head, parts, step, &lds.join[0]);
+}
+
+// -------------------------------------------------------- many rows: shared
+// R = 16 NQ W rows: each wave holds NQ tiles of 16 rows, and the workgroup's
+// waves share the key and value fragments, converted to fp16 once, through
+// LDS.  Steps of G groups alternate between two stages: while one is worked on,
+// the next one's codes are converted into the other and the one after that is
+// on its way from memory in registers; one barrier a step.
+template <int D, int NQ, int W, int G>
+struct Shared {
+  static constexpr int R = 16 * NQ * W, F = D / 32, kThreads = 64 * W;
+  static constexpr int kUnits = G * 2 * F;                 // KiB of codes a step: keys, then values
+  static constexpr int kPer = kUnits / W;                  // of them a wave's
+  static constexpr int kStage = kUnits * 2 * 64;           // 16-byte fragments a stage
+  static constexpr size_t kLds = std::max(2 * (size_t)kStage * 16, (kJoinFloats + 4 * kThreads) * sizeof(float));
+  static_assert(kUnits % W == 0, "every wave carries as many codes");
+};
+
+template <int D, int NQ, int W, int G>
+__global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) {
+  using S = Shared<D, NQ, W, G>;
+  constexpr int R = S::R, F = S::F, C = D / 16;
+  extern __shared__ __align__(16) u32x4 stage[];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
+  const int head = blockIdx.x % A.c.hkv;
+  Item w;
+  if (!find_work<R>(A, blockIdx.x / A.c.hkv, w)) return;
+  const Seq q = load_seq(A.b, w.seq);
+  w.tile = (int)(((int64_t)q.n * A.group + R - 1) / R) - 1 - w.tile;   // the tiles that see most first
+  const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
+  const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+  // this wave's own rows; none of them: it only carries codes
+  const int mine0 = wave * 16 * NQ;
+  const int w_first = q.begin + (x0 + mine0) / A.group, w_last = q.begin + (x0 + min(rows, mine0 + 16 * NQ) - 1) / A.group;
+  const bool working = mine0 < rows;
+
+  half8 qf[NQ][F];
+  float qs[NQ], m[NQ], l[NQ];
+  int pos[NQ];
+  f32x4 o[NQ][C];
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int r = mine0 + t * 16 + lo, x = x0 + r;
+    const bool valid = r < rows;
+    pos[t] = valid ? q.begin + x / A.group : -1;
+    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
+    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
+    m[t] = kLowest;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
+  const Range see = visible(A, p_first, p_last);
+  const int from = (int)((int64_t)see.n * w.split / w.splits), to = (int)((int64_t)see.n * (w.split + 1) / w.splits);
+  const size_t page_bytes = (size_t)D << A.c.page_shift;
+  const int in_page = (1 << (A.c.page_shift - 5)) - 1;
+  // lane i: page and scales of the i-th group from `base`, 64 at a time; the
+  // loads run up to two steps ahead of the work, so theirs are kept apart
+  int id_load = -1, id_work = -1, base_load = from - 64, base_work = from - 64;
+  float ks_work = 0.0f, vs_work = 0.0f;
+  auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
+  auto page_of = [&](int n) { return n < to ? page_id(A.b, A.c.n_pages, w.seq, group_at(n) >> (A.c.page_shift - 5)) : -1; };
+  u32x4 raw[S::kPer];
+  auto load = [&](int n0) {   // groups n0 .. n0 + G - 1; one that is not there: page 0's bytes, hidden later
+    if (n0 - base_load >= 64) {
+      base_load = n0;
+      id_load = page_of(n0 + lane);
+    }
+#pragma unroll
+    for (int u = 0; u < S::kPer; ++u) {
+      const int unit = u * W + wave, g = unit / (2 * F), f = unit % F;
+      const bool key = unit / F % 2 == 0;
+      const int id = max(__builtin_amdgcn_readlane(id_load, n0 - base_load + g), 0);
+      const size_t off = ((size_t)id * A.c.hkv + head) * page_bytes + (size_t)(group_at(n0 + g) & in_page) * 32 * D;
+      raw[u] = *(reinterpret_cast<const u32x4*>((key ? A.c.k : A.c.v) + off) + f * 64 + lane);
+    }
+  };
+  auto store = [&](int which) {
+#pragma unroll
+    for (int u = 0; u < S::kPer; ++u) {
+      u32x4* at = stage + which * S::kStage + (u * W + wave) * 128 + lane;
+      at[0] = __builtin_bit_cast(u32x4, codes_to_half(raw[u][0], raw[u][1]));
+      at[64] = __builtin_bit_cast(u32x4, codes_to_half(raw[u][2], raw[u][3]));
+    }
+  };
+  if (from < to) {
+    load(from);
+    store(0);
+    if (from + G < to) load(from + G);
+    __syncthreads();
+  }
+  for (int n0 = from, which = 0; n0 < to; n0 += G, which ^= 1) {
+    if (n0 - base_work >= 64) {
+      base_work = n0;
+      id_work = page_of(n0 + lane);
+      const size_t at = (size_t)max(id_work, 0) * A.c.hkv + head;
+      ks_work = A.c.ks[at];
+      vs_work = fmaxf(A.c.vs[at], kMinScale);
+    }
+    if (n0 + G < to) {
+      store(which ^ 1);
+      if (n0 + 2 * G < to) load(n0 + 2 * G);
+    }
+    if (working) {
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        if (G > 1 && n0 + g >= to) break;
+        const int i = n0 + g - base_work, first = group_at(n0 + g) * 32;
+        const u32x4* kf = stage + which * S::kStage + g * F * 256 + lane;
+        const u32x4* vf = kf + F * 128;
+        const int id = __builtin_amdgcn_readlane(id_work, i);
+        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_work), i));
+        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_work), i));
+        f32x4 s[NQ][2];
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const half8 a = __builtin_bit_cast(half8, kf[(f * 2 + h) * 64]);
+#pragma unroll
+            for (int t = 0; t < NQ; ++t) s[t][f / (D / 64)] = mfma(a, qf[t][f % (D / 64) * 2 + h], s[t][f / (D / 64)]);
+          }
+        const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
+        const bool edge = id < 0 || first + 31 > w_first ||
+                          (A.window > 0 && first <= w_last - A.window && first + 31 >= A.sinks);
+        half8 pf[NQ];
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          float c = ks * qs[t];
+          float x[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[j] = s[t][j >> 2][j & 3];
+          if (edge) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const int at = first + hi * 4 + (j >> 2) * 16 + (j & 3);
+              const bool seen = id >= 0 && at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
+              x[j] = seen ? x[j] * c : -INFINITY;
+            }
+            c = 1.0f;
+          }
+          float top = x[0];
+#pragma unroll
+          for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
+          top = fmaf(top, c, lv);
+          if (__any(top > m[t] + (kHead + kSlack))) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float next = fmaxf(m[t], top - kHead), down = __builtin_amdgcn_exp2f(m[t] - next);
+            m[t] = next;
+            l[t] *= down;
+#pragma unroll
+            for (int cc = 0; cc < C; ++cc) o[t][cc] *= down;
+          }
+          const float shift = lv - m[t];
+          float sum = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float p = __builtin_amdgcn_exp2f(fmaf(x[j], c, shift));
+            sum += p;
+            pf[t][j] = (_Float16)p;
+          }
+          l[t] = fmaf(sum, rv, l[t]);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const half8 a = __builtin_bit_cast(half8, vf[c * 64]);
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) o[t][c] = mfma(a, pf[t], o[t][c]);
+        }
+      }
+    }
+    __syncthreads();
+  }
+
+  const __amdgpu_buffer_rsrc_t parts = part_buffer(A.part + (size_t)(w.slot * A.c.hkv + head) * kPartFloats<D, R>);
+  const int step = A.c.hkv * kPartFloats<D, R>, mine = w.split * step;
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int r = mine0 + t * 16 + lo, x = x0 + r;
+    float sum = l[t];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (r >= rows) continue;
+    if (w.splits == 1) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const f32x4 y = o[t][c] * inv;
+        *reinterpret_cast<u32x2*>(A.out + to_row * D + c * 16 + hi * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+      }
+      if (hi == 0) write_lse(A, to_row, m[t], sum);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) publish4(parts, mine + r * D + c * 16 + hi * 4, o[t][c]);
+      if (hi == 0) publish2(parts, mine + R * D + r * 2, m[t], sum);
+    }
+  }
+  if (w.splits == 1) return;
+  __syncthreads();   // the stages become join_parts' scratch
+  join_parts<D, R, S::kThreads>(A, w, q, x0, rows, head, parts, step, reinterpret_cast<float*>(stage));
 }
 
 // ------------------------------------------------------------------- launch
-// Rows a tile of the launch holds: as many 16s as an average sequence's rows
-// for one kv head need, up to 64 (32 at D = 256, whose sums fill the
-// registers at 64).
-int tile_rows(int T, int n_seq, int hq, int hkv, int D) {
+// The launch's kernel, by the rows that an average sequence has for one kv head.
+struct Plan {
+  int rows;      // a tile's
+  bool shared;   // attend_shared_kernel (else the streaming one)
+};
+Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  return rows <= 16 ? 16 : rows <= 32 || D == 256 ? 32 : rows <= 48 ? 48 : 64;
+  if (rows <= 16) return {16, false};
+  if (rows <= 64) return {64, true};
+  return {128, true};
 }
 
 int target_items(int hkv) { return std::max(1, kTargetBlocks / hkv); }
 
 size_t workspace_bytes(int T, int n_seq, int hq, int hkv, int D) {
   const size_t slots = 2 * (size_t)target_items(hkv) * hkv;
-  return kArrivedBytes + slots * tile_rows(T, n_seq, hq, hkv, D) * (D + 2) * sizeof(float);
+  return kArrivedBytes + slots * plan_for(T, n_seq, hq, hkv, D).rows * (D + 2) * sizeof(float);
+}
+
+template <int D, int NQ, int W, int G>
+hipError_t launch_shared(const AttendArgs& A, dim3 grid, hipStream_t s) {
+  using S = Shared<D, NQ, W, G>;
+  static bool attr_set = false;
+  if (!attr_set) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_shared_kernel<D, NQ, W, G>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
+    if (e != hipSuccess) return e;
+    attr_set = true;
+  }
+  hipLaunchKernelGGL((attend_shared_kernel<D, NQ, W, G>), grid, dim3(S::kThreads), S::kLds, s, A);
+  return hipSuccess;
 }
 
 template <int D>
-int launch(const AttendArgs& A, int R, hipStream_t s) {
+int launch(const AttendArgs& A, const Plan& plan, hipStream_t s) {
   const int64_t rows = (int64_t)A.b.T * A.group;
+  const int R = plan.rows;
   // tiles: sum over the sequences of ceil(rows / R), each with a row of its own
   const int64_t tiles = std::min<int64_t>((rows + (int64_t)A.b.n_seq * (R - 1)) / R, rows);
   const int64_t grid = (tiles + A.target) * A.c.hkv;
   if (grid > 0x7FFFFFFF) return dh::fail(DH_EUNSUP, "attend: too many rows for one launch");
-  const dim3 g((unsigned)grid), b(kThreads);
-  if (R == 16)
-    hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, b, 0, s, A);
-  else if (R == 32)
-    hipLaunchKernelGGL((attend_stream_kernel<D, 2>), g, b, 0, s, A);
-  else if constexpr (D < 256) {
-    if (R == 48)
-      hipLaunchKernelGGL((attend_stream_kernel<D, 3>), g, b, 0, s, A);
-    else
-      hipLaunchKernelGGL((attend_stream_kernel<D, 4>), g, b, 0, s, A);
-  }
-  return launched("attend_stream_kernel");
+  const dim3 g((unsigned)grid);
+  constexpr int G = D == 256 ? 1 : 2;
+  hipError_t e = hipSuccess;
+  if (!plan.shared)
+    hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, dim3(kThreads), 0, s, A);
+  else if (R == 64)
+    e = launch_shared<D, 1, 4, G>(A, g, s);
+  else if constexpr (D == 256)
+    e = launch_shared<D, 1, 8, 1>(A, g, s);
+  else
+    e = launch_shared<D, 2, 4, G>(A, g, s);
+  if (e != hipSuccess) return dh::fail(DH_EHIP, "attend kernel: %s", hipGetErrorString(e));
+  return launched("attend kernel");
 }
 
 }  // namespace
@@ -567,7 +807,7 @@ int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const
   A.target = target_items(hkv);
   A.arrived = static_cast<uint32_t*>(workspace);
   A.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kArrivedBytes);
-  const int R = tile_rows(T, n_seq, hq, hkv, D);
+  const Plan R = plan_for(T, n_seq, hq, hkv, D);
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   switch (D) {
     case 64: return launch<64>(A, R, st);
