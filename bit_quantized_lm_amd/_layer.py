@@ -119,13 +119,18 @@ def _batch(q_start, kv_len, table, dev, torch):
     return n, m
 
 
-def _out(given, name, shape, dtype, dev, stream, torch):
+def _raw_stream(stream, dev, torch):
+    """The hipStream_t of `stream` (None: the current one, without building torch's object for it)."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else B._stream(stream)
+
+
+def _out(given, name, like, shape, dtype, dev, stream, torch):
     """The caller's tensor, checked, or a new one (kept for `stream`, if that is not the current one)."""
     if given is not None:
         if given.dtype is not dtype or given.shape != shape or not given.is_contiguous() or given.get_device() != dev:
             _wrong(name, given, dtype, shape, dev)
         return given
-    t = torch.empty(shape, dtype=dtype, device=dev)
+    t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
         _keep_for(t, stream, torch)
     return t
@@ -163,7 +168,7 @@ def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_star
     else:
         ldq, hq = _rows3("q", q, dev, None, d, torch), q.shape[1]
         _need(q.shape[0] == rows, "q and k must have as many rows")
-        q_out = _out(q_out, "q_out", (rows, hq, d), torch.bfloat16, dev, stream, torch)
+        q_out = _out(q_out, "q_out", q, (rows, hq, d), torch.bfloat16, dev, stream, torch)
     positions = rot = 0
     if rope is not None:
         if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() or rope.get_device() != dev:
@@ -173,7 +178,7 @@ def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_star
         None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, None if rope is None else rope.data_ptr(),
         positions, rot, 1 if interleaved else 0, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         n_pages, page, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
-        None if q is None else q_out.data_ptr(), B._stream(stream)))
+        None if q is None else q_out.data_ptr(), _raw_stream(stream, dev, torch)))
     return q_out
 
 
@@ -186,12 +191,12 @@ def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table,
     dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
     n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
     shape = (max(rows, 0), hkv, d)
-    k_out = _out(k_out, "k_out", shape, torch.bfloat16, dev, stream, torch)
-    v_out = _out(v_out, "v_out", shape, torch.bfloat16, dev, stream, torch)
+    k_out = _out(k_out, "k_out", k_codes, shape, torch.bfloat16, dev, stream, torch)
+    v_out = _out(v_out, "v_out", k_codes, shape, torch.bfloat16, dev, stream, torch)
     B._check(lib.draft_layer_read(
         k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page, q_start.data_ptr(),
         kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hkv, d, k_out.data_ptr(), v_out.data_ptr(),
-        B._stream(stream)))
+        _raw_stream(stream, dev, torch)))
     return k_out, v_out
 
 
@@ -224,8 +229,8 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
     ldq = _rows3("q", q, dev, None, d, torch)
     rows, hq = q.shape[0], q.shape[1]
-    out = _out(out, "out", (rows, hq, d), torch.bfloat16, dev, stream, torch)
-    lse = _out(lse, "lse", (rows, hq), torch.float32, dev, stream, torch)
+    out = _out(out, "out", q, (rows, hq, d), torch.bfloat16, dev, stream, torch)
+    lse = _out(lse, "lse", q, (rows, hq), torch.float32, dev, stream, torch)
     if workspace is None:
         workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
         if stream is not None:
@@ -236,7 +241,7 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
         q.data_ptr(), ldq, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page,
         q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
         1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), B._stream(stream)))
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev, torch)))
     return out, lse
 
 

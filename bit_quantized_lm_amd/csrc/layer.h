@@ -68,16 +68,35 @@ __device__ __forceinline__ int wave_inclusive_sum(int x) {
   return x;
 }
 
+__device__ __forceinline__ float last_lane(float x) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
+}
+
 // The wave's sum, in every lane.
 __device__ __forceinline__ float wave_sum(float x) {
-  auto add = [&](auto step) { x += __uint_as_float((uint32_t)step((int)__float_as_uint(x))); };
-  add([](int v) { return moved<0x111, 0xf>(v); });
-  add([](int v) { return moved<0x112, 0xf>(v); });
-  add([](int v) { return moved<0x114, 0xf>(v); });
-  add([](int v) { return moved<0x118, 0xf>(v); });
-  add([](int v) { return moved<0x142, 0xa>(v); });
-  add([](int v) { return moved<0x143, 0xc>(v); });
-  return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(x), 63));
+  x += __uint_as_float((uint32_t)moved<0x111, 0xf>((int)__float_as_uint(x)));
+  x += __uint_as_float((uint32_t)moved<0x112, 0xf>((int)__float_as_uint(x)));
+  x += __uint_as_float((uint32_t)moved<0x114, 0xf>((int)__float_as_uint(x)));
+  x += __uint_as_float((uint32_t)moved<0x118, 0xf>((int)__float_as_uint(x)));
+  x += __uint_as_float((uint32_t)moved<0x142, 0xa>((int)__float_as_uint(x)));
+  x += __uint_as_float((uint32_t)moved<0x143, 0xc>((int)__float_as_uint(x)));
+  return last_lane(x);
+}
+
+// The wave's maximum, in every lane; a lane that nothing moves to keeps its own.
+template <int kControl, int kRows>
+__device__ __forceinline__ float max_moved(float x) {
+  const int v = (int)__float_as_uint(x);
+  return fmaxf(x, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(v, v, kControl, kRows, 0xf, false)));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = max_moved<0x111, 0xf>(x);
+  x = max_moved<0x112, 0xf>(x);
+  x = max_moved<0x114, 0xf>(x);
+  x = max_moved<0x118, 0xf>(x);
+  x = max_moved<0x142, 0xa>(x);
+  x = max_moved<0x143, 0xc>(x);
+  return last_lane(x);
 }
 
 // Work items are numbered over the sequences in order, count(sequence) each.

@@ -23,7 +23,7 @@ struct AttendArgs {
   int window, sinks;
   uint16_t* out;
   float* lse;
-  int target;              // work items per head that fill the card
+  int target;              // workgroups a head that fill the card
   uint32_t* arrived;       // [kMaxSlots] zero between calls
   float* part;             // [slot] partial results
 };
@@ -31,16 +31,27 @@ struct AttendArgs {
 // ------------------------------------------------------------------ the work
 // A sequence's rows for one kv head are its query heads' rows, token after
 // token: row x = (x / group)-th new token, head x % group of the kv head's.
-// Tiles of R such rows share each key and value that they load.  A tile's
-// visible tokens, as groups of 32, are cut into `splits` parts where the batch
-// has too few tiles to fill the card, each part a workgroup.
+// Tiles of R such rows share each key and value that they load.
+//
+// Where the batch has at least twice the tiles that fill the card, a workgroup
+// takes one tile.  Where it has fewer, the tiles' visible tokens, as groups of
+// 32, are laid end to end and cut into equal runs, one a workgroup, so that the
+// card is filled and all end together whatever the lengths; a run may hold the
+// end of one tile, whole tiles and the start of another.  A tile that several
+// runs hold parts of is joined by the last of them (join_parts).  Cut by tiles
+// instead, 64 slots over 0.95 GB of mixed lengths waited for the longest: 180 us.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kTargetBlocks = 512;      // workgroups that fill the card
-constexpr int kMinSplitGroups = 4;      // least groups of 32 tokens a workgroup is split down to
-constexpr int kMaxSlots = 2 * (kTargetBlocks + DL_MAX_HEADS);
-constexpr int kJoinFloats = 8192;       // scratch of a tile's joining: a weight for each of its rows and parts
+constexpr int kMinRun = 4;               // least groups of a run
+constexpr int kMaxBlocks = 768;          // most workgroups that a plan takes to fill the card
+constexpr int kMaxSlots = 2 * (kMaxBlocks + DL_MAX_HEADS);
+// Pairs of a row and a part that a tile's joining holds in LDS: what bounds the
+// parts.  Few rows leave room for their parts at 32 KiB, more take 64.
 template <int R>
-constexpr int kMaxSplits = kJoinFloats / R;
+constexpr int kJoinPairs = R <= 16 ? 4096 : 8192;
+template <int R>
+constexpr int kMaxParts = kJoinPairs<R> / R;
+template <int R, int kThreads>
+constexpr int kJoinFloats = 2 * kJoinPairs<R> + 4 * kThreads;
 constexpr size_t kArrivedBytes = (kMaxSlots * sizeof(uint32_t) + 255) / 256 * 256;
 
 struct Range {   // groups of 32 tokens a tile sees: first `ns` groups, then g0 .. g0 + n - ns - 1
@@ -61,61 +72,111 @@ __device__ __forceinline__ Range visible(const AttendArgs& A, int p_first, int p
   return r;
 }
 
-struct Item {
-  int seq, tile, split, splits;
-  int slot;   // partial slot of split 0 (splits > 1)
+// A part of a tile: groups from .. to - 1 of the `of` that the plan counts for
+// it (the most that a tile of the sequence sees; at least 1, so that tiles that
+// see nothing are visited too).
+struct Segment {
+  int seq, tile;
+  int from, to, of;
+  int parts, part;   // the tile's parts, and which this is
+  int first_run;     // the run that holds part 0
 };
 
-// The batch's plan, computed by every wave from the lengths alone: parts of
-// `chunk` groups such that the items per head come near A.target, which fills
-// the card once (one a tile, and at most A.target more).
+// The plan, which every wave computes alike from the lengths, and the walk
+// through one run's segments.
 template <int R>
-__device__ __forceinline__ bool find_work(const AttendArgs& A, int item, Item& w) {
-  const int lane = threadIdx.x & 63;
-  auto tiles_of = [&](const Seq& q) { return (int)(((int64_t)q.n * A.group + R - 1) / R); };
-  auto groups_of = [&](const Seq& q) {   // of the tile that sees most
-    if (q.n == 0) return 0;
-    const int tokens = min(q.n, R / A.group + 2);
-    return visible(A, q.len - tokens, q.len - 1).n;
-  };
-  float sum = 0.0f, all = 0.0f;
-  for (int s = lane; s < A.b.n_seq; s += 64) {
-    const Seq q = load_seq(A.b, s);
-    sum += (float)tiles_of(q) * (float)groups_of(q);
-    all += (float)tiles_of(q);
-  }
-  // 0.1% more than the sum, so that no rounding of it can bring more items than A.target and a tile each
-  sum = wave_sum(sum) * 1.001f;
-  all = wave_sum(all);
-  const float spare = fmaxf((float)A.target - all, 0.125f * (float)A.target);
-  const int chunk = max(kMinSplitGroups, (int)fminf(ceilf(sum / spare), 1e9f));
-  int slot0 = 0;
-  for (int base = 0; base < A.b.n_seq; base += 64) {
-    const int s = base + lane;
-    int tiles = 0, splits = 1;
-    if (s < A.b.n_seq) {
+class Walk {
+ public:
+  // Run (or tile) `run` of a head; false where there is none.
+  __device__ __forceinline__ bool begin(const AttendArgs& A, int run) {
+    const int lane = threadIdx.x & 63;
+    float groups = 0.0f, tiles = 0.0f, most = 0.0f;
+    for (int s = lane; s < A.b.n_seq; s += 64) {
       const Seq q = load_seq(A.b, s);
-      tiles = tiles_of(q);
-      splits = min(max(1, (groups_of(q) + chunk - 1) / chunk), kMaxSplits<R>);
+      const int t = tiles_of(A, q), g = groups_of(A, q);
+      if (s < 64) tiles_ = t, groups_ = g;
+      groups += (float)t * (float)g;
+      tiles += (float)t;
+      most = fmaxf(most, (float)g);
     }
-    const int items = tiles * splits, slots = splits > 1 ? items : 0;
-    const int isum = wave_inclusive_sum(items), ssum = wave_inclusive_sum(slots);
-    const int total = __builtin_amdgcn_readlane(isum, 63);
-    if (item < total) {
-      const int at = __builtin_ctzll(__ballot(isum > item));
-      w.seq = base + at;
-      w.splits = __builtin_amdgcn_readlane(splits, at);
-      const int rest = item - (__builtin_amdgcn_readlane(isum, at) - __builtin_amdgcn_readlane(items, at));
-      w.tile = rest / w.splits;
-      w.split = rest % w.splits;
-      w.slot = slot0 + __builtin_amdgcn_readlane(ssum, at) - __builtin_amdgcn_readlane(slots, at) + rest - w.split;
-      return true;
-    }
-    item -= total;
-    slot0 += __builtin_amdgcn_readlane(ssum, 63);
+    groups = wave_sum(groups);
+    tiles = wave_sum(tiles);
+    most = wave_max(most);
+    whole_ = tiles >= 2.0f * (float)A.target;
+    // lengths are counted in units of 2^shift groups, so that their sum fits 32 bits
+    shift_ = max(0, (int)((__float_as_uint(groups) >> 23) & 255u) - 127 - 28);
+    const float unit = __builtin_ldexpf(1.0f, -shift_);
+    // 0.1% more than the mean: float sums may fall short; tiles: each may be rounded up to a unit
+    const float mean = (groups * unit * 1.001f + (shift_ ? tiles : 0.0f)) / (float)A.target;
+    per_ = max(kMinRun >> min(shift_, 2), (int)ceilf(fmaxf(mean, most * unit / (float)(kMaxParts<R> - 3))));
+    run_ = run;
+    at_ = whole_ ? run : run * per_;
+    end_ = at_ + (whole_ ? 1 : per_);
+    return whole_ || run < A.target;
   }
-  return false;
-}
+
+  // The next segment; false past the run's (or the batch's) last.
+  __device__ __forceinline__ bool next(const AttendArgs& A, Segment& g) {
+    if (at_ >= end_) return false;
+    const int lane = threadIdx.x & 63;
+    int at = at_, before = 0;   // `before`: units of the sequences passed
+    for (int base = 0; base < A.b.n_seq; base += 64) {
+      int tiles = tiles_, groups = groups_;
+      if (A.b.n_seq > 64 && base > 0) {
+        tiles = groups = 0;
+        if (base + lane < A.b.n_seq) {
+          const Seq q = load_seq(A.b, base + lane);
+          tiles = tiles_of(A, q);
+          groups = groups_of(A, q);
+        }
+      } else if (lane >= A.b.n_seq) {
+        tiles = groups = 0;
+      }
+      const int units = (groups + (1 << shift_) - 1) >> shift_;
+      const int mine = whole_ ? tiles : tiles * units, sum = wave_inclusive_sum(mine);
+      const int total = __builtin_amdgcn_readlane(sum, 63);
+      if (at < total) {
+        const int i = __builtin_ctzll(__ballot(sum > at));
+        const int start = __builtin_amdgcn_readlane(sum, i) - __builtin_amdgcn_readlane(mine, i);
+        g.seq = base + i;
+        if (whole_) {
+          g.tile = at - start;
+          g.from = 0;
+          g.to = g.of = 1;
+          g.parts = 1;
+          g.part = g.first_run = 0;
+          at_ = end_;
+          return true;
+        }
+        g.of = __builtin_amdgcn_readlane(units, i);
+        g.tile = (at - start) / g.of;
+        g.from = at - start - g.tile * g.of;
+        g.to = min(g.of, g.from + end_ - at_);
+        const int tile_at = at_ - g.from;   // where the tile starts
+        g.first_run = tile_at / per_;
+        g.parts = (tile_at + g.of - 1) / per_ - g.first_run + 1;
+        g.part = run_ - g.first_run;
+        at_ += g.to - g.from;
+        return true;
+      }
+      at -= total;
+    }
+    return false;
+  }
+
+ private:
+  int tiles_ = 0, groups_ = 0;   // of sequence `lane`
+  bool whole_;                   // a tile a workgroup
+  int shift_, per_, run_, at_, end_;
+
+  static __device__ __forceinline__ int tiles_of(const AttendArgs& A, const Seq& q) {
+    return (int)(((int64_t)q.n * A.group + R - 1) / R);
+  }
+  static __device__ __forceinline__ int groups_of(const AttendArgs& A, const Seq& q) {
+    const int tokens = min(q.n, R / A.group + 2);   // a tile's, at most
+    return q.n == 0 ? 0 : max(1, visible(A, q.len - tokens, q.len - 1).n);
+  }
+};
 
 // --------------------------------------------------------------- conversions
 // Eight code bytes (value + 128) as fp16: 0x6400 | u is 1024 + u, and
@@ -207,22 +268,35 @@ __device__ __forceinline__ void write_lse(const AttendArgs& A, size_t row, float
   if (A.lse) A.lse[row] = sum == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
 }
 
+// A run has a slot for the part of a tile that began in an earlier run (2 run)
+// and one for the tile that it begins and does not end (2 run + 1): part v of a
+// tile that begins in run f is in slot 2f + 1 or, v > 0, 2 (f + v).
+struct Parts {
+  __amdgpu_buffer_rsrc_t buffer;   // slot 2f of this head
+  int step;                        // floats from a slot to the next
+  __device__ __forceinline__ int at(int v) const { return max(2 * v, 1) * step; }
+};
+template <int D, int R>
+__device__ __forceinline__ Parts parts_of(const AttendArgs& A, const Segment& g, int head) {
+  return {part_buffer(A.part + ((size_t)2 * g.first_run * A.c.hkv + head) * kPartFloats<D, R>), A.c.hkv * kPartFloats<D, R>};
+}
+
 // The last of a tile's parts to arrive joins them all, in the parts' order, so
 // the result does not depend on which one that is.  Every part's stores have
 // reached memory (vmcnt 0 in each wave, then the barrier) before its workgroup
-// is counted.  `parts`: part 0 of this tile and head; part v is at v * step
-// floats.  `lds`: kJoinFloats and four a thread.
+// is counted.  The published data come from beyond the L2, a microsecond or two
+// away, so as many loads as the registers allow are under way together.
 template <int D, int R, int kThreads>
-__device__ __forceinline__ void join_parts(const AttendArgs& A, const Item& w, const Seq& q, int x0, int rows, int head,
-                                           __amdgpu_buffer_rsrc_t parts, int step, float* lds) {
+__device__ __forceinline__ void join_parts(const AttendArgs& A, const Segment& w, const Seq& q, int x0, int rows, int head,
+                                           const Parts& parts, float* lds) {
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 63;
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (tid == 0) {
-    uint32_t* count = A.arrived + w.slot * A.c.hkv + head;
+    uint32_t* count = A.arrived + (2 * w.first_run + 1) * A.c.hkv + head;
     const uint32_t before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    last = before == (uint32_t)w.splits - 1;
+    last = before == (uint32_t)w.parts - 1;
     if (last) __hip_atomic_store(count, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
@@ -231,49 +305,89 @@ __device__ __forceinline__ void join_parts(const AttendArgs& A, const Item& w, c
     const int x = x0 + r;
     return (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
   };
-  // a wave a row, a lane a part: the parts' shares of the row
-  for (int r = tid >> 6; r < rows; r += kThreads / 64) {
-    float top = kLowest;
-    for (int v = lane; v < w.splits; v += 64) {
-      const float2 s = published2(parts, v * step + R * D + r * 2);
-      top = fmaxf(top, s.x);
-      lds[r * w.splits + v] = s.x;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    float sum = 0.0f;
-    for (int v = lane; v < w.splits; v += 64) {
-      const float share = __builtin_amdgcn_exp2f(lds[r * w.splits + v] - top);
-      sum += share * published2(parts, v * step + R * D + r * 2).y;
-      lds[r * w.splits + v] = share;
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    for (int v = lane; v < w.splits; v += 64) lds[r * w.splits + v] *= inv;
-    if (lane == 0) write_lse(A, row_of(r), top, sum);
+  // every (row, part)'s reference and sum of weights
+  float* ref = lds;
+  float* sums = lds + kJoinPairs<R>;
+  const int n = w.parts, pairs = rows * n;
+#pragma unroll 4
+  for (int i = tid; i < pairs; i += kThreads) {
+    const float2 s = published2(parts.buffer, parts.at(i % n) + R * D + i / n * 2);
+    ref[i] = s.x;
+    sums[i] = s.y;
   }
   __syncthreads();
-  // four elements of a row a thread; threads that are left over take turns at the parts
-  const int items = rows * (D / 4), turns = max(1, kThreads / items);
-  float* turned = lds + kJoinFloats;
-  for (int i0 = 0; i0 < items; i0 += kThreads) {
-    const int i = turns > 1 ? tid % items : i0 + tid, turn = turns > 1 ? tid / items : 0;
-    const bool busy = i < items && turn < turns;
-    const int r = i / (D / 4), at = r * D + i % (D / 4) * 4;
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (busy) {
-#pragma unroll 8
-      for (int v = turn; v < w.splits; v += turns) y += lds[r * w.splits + v] * published4(parts, v * step + at);
+  // the parts' shares of each row, in ref's place: few parts a thread a row, many a wave a row
+  if (n <= 16) {
+    if (tid < rows) {
+      float top = kLowest, sum = 0.0f;
+      for (int v = 0; v < n; ++v) top = fmaxf(top, ref[tid * n + v]);
+      for (int v = 0; v < n; ++v) sum = fmaf(__builtin_amdgcn_exp2f(ref[tid * n + v] - top), sums[tid * n + v], sum);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int v = 0; v < n; ++v) ref[tid * n + v] = inv * __builtin_amdgcn_exp2f(ref[tid * n + v] - top);
+      write_lse(A, row_of(tid), top, sum);
     }
-    if (turns > 1) {
-      if (busy && turn > 0) *reinterpret_cast<f32x4*>(turned + tid * 4) = y;
-      __syncthreads();
-      if (busy && turn == 0)
-        for (int k = 1; k < turns; ++k) y += *reinterpret_cast<const f32x4*>(turned + (tid + k * items) * 4);
+  } else {
+    for (int r = tid >> 6; r < rows; r += kThreads / 64) {
+      float top = kLowest, sum = 0.0f;
+      for (int v = lane; v < n; v += 64) top = fmaxf(top, ref[r * n + v]);
+      top = wave_max(top);
+      for (int v = lane; v < n; v += 64) {
+        const float share = __builtin_amdgcn_exp2f(ref[r * n + v] - top);
+        sum = fmaf(share, sums[r * n + v], sum);
+        ref[r * n + v] = share;
+      }
+      sum = wave_sum(sum);
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      for (int v = lane; v < n; v += 64) ref[r * n + v] *= inv;
+      if (lane == 0) write_lse(A, row_of(r), top, sum);
     }
-    if (busy && turn == 0)
-      *reinterpret_cast<u32x2*>(A.out + row_of(r) * D + i % (D / 4) * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+  }
+  __syncthreads();
+  const int items = rows * (D / 4);   // four elements of a row each
+  auto put = [&](int i, f32x4 y) {
+    *reinterpret_cast<u32x2*>(A.out + row_of(i / (D / 4)) * D + i % (D / 4) * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+  };
+  // y of items i0 + k * kThreads over parts v0, v0 + by, ...: kItems x kParts loads under way together
+  auto gather = [&](auto items_at_once, auto parts_at_once, int i0, int v0, int by, auto& y) {
+    constexpr int kItems = decltype(items_at_once)::value, kParts = decltype(parts_at_once)::value;
+    for (; v0 < n; v0 += by * kParts) {
+      f32x4 x[kItems][kParts];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+#pragma unroll
+        for (int v = 0; v < kParts; ++v)   // past the end: the last item or part once more, with no share
+          x[k][v] = published4(parts.buffer, parts.at(min(v0 + v * by, n - 1)) + min(i0 + k * kThreads, items - 1) * 4);
+#pragma unroll
+      for (int k = 0; k < kItems; ++k)
+#pragma unroll
+        for (int v = 0; v < kParts; ++v)
+          y[k] += (v0 + v * by < n ? ref[min(i0 + k * kThreads, items - 1) / (D / 4) * n + min(v0 + v * by, n - 1)] : 0.0f) * x[k][v];
+    }
+  };
+  using std::integral_constant;
+  if (items <= kThreads) {
+    // one item a thread; threads that are left over take turns at the parts
+    const int turns = kThreads / items, i = tid % items, turn = tid / items;
+    float* turned = lds + 2 * kJoinPairs<R>;
+    f32x4 y[1] = {{0.0f, 0.0f, 0.0f, 0.0f}};
+    if (turn < turns) gather(integral_constant<int, 1>(), integral_constant<int, 16>(), i, turn, turns, y);
+    if (turn > 0) *reinterpret_cast<f32x4*>(turned + tid * 4) = y[0];
+    __syncthreads();
+    if (turn == 0) {
+      for (int k = 1; k < turns; ++k) y[0] += *reinterpret_cast<const f32x4*>(turned + (i + k * items) * 4);
+      put(i, y[0]);
+    }
+    return;
+  }
+  constexpr int kItems = 4;
+  for (int i0 = tid; i0 < items; i0 += kThreads * kItems) {
+    f32x4 y[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) y[k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    gather(integral_constant<int, kItems>(), integral_constant<int, 4>(), i0, 0, 1, y);
+#pragma unroll
+    for (int k = 0; k < kItems; ++k)
+      if (i0 + k * kThreads < items) put(i0 + k * kThreads, y[k]);
   }
 }
 
@@ -290,19 +404,20 @@ struct Bytes {   // a lane's codes of one group
 };
 
 template <int D, int MT>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 3) void attend_stream_kernel(AttendArgs A) {
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_stream_kernel(AttendArgs A) {
   constexpr int R = 16 * MT, F = D / 32, C = D / 16;
   constexpr int kRow = D + 4;
   constexpr bool kAhead = D * MT <= 256;   // beyond, a second group's bytes do not fit the registers
   __shared__ __align__(16) union {
     float o[kWaves][16][kRow];
-    float join[kJoinFloats + 4 * kThreads];
+    float join[kJoinFloats<R, kThreads>];
   } lds;
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
-  Item w;
-  if (!find_work<R>(A, blockIdx.x / A.c.hkv, w)) return;
+  Walk<R> walk;
+  if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
+  for (Segment w; walk.next(A, w);) {
   const Seq q = load_seq(A.b, w.seq);
   const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
   const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
@@ -325,7 +440,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 3) void attend_stream_kern
   }
 
   const Range see = visible(A, p_first, p_last);
-  const int from = (int)((int64_t)see.n * w.split / w.splits), to = (int)((int64_t)see.n * (w.split + 1) / w.splits);
+  const int from = (int)((int64_t)see.n * w.from / w.of), to = (int)((int64_t)see.n * w.to / w.of);
   const size_t page_bytes = (size_t)D << A.c.page_shift;
   for (int base = from + wave; base < to; base += 64 * kWaves) {
     // lane i: page and scales of the wave's i-th group from here
@@ -439,11 +554,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 3) void attend_stream_kern
 
   // Join the waves, 16 rows at a time, then either the result or this part's
   // share of it.
-  const __amdgpu_buffer_rsrc_t parts = part_buffer(A.part + (size_t)(w.slot * A.c.hkv + head) * kPartFloats<D, R>);
-  const int step = A.c.hkv * kPartFloats<D, R>, mine = w.split * step;
+  const Parts parts = parts_of<D, R>(A, w, head);
+  const int mine = parts.at(w.part);
   for (int t = 0; t < MT; ++t) {
     if (t * 16 >= rows) break;
-    if (t) __syncthreads();
+    __syncthreads();   // lds: the rows or the segment before this one
 #pragma unroll
     for (int tt = 0; tt < MT; ++tt)
       if (tt == t) {
@@ -475,25 +590,26 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 3) void attend_stream_kern
         f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&lds.o[v][r][e]);
-        if (w.splits == 1) {
+        if (w.parts == 1) {
           y *= inv;
           *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
         } else {
-          publish4(parts, mine + (t * 16 + r) * D + e, y);
+          publish4(parts.buffer, mine + (t * 16 + r) * D + e, y);
         }
       }
       if ((tid & 15) == 0) {
-        if (w.splits > 1)
-          publish2(parts, mine + R * D + (t * 16 + r) * 2, top, sum);
+        if (w.parts > 1)
+          publish2(parts.buffer, mine + R * D + (t * 16 + r) * 2, top, sum);
         else
           write_lse(A, to_row, top, sum);
       }
     }
   }
-  if (w.splits == 1) return;
+  if (w.parts == 1) continue;
 
   __syncthreads();   // lds becomes join_parts' scratch
-  join_parts<D, R, kThreads>(A, w, q, x0, rows, head, parts, step, &lds.join[0]);
+  join_parts<D, R, kThreads>(A, w, q, x0, rows, head, parts, &lds.join[0]);
+  }
 }
 
 // -------------------------------------------------------- many rows: shared
@@ -508,9 +624,19 @@ struct Shared {
   static constexpr int kUnits = G * 2 * F;                 // KiB of codes a step: keys, then values
   static constexpr int kPer = kUnits / W;                  // of them a wave's
   static constexpr int kStage = kUnits * 2 * 64;           // 16-byte fragments a stage
-  static constexpr size_t kLds = std::max(2 * (size_t)kStage * 16, (kJoinFloats + 4 * kThreads) * sizeof(float));
+  static constexpr size_t kLds = std::max(2 * (size_t)kStage * 16, kJoinFloats<R, kThreads> * sizeof(float));
   static_assert(kUnits % W == 0, "every wave carries as many codes");
 };
+
+// Four of a group's fragments out of LDS.  What follows stays behind the reads
+// (only arithmetic may pass), so that they are under way while the four before
+// them are used: left to itself the compiler reads one, waits, uses it and reads
+// the next.
+__device__ __forceinline__ void read4(half8 (&to)[4], const u32x4* at) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) to[i] = __builtin_bit_cast(half8, at[i * 64]);
+  __builtin_amdgcn_sched_barrier(0x16);
+}
 
 template <int D, int NQ, int W, int G>
 __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) {
@@ -519,8 +645,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   extern __shared__ __align__(16) u32x4 stage[];
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
-  Item w;
-  if (!find_work<R>(A, blockIdx.x / A.c.hkv, w)) return;
+  Walk<R> walk;
+  if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
+  for (Segment w; walk.next(A, w);) {
   const Seq q = load_seq(A.b, w.seq);
   w.tile = (int)(((int64_t)q.n * A.group + R - 1) / R) - 1 - w.tile;   // the tiles that see most first
   const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
@@ -548,7 +675,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   }
 
   const Range see = visible(A, p_first, p_last);
-  const int from = (int)((int64_t)see.n * w.split / w.splits), to = (int)((int64_t)see.n * (w.split + 1) / w.splits);
+  const int from = (int)((int64_t)see.n * w.from / w.of), to = (int)((int64_t)see.n * w.to / w.of);
   const size_t page_bytes = (size_t)D << A.c.page_shift;
   const int in_page = (1 << (A.c.page_shift - 5)) - 1;
   // lane i: page and scales of the i-th group from `base`, 64 at a time; the
@@ -593,6 +720,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
       const size_t at = (size_t)max(id_work, 0) * A.c.hkv + head;
       ks_work = A.c.ks[at];
       vs_work = fmaxf(A.c.vs[at], kMinScale);
+      // waited for here, once in 64 groups: a use further down would wait for
+      // the codes too that are loaded in between, in every step
+      __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt 0
     }
     if (n0 + G < to) {
       store(which ^ 1);
@@ -611,14 +741,21 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
         f32x4 s[NQ][2];
 #pragma unroll
         for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        half8 now[4], next[4];
+        read4(now, kf);
 #pragma unroll
-        for (int f = 0; f < F; ++f)
+        for (int c = 0; c < C / 4; ++c) {
+          read4(next, c + 1 < C / 4 ? kf + (c + 1) * 256 : vf);
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const half8 a = __builtin_bit_cast(half8, kf[(f * 2 + h) * 64]);
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int t = 0; t < NQ; ++t) s[t][f / (D / 64)] = mfma(a, qf[t][f % (D / 64) * 2 + h], s[t][f / (D / 64)]);
-          }
+            for (int t = 0; t < NQ; ++t) {
+              const int n = c * 4 + i, tt = n / (D / 32);
+              s[t][tt] = mfma(now[i], qf[t][n % (D / 32)], s[t][tt]);
+            }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now[i] = next[i];
+        }
         const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
         const bool edge = id < 0 || first + 31 > w_first ||
                           (A.window > 0 && first <= w_last - A.window && first + 31 >= A.sinks);
@@ -662,18 +799,22 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
           l[t] = fmaf(sum, rv, l[t]);
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-          const half8 a = __builtin_bit_cast(half8, vf[c * 64]);
+        for (int c = 0; c < C / 4; ++c) {
+          if (c + 1 < C / 4) read4(next, vf + (c + 1) * 256);
 #pragma unroll
-          for (int t = 0; t < NQ; ++t) o[t][c] = mfma(a, pf[t], o[t][c]);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < NQ; ++t) o[t][c * 4 + i] = mfma(now[i], pf[t], o[t][c * 4 + i]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) now[i] = next[i];
         }
       }
     }
     __syncthreads();
   }
 
-  const __amdgpu_buffer_rsrc_t parts = part_buffer(A.part + (size_t)(w.slot * A.c.hkv + head) * kPartFloats<D, R>);
-  const int step = A.c.hkv * kPartFloats<D, R>, mine = w.split * step;
+  const Parts parts = parts_of<D, R>(A, w, head);
+  const int mine = parts.at(w.part);
 #pragma unroll
   for (int t = 0; t < NQ; ++t) {
     const int r = mine0 + t * 16 + lo, x = x0 + r;
@@ -681,7 +822,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
     sum += __shfl_xor(sum, 16);
     sum += __shfl_xor(sum, 32);
     if (r >= rows) continue;
-    if (w.splits == 1) {
+    if (w.parts == 1) {
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
 #pragma unroll
@@ -692,13 +833,15 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
       if (hi == 0) write_lse(A, to_row, m[t], sum);
     } else {
 #pragma unroll
-      for (int c = 0; c < C; ++c) publish4(parts, mine + r * D + c * 16 + hi * 4, o[t][c]);
-      if (hi == 0) publish2(parts, mine + R * D + r * 2, m[t], sum);
+      for (int c = 0; c < C; ++c) publish4(parts.buffer, mine + r * D + c * 16 + hi * 4, o[t][c]);
+      if (hi == 0) publish2(parts.buffer, mine + R * D + r * 2, m[t], sum);
     }
   }
-  if (w.splits == 1) return;
+  if (w.parts == 1) continue;
   __syncthreads();   // the stages become join_parts' scratch
-  join_parts<D, R, S::kThreads>(A, w, q, x0, rows, head, parts, step, reinterpret_cast<float*>(stage));
+  join_parts<D, R, S::kThreads>(A, w, q, x0, rows, head, parts, reinterpret_cast<float*>(stage));
+  __syncthreads();   // and the next segment's stages
+  }
 }
 
 // ------------------------------------------------------------------- launch
@@ -706,19 +849,20 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
 struct Plan {
   int rows;      // a tile's
   bool shared;   // attend_shared_kernel (else the streaming one)
+  int blocks;    // workgroups that fill the card: those that 256 CUs hold at once
 };
 Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  if (rows <= 16) return {16, false};
-  if (rows <= 64) return {64, true};
-  return {128, true};
+  if (rows <= 16) return {16, false, 512};
+  if (rows <= 64) return {64, true, 512};
+  return {128, true, D == 256 ? 256 : 512};
 }
 
-int target_items(int hkv) { return std::max(1, kTargetBlocks / hkv); }
+int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }
 
-size_t workspace_bytes(int T, int n_seq, int hq, int hkv, int D) {
-  const size_t slots = 2 * (size_t)target_items(hkv) * hkv;
-  return kArrivedBytes + slots * plan_for(T, n_seq, hq, hkv, D).rows * (D + 2) * sizeof(float);
+size_t workspace_bytes(const Plan& p, int hkv, int D) {
+  const size_t slots = 2 * (size_t)target_items(p.blocks, hkv) * hkv;
+  return kArrivedBytes + slots * p.rows * (D + 2) * sizeof(float);
 }
 
 template <int D, int NQ, int W, int G>
@@ -741,7 +885,7 @@ int launch(const AttendArgs& A, const Plan& plan, hipStream_t s) {
   const int R = plan.rows;
   // tiles: sum over the sequences of ceil(rows / R), each with a row of its own
   const int64_t tiles = std::min<int64_t>((rows + (int64_t)A.b.n_seq * (R - 1)) / R, rows);
-  const int64_t grid = (tiles + A.target) * A.c.hkv;
+  const int64_t grid = std::max<int64_t>(tiles, A.target) * A.c.hkv;   // a tile a workgroup, or A.target runs a head
   if (grid > 0x7FFFFFFF) return dh::fail(DH_EUNSUP, "attend: too many rows for one launch");
   const dim3 g((unsigned)grid);
   constexpr int G = D == 256 ? 1 : 2;
@@ -767,7 +911,7 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
   int rc = check_heads("workspace_bytes", hq, hkv, D);
   if (rc) return rc;
   if ((rc = check_rows("workspace_bytes", T, n_seq))) return rc;
-  *bytes = workspace_bytes(T, n_seq, hq, hkv, D);
+  *bytes = workspace_bytes(plan_for(T, n_seq, hq, hkv, D), hkv, D);
   return dh::ok();
 }
 
@@ -792,7 +936,8 @@ int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const
   if (!out || !aligned(out, 16)) return dh::fail(DH_EINVAL, "attend: out must be a 16-byte aligned pointer");
   if (lse && !aligned(lse, 4)) return dh::fail(DH_EINVAL, "attend: lse must be 4-byte aligned");
   if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "attend: workspace must be a 16-byte aligned pointer");
-  const size_t need = workspace_bytes(T, n_seq, hq, hkv, D);
+  const Plan plan = plan_for(T, n_seq, hq, hkv, D);
+  const size_t need = workspace_bytes(plan, hkv, D);
   if (workspace_bytes_given < need)
     return dh::fail(DH_EINVAL, "attend: workspace of %zu bytes is below the %zu needed", workspace_bytes_given, need);
   A.q = static_cast<const uint16_t*>(q);
@@ -804,15 +949,14 @@ int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const
   A.sinks = std::min(sinks, DL_MAX_POSITIONS);
   A.out = static_cast<uint16_t*>(out);
   A.lse = lse;
-  A.target = target_items(hkv);
+  A.target = target_items(plan.blocks, hkv);
   A.arrived = static_cast<uint32_t*>(workspace);
   A.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kArrivedBytes);
-  const Plan R = plan_for(T, n_seq, hq, hkv, D);
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   switch (D) {
-    case 64: return launch<64>(A, R, st);
-    case 128: return launch<128>(A, R, st);
-    default: return launch<256>(A, R, st);
+    case 64: return launch<64>(A, plan, st);
+    case 128: return launch<128>(A, plan, st);
+    default: return launch<256>(A, plan, st);
   }
 }
 
