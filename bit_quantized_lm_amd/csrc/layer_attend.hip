@@ -179,22 +179,28 @@ class Walk {
 };
 
 // --------------------------------------------------------------- conversions
-// Eight code bytes (value + 128) as fp16: 0x6400 | u is 1024 + u, and
-// subtracting 1152 leaves the signed code exactly.
-__device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
+// Code bytes (value + 128) as fp16: 0x6400 | u is 1024 + u, and subtracting
+// 1152 leaves the signed code exactly.
+__device__ __forceinline__ u32x2 codes_to_half4(uint32_t a) {
   const half2v off = {(_Float16)1152.0f, (_Float16)1152.0f};
-  u32x4 w;
-  const uint32_t src[2] = {a, b};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    w[2 * i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, src[i], 0x04010400u)) - off);
-    w[2 * i + 1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, src[i], 0x04030402u)) - off);
-  }
-  return __builtin_bit_cast(half8, w);
+  return u32x2{__builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, a, 0x04010400u)) - off),
+               __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, a, 0x04030402u)) - off)};
+}
+__device__ __forceinline__ half8 codes_to_half(uint32_t a, uint32_t b) {
+  const u32x2 x = codes_to_half4(a), y = codes_to_half4(b);
+  return __builtin_bit_cast(half8, u32x4{x[0], x[1], y[0], y[1]});
 }
 
 __device__ __forceinline__ f32x4 mfma(half8 a, half8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+
+// A lane's 16 bytes of KiB `f` of the codes at `at` (one address for the wave).
+constexpr int kOnce = 2;   // nt: read by this workgroup alone, not worth keeping
+template <int kPolicy>
+__device__ __forceinline__ u32x4 load_codes(const uint8_t* at, int f) {
+  const __amdgpu_buffer_rsrc_t b = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(at), 0, 0x7FFFFFFF, 0x00027000);
+  return __builtin_amdgcn_raw_buffer_load_b128(b, (threadIdx.x & 63) * 16, f * 1024, kPolicy);
 }
 
 // A row's query fragments, lane (hi, lo) holding elements 64 f + 16 hi ..
@@ -229,11 +235,12 @@ __device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bo
 // Online softmax of one row: weights are 2^(x - m) with x = z log2(e) +
 // log2(value scale), so that a weight times a value code is the value's whole
 // share, whatever its page's scale, and m near the running maximum of x; l sums
-// the weights over the value scales again.  m is set kHead below the maximum and
-// moves only when some x exceeds it by more than kHead + kSlack: the sums need
-// no rescaling in most steps, weights stay below 2^15 (fp16's largest is just
-// under 2^16), and one keeps its 11 bits down to 2^-21 of the largest.
-constexpr float kHead = 7.0f, kSlack = 8.0f;
+// the weights over the value scales again.  m is set kHead below the maximum
+// and stays until a weight passes 2^kFit, which a lane's sum of them tells: most
+// steps then need neither a maximum nor a rescaling, weights fit fp16 (its
+// largest is just under 2^16), and one keeps its 11 bits down to 2^-21 of the
+// largest.
+constexpr float kHead = 7.0f, kFit = 15.0f, kMost = 0x1p15f;
 constexpr float kLowest = -1e30f;   // m before the first visible token; finite, so no inf - inf arises
 
 // --------------------------------------------------------------- split parts
@@ -391,6 +398,89 @@ __device__ __forceinline__ void join_parts(const AttendArgs& A, const Segment& w
   }
 }
 
+// Whether some row at p_first .. p_last does not see some of the tokens first .. first + 31.
+__device__ __forceinline__ bool hides(const AttendArgs& A, int first, int p_first, int p_last) {
+  return first + 31 > p_first || (A.window > 0 && first <= p_last - A.window && first + 31 >= A.sinks);
+}
+
+// What is common to a group's scores: where its tokens are and its scales.
+struct Group {
+  int id, first;       // page (-1: nothing there), position of token 0
+  float ks, lv, rv;    // key scale, log2(value scale), 1 / (value scale)
+  bool edge;           // some row does not see some of its tokens
+};
+
+// A group's weights of all row tiles, from its scores x in code units.  In
+// three steps, so that a caller can put other work between them: hidden scores
+// to -inf; weights under the present references; and, where some weight may have
+// passed 2^kFit, which the lanes' sums tell, the references and what was summed
+// under them moved and the weights formed again.  One test for all tiles: tile by
+// tile, each waits for the one before.
+template <int N>
+struct Weights {
+  float c[N], p[N][8], sum[N];   // scale of x, weights, this lane's sum of them
+
+  __device__ __forceinline__ void hide(const AttendArgs& A, const Group& g, f32x4 (&x)[N][2], const float (&qs)[N], const int (&pos)[N]) {
+#pragma unroll
+    for (int t = 0; t < N; ++t) c[t] = g.ks * qs[t];
+    if (!g.edge) return;
+    const int hi = (threadIdx.x & 63) >> 4;
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int at = g.first + hi * 4 + (j >> 2) * 16 + (j & 3);
+        // & and |, not && and ||: selects, no branch a score
+        const bool seen = (g.id >= 0) & (at <= pos[t]) & ((A.window == 0) | (at > pos[t] - A.window) | (at < A.sinks));
+        x[t][j >> 2][j & 3] = seen ? x[t][j >> 2][j & 3] * c[t] : -INFINITY;
+      }
+      c[t] = 1.0f;
+    }
+  }
+
+  // weights `from` .. `to` - 1 of the 8 N
+  __device__ __forceinline__ void form(const Group& g, const f32x4 (&x)[N][2], const float (&m)[N], int from = 0, int to = 8 * N) {
+#pragma unroll
+    for (int i = 0; i < 8 * N; ++i) {
+      if (i < from || i >= to) continue;
+      const int t = i / 8, j = i % 8;
+      p[t][j] = __builtin_amdgcn_exp2f(fmaf(x[t][j >> 2][j & 3], c[t], g.lv - m[t]));
+      sum[t] = j == 0 ? p[t][j] : sum[t] + p[t][j];
+    }
+  }
+
+  template <int C>
+  __device__ __forceinline__ void settle(const Group& g, const f32x4 (&x)[N][2], float (&m)[N], float (&l)[N], f32x4 (&o)[N][C], half8 (&w)[N]) {
+    float most = sum[0];
+#pragma unroll
+    for (int t = 1; t < N; ++t) most = fmaxf(most, sum[t]);
+    if (__any(most > kMost)) {
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        float top = x[t][0][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, x[t][j >> 2][j & 3]);
+        top = fmaf(top, c[t], g.lv);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        // by each row's own maximum, whichever row asked: rows do not touch each other's bits
+        const float next = top > m[t] + kFit ? top - kHead : m[t], down = __builtin_amdgcn_exp2f(m[t] - next);
+        m[t] = next;
+        l[t] *= down;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[t][i] *= down;
+      }
+      form(g, x, m);
+    }
+#pragma unroll
+    for (int t = 0; t < N; ++t) {
+      l[t] = fmaf(sum[t], g.rv, l[t]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[t][j] = (_Float16)p[t][j];
+    }
+  }
+};
+
 // ------------------------------------------------------- few rows: streaming
 // R = 16 MT rows against a stream of groups of 32 tokens.  Each wave takes
 // every kWaves-th group of its workgroup's part, straight from global memory
@@ -413,7 +503,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
     float join[kJoinFloats<R, kThreads>];
   } lds;
   __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
   Walk<R> walk;
   if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
@@ -448,6 +538,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
     const int id_mine = n_mine < to ? page_id(A.b, A.c.n_pages, w.seq, g_mine >> (A.c.page_shift - 5)) : -1;
     const size_t at_mine = (size_t)max(id_mine, 0) * A.c.hkv + head;
     const float ks_mine = A.c.ks[at_mine], vs_mine = fmaxf(A.c.vs[at_mine], kMinScale);
+    const float lv_mine = __builtin_amdgcn_logf(vs_mine), rv_mine = __builtin_amdgcn_rcpf(vs_mine);
     const int count = min(64, (to - base + kWaves - 1) / kWaves);
     auto group_at = [&](int i) {
       const int n = base + i * kWaves;
@@ -456,17 +547,16 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
     auto load = [&](int i, Bytes<F>& w) {   // a page that is not there: page 0's bytes, which step() hides
       const size_t off = ((size_t)max(__builtin_amdgcn_readlane(id_mine, i), 0) * A.c.hkv + head) * page_bytes +
                          (size_t)(group_at(i) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
-      const u32x4* kc = reinterpret_cast<const u32x4*>(A.c.k + off) + lane;
-      const u32x4* vc = reinterpret_cast<const u32x4*>(A.c.v + off) + lane;
 #pragma unroll
-      for (int f = 0; f < F; ++f) w.k[f] = __builtin_nontemporal_load(kc + f * 64);
+      for (int f = 0; f < F; ++f) w.k[f] = load_codes<kOnce>(A.c.k + off, f);
 #pragma unroll
-      for (int f = 0; f < F; ++f) w.v[f] = __builtin_nontemporal_load(vc + f * 64);
+      for (int f = 0; f < F; ++f) w.v[f] = load_codes<kOnce>(A.c.v + off, f);
     };
     auto step = [&](int i, const Bytes<F>& w) {
       const int g = group_at(i), id = __builtin_amdgcn_readlane(id_mine, i);
       const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i));
-      const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_mine), i));
+      const float lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv_mine), i));
+      const float rv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rv_mine), i));
       f32x4 s[MT][2];
 #pragma unroll
       for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -480,48 +570,12 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
           s[t][tt] = mfma(b, qf[t][2 * c + 1], s[t][tt]);
         }
       }
-      const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
-      const int tok = g * 32 + hi * 4;
-      const bool edge = id < 0 || g * 32 + 31 > p_first ||
-                        (A.window > 0 && g * 32 <= p_last - A.window && g * 32 + 31 >= A.sinks);
       half8 pf[MT];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const float c = ks * qs[t];
-        float x[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = s[t][j >> 2][j & 3] * c;
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int at = tok + (j >> 2) * 16 + (j & 3);
-            const bool seen = id >= 0 && at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
-            x[j] = seen ? x[j] : -INFINITY;
-          }
-        }
-        float top = x[0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-        top += lv;
-        if (__any(top > m[t] + (kHead + kSlack))) {
-          top = fmaxf(top, __shfl_xor(top, 16));
-          top = fmaxf(top, __shfl_xor(top, 32));
-          const float next = fmaxf(m[t], top - kHead), down = __builtin_amdgcn_exp2f(m[t] - next);
-          m[t] = next;
-          l[t] *= down;
-#pragma unroll
-          for (int cc = 0; cc < C; ++cc) o[t][cc] *= down;
-        }
-        const float shift = lv - m[t];
-        float sum = 0.0f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float p = __builtin_amdgcn_exp2f(x[j] + shift);
-          sum += p;
-          pf[t][j] = (_Float16)p;
-        }
-        l[t] = fmaf(sum, rv, l[t]);
-      }
+      const Group group{id, g * 32, ks, lv, rv, id < 0 || hides(A, g * 32, p_first, p_last)};
+      Weights<MT> weights;
+      weights.hide(A, group, s, qs, pos);
+      weights.form(group, s, m);
+      weights.settle(group, s, m, l, o, pf);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
         const half8 a = codes_to_half(w.v[f][0], w.v[f][1]), b = codes_to_half(w.v[f][2], w.v[f][3]);
@@ -614,36 +668,34 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
 
 // -------------------------------------------------------- many rows: shared
 // R = 16 NQ W rows: each wave holds NQ tiles of 16 rows, and the workgroup's
-// waves share the key and value fragments, converted to fp16 once, through
-// LDS.  Steps of G groups alternate between two stages: while one is worked on,
-// the next one's codes are converted into the other and the one after that is
-// on its way from memory in registers; one barrier a step.
-template <int D, int NQ, int W, int G>
+// waves share the key and value fragments, converted to fp16 once, through LDS.
+//
+// A step works on one group of 32 tokens.  The matrix cores and the vector
+// units run side by side only where one wave's instructions alternate between
+// them (two waves a SIMD, each with its products and its exponentials in blocks,
+// overlapped in a fifth of the matrix cycles), so a step forms the next group's
+// scores between the exponentials of its own, and sums its own values between the
+// conversions of the codes to come.  Bundle n is what step n needs from LDS: the
+// keys of group n + 1 and the values of group n.  Bundles alternate between two
+// places: while one is read, the next one's codes are converted into the other and
+// the one after that is on its way from memory in registers; one barrier a step.
+template <int D, int NQ, int W>
 struct Shared {
   static constexpr int R = 16 * NQ * W, F = D / 32, kThreads = 64 * W;
-  static constexpr int kUnits = G * 2 * F;                 // KiB of codes a step: keys, then values
-  static constexpr int kPer = kUnits / W;                  // of them a wave's
-  static constexpr int kStage = kUnits * 2 * 64;           // 16-byte fragments a stage
-  static constexpr size_t kLds = std::max(2 * (size_t)kStage * 16, kJoinFloats<R, kThreads> * sizeof(float));
-  static_assert(kUnits % W == 0, "every wave carries as many codes");
+  static constexpr int kPer = 2 * F / W;            // KiB of codes a wave carries of a bundle: keys are the first F, then values
+  static constexpr int kBundle = 2 * F * 128;       // 16-byte fragments of a bundle
+  static constexpr int kTable = kThreads;           // groups whose page and scales are at hand
+  static constexpr size_t kLds = std::max((2 * (size_t)kBundle + kTable) * 16, kJoinFloats<R, kThreads> * sizeof(float));
+  static_assert(2 * F % W == 0, "every wave carries as many codes");
 };
 
-// Four of a group's fragments out of LDS.  What follows stays behind the reads
-// (only arithmetic may pass), so that they are under way while the four before
-// them are used: left to itself the compiler reads one, waits, uses it and reads
-// the next.
-__device__ __forceinline__ void read4(half8 (&to)[4], const u32x4* at) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) to[i] = __builtin_bit_cast(half8, at[i * 64]);
-  __builtin_amdgcn_sched_barrier(0x16);
-}
-
-template <int D, int NQ, int W, int G>
+template <int D, int NQ, int W>
 __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) {
-  using S = Shared<D, NQ, W, G>;
+  using S = Shared<D, NQ, W>;
   constexpr int R = S::R, F = S::F, C = D / 16;
   extern __shared__ __align__(16) u32x4 stage[];
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, hi = lane >> 4, lo = lane & 15;
+  u32x4* table = stage + 2 * S::kBundle;   // number in the code arrays, key scale, log2 and reciprocal of the value scale
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
   Walk<R> walk;
   if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
@@ -675,142 +727,140 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   }
 
   const Range see = visible(A, p_first, p_last);
-  const int from = (int)((int64_t)see.n * w.from / w.of), to = (int)((int64_t)see.n * w.to / w.of);
-  const size_t page_bytes = (size_t)D << A.c.page_shift;
+  const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.from / w.of));
+  const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.to / w.of));
   const int in_page = (1 << (A.c.page_shift - 5)) - 1;
-  // lane i: page and scales of the i-th group from `base`, 64 at a time; the
-  // loads run up to two steps ahead of the work, so theirs are kept apart
-  int id_load = -1, id_work = -1, base_load = from - 64, base_work = from - 64;
-  float ks_work = 0.0f, vs_work = 0.0f;
   auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
-  auto page_of = [&](int n) { return n < to ? page_id(A.b, A.c.n_pages, w.seq, group_at(n) >> (A.c.page_shift - 5)) : -1; };
-  u32x4 raw[S::kPer];
-  auto load = [&](int n0) {   // groups n0 .. n0 + G - 1; one that is not there: page 0's bytes, hidden later
-    if (n0 - base_load >= 64) {
-      base_load = n0;
-      id_load = page_of(n0 + lane);
-    }
+  int table_at = 0;   // group of the table's first entry
+  auto fill = [&](int n) {
+    const int i = max(n + tid, from), g = group_at(i);
+    const int id = i < to ? page_id(A.b, A.c.n_pages, w.seq, g >> (A.c.page_shift - 5)) : -1;
+    const size_t at = (size_t)max(id, 0) * A.c.hkv + head;
+    const float ks = A.c.ks[at], vs = fmaxf(A.c.vs[at], kMinScale);
+    const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
+    __syncthreads();
+    table[tid] = u32x4{(uint32_t)where, __float_as_uint(ks), __float_as_uint(__builtin_amdgcn_logf(vs)),
+                       __float_as_uint(__builtin_amdgcn_rcpf(vs))};
+    table_at = n;
+    __syncthreads();
+  };
+  auto entry = [&](int n) { return table[n - table_at]; };
+  using Raw = u32x4[S::kPer];
+  // a bundle: the keys at `k`, the values at `v` (numbers of groups in the code
+  // arrays; one that is not there: the arrays' first, hidden later)
+  auto load = [&](int k, int v, Raw& raw) {
 #pragma unroll
     for (int u = 0; u < S::kPer; ++u) {
-      const int unit = u * W + wave, g = unit / (2 * F), f = unit % F;
-      const bool key = unit / F % 2 == 0;
-      const int id = max(__builtin_amdgcn_readlane(id_load, n0 - base_load + g), 0);
-      const size_t off = ((size_t)id * A.c.hkv + head) * page_bytes + (size_t)(group_at(n0 + g) & in_page) * 32 * D;
-      raw[u] = *(reinterpret_cast<const u32x4*>((key ? A.c.k : A.c.v) + off) + f * 64 + lane);
+      const int unit = u * W + wave;
+      const bool key = unit < F;
+      raw[u] = load_codes<0>((key ? A.c.k : A.c.v) + (size_t)max(key ? k : v, 0) * (32 * D), unit % F);
     }
   };
-  auto store = [&](int which) {
+  auto uniform = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane((int)x); };
+  // pieces `from` .. `to` - 1 of the 4 kPer that the wave's codes are converted in
+  u32x4 made[2];
+  auto store = [&](int n, const Raw& raw, int from, int to) {
 #pragma unroll
-    for (int u = 0; u < S::kPer; ++u) {
-      u32x4* at = stage + which * S::kStage + (u * W + wave) * 128 + lane;
-      at[0] = __builtin_bit_cast(u32x4, codes_to_half(raw[u][0], raw[u][1]));
-      at[64] = __builtin_bit_cast(u32x4, codes_to_half(raw[u][2], raw[u][3]));
+    for (int i = 0; i < 4 * S::kPer; ++i) {
+      if (i < from || i >= to) continue;
+      const u32x2 h = codes_to_half4(raw[i / 4][i % 4]);
+      made[i / 2 % 2][i % 2 * 2] = h[0];
+      made[i / 2 % 2][i % 2 * 2 + 1] = h[1];
+      if (i % 2) stage[(n & 1) * S::kBundle + (i / 4 * W + wave) * 128 + i / 2 % 2 * 64 + lane] = made[i / 2 % 2];
     }
+  };
+  // Products of a bundle's C key or value fragments, other() work between them;
+  // `ring` holds the first kRing fragments when it begins and those of `then`
+  // when it ends.  The compiler keeps the order: arithmetic on its own may pass,
+  // matrix instructions and LDS reads may not.
+  constexpr int kRing = 4;
+  half8 ring[kRing];
+  auto fetch = [&](const u32x4* at, int i) { ring[i % kRing] = __builtin_bit_cast(half8, at[i * 64]); };
+  auto products = [&](const u32x4* at, const u32x4* then, auto product, auto other) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+      product(i, ring[i % kRing]);
+      if (i + kRing < C)
+        fetch(at, i + kRing);
+      else if (then)
+        fetch(then, i + kRing - C);
+      other(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // scores of the keys in bundle n
+  auto score = [&](f32x4 (&s)[NQ][2]) {
+    return [&](int i, half8 k) {
+#pragma unroll
+      for (int t = 0; t < NQ; ++t) {
+        f32x4& to = s[t][i / (D / 32)];
+        to = mfma(k, qf[t][i % (D / 32)], i % (D / 32) ? to : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      }
+    };
+  };
+  auto bundle = [&](int n) { return stage + (n & 1) * S::kBundle + lane; };
+  // What a step needs of the table is read a step before: `here` is the entry of
+  // its group, `far` that of the keys it loads; the values it loads are those of
+  // the keys loaded by the step before.
+  u32x4 here;
+  uint32_t far;
+  int v_at;
+  // `ready` holds bundle n + 1's codes, `coming` takes bundle n + 2's
+  auto step = [&](int n, f32x4 (&now)[NQ][2], f32x4 (&next)[NQ][2], const Raw& ready, Raw& coming) {
+    const int k_at = uniform(far), id = uniform(here[0]);
+    const float ks = __uint_as_float(uniform(here[1])), lv = __uint_as_float(uniform(here[2])), rv = __uint_as_float(uniform(here[3]));
+    load(k_at, v_at, coming);
+    v_at = k_at;
+    if (n + 4 >= table_at + S::kTable) fill(n);
+    here = entry(n + 1);
+    far = entry(n + 4)[0];
+    if (working) {
+      const u32x4* kf = bundle(n);
+      const u32x4* vf = kf + F * 128;
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) fetch(kf, i);
+      const int first = group_at(n) * 32;
+      const Group group{id, first, ks, lv, rv, id < 0 || hides(A, first, w_first, w_last)};
+      Weights<NQ> weights;
+      weights.hide(A, group, now, qs, pos);
+      products(kf, vf, score(next), [&](int i) { weights.form(group, now, m, i * 8 * NQ / C, (i + 1) * 8 * NQ / C); });
+      half8 pf[NQ];
+      weights.settle(group, now, m, l, o, pf);
+      products(vf, static_cast<const u32x4*>(nullptr), [&](int i, half8 v) {
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) o[t][i] = mfma(v, pf[t], o[t][i]);
+      }, [&](int i) { store(n + 1, ready, i * 4 * S::kPer / C, (i + 1) * 4 * S::kPer / C); });
+    } else {
+      store(n + 1, ready, 0, 4 * S::kPer);
+    }
+    __syncthreads();
   };
   if (from < to) {
-    load(from);
-    store(0);
-    if (from + G < to) load(from + G);
+    f32x4 even[NQ][2], odd[NQ][2];
+    Raw one, two;
+    fill(from);
+    int at[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = uniform(entry(from + i)[0]);
+    load(at[0], at[0], one);   // of bundle from - 1 only the keys are used
+    load(at[1], at[0], two);
+    store(from - 1, one, 0, 4 * S::kPer);
+    load(at[2], at[1], one);
+    store(from, two, 0, 4 * S::kPer);
+    v_at = at[2];
+    here = entry(from);
+    far = (uint32_t)at[3];
     __syncthreads();
-  }
-  for (int n0 = from, which = 0; n0 < to; n0 += G, which ^= 1) {
-    if (n0 - base_work >= 64) {
-      base_work = n0;
-      id_work = page_of(n0 + lane);
-      const size_t at = (size_t)max(id_work, 0) * A.c.hkv + head;
-      ks_work = A.c.ks[at];
-      vs_work = fmaxf(A.c.vs[at], kMinScale);
-      // waited for here, once in 64 groups: a use further down would wait for
-      // the codes too that are loaded in between, in every step
-      __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt 0
+#pragma unroll
+    for (int i = 0; i < kRing; ++i) fetch(bundle(from - 1), i);
+    products(bundle(from - 1), static_cast<const u32x4*>(nullptr), score(even), [](int) {});
+    __syncthreads();   // its keys' place is the next bundle's
+    for (int n = from;;) {
+      step(n, even, odd, one, two);
+      if (++n >= to) break;
+      step(n, odd, even, two, one);
+      if (++n >= to) break;
     }
-    if (n0 + G < to) {
-      store(which ^ 1);
-      if (n0 + 2 * G < to) load(n0 + 2 * G);
-    }
-    if (working) {
-#pragma unroll
-      for (int g = 0; g < G; ++g) {
-        if (G > 1 && n0 + g >= to) break;
-        const int i = n0 + g - base_work, first = group_at(n0 + g) * 32;
-        const u32x4* kf = stage + which * S::kStage + g * F * 256 + lane;
-        const u32x4* vf = kf + F * 128;
-        const int id = __builtin_amdgcn_readlane(id_work, i);
-        const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_work), i));
-        const float vs = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vs_work), i));
-        f32x4 s[NQ][2];
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        half8 now[4], next[4];
-        read4(now, kf);
-#pragma unroll
-        for (int c = 0; c < C / 4; ++c) {
-          read4(next, c + 1 < C / 4 ? kf + (c + 1) * 256 : vf);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < NQ; ++t) {
-              const int n = c * 4 + i, tt = n / (D / 32);
-              s[t][tt] = mfma(now[i], qf[t][n % (D / 32)], s[t][tt]);
-            }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[i] = next[i];
-        }
-        const float lv = __builtin_amdgcn_logf(vs), rv = __builtin_amdgcn_rcpf(vs);
-        const bool edge = id < 0 || first + 31 > w_first ||
-                          (A.window > 0 && first <= w_last - A.window && first + 31 >= A.sinks);
-        half8 pf[NQ];
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) {
-          float c = ks * qs[t];
-          float x[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) x[j] = s[t][j >> 2][j & 3];
-          if (edge) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const int at = first + hi * 4 + (j >> 2) * 16 + (j & 3);
-              const bool seen = id >= 0 && at <= pos[t] && (A.window == 0 || at > pos[t] - A.window || at < A.sinks);
-              x[j] = seen ? x[j] * c : -INFINITY;
-            }
-            c = 1.0f;
-          }
-          float top = x[0];
-#pragma unroll
-          for (int j = 1; j < 8; ++j) top = fmaxf(top, x[j]);
-          top = fmaf(top, c, lv);
-          if (__any(top > m[t] + (kHead + kSlack))) {
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float next = fmaxf(m[t], top - kHead), down = __builtin_amdgcn_exp2f(m[t] - next);
-            m[t] = next;
-            l[t] *= down;
-#pragma unroll
-            for (int cc = 0; cc < C; ++cc) o[t][cc] *= down;
-          }
-          const float shift = lv - m[t];
-          float sum = 0.0f;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float p = __builtin_amdgcn_exp2f(fmaf(x[j], c, shift));
-            sum += p;
-            pf[t][j] = (_Float16)p;
-          }
-          l[t] = fmaf(sum, rv, l[t]);
-        }
-#pragma unroll
-        for (int c = 0; c < C / 4; ++c) {
-          if (c + 1 < C / 4) read4(next, vf + (c + 1) * 256);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int t = 0; t < NQ; ++t) o[t][c * 4 + i] = mfma(now[i], pf[t], o[t][c * 4 + i]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) now[i] = next[i];
-        }
-      }
-    }
-    __syncthreads();
   }
 
   const Parts parts = parts_of<D, R>(A, w, head);
@@ -865,17 +915,17 @@ size_t workspace_bytes(const Plan& p, int hkv, int D) {
   return kArrivedBytes + slots * p.rows * (D + 2) * sizeof(float);
 }
 
-template <int D, int NQ, int W, int G>
+template <int D, int NQ, int W>
 hipError_t launch_shared(const AttendArgs& A, dim3 grid, hipStream_t s) {
-  using S = Shared<D, NQ, W, G>;
+  using S = Shared<D, NQ, W>;
   static bool attr_set = false;
   if (!attr_set) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_shared_kernel<D, NQ, W, G>),
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_shared_kernel<D, NQ, W>),
                                              hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
     if (e != hipSuccess) return e;
     attr_set = true;
   }
-  hipLaunchKernelGGL((attend_shared_kernel<D, NQ, W, G>), grid, dim3(S::kThreads), S::kLds, s, A);
+  hipLaunchKernelGGL((attend_shared_kernel<D, NQ, W>), grid, dim3(S::kThreads), S::kLds, s, A);
   return hipSuccess;
 }
 
@@ -888,16 +938,15 @@ int launch(const AttendArgs& A, const Plan& plan, hipStream_t s) {
   const int64_t grid = std::max<int64_t>(tiles, A.target) * A.c.hkv;   // a tile a workgroup, or A.target runs a head
   if (grid > 0x7FFFFFFF) return dh::fail(DH_EUNSUP, "attend: too many rows for one launch");
   const dim3 g((unsigned)grid);
-  constexpr int G = D == 256 ? 1 : 2;
   hipError_t e = hipSuccess;
   if (!plan.shared)
     hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, dim3(kThreads), 0, s, A);
   else if (R == 64)
-    e = launch_shared<D, 1, 4, G>(A, g, s);
+    e = launch_shared<D, 1, 4>(A, g, s);
   else if constexpr (D == 256)
-    e = launch_shared<D, 1, 8, 1>(A, g, s);
+    e = launch_shared<D, 1, 8>(A, g, s);
   else
-    e = launch_shared<D, 2, 4, G>(A, g, s);
+    e = launch_shared<D, 2, 4>(A, g, s);
   if (e != hipSuccess) return dh::fail(DH_EHIP, "attend kernel: %s", hipGetErrorString(e));
   return launched("attend kernel");
 }
