@@ -75,8 +75,8 @@ def _need(ok, text):
 
 
 def _wrong(name, t, dtype, shape, dev):
-    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {dev} "
-                     f"(the current one), not {t.dtype} {tuple(t.shape)} on {t.device}")
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on GPU {dev}, "
+                     f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _rows3(name, t, dev, heads, d, torch):
@@ -94,9 +94,11 @@ def _rows3(name, t, dev, heads, d, torch):
 
 def _cache(k_codes, v_codes, k_scale, v_scale, torch):
     """Checks a cache's four tensors; (GPU index, pages, kv heads, page, D)."""
-    dev, shape = torch.cuda.current_device(), k_codes.shape
+    dev, shape = k_codes.get_device(), k_codes.shape
     if len(shape) != 4:
         raise ValueError("k_codes must be [pages][heads][page][D]")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"the cache must be on the current GPU, not on {k_codes.device}")
     for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
         if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
             _wrong(name, t, torch.uint8, shape, dev)

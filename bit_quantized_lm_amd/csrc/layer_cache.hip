@@ -13,7 +13,7 @@ struct AppendArgs {
   Cache c;
   const uint16_t *q, *k, *v;
   int64_t ldq, ldk, ldv;
-  const u32x2* rope;   // [positions][rot/2] of (cos, sin)
+  const u32x4* rope;   // [positions][rot/2] of (cos, sin), two an element
   int rot, interleaved, hq;
   uint16_t* q_out;
   int q_blocks;        // workgroups that rotate queries, before those that write pages
@@ -25,23 +25,38 @@ constexpr int kThreads = 256;
 // unit u < rot/16 holds eight rotary pairs ((d0 + i, d1 + i) in halves, or
 // (2i, 2i + 1) of the sixteen from 16u interleaved), a later one sixteen
 // elements that no rotation touches.
+struct Place {
+  int d0, d1;
+  bool turned, halves;
+};
+__device__ __forceinline__ Place place_of(int u, int rot, bool interleaved) {
+  Place p;
+  p.turned = u * 16 < rot;
+  p.halves = p.turned && !interleaved;
+  p.d0 = p.halves ? 8 * u : 16 * u;
+  p.d1 = p.halves ? 8 * u + rot / 2 : 16 * u + 8;
+  return p;
+}
+
+struct Turn {   // cos and sin of a unit's eight pairs
+  u32x4 cs[4];
+};
+__device__ __forceinline__ Turn load_turn(const u32x4* __restrict__ rope, int64_t position, int rot, int u) {
+  Turn t;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t.cs[i] = rope[position * (rot / 4) + 4 * u + i];
+  return t;
+}
+
 struct Unit {
   float x[16];
-  int d0, d1;
 };
 
 // Each operation is rounded on its own (no fused multiply-add), so that the
 // result is what the documented fp32 steps give, bit for bit.
-__device__ __forceinline__ Unit load_unit(const uint16_t* __restrict__ row, const u32x2* __restrict__ turn, int rot,
-                                          bool interleaved, int u) {
+__device__ __forceinline__ Unit make_unit(u32x4 a, u32x4 b, const Turn& turn, const Place& p) {
 #pragma clang fp contract(off)
   Unit r;
-  const bool turned = u * 16 < rot;
-  const bool halves = turned && !interleaved;
-  r.d0 = halves ? 8 * u : 16 * u;
-  r.d1 = halves ? 8 * u + rot / 2 : 16 * u + 8;
-  const u32x4 a = *reinterpret_cast<const u32x4*>(row + r.d0);
-  const u32x4 b = *reinterpret_cast<const u32x4*>(row + r.d1);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     r.x[2 * i] = bf16_lo(a[i]);
@@ -51,21 +66,22 @@ __device__ __forceinline__ Unit load_unit(const uint16_t* __restrict__ row, cons
   }
   auto turn_pair = [&](float& xa, float& xb, int i) {
 #pragma clang fp contract(off)
-    const u32x2 t = turn[8 * u + i];
-    const float c = __uint_as_float(t[0]), s = __uint_as_float(t[1]);
+    const float c = __uint_as_float(turn.cs[i / 2][i % 2 * 2]), s = __uint_as_float(turn.cs[i / 2][i % 2 * 2 + 1]);
     const float ac = xa * c, bs = xb * s, bc = xb * c, as = xa * s;
     xa = ac - bs;
     xb = bc + as;
   };
-  if (halves) {
+  if (p.halves) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn_pair(r.x[i], r.x[8 + i], i);
-  } else if (turned) {
+  } else if (p.turned) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) turn_pair(r.x[2 * i], r.x[2 * i + 1], i);
   }
   return r;
 }
+
+__device__ __forceinline__ u32x4 load8(const uint16_t* at) { return *reinterpret_cast<const u32x4*>(at); }
 
 __device__ __forceinline__ u32x4 pack8(const float* x) {
   return u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]), bf16_pair(x[6], x[7])};
@@ -82,118 +98,206 @@ __device__ __forceinline__ uint32_t again(uint32_t code, float ratio) {
   return (uint32_t)((int)__builtin_rintf((float)((int)code - 128) * ratio) + 128);
 }
 
-// Rotates the queries: one Unit a thread and step.
+// Rotates the queries, a row a wave: a lane keeps one unit's cosines and sines
+// for all heads of the row (64/U heads a turn of the wave).
 template <int D>
 __device__ __forceinline__ void rotate_queries(const AppendArgs& A) {
   constexpr int U = D / 16;
-  const int per_row = A.hq * U, half = A.rot / 2;
-  const int64_t units = (int64_t)A.b.T * per_row;
-  const int last = (A.b.max_pages << A.c.page_shift) - 1;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < units; i += (int64_t)A.q_blocks * kThreads) {
-    const int r = (int)(i / per_row), x = (int)(i % per_row), h = x / U, u = x % U;
-    int s = 0;   // the row's sequence: the last that starts at or before it
-    for (int lo = 0, hi = A.b.n_seq; hi - lo > 1;) {
-      const int mid = (lo + hi) / 2;
-      (A.b.q_start[mid] <= r ? lo : hi) = mid;
-      s = lo;
-    }
-    const Seq q = load_seq(A.b, s);
-    const int p = min(max(q.begin + r - q.row0, 0), last);
-    const Unit t = load_unit(A.q + r * A.ldq + h * D, A.rope + (size_t)p * half, A.rot, A.interleaved, u);
-    uint16_t* out = A.q_out + ((size_t)r * A.hq + h) * D;
-    *reinterpret_cast<u32x4*>(out + t.d0) = pack8(t.x);
-    *reinterpret_cast<u32x4*>(out + t.d1) = pack8(t.x + 8);
+  const int lane = threadIdx.x & 63, u = lane % U, r = blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6);
+  if (r >= A.b.T) return;
+  // the row's sequence: the last that starts at or before it, 64 a look
+  int s = -1;
+  for (int base = 0; base < A.b.n_seq; base += 64) {
+    const int before = __popcll(__ballot(base + lane < A.b.n_seq && A.b.q_start[min(base + lane, A.b.n_seq - 1)] <= r));
+    s += before;
+    if (before < 64) break;
+  }
+  const Seq q = load_seq(A.b, max(s, 0));
+  const int last = (A.b.max_pages << A.c.page_shift) - 1, position = min(max(q.begin + r - q.row0, 0), last);
+  const Place p = place_of(u, A.rot, A.interleaved);
+  const Turn turn = p.turned ? load_turn(A.rope, position, A.rot, u) : Turn{};
+  const uint16_t* in = A.q + r * A.ldq;
+  uint16_t* out = A.q_out + (size_t)r * A.hq * D;
+#pragma unroll 4
+  for (int h = lane / U; h < A.hq; h += 64 / U) {
+    const Unit x = make_unit(load8(in + h * D + p.d0), load8(in + h * D + p.d1), turn, p);
+    *reinterpret_cast<u32x4*>(out + h * D + p.d0) = pack8(x.x);
+    *reinterpret_cast<u32x4*>(out + h * D + p.d1) = pack8(x.x + 8);
   }
 }
 
 // One (page, head) of keys or values: the scale from the new values' largest
-// magnitude, the new codes in token order in LDS, then the 16-byte units of
-// the fragment order out of LDS.  The page has one writer, so an older
-// token's code is re-rounded here without a race, and only where the scale rose.
-template <int D, bool kKeys>
-__device__ __forceinline__ void write_page(const AppendArgs& A, int s, int page_no, int head, uint8_t* lds) {
+// magnitude, the new codes in LDS in the fragment order, then its 16-byte units
+// out of LDS.  The page has one writer, so an older token's code is re-rounded
+// here without a race, and only where the scale rose.  Values that a thread has
+// read for the scale it keeps for the codes, as far as its registers go; a
+// larger page's are read again.
+struct Page {
+  const uint16_t* x;   // token 0's head (tokens before t0 are not there)
+  int64_t ld;
+  int p0, t0, t1;      // position of token 0; new tokens
+};
+
+// Keys: a unit of a token a thread and turn.
+template <int D>
+struct KeyCodes {
+  static constexpr int kKept = 2;
+  Unit kept[kKept];
+  __device__ __forceinline__ Unit unit(const AppendArgs& A, const Page& g, int i) const {
+    const int t = g.t0 + i / (D / 16), u = i % (D / 16);
+    const Place p = place_of(u, A.rot, A.interleaved);
+    const uint16_t* at = g.x + t * g.ld;
+    return make_unit(load8(at + p.d0), load8(at + p.d1), p.turned ? load_turn(A.rope, g.p0 + t, A.rot, u) : Turn{}, p);
+  }
+  __device__ __forceinline__ float largest(const AppendArgs& A, const Page& g) {
+    const int units = (g.t1 - g.t0) * (D / 16);
+    float top = 0.0f;
+    auto take = [&](const Unit& x) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x.x[j]));
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < units) take(kept[k] = unit(A, g, i));
+    }
+    for (int i = threadIdx.x + kKept * kThreads; i < units; i += kThreads) take(unit(A, g, i));
+    return top;
+  }
+  __device__ __forceinline__ void write(const AppendArgs& A, const Page& g, float inv, uint8_t* lds) const {
+    const int units = (g.t1 - g.t0) * (D / 16);
+    auto put = [&](const Unit& x, int i) {
+      const int t = g.t0 + i / (D / 16);
+      const Place p = place_of(i % (D / 16), A.rot, A.interleaved);
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 16; ++j) w[j >> 2] |= code_of(x.x[j], inv) << (8 * (j & 3));
+      auto at = [&](int e) {
+        return lds + t / 32 * 32 * D + ((t % 32 / 16 * (D / 64) + e / 64) * 64 + e % 64 / 16 * 16 + t % 16) * 16 + e % 16;
+      };
+      *reinterpret_cast<u32x2*>(at(p.d0)) = u32x2{w[0], w[1]};
+      *reinterpret_cast<u32x2*>(at(p.d1)) = u32x2{w[2], w[3]};
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < units) put(kept[k], i);
+    }
+    for (int i = threadIdx.x + kKept * kThreads; i < units; i += kThreads) put(unit(A, g, i), i);
+  }
+  // token of byte j of the fragment order's unit i
+  static __device__ __forceinline__ int token(int i, int) { return i / (2 * D) * 32 + i % (2 * D) / 64 / (D / 64) * 16 + (i & 15); }
+};
+
+// Values: eight elements of four tokens a thread and turn, whose codes stand in
+// fours of one element in the fragment order.
+template <int D>
+struct ValueCodes {
+  static constexpr int kKept = 2;
+  struct Four {
+    u32x4 x[4];
+  };
+  Four kept[kKept];
+  static __device__ __forceinline__ int quads(const Page& g) { return ((g.t1 - 1) / 4 - g.t0 / 4 + 1) * (D / 8); }
+  __device__ __forceinline__ Four four(const Page& g, int i) const {
+    const int t = (g.t0 / 4 + i / (D / 8)) * 4, e = i % (D / 8) * 8;
+    Four f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f.x[k] = t + k >= g.t0 && t + k < g.t1 ? load8(g.x + (t + k) * g.ld + e) : u32x4{0u, 0u, 0u, 0u};
+    return f;
+  }
+  __device__ __forceinline__ float largest(const AppendArgs&, const Page& g) {
+    const int n = quads(g);
+    uint32_t top = 0u;   // bf16 magnitudes compare as integers
+    auto take = [&](const Four& f) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) top = max(top, max(f.x[k][j] & 0x7FFFu, f.x[k][j] >> 16 & 0x7FFFu));
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < n) take(kept[k] = four(g, i));
+    }
+    for (int i = threadIdx.x + kKept * kThreads; i < n; i += kThreads) take(four(g, i));
+    return __uint_as_float(top << 16);
+  }
+  __device__ __forceinline__ void write(const AppendArgs&, const Page& g, float inv, uint8_t* lds) const {
+    const int n = quads(g);
+    auto put = [&](const Four& f, int i) {
+      const int t = (g.t0 / 4 + i / (D / 8)) * 4, e0 = i % (D / 8) * 8;
+      uint8_t* at = lds + t / 32 * 32 * D + ((e0 / 32 * 4 + t % 16 / 4) * 16 + e0 % 16) * 16 + e0 % 32 / 16 * 8 + t % 32 / 16 * 4;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        uint32_t w = 0u;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w |= code_of(j % 2 ? bf16_hi(f.x[k][j / 2]) : bf16_lo(f.x[k][j / 2]), inv) << (8 * k);
+        *reinterpret_cast<uint32_t*>(at + j * 16) = w;
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      const int i = threadIdx.x + k * kThreads;
+      if (i < n) put(kept[k], i);
+    }
+    for (int i = threadIdx.x + kKept * kThreads; i < n; i += kThreads) put(four(g, i), i);
+  }
+  static __device__ __forceinline__ int token(int i, int j) { return i / (2 * D) * 32 + i % 64 / 16 * 4 + j % 8 / 4 * 16 + j % 4; }
+};
+
+template <int D, class Codes>
+__device__ __forceinline__ void write_page(const AppendArgs& A, int s, int page_no, int head, const uint16_t* x, int64_t ld,
+                                           uint8_t* codes_base, float* scale_base, uint8_t* lds) {
 #pragma clang fp contract(off)
-  constexpr int U = D / 16;
-  __shared__ float wave_max[kThreads / 64];
+  __shared__ float wave_top[kThreads / 64];
   const int tid = threadIdx.x, page = 1 << A.c.page_shift;
   const int id = page_id(A.b, A.c.n_pages, s, page_no);
   if (id < 0) return;
   const Seq q = load_seq(A.b, s);
-  const int p0 = page_no << A.c.page_shift;
-  const int t0 = max(q.begin - p0, 0), t1 = min(q.len - p0, page);   // new tokens of the page
-  const uint16_t* x = kKeys ? A.k : A.v;
-  const int64_t ld = kKeys ? A.ldk : A.ldv;
-  const int half = A.rot / 2, rot = kKeys ? A.rot : 0;
-  float* scale = (kKeys ? A.c.ks : A.c.vs) + (size_t)id * A.c.hkv + head;
-  u32x4* codes = reinterpret_cast<u32x4*>((kKeys ? A.c.k : A.c.v) + ((size_t)id * A.c.hkv + head) * ((size_t)page * D));
-  const int64_t row0 = (int64_t)q.row0 + p0 - q.begin;   // row of token 0 of the page
-  auto unit = [&](int i) {
-    const int t = t0 + i / U;
-    return load_unit(x + (row0 + t) * ld + head * D, A.rope + (size_t)(p0 + t) * half, rot, A.interleaved, i % U);
-  };
-  const int units = (t1 - t0) * U;
-  float top = 0.0f;
-  for (int i = tid; i < units; i += kThreads) {
-    const Unit r = unit(i);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(r.x[j]));
-  }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  if ((tid & 63) == 0) wave_max[tid >> 6] = top;
+  Page g;
+  g.p0 = page_no << A.c.page_shift;
+  g.t0 = max(q.begin - g.p0, 0);
+  g.t1 = min(q.len - g.p0, page);
+  g.x = x + ((int64_t)q.row0 + g.p0 - q.begin) * ld + head * D;
+  g.ld = ld;
+  float* scale = scale_base + (size_t)id * A.c.hkv + head;
+  u32x4* codes = reinterpret_cast<u32x4*>(codes_base + ((size_t)id * A.c.hkv + head) * ((size_t)page * D));
+  Codes values;
+  float top = wave_max(values.largest(A, g));
+  if ((tid & 63) == 0) wave_top[tid >> 6] = top;
   const float before = *scale;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, wave_max[w]);
+  for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, wave_top[w]);
   float step = fmaxf(top / 127.0f, kMinScale);
-  if (t0 > 0) step = fmaxf(step, before);
-  const float inv = 1.0f / step, ratio = before / step;
-  const bool raised = t0 > 0 && step > before;
-  for (int i = tid; i < units; i += kThreads) {
-    const Unit r = unit(i);
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 16; ++j) w[j >> 2] |= code_of(r.x[j], inv) << (8 * (j & 3));
-    uint8_t* at = lds + (t0 + i / U) * D;
-    *reinterpret_cast<u32x2*>(at + r.d0) = u32x2{w[0], w[1]};
-    *reinterpret_cast<u32x2*>(at + r.d1) = u32x2{w[2], w[3]};
-  }
+  if (g.t0 > 0) step = fmaxf(step, before);
+  const float ratio = before / step;
+  const bool raised = g.t0 > 0 && step > before;
+  values.write(A, g, 1.0f / step, lds);
   __syncthreads();
   if (tid == 0) *scale = step;
-  // 16-byte units of the fragment order
-  for (int i = tid; i < page * U; i += kThreads) {
-    const int g = i / (2 * D), f = i % (2 * D) / 64, lane = i & 63, hi = lane >> 4, lo = lane & 15;
-    if (kKeys) {
-      const int t = g * 32 + f / (D / 64) * 16 + lo, e = f % (D / 64) * 64 + hi * 16;
-      if (t >= t0 && t < t1) {
-        codes[i] = *reinterpret_cast<const u32x4*>(lds + t * D + e);
-      } else if (raised && t < t0) {
-        u32x4 w = codes[i];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const uint32_t c = again((w[j >> 2] >> (8 * (j & 3))) & 255u, ratio);
-          w[j >> 2] = (w[j >> 2] & ~(255u << (8 * (j & 3)))) | c << (8 * (j & 3));
-        }
-        codes[i] = w;
-      }
-    } else {
-      // tokens g*32 + hi*4 + {0..3, 16..19}, elements f*32 + lo and + 16
-      const int tb = g * 32 + hi * 4, e = f * 32 + lo;
-      if (tb >= t1 || (tb + 19 < t0 && !raised)) continue;
-      const bool whole = tb >= t0 && tb + 19 < t1;
-      u32x4 w = whole ? u32x4{0u, 0u, 0u, 0u} : codes[i];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int t = tb + (j & 7) / 4 * 16 + (j & 3);
-        uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 255u;
-        if (t >= t0 && t < t1)
-          c = lds[t * D + e + j / 8 * 16];
-        else if (raised && t < t0)
-          c = again(c, ratio);
-        w[j >> 2] = (w[j >> 2] & ~(255u << (8 * (j & 3)))) | c << (8 * (j & 3));
-      }
-      codes[i] = w;
+  const u32x4* made = reinterpret_cast<const u32x4*>(lds);
+  for (int i = tid; i < page * (D / 16); i += kThreads) {
+    const int first = Codes::token(i, 0), last = Codes::token(i, 15);
+    if (first >= g.t0 && last < g.t1) {
+      codes[i] = made[i];
+      continue;
     }
+    if (first >= g.t1 || (last < g.t0 && !raised)) continue;
+    u32x4 w = codes[i];
+    const u32x4 n = made[i];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const int t = Codes::token(i, j);
+      uint32_t c = (w[j >> 2] >> (8 * (j & 3))) & 255u;
+      if (t >= g.t0 && t < g.t1)
+        c = (n[j >> 2] >> (8 * (j & 3))) & 255u;
+      else if (raised && t < g.t0)
+        c = again(c, ratio);
+      w[j >> 2] = (w[j >> 2] & ~(255u << (8 * (j & 3)))) | c << (8 * (j & 3));
+    }
+    codes[i] = w;
   }
 }
 
@@ -217,9 +321,9 @@ __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   s = __builtin_amdgcn_readfirstlane(s);
   j = __builtin_amdgcn_readfirstlane(j) + (max(load_seq(A.b, s).begin, 0) >> shift);
   if (kind == 0)
-    write_page<D, true>(A, s, j, head, lds);
+    write_page<D, KeyCodes<D>>(A, s, j, head, A.k, A.ldk, A.c.k, A.c.ks, lds);
   else
-    write_page<D, false>(A, s, j, head, lds);
+    write_page<D, ValueCodes<D>>(A, s, j, head, A.v, A.ldv, A.c.v, A.c.vs, lds);
 }
 
 struct ReadArgs {
@@ -310,7 +414,7 @@ int draft_layer_append(const void* q, int64_t ldq, const void* k, int64_t ldk, c
   if ((rc = check_cache(who, A.c, page, A.b))) return rc;
   if (rot < 0 || rot > D || rot % 16 != 0)
     return dh::fail(DH_ESHAPE, "append: rot must be a multiple of 16 in 0..D (got %d)", rot);
-  if (rot > 0 && (!rope || !aligned(rope, 8))) return dh::fail(DH_EINVAL, "append: rope must be an 8-byte aligned pointer");
+  if (rot > 0 && (!rope || !aligned(rope, 16))) return dh::fail(DH_EINVAL, "append: rope must be a 16-byte aligned pointer");
   if (rot > 0 && positions < max_pages * page)
     return dh::fail(DH_ESHAPE, "append: rope has %d positions, the table reaches %d", positions, max_pages * page);
   if (!q != !q_out) return dh::fail(DH_EINVAL, "append: q and q_out go together");
@@ -321,8 +425,7 @@ int draft_layer_append(const void* q, int64_t ldq, const void* k, int64_t ldk, c
     if ((rc = check_stride(who, "q", q, ldq, (int64_t)hq * D))) return rc;
     if (!aligned(q_out, 16)) return dh::fail(DH_EINVAL, "append: q_out must be 16-byte aligned");
     if (q == q_out && ldq != (int64_t)hq * D) return dh::fail(DH_EINVAL, "append: q_out may be q only where q has no gaps");
-    const int64_t want = ((int64_t)T * hq * (D / 16) + kThreads - 1) / kThreads;
-    A.q_blocks = (int)(want < 4096 ? want : 4096);
+    A.q_blocks = (T + kThreads / 64 - 1) / (kThreads / 64);   // a row a wave
   }
   A.q = static_cast<const uint16_t*>(q);
   A.k = static_cast<const uint16_t*>(k);
@@ -330,7 +433,7 @@ int draft_layer_append(const void* q, int64_t ldq, const void* k, int64_t ldk, c
   A.ldq = ldq;
   A.ldk = ldk;
   A.ldv = ldv;
-  A.rope = reinterpret_cast<const u32x2*>(rope);
+  A.rope = reinterpret_cast<const u32x4*>(rope);
   A.rot = rot;
   A.interleaved = interleaved != 0;
   A.hq = hq;

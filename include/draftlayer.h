@@ -102,7 +102,7 @@ int draft_layer_rope_table(int positions, int rot, double base, double factor, i
  *   rope     device, fp32 [positions][rot/2][2], positions >= max_pages*page
  *   q_out    out, bf16 [T][hq][D] without gaps; may be q itself if ldq = hq*D
  * Row strides are in elements, multiples of 8 and at least the heads' D each;
- * q, k, v, q_out are 16-byte aligned, rope 8-byte.  Two sequences of one call
+ * q, k, v, q_out and rope are 16-byte aligned.  Two sequences of one call
  * must not write the same page.  Values must be finite with |x| < 2^60.
  * Limits: rot a multiple of 16 in 0..D (0: nothing is rotated, rope unused).
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
