@@ -33,13 +33,14 @@ struct AttendArgs {
 // token: row x = (x / group)-th new token, head x % group of the kv head's.
 // Tiles of R such rows share each key and value that they load.
 //
-// Where the batch has at least twice the tiles that fill the card, a workgroup
-// takes one tile.  Where it has fewer, the tiles' visible tokens, as groups of
-// 32, are laid end to end and cut into equal runs, one a workgroup, so that the
-// card is filled and all end together whatever the lengths; a run may hold the
-// end of one tile, whole tiles and the start of another.  A tile that several
-// runs hold parts of is joined by the last of them (join_parts).  Cut by tiles
-// instead, 64 slots over 0.95 GB of mixed lengths waited for the longest: 180 us.
+// Where the batch has at least twice the tiles that fill the card, or fills it
+// once with tiles of much the same length, a workgroup takes one tile.  Else the
+// tiles' visible tokens, as groups of 32, are laid end to end and cut into equal
+// runs, one a workgroup, so that the card is filled and all end together whatever
+// the lengths; a run may hold the end of one tile, whole tiles and the start of
+// another.  A tile that several runs hold parts of is joined by the last of them
+// (join_parts).  64 slots over 0.95 GB of mixed lengths: 158 us in runs, 180 a
+// tile a workgroup; a windowed batch, equal lengths: 54.6 us in runs, 49.5 by tiles.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMinRun = 4;               // least groups of a run
 constexpr int kMaxBlocks = 768;          // most workgroups that a plan takes to fill the card
@@ -76,6 +77,7 @@ __device__ __forceinline__ Range visible(const AttendArgs& A, int p_first, int p
 // it (the most that a tile of the sequence sees; at least 1, so that tiles that
 // see nothing are visited too).
 struct Segment {
+  Seq q;
   int seq, tile;
   int from, to, of;
   int parts, part;   // the tile's parts, and which this is
@@ -94,7 +96,7 @@ class Walk {
     for (int s = lane; s < A.b.n_seq; s += 64) {
       const Seq q = load_seq(A.b, s);
       const int t = tiles_of(A, q), g = groups_of(A, q);
-      if (s < 64) tiles_ = t, groups_ = g;
+      if (s < 64) seq_ = q, tiles_ = t, groups_ = g;
       groups += (float)t * (float)g;
       tiles += (float)t;
       most = fmaxf(most, (float)g);
@@ -102,7 +104,7 @@ class Walk {
     groups = wave_sum(groups);
     tiles = wave_sum(tiles);
     most = wave_max(most);
-    whole_ = tiles >= 2.0f * (float)A.target;
+    whole_ = tiles >= 2.0f * (float)A.target || (tiles <= (float)A.target && most * (float)A.target <= 1.25f * groups);
     // lengths are counted in units of 2^shift groups, so that their sum fits 32 bits
     shift_ = max(0, (int)((__float_as_uint(groups) >> 23) & 255u) - 127 - 28);
     const float unit = __builtin_ldexpf(1.0f, -shift_);
@@ -121,16 +123,15 @@ class Walk {
     const int lane = threadIdx.x & 63;
     int at = at_, before = 0;   // `before`: units of the sequences passed
     for (int base = 0; base < A.b.n_seq; base += 64) {
-      int tiles = tiles_, groups = groups_;
-      if (A.b.n_seq > 64 && base > 0) {
+      Seq q = seq_;
+      int tiles = tiles_, groups = groups_;   // 0 past the last sequence
+      if (base > 0) {
         tiles = groups = 0;
         if (base + lane < A.b.n_seq) {
-          const Seq q = load_seq(A.b, base + lane);
+          q = load_seq(A.b, base + lane);
           tiles = tiles_of(A, q);
           groups = groups_of(A, q);
         }
-      } else if (lane >= A.b.n_seq) {
-        tiles = groups = 0;
       }
       const int units = (groups + (1 << shift_) - 1) >> shift_;
       const int mine = whole_ ? tiles : tiles * units, sum = wave_inclusive_sum(mine);
@@ -139,6 +140,10 @@ class Walk {
         const int i = __builtin_ctzll(__ballot(sum > at));
         const int start = __builtin_amdgcn_readlane(sum, i) - __builtin_amdgcn_readlane(mine, i);
         g.seq = base + i;
+        g.q.row0 = __builtin_amdgcn_readlane(q.row0, i);
+        g.q.n = __builtin_amdgcn_readlane(q.n, i);
+        g.q.len = __builtin_amdgcn_readlane(q.len, i);
+        g.q.begin = g.q.len - g.q.n;
         if (whole_) {
           g.tile = at - start;
           g.from = 0;
@@ -165,7 +170,8 @@ class Walk {
   }
 
  private:
-  int tiles_ = 0, groups_ = 0;   // of sequence `lane`
+  Seq seq_{};                    // sequence `lane`
+  int tiles_ = 0, groups_ = 0;   // its tiles, and what one sees at most
   bool whole_;                   // a tile a workgroup
   int shift_, per_, run_, at_, end_;
 
@@ -482,114 +488,101 @@ struct Weights {
 };
 
 // ------------------------------------------------------- few rows: streaming
-// R = 16 MT rows against a stream of groups of 32 tokens.  Each wave takes
-// every kWaves-th group of its workgroup's part, straight from global memory
-// into the fragments (each load instruction 1 KiB without gaps), so nothing is
-// shared until the waves' results are joined.  S^T = K Q^T puts a row's
-// weights into the lanes and order that the next product takes its columns in
-// (O^T = V^T P^T), so they never leave their registers.
+// 16 rows against a stream of groups of 32 tokens.  Each wave takes every
+// kWaves-th group of its workgroup's run, straight from global memory into the
+// fragments (each load instruction 1 KiB without gaps), a step ahead, so
+// nothing is shared until the waves' results are joined.  S^T = K Q^T puts a
+// row's weights into the lanes and order that the next product takes its columns
+// in (O^T = V^T P^T), so they never leave their registers.  Bound by memory: KSTREAM
 template <int F>
 struct Bytes {   // a lane's codes of one group
   u32x4 k[F], v[F];
 };
 
-template <int D, int MT>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_stream_kernel(AttendArgs A) {
-  constexpr int R = 16 * MT, F = D / 32, C = D / 16;
-  constexpr int kRow = D + 4;
-  constexpr bool kAhead = D * MT <= 256;   // beyond, a second group's bytes do not fit the registers
+template <int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kernel(AttendArgs A) {
+  constexpr int R = 16, F = D / 32, C = D / 16;
   __shared__ __align__(16) union {
-    float o[kWaves][16][kRow];
+    float o[kWaves][R][D + 4];
     float join[kJoinFloats<R, kThreads>];
   } lds;
-  __shared__ float m_lds[kWaves][16], l_lds[kWaves][16];
+  __shared__ float m_lds[kWaves][R], l_lds[kWaves][R];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
   Walk<R> walk;
   if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
   for (Segment w; walk.next(A, w);) {
-  const Seq q = load_seq(A.b, w.seq);
-  const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
-  const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+    const Seq q = w.q;
+    const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
+    const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+    const Range see = visible(A, p_first, p_last);
+    const int from = (int)((int64_t)see.n * w.from / w.of), to = (int)((int64_t)see.n * w.to / w.of);
+    const size_t page_bytes = (size_t)D << A.c.page_shift;
 
-  half8 qf[MT][F];
-  float qs[MT], m[MT], l[MT];
-  int pos[MT];
-  f32x4 o[MT][C];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) {
-    const int x = x0 + t * 16 + lo;
-    const bool valid = t * 16 + lo < rows;
-    pos[t] = valid ? q.begin + x / A.group : -1;
-    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
-    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
-    m[t] = kLowest;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  const Range see = visible(A, p_first, p_last);
-  const int from = (int)((int64_t)see.n * w.from / w.of), to = (int)((int64_t)see.n * w.to / w.of);
-  const size_t page_bytes = (size_t)D << A.c.page_shift;
-  for (int base = from + wave; base < to; base += 64 * kWaves) {
-    // lane i: page and scales of the wave's i-th group from here
-    const int n_mine = base + lane * kWaves, g_mine = n_mine < see.ns ? n_mine : n_mine - see.ns + see.g0;
-    const int id_mine = n_mine < to ? page_id(A.b, A.c.n_pages, w.seq, g_mine >> (A.c.page_shift - 5)) : -1;
-    const size_t at_mine = (size_t)max(id_mine, 0) * A.c.hkv + head;
-    const float ks_mine = A.c.ks[at_mine], vs_mine = fmaxf(A.c.vs[at_mine], kMinScale);
-    const float lv_mine = __builtin_amdgcn_logf(vs_mine), rv_mine = __builtin_amdgcn_rcpf(vs_mine);
-    const int count = min(64, (to - base + kWaves - 1) / kWaves);
-    auto group_at = [&](int i) {
-      const int n = base + i * kWaves;
-      return n < see.ns ? n : n - see.ns + see.g0;
+    // lane i: page and scales of the wave's i-th group from `base`, 64 at a time
+    int base = from + wave, id_mine;
+    float ks_mine, lv_mine, rv_mine;
+    auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
+    auto look = [&] {
+      const int n = base + lane * kWaves;
+      id_mine = n < to ? page_id(A.b, A.c.n_pages, w.seq, group_at(n) >> (A.c.page_shift - 5)) : -1;
+      const size_t at = (size_t)max(id_mine, 0) * A.c.hkv + head;
+      const float vs = id_mine < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
+      ks_mine = A.c.ks[at];
+      lv_mine = __builtin_amdgcn_logf(vs);
+      rv_mine = __builtin_amdgcn_rcpf(vs);
     };
-    auto load = [&](int i, Bytes<F>& w) {   // a page that is not there: page 0's bytes, which step() hides
+    auto load = [&](int i, Bytes<F>& b) {   // of a group that is not there page 0's bytes, which step() hides
       const size_t off = ((size_t)max(__builtin_amdgcn_readlane(id_mine, i), 0) * A.c.hkv + head) * page_bytes +
-                         (size_t)(group_at(i) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
+                         (size_t)(group_at(base + i * kWaves) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
 #pragma unroll
-      for (int f = 0; f < F; ++f) w.k[f] = load_codes<kOnce>(A.c.k + off, f);
+      for (int f = 0; f < F; ++f) b.k[f] = load_codes<kOnce>(A.c.k + off, f);
 #pragma unroll
-      for (int f = 0; f < F; ++f) w.v[f] = load_codes<kOnce>(A.c.v + off, f);
+      for (int f = 0; f < F; ++f) b.v[f] = load_codes<kOnce>(A.c.v + off, f);
     };
-    auto step = [&](int i, const Bytes<F>& w) {
-      const int g = group_at(i), id = __builtin_amdgcn_readlane(id_mine, i);
-      const float ks = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i));
-      const float lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv_mine), i));
-      const float rv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rv_mine), i));
-      f32x4 s[MT][2];
+    // the first codes are on their way before the queries are looked at
+    Bytes<F> even, odd;
+    if (base < to) {
+      look();
+      load(0, even);
+    }
+    half8 qf[F], pf[1];
+    float qs[1], m[1] = {kLowest}, l[1] = {0.0f};
+    int pos[1];
+    f32x4 o[1][C];
+    {
+      const int x = x0 + lo;
+      pos[0] = lo < rows ? q.begin + x / A.group : -1;
+      const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
+      qs[0] = load_query<D>(row, lo < rows, A.scale_log2, qf);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int c = 0; c < C; ++c) o[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+    auto step = [&](int i, const Bytes<F>& b) {
+      const int first = group_at(base + i * kWaves) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
+      const Group group{id, first, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i)),
+                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv_mine), i)),
+                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rv_mine), i)),
+                        id < 0 || hides(A, first, p_first, p_last)};
+      f32x4 s[1][2] = {{{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}}};
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const half8 a = codes_to_half(w.k[f][0], w.k[f][1]), b = codes_to_half(w.k[f][2], w.k[f][3]);
-        const int tt = f / (D / 64), c = f % (D / 64);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          s[t][tt] = mfma(a, qf[t][2 * c], s[t][tt]);
-          s[t][tt] = mfma(b, qf[t][2 * c + 1], s[t][tt]);
-        }
+        const int half = f / (D / 64), c = f % (D / 64);
+        s[0][half] = mfma(codes_to_half(b.k[f][0], b.k[f][1]), qf[2 * c], s[0][half]);
+        s[0][half] = mfma(codes_to_half(b.k[f][2], b.k[f][3]), qf[2 * c + 1], s[0][half]);
       }
-      half8 pf[MT];
-      const Group group{id, g * 32, ks, lv, rv, id < 0 || hides(A, g * 32, p_first, p_last)};
-      Weights<MT> weights;
+      Weights<1> weights;
       weights.hide(A, group, s, qs, pos);
       weights.form(group, s, m);
       weights.settle(group, s, m, l, o, pf);
 #pragma unroll
       for (int f = 0; f < F; ++f) {
-        const half8 a = codes_to_half(w.v[f][0], w.v[f][1]), b = codes_to_half(w.v[f][2], w.v[f][3]);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          o[t][2 * f] = mfma(a, pf[t], o[t][2 * f]);
-          o[t][2 * f + 1] = mfma(b, pf[t], o[t][2 * f + 1]);
-        }
+        o[0][2 * f] = mfma(codes_to_half(b.v[f][0], b.v[f][1]), pf[0], o[0][2 * f]);
+        o[0][2 * f + 1] = mfma(codes_to_half(b.v[f][2], b.v[f][3]), pf[0], o[0][2 * f + 1]);
       }
     };
-    if constexpr (kAhead) {
-      // one group's loads are under way while the one before is worked on
-      Bytes<F> even, odd;
-      load(0, even);
+    while (base < to) {
+      const int count = min(64, (to - base + kWaves - 1) / kWaves);
       for (int i = 0; i < count; i += 2) {
         if (i + 1 < count) load(i + 1, odd);
         step(i, even);
@@ -597,38 +590,29 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
         if (i + 2 < count) load(i + 2, even);
         step(i + 1, odd);
       }
-    } else {
-      for (int i = 0; i < count; ++i) {
-        Bytes<F> w;
-        load(i, w);
-        step(i, w);
+      base += 64 * kWaves;
+      if (base < to) {
+        look();
+        load(0, even);
       }
     }
-  }
 
-  // Join the waves, 16 rows at a time, then either the result or this part's
-  // share of it.
-  const Parts parts = parts_of<D, R>(A, w, head);
-  const int mine = parts.at(w.part);
-  for (int t = 0; t < MT; ++t) {
-    if (t * 16 >= rows) break;
-    __syncthreads();   // lds: the rows or the segment before this one
+    // join the waves; then either the result or this part's share of it
+    const Parts parts = parts_of<D, R>(A, w, head);
+    const int mine = parts.at(w.part);
+    __syncthreads();   // lds: the segment before this one
+    float sum_mine = l[0];
+    sum_mine += __shfl_xor(sum_mine, 16);
+    sum_mine += __shfl_xor(sum_mine, 32);
+    if (hi == 0) {
+      m_lds[wave][lo] = m[0];
+      l_lds[wave][lo] = sum_mine;
+    }
 #pragma unroll
-    for (int tt = 0; tt < MT; ++tt)
-      if (tt == t) {
-        float sum = l[tt];
-        sum += __shfl_xor(sum, 16);
-        sum += __shfl_xor(sum, 32);
-        if (hi == 0) {
-          m_lds[wave][lo] = m[tt];
-          l_lds[wave][lo] = sum;
-        }
-#pragma unroll
-        for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&lds.o[wave][lo][c * 16 + hi * 4]) = o[tt][c];
-      }
+    for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&lds.o[wave][lo][c * 16 + hi * 4]) = o[0][c];
     __syncthreads();
-    const int r = tid >> 4, x = x0 + t * 16 + r;
-    if (t * 16 + r < rows) {
+    const int r = tid >> 4, x = x0 + r;
+    if (r < rows) {
       float top = m_lds[0][r], sum = 0.0f, share[kWaves];
 #pragma unroll
       for (int v = 1; v < kWaves; ++v) top = fmaxf(top, m_lds[v][r]);
@@ -648,21 +632,19 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : D == 128 ? 2 : 3) void att
           y *= inv;
           *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
         } else {
-          publish4(parts.buffer, mine + (t * 16 + r) * D + e, y);
+          publish4(parts.buffer, mine + r * D + e, y);
         }
       }
       if ((tid & 15) == 0) {
         if (w.parts > 1)
-          publish2(parts.buffer, mine + R * D + (t * 16 + r) * 2, top, sum);
+          publish2(parts.buffer, mine + R * D + r * 2, top, sum);
         else
           write_lse(A, to_row, top, sum);
       }
     }
-  }
-  if (w.parts == 1) continue;
-
-  __syncthreads();   // lds becomes join_parts' scratch
-  join_parts<D, R, kThreads>(A, w, q, x0, rows, head, parts, &lds.join[0]);
+    if (w.parts == 1) continue;
+    __syncthreads();   // lds becomes join_parts' scratch
+    join_parts<D, R, kThreads>(A, w, q, x0, rows, head, parts, &lds.join[0]);
   }
 }
 
@@ -700,7 +682,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   Walk<R> walk;
   if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
   for (Segment w; walk.next(A, w);) {
-  const Seq q = load_seq(A.b, w.seq);
+  const Seq q = w.q;
   w.tile = (int)(((int64_t)q.n * A.group + R - 1) / R) - 1 - w.tile;   // the tiles that see most first
   const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
   const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
@@ -708,23 +690,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   const int mine0 = wave * 16 * NQ;
   const int w_first = q.begin + (x0 + mine0) / A.group, w_last = q.begin + (x0 + min(rows, mine0 + 16 * NQ) - 1) / A.group;
   const bool working = mine0 < rows;
-
-  half8 qf[NQ][F];
-  float qs[NQ], m[NQ], l[NQ];
-  int pos[NQ];
-  f32x4 o[NQ][C];
-#pragma unroll
-  for (int t = 0; t < NQ; ++t) {
-    const int r = mine0 + t * 16 + lo, x = x0 + r;
-    const bool valid = r < rows;
-    pos[t] = valid ? q.begin + x / A.group : -1;
-    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
-    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
-    m[t] = kLowest;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
 
   const Range see = visible(A, p_first, p_last);
   const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.from / w.of));
@@ -736,7 +701,7 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
     const int i = max(n + tid, from), g = group_at(i);
     const int id = i < to ? page_id(A.b, A.c.n_pages, w.seq, g >> (A.c.page_shift - 5)) : -1;
     const size_t at = (size_t)max(id, 0) * A.c.hkv + head;
-    const float ks = A.c.ks[at], vs = fmaxf(A.c.vs[at], kMinScale);
+    const float ks = A.c.ks[at], vs = id < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
     const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
     __syncthreads();
     table[tid] = u32x4{(uint32_t)where, __float_as_uint(ks), __float_as_uint(__builtin_amdgcn_logf(vs)),
@@ -757,6 +722,34 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
     }
   };
   auto uniform = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane((int)x); };
+  // the first codes are on their way before the queries are looked at
+  Raw one, two;
+  int at[4];
+  if (from < to) {
+    fill(from);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) at[i] = uniform(entry(from + i)[0]);
+    load(at[0], at[0], one);   // of bundle from - 1 only the keys are used
+    load(at[1], at[0], two);
+  }
+
+  half8 qf[NQ][F];
+  float qs[NQ], m[NQ], l[NQ];
+  int pos[NQ];
+  f32x4 o[NQ][C];
+#pragma unroll
+  for (int t = 0; t < NQ; ++t) {
+    const int r = mine0 + t * 16 + lo, x = x0 + r;
+    const bool valid = r < rows;
+    pos[t] = valid ? q.begin + x / A.group : -1;
+    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
+    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
+    m[t] = kLowest;
+    l[t] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+
   // pieces `from` .. `to` - 1 of the 4 kPer that the wave's codes are converted in
   u32x4 made[2];
   auto store = [&](int n, const Raw& raw, int from, int to) {
@@ -837,13 +830,6 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   };
   if (from < to) {
     f32x4 even[NQ][2], odd[NQ][2];
-    Raw one, two;
-    fill(from);
-    int at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = uniform(entry(from + i)[0]);
-    load(at[0], at[0], one);   // of bundle from - 1 only the keys are used
-    load(at[1], at[0], two);
     store(from - 1, one, 0, 4 * S::kPer);
     load(at[2], at[1], one);
     store(from, two, 0, 4 * S::kPer);
@@ -940,7 +926,7 @@ int launch(const AttendArgs& A, const Plan& plan, hipStream_t s) {
   const dim3 g((unsigned)grid);
   hipError_t e = hipSuccess;
   if (!plan.shared)
-    hipLaunchKernelGGL((attend_stream_kernel<D, 1>), g, dim3(kThreads), 0, s, A);
+    hipLaunchKernelGGL(attend_stream_kernel<D>, g, dim3(kThreads), 0, s, A);
   else if (R == 64)
     e = launch_shared<D, 1, 4>(A, g, s);
   else if constexpr (D == 256)

@@ -217,6 +217,22 @@ def test_bad_pages_are_left_alone(dev):
     check_attend(c, window=0, sinks=0)
 
 
+@pytest.mark.parametrize("new", [1, 40])
+def test_missing_page_takes_nothing_from_page_zero(dev, new):
+    """A page that is not there is hidden whatever the pool's first page holds."""
+    c = Case(dev, [(new, 200)], 4, 1, 64, 32, seed=21, spare=4)
+    used = c.table[0, :7].copy()
+    other = next(p for p in range(c.n_pages) if p not in used and p != 0)
+    c.table[0, :7] = np.where(used == 0, other, used)     # page 0 is nobody's
+    c.table[0, 3] = -1
+    c.ks[0], c.vs[0], c.kc[0], c.vc[0] = np.inf, np.inf, 255, 255
+    c.upload()
+    check_attend(c, 0, 0)
+    c.ks[0], c.vs[0] = np.nan, np.nan
+    c.upload()
+    check_attend(c, 0, 0)
+
+
 # --------------------------------------------------------------------- read
 @pytest.mark.parametrize("lens,hkv,d,page", [
     ([(1, 1)], 1, 64, 32), ([(500, 500)], 8, 128, 64), ([(33, 97), (0, 5), (64, 64), (1, 300)], 5, 128, 128),
