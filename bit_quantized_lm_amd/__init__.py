@@ -29,9 +29,10 @@ __all__ = list(_BINDING_NAMES + _LAYER_NAMES)
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        from . import _binding
-        return getattr(_binding, name)
-    if name in _LAYER_NAMES:
-        from . import _layer
-        return getattr(_layer, name)
-    raise AttributeError(name)
+        from . import _binding as home
+    elif name in _LAYER_NAMES:
+        from . import _layer as home
+    else:
+        raise AttributeError(name)
+    value = globals()[name] = getattr(home, name)   # found here from now on
+    return value

@@ -43,6 +43,19 @@ def _load():
     return _lib
 
 
+torch = None     # set by the first device call
+_U8 = _F32 = _I32 = _BF16 = None
+
+
+def _device_lib():
+    """The library, with torch at hand (host functions need none)."""
+    global torch, _U8, _F32, _I32, _BF16
+    if torch is None:
+        import torch as t
+        torch, _U8, _F32, _I32, _BF16 = t, t.uint8, t.float32, t.int32, t.bfloat16
+    return _load()
+
+
 def layer_header_functions() -> list[str]:
     """Names of the functions include/draftlayer.h declares."""
     with open(_HEADER) as f:
@@ -67,8 +80,8 @@ def draft_layer_rope_table(positions: int, rot: int, base: float = 10000.0, fact
 
 
 # ------------------------------------------------------------------ device side
-# The checks run before every launch, so each is one expression that formats
-# nothing unless it fails.
+# The checks run before every launch: each is one expression of the cheapest
+# calls, and says what is wrong only once something is.
 def _need(ok, text):
     if not ok:
         raise ValueError(text)
@@ -79,11 +92,15 @@ def _wrong(name, t, dtype, shape, dev):
                      f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _rows3(name, t, dev, heads, d, torch):
+def _is(t, dtype, shape, dev):
+    return t.dtype is dtype and t.get_device() == dev and t.is_contiguous() and t.shape == shape
+
+
+def _rows3(name, t, dev, heads, d):
     """Row stride of a bf16 [T][heads][D] tensor whose rows may have gaps (heads None: any number)."""
     shape = t.shape
-    if t.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or t.get_device() != dev:
-        _wrong(name, t, torch.bfloat16, ("T", "heads" if heads is None else heads, d), dev)
+    if t.dtype is not _BF16 or len(shape) != 3 or shape[2] != d or (heads is not None and shape[1] != heads) or t.get_device() != dev:
+        _wrong(name, t, _BF16, ("T", "heads" if heads is None else heads, d), dev)
     if shape[0] == 0:
         return shape[1] * d
     row, head, one = t.stride()
@@ -92,53 +109,54 @@ def _rows3(name, t, dev, heads, d, torch):
     return row if shape[0] > 1 else shape[1] * d
 
 
-def _cache(k_codes, v_codes, k_scale, v_scale, torch):
+def _cache(k_codes, v_codes, k_scale, v_scale):
     """Checks a cache's four tensors; (GPU index, pages, kv heads, page, D)."""
     dev, shape = k_codes.get_device(), k_codes.shape
     if len(shape) != 4:
         raise ValueError("k_codes must be [pages][heads][page][D]")
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"the cache must be on the current GPU, not on {k_codes.device}")
-    for name, t in (("k_codes", k_codes), ("v_codes", v_codes)):
-        if t.dtype is not torch.uint8 or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
-            _wrong(name, t, torch.uint8, shape, dev)
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if t.dtype is not torch.float32 or t.shape != shape[:2] or not t.is_contiguous() or t.get_device() != dev:
-            _wrong(name, t, torch.float32, shape[:2], dev)
-    return dev, *shape
+    pages, heads, page, d = shape
+    flat = (pages, heads)
+    if not (_is(k_codes, _U8, shape, dev) and _is(v_codes, _U8, shape, dev) and _is(k_scale, _F32, flat, dev)
+            and _is(v_scale, _F32, flat, dev)):
+        for name, t, dtype, want in (("k_codes", k_codes, _U8, shape), ("v_codes", v_codes, _U8, shape),
+                                     ("k_scale", k_scale, _F32, flat), ("v_scale", v_scale, _F32, flat)):
+            if not _is(t, dtype, want, dev):
+                _wrong(name, t, dtype, want, dev)
+    return dev, pages, heads, page, d
 
 
-def _batch(q_start, kv_len, table, dev, torch):
+def _batch(q_start, kv_len, table, dev):
     """Checks a batch's tensors; (sequences, pages a sequence)."""
-    if kv_len.dim() != 1 or table.dim() != 2:
-        raise ValueError("kv_len must be [sequences] and table [sequences][pages]")
+    if table.dim() != 2:
+        raise ValueError("table must be [sequences][pages]")
     n, m = table.shape
-    for name, t, size in (("kv_len", kv_len, n), ("q_start", q_start, n + 1), ("table", table, n)):
-        if t.dtype is not torch.int32 or t.shape[0] != size or not t.is_contiguous() or t.get_device() != dev:
-            _wrong(name, t, torch.int32, (size, m) if name == "table" else (size,), dev)
-    if q_start.dim() != 1:
-        _wrong("q_start", q_start, torch.int32, (n + 1,), dev)
+    if not (_is(q_start, _I32, (n + 1,), dev) and _is(kv_len, _I32, (n,), dev) and _is(table, _I32, (n, m), dev)):
+        for name, t, want in (("q_start", q_start, (n + 1,)), ("kv_len", kv_len, (n,)), ("table", table, (n, m))):
+            if not _is(t, _I32, want, dev):
+                _wrong(name, t, _I32, want, dev)
     return n, m
 
 
-def _raw_stream(stream, dev, torch):
+def _raw_stream(stream, dev):
     """The hipStream_t of `stream` (None: the current one, without building torch's object for it)."""
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else B._stream(stream)
 
 
-def _out(given, name, like, shape, dtype, dev, stream, torch):
+def _out(given, name, like, shape, dtype, dev, stream):
     """The caller's tensor, checked, or a new one (kept for `stream`, if that is not the current one)."""
     if given is not None:
-        if given.dtype is not dtype or given.shape != shape or not given.is_contiguous() or given.get_device() != dev:
+        if not _is(given, dtype, shape, dev):
             _wrong(name, given, dtype, shape, dev)
         return given
     t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
-        _keep_for(t, stream, torch)
+        _keep_for(t, stream)
     return t
 
 
-def _keep_for(t, stream, torch):
+def _keep_for(t, stream):
     """Tells torch's allocator that `t`, made on the current stream, is used on `stream` too."""
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
@@ -157,30 +175,29 @@ def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_star
     [positions][rot/2][2] (None: no rotation); the cache and the batch as
     include/draftlayer.h has them.  Returns the rotated q, bf16 [T][hq][D]
     (q_out may be q itself where q has no gaps)."""
-    import torch
-    lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
-    ldk, ldv = _rows3("k", k, dev, hkv, d, torch), _rows3("v", v, dev, hkv, d, torch)
+    lib = _device_lib()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    ldk, ldv = _rows3("k", k, dev, hkv, d), _rows3("v", v, dev, hkv, d)
     rows = k.shape[0]
     _need(v.shape[0] == rows, "k and v must have as many rows")
     hq, ldq = hkv, 0
     if q is None:
         _need(q_out is None, "q_out needs q")
     else:
-        ldq, hq = _rows3("q", q, dev, None, d, torch), q.shape[1]
+        ldq, hq = _rows3("q", q, dev, None, d), q.shape[1]
         _need(q.shape[0] == rows, "q and k must have as many rows")
-        q_out = _out(q_out, "q_out", q, (rows, hq, d), torch.bfloat16, dev, stream, torch)
+        q_out = _out(q_out, "q_out", q, (rows, hq, d), _BF16, dev, stream)
     positions = rot = 0
     if rope is not None:
-        if rope.dtype is not torch.float32 or rope.dim() != 3 or rope.shape[2] != 2 or not rope.is_contiguous() or rope.get_device() != dev:
-            _wrong("rope", rope, torch.float32, ("positions", "rot/2", 2), dev)
+        if rope.dim() != 3 or rope.shape[2] != 2 or not _is(rope, _F32, rope.shape, dev):
+            _wrong("rope", rope, _F32, ("positions", "rot/2", 2), dev)
         positions, rot = rope.shape[0], rope.shape[1] * 2
     B._check(lib.draft_layer_append(
         None if q is None else q.data_ptr(), ldq, k.data_ptr(), ldk, v.data_ptr(), ldv, None if rope is None else rope.data_ptr(),
         positions, rot, 1 if interleaved else 0, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
         n_pages, page, q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
-        None if q is None else q_out.data_ptr(), _raw_stream(stream, dev, torch)))
+        None if q is None else q_out.data_ptr(), _raw_stream(stream, dev)))
     return q_out
 
 
@@ -188,17 +205,16 @@ def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table,
     """The last tokens of each sequence out of the cache: sequence s's
     q_start[s+1] - q_start[s] last ones, `rows` in all.  Returns (k, v), bf16
     [rows][hkv][D]."""
-    import torch
-    lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
+    lib = _device_lib()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
     shape = (max(rows, 0), hkv, d)
-    k_out = _out(k_out, "k_out", k_codes, shape, torch.bfloat16, dev, stream, torch)
-    v_out = _out(v_out, "v_out", k_codes, shape, torch.bfloat16, dev, stream, torch)
+    k_out = _out(k_out, "k_out", k_codes, shape, _BF16, dev, stream)
+    v_out = _out(v_out, "v_out", k_codes, shape, _BF16, dev, stream)
     B._check(lib.draft_layer_read(
         k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page, q_start.data_ptr(),
         kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hkv, d, k_out.data_ptr(), v_out.data_ptr(),
-        _raw_stream(stream, dev, torch)))
+        _raw_stream(stream, dev)))
     return k_out, v_out
 
 
@@ -225,25 +241,24 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     1/sqrt(D); window > 0: a row sees the last `window` tokens up to its own and
     the first `sinks`; workspace: from draft_layer_workspace (allocated when
     None).  Returns (out bf16 [T][hq][D], lse fp32 [T][hq])."""
-    import torch
-    lib = _load()
-    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale, torch)
-    n_seq, max_pages = _batch(q_start, kv_len, table, dev, torch)
-    ldq = _rows3("q", q, dev, None, d, torch)
+    lib = _device_lib()
+    dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = _batch(q_start, kv_len, table, dev)
+    ldq = _rows3("q", q, dev, None, d)
     rows, hq = q.shape[0], q.shape[1]
-    out = _out(out, "out", q, (rows, hq, d), torch.bfloat16, dev, stream, torch)
-    lse = _out(lse, "lse", q, (rows, hq), torch.float32, dev, stream, torch)
+    out = _out(out, "out", q, (rows, hq, d), _BF16, dev, stream)
+    lse = _out(lse, "lse", q, (rows, hq), _F32, dev, stream)
     if workspace is None:
         workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
         if stream is not None:
-            _keep_for(workspace, stream, torch)
+            _keep_for(workspace, stream)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on GPU {dev}")
     B._check(lib.draft_layer_attend(
         q.data_ptr(), ldq, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page,
         q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, rows, hq, hkv, d,
         1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev, torch)))
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev)))
     return out, lse
 
 

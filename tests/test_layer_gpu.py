@@ -488,3 +488,19 @@ def test_binding_refuses(dev):
         a = {**dict(q=q, k=k, v=k, rope=None), **change}
         with pytest.raises(ValueError):
             L.draft_layer_append(*a.values(), *c.cache, *c.batch)
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (96, 4)])
+def test_example_runs(dev, window, sinks):
+    """The draft step with cache and head together: the same drafts twice, all of them tokens."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "draft_step.py")
+    spec = importlib.util.spec_from_file_location("draft_step", path)
+    mod = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(mod)
+    kw = dict(seqs=3, prompt=150, slots=4, rounds=2, hidden=512, vocab=3000, hq=5, hkv=1, d=64, page=32, window=window, sinks=sinks,
+              say=lambda *_: None)
+    a, b = mod.run(**kw), mod.run(**kw)
+    assert a.shape == (2, 3, 4) and int(a.min()) >= 0 and int(a.max()) < 3000
+    assert torch.equal(a, b)
