@@ -33,14 +33,20 @@ struct AttendArgs {
 // token: row x = (x / group)-th new token, head x % group of the kv head's.
 // Tiles of R such rows share each key and value that they load.
 //
-// Where the batch has at least twice the tiles that fill the card, or fills it
-// once with tiles of much the same length, a workgroup takes one tile.  Else the
-// tiles' visible tokens, as groups of 32, are laid end to end and cut into equal
-// runs, one a workgroup, so that the card is filled and all end together whatever
-// the lengths; a run may hold the end of one tile, whole tiles and the start of
-// another.  A tile that several runs hold parts of is joined by the last of them
-// (join_parts).  64 slots over 0.95 GB of mixed lengths: 158 us in runs, 180 a
-// tile a workgroup; a windowed batch, equal lengths: 54.6 us in runs, 49.5 by tiles.
+// How the tiles become workgroups goes by their number against the `target` that
+// fills the card:
+//   twice the target or more, or up to the target and much the same length: a
+//     tile a workgroup;
+//   a quarter of the target or fewer: each tile cut into equal parts of about the
+//     same length for all, a part a workgroup;
+//   else the tiles' visible tokens, as groups of 32, are laid end to end and cut
+//     into equal runs, one a workgroup, so that all end together whatever the
+//     lengths; a run may hold the end of one tile, whole tiles and the start of
+//     another, which costs it a beginning and an end each.
+// A tile of several parts is joined by the last of them (join_parts).  64 slots
+// over 0.95 GB of mixed lengths (64 tiles a head, target 64): 158 us in runs, 180 a
+// tile a workgroup.  A windowed batch of equal lengths (32, 32): 54.6 us in runs,
+// 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMinRun = 4;               // least groups of a run
 constexpr int kMaxBlocks = 768;          // most workgroups that a plan takes to fill the card
@@ -73,9 +79,9 @@ __device__ __forceinline__ Range visible(const AttendArgs& A, int p_first, int p
   return r;
 }
 
-// A part of a tile: groups from .. to - 1 of the `of` that the plan counts for
-// it (the most that a tile of the sequence sees; at least 1, so that tiles that
-// see nothing are visited too).
+// A part of a tile: from .. to of the `of` that the plan counts for it (groups,
+// of which every tile has at least 1, so that one that sees nothing is visited
+// too, or parts).
 struct Segment {
   Seq q;
   int seq, tile;
@@ -104,24 +110,36 @@ class Walk {
     groups = wave_sum(groups);
     tiles = wave_sum(tiles);
     most = wave_max(most);
-    whole_ = tiles >= 2.0f * (float)A.target || (tiles <= (float)A.target && most * (float)A.target <= 1.25f * groups);
+    const float target = (float)A.target;
+    by_tile_ = true;
+    run_ = run;
+    if (tiles >= 2.0f * target || (tiles <= target && most * target <= 1.25f * groups)) {
+      chunk_ = INT32_MAX;
+      return true;
+    }
+    if (tiles * 4.0f <= target) {
+      // the items are at most a tile's rounding up each more than groups / chunk
+      const float chunk = fmaxf(groups * 1.001f / (target - tiles), most / (float)(kMaxParts<R> - 1));
+      chunk_ = max(kMinRun, (int)fminf(ceilf(chunk), 1e9f));
+      return true;
+    }
+    by_tile_ = false;
     // lengths are counted in units of 2^shift groups, so that their sum fits 32 bits
     shift_ = max(0, (int)((__float_as_uint(groups) >> 23) & 255u) - 127 - 28);
     const float unit = __builtin_ldexpf(1.0f, -shift_);
     // 0.1% more than the mean: float sums may fall short; tiles: each may be rounded up to a unit
-    const float mean = (groups * unit * 1.001f + (shift_ ? tiles : 0.0f)) / (float)A.target;
+    const float mean = (groups * unit * 1.001f + (shift_ ? tiles : 0.0f)) / target;
     per_ = max(kMinRun >> min(shift_, 2), (int)ceilf(fmaxf(mean, most * unit / (float)(kMaxParts<R> - 3))));
-    run_ = run;
-    at_ = whole_ ? run : run * per_;
-    end_ = at_ + (whole_ ? 1 : per_);
-    return whole_ || run < A.target;
+    at_ = run * per_;
+    end_ = at_ + per_;
+    return run < A.target;
   }
 
   // The next segment; false past the run's (or the batch's) last.
   __device__ __forceinline__ bool next(const AttendArgs& A, Segment& g) {
-    if (at_ >= end_) return false;
+    if (!by_tile_ && at_ >= end_) return false;
     const int lane = threadIdx.x & 63;
-    int at = at_, before = 0;   // `before`: units of the sequences passed
+    int at = by_tile_ ? run_ : at_;
     for (int base = 0; base < A.b.n_seq; base += 64) {
       Seq q = seq_;
       int tiles = tiles_, groups = groups_;   // 0 past the last sequence
@@ -133,8 +151,9 @@ class Walk {
           groups = groups_of(A, q);
         }
       }
-      const int units = (groups + (1 << shift_) - 1) >> shift_;
-      const int mine = whole_ ? tiles : tiles * units, sum = wave_inclusive_sum(mine);
+      // a tile's parts, or its length
+      const int each = by_tile_ ? groups / chunk_ + (groups % chunk_ != 0) : (groups + (1 << shift_) - 1) >> shift_;
+      const int mine = tiles * each, sum = wave_inclusive_sum(mine);
       const int total = __builtin_amdgcn_readlane(sum, 63);
       if (at < total) {
         const int i = __builtin_ctzll(__ballot(sum > at));
@@ -144,18 +163,18 @@ class Walk {
         g.q.n = __builtin_amdgcn_readlane(q.n, i);
         g.q.len = __builtin_amdgcn_readlane(q.len, i);
         g.q.begin = g.q.len - g.q.n;
-        if (whole_) {
-          g.tile = at - start;
-          g.from = 0;
-          g.to = g.of = 1;
-          g.parts = 1;
-          g.part = g.first_run = 0;
-          at_ = end_;
-          return true;
-        }
-        g.of = __builtin_amdgcn_readlane(units, i);
+        g.of = __builtin_amdgcn_readlane(each, i);
         g.tile = (at - start) / g.of;
         g.from = at - start - g.tile * g.of;
+        if (by_tile_) {
+          g.to = g.from + 1;
+          g.parts = g.of;
+          g.part = g.from;
+          g.first_run = run_ - g.part;
+          by_tile_ = false;   // the only one
+          at_ = end_ = 0;
+          return true;
+        }
         g.to = min(g.of, g.from + end_ - at_);
         const int tile_at = at_ - g.from;   // where the tile starts
         g.first_run = tile_at / per_;
@@ -172,8 +191,9 @@ class Walk {
  private:
   Seq seq_{};                    // sequence `lane`
   int tiles_ = 0, groups_ = 0;   // its tiles, and what one sees at most
-  bool whole_;                   // a tile a workgroup
-  int shift_, per_, run_, at_, end_;
+  bool by_tile_;                 // a tile, or one of its parts of up to chunk_ groups, a workgroup
+  int chunk_, run_;
+  int shift_ = 0, per_ = 0, at_ = 0, end_ = 0;   // runs of per_ units of 2^shift_ groups: this one's
 
   static __device__ __forceinline__ int tiles_of(const AttendArgs& A, const Seq& q) {
     return (int)(((int64_t)q.n * A.group + R - 1) / R);
