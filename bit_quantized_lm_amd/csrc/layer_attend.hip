@@ -49,7 +49,7 @@ struct AttendArgs {
 // 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kMinRun = 4;               // least groups of a run
-constexpr int kMaxBlocks = 768;          // most workgroups that a plan takes to fill the card
+constexpr int kMaxBlocks = 512;          // most workgroups that a plan takes to fill the card
 constexpr int kMaxSlots = 2 * (kMaxBlocks + DL_MAX_HEADS);
 // Pairs of a row and a part that a tile's joining holds in LDS: what bounds the
 // parts.  Few rows leave room for their parts at 32 KiB, more take 64.
@@ -513,7 +513,12 @@ struct Weights {
 // fragments (each load instruction 1 KiB without gaps), a step ahead, so
 // nothing is shared until the waves' results are joined.  S^T = K Q^T puts a
 // row's weights into the lanes and order that the next product takes its columns
-// in (O^T = V^T P^T), so they never leave their registers.  Bound by memory: KSTREAM
+// in (O^T = V^T P^T), so they never leave their registers.
+//
+// Bound by memory: 64 slots over 0.95 GB of cache 157 us, 6.1 TB/s against 6.9 for
+// a plain read of 1 GiB.  Loads marked as not worth keeping: 58 us instead of 66
+// for one row over 131,072 tokens (268 MB), whose time is now 52 us, 37 of them
+// reading (7.2 TB/s), the rest beginning, handing over and joining 64 parts.
 template <int F>
 struct Bytes {   // a lane's codes of one group
   u32x4 k[F], v[F];
@@ -681,6 +686,13 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
 // keys of group n + 1 and the values of group n.  Bundles alternate between two
 // places: while one is read, the next one's codes are converted into the other and
 // the one after that is on its way from memory in registers; one barrier a step.
+//
+// Bound by instruction issue, at the clock that the matrix cores leave: a prompt
+// of 4096 rows, 40 on 8 heads of 128, takes 200 us (860 TFLOP/s against 1,240 for a
+// large bf16 matrix product).  Per group and wave 32 matrix instructions (512
+// cycles) and about 115 vector ones (650 with the exponentials' four cycles each),
+// 38% of the matrix cycles with a vector instruction beside them; with products
+// and exponentials in blocks that was 19%, and 212 us.
 template <int D, int NQ, int W>
 struct Shared {
   static constexpr int R = 16 * NQ * W, F = D / 32, kThreads = 64 * W;

@@ -302,7 +302,9 @@ __device__ __forceinline__ void write_page(const AppendArgs& A, int s, int page_
 }
 
 // Grid: q_blocks workgroups for the queries, then one per (page that a new
-// token touches, head, keys or values).
+// token touches, head, keys or values).  Bound by memory: prompts of four
+// sequences, 287 MB in and out, 58 us (5.0 TB/s against 4.8 for a large copy); one
+// token 5.3 us, a launch and its chain of loads (lengths, page, old scale).
 template <int D>
 __global__ __launch_bounds__(kThreads) void append_kernel(AppendArgs A) {
   extern __shared__ __align__(16) uint8_t lds[];
@@ -334,7 +336,8 @@ struct ReadArgs {
 
 // Reading back: a wave takes one head's 32 tokens of one sequence (a group of
 // the fragment order; its values pass through LDS, where they turn from eight
-// tokens a lane into rows of one).
+// tokens a lane into rows of one).  Bound by memory: eight long contexts, 371 MB
+// in and out, 82 us (4.5 TB/s against 4.8 for a large copy).
 template <int D>
 __global__ __launch_bounds__(kThreads) void read_kernel(ReadArgs A) {
   __shared__ __align__(16) uint16_t lds[kThreads / 64][32][D + 8];
