@@ -24,6 +24,7 @@ struct AttendArgs {
   uint16_t* out;
   float* lse;
   int target;              // workgroups a head that fill the card
+  int min_run, alone;      // least groups of a part or run; most of a tile that is not worth splitting
   uint32_t* arrived;       // [kMaxSlots] zero between calls
   float* part;             // [slot] partial results
 };
@@ -35,8 +36,8 @@ struct AttendArgs {
 //
 // How the tiles become workgroups goes by their number against the `target` that
 // fills the card:
-//   twice the target or more, or up to the target and much the same length: a
-//     tile a workgroup;
+//   twice the target or more, or up to the target and short, or much the same
+//     length: a tile a workgroup;
 //   a quarter of the target or fewer: each tile cut into equal parts of about the
 //     same length for all, a part a workgroup;
 //   else the tiles' visible tokens, as groups of 32, are laid end to end and cut
@@ -47,8 +48,6 @@ struct AttendArgs {
 // over 0.95 GB of mixed lengths (64 tiles a head, target 64): 158 us in runs, 180 a
 // tile a workgroup.  A windowed batch of equal lengths (32, 32): 54.6 us in runs,
 // 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.
-constexpr int kThreads = 256, kWaves = kThreads / 64;
-constexpr int kMinRun = 4;               // least groups of a run
 constexpr int kMaxBlocks = 512;          // most workgroups that a plan takes to fill the card
 constexpr int kMaxSlots = 2 * (kMaxBlocks + DL_MAX_HEADS);
 // Pairs of a row and a part that a tile's joining holds in LDS: what bounds the
@@ -113,14 +112,14 @@ class Walk {
     const float target = (float)A.target;
     by_tile_ = true;
     run_ = run;
-    if (tiles >= 2.0f * target || (tiles <= target && most * target <= 1.25f * groups)) {
+    if (tiles >= 2.0f * target || (tiles <= target && (most <= (float)A.alone || most * target <= 1.25f * groups))) {
       chunk_ = INT32_MAX;
       return true;
     }
     if (tiles * 4.0f <= target) {
       // the items are at most a tile's rounding up each more than groups / chunk
       const float chunk = fmaxf(groups * 1.001f / (target - tiles), most / (float)(kMaxParts<R> - 1));
-      chunk_ = max(kMinRun, (int)fminf(ceilf(chunk), 1e9f));
+      chunk_ = max(A.min_run, (int)fminf(ceilf(chunk), 1e9f));
       return true;
     }
     by_tile_ = false;
@@ -129,7 +128,7 @@ class Walk {
     const float unit = __builtin_ldexpf(1.0f, -shift_);
     // 0.1% more than the mean: float sums may fall short; tiles: each may be rounded up to a unit
     const float mean = (groups * unit * 1.001f + (shift_ ? tiles : 0.0f)) / target;
-    per_ = max(kMinRun >> min(shift_, 2), (int)ceilf(fmaxf(mean, most * unit / (float)(kMaxParts<R> - 3))));
+    per_ = max(max(A.min_run >> min(shift_, 8), 1), (int)ceilf(fmaxf(mean, most * unit / (float)(kMaxParts<R> - 3))));
     at_ = run * per_;
     end_ = at_ + per_;
     return run < A.target;
@@ -508,8 +507,8 @@ struct Weights {
 };
 
 // ------------------------------------------------------- few rows: streaming
-// 16 rows against a stream of groups of 32 tokens.  Each wave takes every
-// kWaves-th group of its workgroup's run, straight from global memory into the
+// 16 rows against a stream of groups of 32 tokens.  Each wave takes every W-th
+// group of its workgroup's part or run, straight from global memory into the
 // fragments (each load instruction 1 KiB without gaps), a step ahead, so
 // nothing is shared until the waves' results are joined.  S^T = K Q^T puts a
 // row's weights into the lanes and order that the next product takes its columns
@@ -524,14 +523,14 @@ struct Bytes {   // a lane's codes of one group
   u32x4 k[F], v[F];
 };
 
-template <int D>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kernel(AttendArgs A) {
-  constexpr int R = 16, F = D / 32, C = D / 16;
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel(AttendArgs A) {
+  constexpr int R = 16, F = D / 32, C = D / 16, kThreads = 64 * W;
   __shared__ __align__(16) union {
-    float o[kWaves][R][D + 4];
+    float o[W][R][D + 4];
     float join[kJoinFloats<R, kThreads>];
   } lds;
-  __shared__ float m_lds[kWaves][R], l_lds[kWaves][R];
+  __shared__ float m_lds[W][R], l_lds[W][R];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
   const int head = blockIdx.x % A.c.hkv;
   Walk<R> walk;
@@ -549,7 +548,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
     float ks_mine, lv_mine, rv_mine;
     auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
     auto look = [&] {
-      const int n = base + lane * kWaves;
+      const int n = base + lane * W;
       id_mine = n < to ? page_id(A.b, A.c.n_pages, w.seq, group_at(n) >> (A.c.page_shift - 5)) : -1;
       const size_t at = (size_t)max(id_mine, 0) * A.c.hkv + head;
       const float vs = id_mine < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
@@ -559,7 +558,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
     };
     auto load = [&](int i, Bytes<F>& b) {   // of a group that is not there page 0's bytes, which step() hides
       const size_t off = ((size_t)max(__builtin_amdgcn_readlane(id_mine, i), 0) * A.c.hkv + head) * page_bytes +
-                         (size_t)(group_at(base + i * kWaves) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
+                         (size_t)(group_at(base + i * W) & ((1 << (A.c.page_shift - 5)) - 1)) * 32 * D;
 #pragma unroll
       for (int f = 0; f < F; ++f) b.k[f] = load_codes<kOnce>(A.c.k + off, f);
 #pragma unroll
@@ -584,7 +583,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
       for (int c = 0; c < C; ++c) o[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
     auto step = [&](int i, const Bytes<F>& b) {
-      const int first = group_at(base + i * kWaves) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
+      const int first = group_at(base + i * W) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
       const Group group{id, first, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i)),
                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv_mine), i)),
                         __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rv_mine), i)),
@@ -607,7 +606,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
       }
     };
     while (base < to) {
-      const int count = min(64, (to - base + kWaves - 1) / kWaves);
+      const int count = min(64, (to - base + W - 1) / W);
       for (int i = 0; i < count; i += 2) {
         if (i + 1 < count) load(i + 1, odd);
         step(i, even);
@@ -615,7 +614,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
         if (i + 2 < count) load(i + 2, even);
         step(i + 1, odd);
       }
-      base += 64 * kWaves;
+      base += 64 * W;
       if (base < to) {
         look();
         load(0, even);
@@ -636,23 +635,23 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
 #pragma unroll
     for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(&lds.o[wave][lo][c * 16 + hi * 4]) = o[0][c];
     __syncthreads();
-    const int r = tid >> 4, x = x0 + r;
+    const int r = tid / (4 * W), x = x0 + r;   // 4 W threads a row
     if (r < rows) {
-      float top = m_lds[0][r], sum = 0.0f, share[kWaves];
+      float top = m_lds[0][r], sum = 0.0f, share[W];
 #pragma unroll
-      for (int v = 1; v < kWaves; ++v) top = fmaxf(top, m_lds[v][r]);
+      for (int v = 1; v < W; ++v) top = fmaxf(top, m_lds[v][r]);
 #pragma unroll
-      for (int v = 0; v < kWaves; ++v) {
+      for (int v = 0; v < W; ++v) {
         share[v] = __builtin_amdgcn_exp2f(m_lds[v][r] - top);
         sum += l_lds[v][r] * share[v];
       }
       const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
       const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
 #pragma unroll
-      for (int e = (tid & 15) * 4; e < D; e += 64) {
+      for (int e = tid % (4 * W) * 4; e < D; e += 16 * W) {
         f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&lds.o[v][r][e]);
+        for (int v = 0; v < W; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(&lds.o[v][r][e]);
         if (w.parts == 1) {
           y *= inv;
           *reinterpret_cast<u32x2*>(A.out + to_row * D + e) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
@@ -660,7 +659,7 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void attend_stream_kern
           publish4(parts.buffer, mine + r * D + e, y);
         }
       }
-      if ((tid & 15) == 0) {
+      if (tid % (4 * W) == 0) {
         if (w.parts > 1)
           publish2(parts.buffer, mine + R * D + r * 2, top, sum);
         else
@@ -913,17 +912,23 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
 }
 
 // ------------------------------------------------------------------- launch
-// The launch's kernel, by the rows that an average sequence has for one kv head.
+// The launch's kernel, by the rows that an average sequence has for one kv head,
+// and for few rows by the tiles: under 64 of them, which are split anyway, eight
+// waves a workgroup leave half the parts to join (4 sequences of 8,000 tokens, 2 kv
+// heads: 13.8 us instead of 16.2; 16 of 4,000, 8 heads: 36 instead of 31.7 with
+// four); heads of 256 hold too many registers for it.
 struct Plan {
   int rows;      // a tile's
-  bool shared;   // attend_shared_kernel (else the streaming one)
+  int waves;     // of the streaming kernel's workgroup; 0: attend_shared_kernel
   int blocks;    // workgroups that fill the card: those that 256 CUs hold at once
+  int min_run;   // least groups of a part: one a wave, or as many steps as its beginning takes
+  int alone;     // most groups of a tile that joining parts would not make faster (4 us and more)
 };
 Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  if (rows <= 16) return {16, false, 512};
-  if (rows <= 64) return {64, true, 512};
-  return {128, true, D == 256 ? 256 : 512};
+  if (rows <= 16) return (int64_t)n_seq * hkv < 64 && D < 256 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
+  if (rows <= 64) return {64, 0, 512, 10, 14};
+  return {128, 0, D == 256 ? 256 : 512, 10, 14};
 }
 
 int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }
@@ -957,9 +962,11 @@ int launch(const AttendArgs& A, const Plan& plan, hipStream_t s) {
   if (grid > 0x7FFFFFFF) return dh::fail(DH_EUNSUP, "attend: too many rows for one launch");
   const dim3 g((unsigned)grid);
   hipError_t e = hipSuccess;
-  if (!plan.shared)
-    hipLaunchKernelGGL(attend_stream_kernel<D>, g, dim3(kThreads), 0, s, A);
-  else if (R == 64)
+  if (plan.waves == 4) {
+    hipLaunchKernelGGL((attend_stream_kernel<D, 4>), g, dim3(256), 0, s, A);
+  } else if (plan.waves == 8) {
+    if constexpr (D < 256) hipLaunchKernelGGL((attend_stream_kernel<D, 8>), g, dim3(512), 0, s, A);
+  } else if (R == 64)
     e = launch_shared<D, 1, 4>(A, g, s);
   else if constexpr (D == 256)
     e = launch_shared<D, 1, 8>(A, g, s);
@@ -1017,6 +1024,8 @@ int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const
   A.out = static_cast<uint16_t*>(out);
   A.lse = lse;
   A.target = target_items(plan.blocks, hkv);
+  A.min_run = plan.min_run;
+  A.alone = plan.alone;
   A.arrived = static_cast<uint32_t*>(workspace);
   A.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kArrivedBytes);
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
