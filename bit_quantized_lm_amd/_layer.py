@@ -111,32 +111,39 @@ def _rows3(name, t, dev, heads, d):
 
 def _cache(k_codes, v_codes, k_scale, v_scale):
     """Checks a cache's four tensors; (GPU index, pages, kv heads, page, D)."""
-    dev, shape = k_codes.get_device(), k_codes.shape
+    shape = k_codes.shape
     if len(shape) != 4:
         raise ValueError("k_codes must be [pages][heads][page][D]")
+    dev = k_codes.get_device()
     if dev < 0 or dev != torch.cuda.current_device():
         raise ValueError(f"the cache must be on the current GPU, not on {k_codes.device}")
     pages, heads, page, d = shape
     flat = (pages, heads)
-    if not (_is(k_codes, _U8, shape, dev) and _is(v_codes, _U8, shape, dev) and _is(k_scale, _F32, flat, dev)
-            and _is(v_scale, _F32, flat, dev)):
-        for name, t, dtype, want in (("k_codes", k_codes, _U8, shape), ("v_codes", v_codes, _U8, shape),
-                                     ("k_scale", k_scale, _F32, flat), ("v_scale", v_scale, _F32, flat)):
-            if not _is(t, dtype, want, dev):
-                _wrong(name, t, dtype, want, dev)
-    return dev, pages, heads, page, d
+    if (k_codes.dtype is _U8 and v_codes.dtype is _U8 and k_scale.dtype is _F32 and v_scale.dtype is _F32
+            and v_codes.get_device() == dev and k_scale.get_device() == dev and v_scale.get_device() == dev
+            and k_codes.is_contiguous() and v_codes.is_contiguous() and k_scale.is_contiguous() and v_scale.is_contiguous()
+            and v_codes.shape == shape and k_scale.shape == flat and v_scale.shape == flat):
+        return dev, pages, heads, page, d
+    for name, t, dtype, want in (("k_codes", k_codes, _U8, shape), ("v_codes", v_codes, _U8, shape),
+                                 ("k_scale", k_scale, _F32, flat), ("v_scale", v_scale, _F32, flat)):
+        if not _is(t, dtype, want, dev):
+            _wrong(name, t, dtype, want, dev)
 
 
 def _batch(q_start, kv_len, table, dev):
     """Checks a batch's tensors; (sequences, pages a sequence)."""
-    if table.dim() != 2:
+    shape = table.shape
+    if len(shape) != 2:
         raise ValueError("table must be [sequences][pages]")
-    n, m = table.shape
-    if not (_is(q_start, _I32, (n + 1,), dev) and _is(kv_len, _I32, (n,), dev) and _is(table, _I32, (n, m), dev)):
-        for name, t, want in (("q_start", q_start, (n + 1,)), ("kv_len", kv_len, (n,)), ("table", table, (n, m))):
-            if not _is(t, _I32, want, dev):
-                _wrong(name, t, _I32, want, dev)
-    return n, m
+    n = shape[0]
+    if (q_start.dtype is _I32 and kv_len.dtype is _I32 and table.dtype is _I32
+            and q_start.get_device() == dev and kv_len.get_device() == dev and table.get_device() == dev
+            and q_start.is_contiguous() and kv_len.is_contiguous() and table.is_contiguous()
+            and q_start.shape == (n + 1,) and kv_len.shape == (n,)):
+        return shape
+    for name, t, want in (("q_start", q_start, (n + 1,)), ("kv_len", kv_len, (n,)), ("table", table, shape)):
+        if not _is(t, _I32, want, dev):
+            _wrong(name, t, _I32, want, dev)
 
 
 def _raw_stream(stream, dev):
@@ -150,7 +157,7 @@ def _out(given, name, like, shape, dtype, dev, stream):
         if not _is(given, dtype, shape, dev):
             _wrong(name, given, dtype, shape, dev)
         return given
-    t = like.new_empty(shape, dtype=dtype)
+    t = like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
     if stream is not None:
         _keep_for(t, stream)
     return t
@@ -247,7 +254,7 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     ldq = _rows3("q", q, dev, None, d)
     rows, hq = q.shape[0], q.shape[1]
     out = _out(out, "out", q, (rows, hq, d), _BF16, dev, stream)
-    lse = _out(lse, "lse", q, (rows, hq), _F32, dev, stream)
+    lse = _out(lse, "lse", k_scale, (rows, hq), _F32, dev, stream)
     if workspace is None:
         workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
         if stream is not None:
