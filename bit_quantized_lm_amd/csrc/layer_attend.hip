@@ -36,8 +36,9 @@ struct AttendArgs {
 //
 // How the tiles become workgroups goes by their number against the `target` that
 // fills the card:
-//   twice the target or more, or up to the target and short, or much the same
-//     length: a tile a workgroup;
+//   twice the target or more, or up to the target and short or much the same
+//     length, or a prompt whose first tiles see so much less than its last that
+//     those set the pace: a tile a workgroup, the longest first;
 //   a quarter of the target or fewer: each tile cut into equal parts of about the
 //     same length for all, a part a workgroup;
 //   else the tiles' visible tokens, as groups of 32, are laid end to end and cut
@@ -47,7 +48,8 @@ struct AttendArgs {
 // A tile of several parts is joined by the last of them (join_parts).  64 slots
 // over 0.95 GB of mixed lengths (64 tiles a head, target 64): 158 us in runs, 180 a
 // tile a workgroup.  A windowed batch of equal lengths (32, 32): 54.6 us in runs,
-// 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.
+// 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.  A prompt of 512
+// rows (20, 64): 34 us in runs, 23 by tiles; of 2,048 (80, 64): 94 in runs, 67.
 constexpr int kMaxBlocks = 512;          // most workgroups that a plan takes to fill the card
 constexpr int kMaxSlots = 2 * (kMaxBlocks + DL_MAX_HEADS);
 // Pairs of a row and a part that a tile's joining holds in LDS: what bounds the
@@ -97,22 +99,25 @@ class Walk {
   // Run (or tile) `run` of a head; false where there is none.
   __device__ __forceinline__ bool begin(const AttendArgs& A, int run) {
     const int lane = threadIdx.x & 63;
-    float groups = 0.0f, tiles = 0.0f, most = 0.0f;
+    float groups = 0.0f, real = 0.0f, tiles = 0.0f, most = 0.0f;   // real: with the tiles that see less than the last
     for (int s = lane; s < A.b.n_seq; s += 64) {
       const Seq q = load_seq(A.b, s);
       const int t = tiles_of(A, q), g = groups_of(A, q);
       if (s < 64) seq_ = q, tiles_ = t, groups_ = g;
       groups += (float)t * (float)g;
+      real += (float)t * 0.5f * (float)(g + (t > 0 ? first_groups_of(A, q) : 0));
       tiles += (float)t;
       most = fmaxf(most, (float)g);
     }
     groups = wave_sum(groups);
+    real = wave_sum(real);
     tiles = wave_sum(tiles);
     most = wave_max(most);
     const float target = (float)A.target;
     by_tile_ = true;
     run_ = run;
-    if (tiles >= 2.0f * target || (tiles <= target && (most <= (float)A.alone || most * target <= 1.25f * groups))) {
+    const bool short_or_even = most <= (float)A.alone || most * target <= 1.25f * groups;
+    if (tiles >= 2.0f * target || (tiles <= target && short_or_even) || fmaxf(most * target, 1.15f * real) < groups) {
       chunk_ = INT32_MAX;
       return true;
     }
@@ -200,6 +205,9 @@ class Walk {
   static __device__ __forceinline__ int groups_of(const AttendArgs& A, const Seq& q) {
     const int tokens = min(q.n, R / A.group + 2);   // a tile's, at most
     return q.n == 0 ? 0 : max(1, visible(A, q.len - tokens, q.len - 1).n);
+  }
+  static __device__ __forceinline__ int first_groups_of(const AttendArgs& A, const Seq& q) {
+    return max(1, visible(A, q.begin, q.begin + min(q.n, R / A.group + 1) - 1).n);
   }
 };
 
@@ -928,7 +936,7 @@ Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
   if (rows <= 16) return (int64_t)n_seq * hkv < 64 && D < 256 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
   if (rows <= 64) return {64, 0, 512, 10, 14};
-  return {128, 0, D == 256 ? 256 : 512, 10, 14};
+  return {128, 0, D == 256 ? 256 : 512, 10, 32};
 }
 
 int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }
