@@ -524,8 +524,8 @@ struct Weights {
 //
 // Bound by memory: 64 slots over 0.95 GB of cache 157 us, 6.1 TB/s against 6.9 for
 // a plain read of 1 GiB.  Loads marked as not worth keeping: 58 us instead of 66
-// for one row over 131,072 tokens (268 MB), whose time is now 52 us, 37 of them
-// reading (7.2 TB/s), the rest beginning, handing over and joining 64 parts.
+// for one row over 131,072 tokens (268 MB), whose time is now 48 us, 37 of them
+// reading (7.2 TB/s), the rest beginning, handing over and joining 31 parts.
 template <int F>
 struct Bytes {   // a lane's codes of one group
   u32x4 k[F], v[F];
@@ -695,7 +695,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel
 // the one after that is on its way from memory in registers; one barrier a step.
 //
 // Bound by instruction issue, at the clock that the matrix cores leave: a prompt
-// of 4096 rows, 40 on 8 heads of 128, takes 200 us (860 TFLOP/s against 1,240 for a
+// of 4096 rows, 40 on 8 heads of 128, takes 190 to 200 us (860 to 900 TFLOP/s against 1,240 for a
 // large bf16 matrix product).  Per group and wave 32 matrix instructions (512
 // cycles) and about 115 vector ones (650 with the exponentials' four cycles each),
 // 38% of the matrix cycles with a vector instruction beside them; with products
@@ -936,7 +936,7 @@ Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
   if (rows <= 16) return (int64_t)n_seq * hkv < 64 && D < 256 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
   if (rows <= 64) return {64, 0, 512, 10, 14};
-  return {128, 0, D == 256 ? 256 : 512, 10, 32};
+  return {128, 0, D == 256 ? 256 : 512, 30, 32};
 }
 
 int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }

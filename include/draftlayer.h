@@ -144,12 +144,14 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
  * A row that sees nothing gets out = 0 and lse = -inf.  Products run on the
  * matrix cores in fp16 with fp32 sums: codes are exact there, a query row is
  * scaled by a power of two to its largest element (elements 2^-28 below it
- * lose bits), and the softmax's weights are rounded once to 11 bits; the
- * statistics stay in fp32.
+ * lose bits), and a token's weight times its value scale is rounded once to 11
+ * bits (to fewer below 2^-21 of the row's largest); the statistics stay in
+ * fp32.  Rows of the batch that no sequence covers are not written.
  *   q  device, bf16, row r head h at q + r*ldq + h*D, 16-byte aligned, ldq a
  *      multiple of 8, at least hq*D
  *   workspace  16-byte aligned, of draft_layer_workspace_bytes() bytes
- * Limits: scale finite and > 0, window >= 0, sinks >= 0.
+ * Limits: scale finite and > 0, window >= 0, sinks >= 0; scales of seen pages
+ * as draft_layer_append leaves them (finite, at least 2^-40, below 2^53).
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */
 int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const uint8_t* v_codes,
