@@ -695,11 +695,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel
 // the one after that is on its way from memory in registers; one barrier a step.
 //
 // Bound by instruction issue, at the clock that the matrix cores leave: a prompt
-// of 4096 rows, 40 on 8 heads of 128, takes 190 to 200 us (860 to 900 TFLOP/s against 1,240 for a
-// large bf16 matrix product).  Per group and wave 32 matrix instructions (512
-// cycles) and about 115 vector ones (650 with the exponentials' four cycles each),
-// 38% of the matrix cycles with a vector instruction beside them; with products
-// and exponentials in blocks that was 19%, and 212 us.
+// of 4096 rows, 40 on 8 heads of 128, takes 190 to 200 us (860 to 900 TFLOP/s
+// against 1,240 for a large bf16 matrix product).  Per group and wave 32 matrix
+// instructions (512 cycles) and about 115 vector ones (650 cycles: four each, an
+// exponential sixteen), 38% of the matrix cycles with a vector instruction beside
+// them; with products and exponentials in blocks that was 19%, and 212 us.
 template <int D, int NQ, int W>
 struct Shared {
   static constexpr int R = 16 * NQ * W, F = D / 32, kThreads = 64 * W;
@@ -721,201 +721,201 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
   Walk<R> walk;
   if (!walk.begin(A, blockIdx.x / A.c.hkv)) return;
   for (Segment w; walk.next(A, w);) {
-  const Seq q = w.q;
-  w.tile = (int)(((int64_t)q.n * A.group + R - 1) / R) - 1 - w.tile;   // the tiles that see most first
-  const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
-  const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
-  // this wave's own rows; none of them: it only carries codes
-  const int mine0 = wave * 16 * NQ;
-  const int w_first = q.begin + (x0 + mine0) / A.group, w_last = q.begin + (x0 + min(rows, mine0 + 16 * NQ) - 1) / A.group;
-  const bool working = mine0 < rows;
+    const Seq q = w.q;
+    w.tile = (int)(((int64_t)q.n * A.group + R - 1) / R) - 1 - w.tile;   // the tiles that see most first
+    const int x0 = w.tile * R, rows = min(R, q.n * A.group - x0);
+    const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+    // this wave's own rows; none of them: it only carries codes
+    const int mine0 = wave * 16 * NQ;
+    const int w_first = q.begin + (x0 + mine0) / A.group, w_last = q.begin + (x0 + min(rows, mine0 + 16 * NQ) - 1) / A.group;
+    const bool working = mine0 < rows;
 
-  const Range see = visible(A, p_first, p_last);
-  const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.from / w.of));
-  const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.to / w.of));
-  const int in_page = (1 << (A.c.page_shift - 5)) - 1;
-  auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
-  int table_at = 0;   // group of the table's first entry
-  auto fill = [&](int n) {
-    const int i = max(n + tid, from), g = group_at(i);
-    const int id = i < to ? page_id(A.b, A.c.n_pages, w.seq, g >> (A.c.page_shift - 5)) : -1;
-    const size_t at = (size_t)max(id, 0) * A.c.hkv + head;
-    const float ks = A.c.ks[at], vs = id < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
-    const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
-    __syncthreads();
-    table[tid] = u32x4{(uint32_t)where, __float_as_uint(ks), __float_as_uint(__builtin_amdgcn_logf(vs)),
-                       __float_as_uint(__builtin_amdgcn_rcpf(vs))};
-    table_at = n;
-    __syncthreads();
-  };
-  auto entry = [&](int n) { return table[n - table_at]; };
-  using Raw = u32x4[S::kPer];
-  // a bundle: the keys at `k`, the values at `v` (numbers of groups in the code
-  // arrays; one that is not there: the arrays' first, hidden later)
-  auto load = [&](int k, int v, Raw& raw) {
+    const Range see = visible(A, p_first, p_last);
+    const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.from / w.of));
+    const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.to / w.of));
+    const int in_page = (1 << (A.c.page_shift - 5)) - 1;
+    auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
+    int table_at = 0;   // group of the table's first entry
+    auto fill = [&](int n) {
+      const int i = max(n + tid, from), g = group_at(i);
+      const int id = i < to ? page_id(A.b, A.c.n_pages, w.seq, g >> (A.c.page_shift - 5)) : -1;
+      const size_t at = (size_t)max(id, 0) * A.c.hkv + head;
+      const float ks = A.c.ks[at], vs = id < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
+      const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
+      __syncthreads();
+      table[tid] = u32x4{(uint32_t)where, __float_as_uint(ks), __float_as_uint(__builtin_amdgcn_logf(vs)),
+                         __float_as_uint(__builtin_amdgcn_rcpf(vs))};
+      table_at = n;
+      __syncthreads();
+    };
+    auto entry = [&](int n) { return table[n - table_at]; };
+    using Raw = u32x4[S::kPer];
+    // a bundle: the keys at `k`, the values at `v` (numbers of groups in the code
+    // arrays; one that is not there: the arrays' first, hidden later)
+    auto load = [&](int k, int v, Raw& raw) {
 #pragma unroll
-    for (int u = 0; u < S::kPer; ++u) {
-      const int unit = u * W + wave;
-      const bool key = unit < F;
-      raw[u] = load_codes<0>((key ? A.c.k : A.c.v) + (size_t)max(key ? k : v, 0) * (32 * D), unit % F);
-    }
-  };
-  auto uniform = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane((int)x); };
-  // the first codes are on their way before the queries are looked at
-  Raw one, two;
-  int at[4];
-  if (from < to) {
-    fill(from);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = uniform(entry(from + i)[0]);
-    load(at[0], at[0], one);   // of bundle from - 1 only the keys are used
-    load(at[1], at[0], two);
-  }
-
-  half8 qf[NQ][F];
-  float qs[NQ], m[NQ], l[NQ];
-  int pos[NQ];
-  f32x4 o[NQ][C];
-#pragma unroll
-  for (int t = 0; t < NQ; ++t) {
-    const int r = mine0 + t * 16 + lo, x = x0 + r;
-    const bool valid = r < rows;
-    pos[t] = valid ? q.begin + x / A.group : -1;
-    const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
-    qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
-    m[t] = kLowest;
-    l[t] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  // pieces `from` .. `to` - 1 of the 4 kPer that the wave's codes are converted in
-  u32x4 made[2];
-  auto store = [&](int n, const Raw& raw, int from, int to) {
-#pragma unroll
-    for (int i = 0; i < 4 * S::kPer; ++i) {
-      if (i < from || i >= to) continue;
-      const u32x2 h = codes_to_half4(raw[i / 4][i % 4]);
-      made[i / 2 % 2][i % 2 * 2] = h[0];
-      made[i / 2 % 2][i % 2 * 2 + 1] = h[1];
-      if (i % 2) stage[(n & 1) * S::kBundle + (i / 4 * W + wave) * 128 + i / 2 % 2 * 64 + lane] = made[i / 2 % 2];
-    }
-  };
-  // Products of a bundle's C key or value fragments, other() work between them;
-  // `ring` holds the first kRing fragments when it begins and those of `then`
-  // when it ends.  The compiler keeps the order: arithmetic on its own may pass,
-  // matrix instructions and LDS reads may not.
-  constexpr int kRing = 4;
-  half8 ring[kRing];
-  auto fetch = [&](const u32x4* at, int i) { ring[i % kRing] = __builtin_bit_cast(half8, at[i * 64]); };
-  auto products = [&](const u32x4* at, const u32x4* then, auto product, auto other) {
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-      product(i, ring[i % kRing]);
-      if (i + kRing < C)
-        fetch(at, i + kRing);
-      else if (then)
-        fetch(then, i + kRing - C);
-      other(i);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  // scores of the keys in bundle n
-  auto score = [&](f32x4 (&s)[NQ][2]) {
-    return [&](int i, half8 k) {
-#pragma unroll
-      for (int t = 0; t < NQ; ++t) {
-        f32x4& to = s[t][i / (D / 32)];
-        to = mfma(k, qf[t][i % (D / 32)], i % (D / 32) ? to : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      for (int u = 0; u < S::kPer; ++u) {
+        const int unit = u * W + wave;
+        const bool key = unit < F;
+        raw[u] = load_codes<0>((key ? A.c.k : A.c.v) + (size_t)max(key ? k : v, 0) * (32 * D), unit % F);
       }
     };
-  };
-  auto bundle = [&](int n) { return stage + (n & 1) * S::kBundle + lane; };
-  // What a step needs of the table is read a step before: `here` is the entry of
-  // its group, `far` that of the keys it loads; the values it loads are those of
-  // the keys loaded by the step before.
-  u32x4 here;
-  uint32_t far;
-  int v_at;
-  // `ready` holds bundle n + 1's codes, `coming` takes bundle n + 2's
-  auto step = [&](int n, f32x4 (&now)[NQ][2], f32x4 (&next)[NQ][2], const Raw& ready, Raw& coming) {
-    const int k_at = uniform(far), id = uniform(here[0]);
-    const float ks = __uint_as_float(uniform(here[1])), lv = __uint_as_float(uniform(here[2])), rv = __uint_as_float(uniform(here[3]));
-    load(k_at, v_at, coming);
-    v_at = k_at;
-    if (n + 4 >= table_at + S::kTable) fill(n);
-    here = entry(n + 1);
-    far = entry(n + 4)[0];
-    if (working) {
-      const u32x4* kf = bundle(n);
-      const u32x4* vf = kf + F * 128;
+    auto uniform = [](uint32_t x) { return (int)__builtin_amdgcn_readfirstlane((int)x); };
+    // the first codes are on their way before the queries are looked at
+    Raw one, two;
+    int at[4];
+    if (from < to) {
+      fill(from);
 #pragma unroll
-      for (int i = 0; i < kRing; ++i) fetch(kf, i);
-      const int first = group_at(n) * 32;
-      const Group group{id, first, ks, lv, rv, id < 0 || hides(A, first, w_first, w_last)};
-      Weights<NQ> weights;
-      weights.hide(A, group, now, qs, pos);
-      products(kf, vf, score(next), [&](int i) { weights.form(group, now, m, i * 8 * NQ / C, (i + 1) * 8 * NQ / C); });
-      half8 pf[NQ];
-      weights.settle(group, now, m, l, o, pf);
-      products(vf, static_cast<const u32x4*>(nullptr), [&](int i, half8 v) {
-#pragma unroll
-        for (int t = 0; t < NQ; ++t) o[t][i] = mfma(v, pf[t], o[t][i]);
-      }, [&](int i) { store(n + 1, ready, i * 4 * S::kPer / C, (i + 1) * 4 * S::kPer / C); });
-    } else {
-      store(n + 1, ready, 0, 4 * S::kPer);
+      for (int i = 0; i < 4; ++i) at[i] = uniform(entry(from + i)[0]);
+      load(at[0], at[0], one);   // of bundle from - 1 only the keys are used
+      load(at[1], at[0], two);
     }
-    __syncthreads();
-  };
-  if (from < to) {
-    f32x4 even[NQ][2], odd[NQ][2];
-    store(from - 1, one, 0, 4 * S::kPer);
-    load(at[2], at[1], one);
-    store(from, two, 0, 4 * S::kPer);
-    v_at = at[2];
-    here = entry(from);
-    far = (uint32_t)at[3];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kRing; ++i) fetch(bundle(from - 1), i);
-    products(bundle(from - 1), static_cast<const u32x4*>(nullptr), score(even), [](int) {});
-    __syncthreads();   // its keys' place is the next bundle's
-    for (int n = from;;) {
-      step(n, even, odd, one, two);
-      if (++n >= to) break;
-      step(n, odd, even, two, one);
-      if (++n >= to) break;
-    }
-  }
 
-  const Parts parts = parts_of<D, R>(A, w, head);
-  const int mine = parts.at(w.part);
+    half8 qf[NQ][F];
+    float qs[NQ], m[NQ], l[NQ];
+    int pos[NQ];
+    f32x4 o[NQ][C];
 #pragma unroll
-  for (int t = 0; t < NQ; ++t) {
-    const int r = mine0 + t * 16 + lo, x = x0 + r;
-    float sum = l[t];
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    if (r >= rows) continue;
-    if (w.parts == 1) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+    for (int t = 0; t < NQ; ++t) {
+      const int r = mine0 + t * 16 + lo, x = x0 + r;
+      const bool valid = r < rows;
+      pos[t] = valid ? q.begin + x / A.group : -1;
+      const uint16_t* row = A.q + (int64_t)(q.row0 + x / A.group) * A.ldq + (head * A.group + x % A.group) * D;
+      qs[t] = load_query<D>(row, valid, A.scale_log2, qf[t]);
+      m[t] = kLowest;
+      l[t] = 0.0f;
 #pragma unroll
-      for (int c = 0; c < C; ++c) {
-        const f32x4 y = o[t][c] * inv;
-        *reinterpret_cast<u32x2*>(A.out + to_row * D + c * 16 + hi * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
-      }
-      if (hi == 0) write_lse(A, to_row, m[t], sum);
-    } else {
-#pragma unroll
-      for (int c = 0; c < C; ++c) publish4(parts.buffer, mine + r * D + c * 16 + hi * 4, o[t][c]);
-      if (hi == 0) publish2(parts.buffer, mine + R * D + r * 2, m[t], sum);
+      for (int c = 0; c < C; ++c) o[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-  }
-  if (w.parts == 1) continue;
-  __syncthreads();   // the stages become join_parts' scratch
-  join_parts<D, R, S::kThreads>(A, w, q, x0, rows, head, parts, reinterpret_cast<float*>(stage));
-  __syncthreads();   // and the next segment's stages
+
+    // pieces `from` .. `to` - 1 of the 4 kPer that the wave's codes are converted in
+    u32x4 made[2];
+    auto store = [&](int n, const Raw& raw, int from, int to) {
+#pragma unroll
+      for (int i = 0; i < 4 * S::kPer; ++i) {
+        if (i < from || i >= to) continue;
+        const u32x2 h = codes_to_half4(raw[i / 4][i % 4]);
+        made[i / 2 % 2][i % 2 * 2] = h[0];
+        made[i / 2 % 2][i % 2 * 2 + 1] = h[1];
+        if (i % 2) stage[(n & 1) * S::kBundle + (i / 4 * W + wave) * 128 + i / 2 % 2 * 64 + lane] = made[i / 2 % 2];
+      }
+    };
+    // Products of a bundle's C key or value fragments, other() work between them;
+    // `ring` holds the first kRing fragments when it begins and those of `then`
+    // when it ends.  The compiler keeps the order: arithmetic on its own may pass,
+    // matrix instructions and LDS reads may not.
+    constexpr int kRing = 4;
+    half8 ring[kRing];
+    auto fetch = [&](const u32x4* at, int i) { ring[i % kRing] = __builtin_bit_cast(half8, at[i * 64]); };
+    auto products = [&](const u32x4* at, const u32x4* then, auto product, auto other) {
+#pragma unroll
+      for (int i = 0; i < C; ++i) {
+        product(i, ring[i % kRing]);
+        if (i + kRing < C)
+          fetch(at, i + kRing);
+        else if (then)
+          fetch(then, i + kRing - C);
+        other(i);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // scores of the keys in bundle n
+    auto score = [&](f32x4 (&s)[NQ][2]) {
+      return [&](int i, half8 k) {
+#pragma unroll
+        for (int t = 0; t < NQ; ++t) {
+          f32x4& to = s[t][i / (D / 32)];
+          to = mfma(k, qf[t][i % (D / 32)], i % (D / 32) ? to : f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        }
+      };
+    };
+    auto bundle = [&](int n) { return stage + (n & 1) * S::kBundle + lane; };
+    // What a step needs of the table is read a step before: `here` is the entry of
+    // its group, `far` that of the keys it loads; the values it loads are those of
+    // the keys loaded by the step before.
+    u32x4 here;
+    uint32_t far;
+    int v_at;
+    // `ready` holds bundle n + 1's codes, `coming` takes bundle n + 2's
+    auto step = [&](int n, f32x4 (&now)[NQ][2], f32x4 (&next)[NQ][2], const Raw& ready, Raw& coming) {
+      const int k_at = uniform(far), id = uniform(here[0]);
+      const float ks = __uint_as_float(uniform(here[1])), lv = __uint_as_float(uniform(here[2])), rv = __uint_as_float(uniform(here[3]));
+      load(k_at, v_at, coming);
+      v_at = k_at;
+      if (n + 4 >= table_at + S::kTable) fill(n);
+      here = entry(n + 1);
+      far = entry(n + 4)[0];
+      if (working) {
+        const u32x4* kf = bundle(n);
+        const u32x4* vf = kf + F * 128;
+#pragma unroll
+        for (int i = 0; i < kRing; ++i) fetch(kf, i);
+        const int first = group_at(n) * 32;
+        const Group group{id, first, ks, lv, rv, id < 0 || hides(A, first, w_first, w_last)};
+        Weights<NQ> weights;
+        weights.hide(A, group, now, qs, pos);
+        products(kf, vf, score(next), [&](int i) { weights.form(group, now, m, i * 8 * NQ / C, (i + 1) * 8 * NQ / C); });
+        half8 pf[NQ];
+        weights.settle(group, now, m, l, o, pf);
+        products(vf, static_cast<const u32x4*>(nullptr), [&](int i, half8 v) {
+#pragma unroll
+          for (int t = 0; t < NQ; ++t) o[t][i] = mfma(v, pf[t], o[t][i]);
+        }, [&](int i) { store(n + 1, ready, i * 4 * S::kPer / C, (i + 1) * 4 * S::kPer / C); });
+      } else {
+        store(n + 1, ready, 0, 4 * S::kPer);
+      }
+      __syncthreads();
+    };
+    if (from < to) {
+      f32x4 even[NQ][2], odd[NQ][2];
+      store(from - 1, one, 0, 4 * S::kPer);
+      load(at[2], at[1], one);
+      store(from, two, 0, 4 * S::kPer);
+      v_at = at[2];
+      here = entry(from);
+      far = (uint32_t)at[3];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kRing; ++i) fetch(bundle(from - 1), i);
+      products(bundle(from - 1), static_cast<const u32x4*>(nullptr), score(even), [](int) {});
+      __syncthreads();   // its keys' place is the next bundle's
+      for (int n = from;;) {
+        step(n, even, odd, one, two);
+        if (++n >= to) break;
+        step(n, odd, even, two, one);
+        if (++n >= to) break;
+      }
+    }
+
+    const Parts parts = parts_of<D, R>(A, w, head);
+    const int mine = parts.at(w.part);
+#pragma unroll
+    for (int t = 0; t < NQ; ++t) {
+      const int r = mine0 + t * 16 + lo, x = x0 + r;
+      float sum = l[t];
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (r >= rows) continue;
+      if (w.parts == 1) {
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const size_t to_row = (size_t)(q.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+          const f32x4 y = o[t][c] * inv;
+          *reinterpret_cast<u32x2*>(A.out + to_row * D + c * 16 + hi * 4) = u32x2{bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3])};
+        }
+        if (hi == 0) write_lse(A, to_row, m[t], sum);
+      } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) publish4(parts.buffer, mine + r * D + c * 16 + hi * 4, o[t][c]);
+        if (hi == 0) publish2(parts.buffer, mine + R * D + r * 2, m[t], sum);
+      }
+    }
+    if (w.parts == 1) continue;
+    __syncthreads();   // the stages become join_parts' scratch
+    join_parts<D, R, S::kThreads>(A, w, q, x0, rows, head, parts, reinterpret_cast<float*>(stage));
+    __syncthreads();   // and the next segment's stages
   }
 }
 
