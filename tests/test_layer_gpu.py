@@ -233,6 +233,36 @@ def test_missing_page_takes_nothing_from_page_zero(dev, new):
     check_attend(c, 0, 0)
 
 
+def test_past_the_tables_end(dev):
+    """Positions that the table has no entry for are not written, read as zero and not seen."""
+    c = Case(dev, [(40, 100), (2, 300)], 2, 1, 64, 32, seed=22, max_pages=2).upload()
+    before = c.naturals()
+    rope = L.draft_layer_rope_table(64, 64)
+    k, v = bf16(c.rng, c.rows, 1, 64), bf16(c.rng, c.rows, 1, 64)
+    got = L.draft_layer_append(c.q.to(dev), k.to(dev), v.to(dev), torch.from_numpy(rope).to(dev), *c.cache, *c.batch)
+    torch.cuda.synchronize()
+    check_append(c, got, rope, False, k, v, before)
+    kb, vb = L.draft_layer_read(*c.cache, *c.batch, c.rows)
+    assert kb.cpu()[:4].any() and not kb.cpu()[4:].any() and not vb.cpu()[4:].any()
+    c.kc, c.vc, c.ks, c.vs = (t.cpu().numpy() for t in c.cache)
+    for window, sinks in ((0, 0), (50, 3)):
+        check_attend(c, window, sinks)
+
+
+@pytest.mark.parametrize("hkv,new", [(1, 20), (8, 20), (8, 3), (2, 40)])
+def test_attend_many_sequences(dev, hkv, new):
+    """More sequences than a wave has lanes, in each way that tiles become workgroups."""
+    lens = [(new + i % 5 if i % 9 else 0, 60 + (37 * i) % 400) for i in range(70)]
+    check_attend(Case(dev, lens, hkv * 2, hkv, 64, 32, seed=hkv + new).upload(), 0, 0)
+
+
+@pytest.mark.parametrize("new,d,hkv,window", [(1, 64, 8, 0), (9, 64, 8, 0), (1, 128, 8, 700), (70, 64, 4, 0)])
+def test_attend_uneven_lengths(dev, new, d, hkv, window):
+    """Thirty tiles a head of lengths far apart: runs that hold the end of one tile and the start of another."""
+    lens = [(new, new + 5 + 200 * i) for i in range(30)]
+    check_attend(Case(dev, lens, hkv * 2, hkv, d, 64, seed=new + d).upload(), window, 4 if window else 0)
+
+
 # --------------------------------------------------------------------- read
 @pytest.mark.parametrize("lens,hkv,d,page", [
     ([(1, 1)], 1, 64, 32), ([(500, 500)], 8, 128, 64), ([(33, 97), (0, 5), (64, 64), (1, 300)], 5, 128, 128),
