@@ -924,7 +924,9 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
 // and for few rows by the tiles: under 64 of them, which are split anyway, eight
 // waves a workgroup leave half the parts to join (4 sequences of 8,000 tokens, 2 kv
 // heads: 13.8 us instead of 16.2; 16 of 4,000, 8 heads: 36 instead of 31.7 with
-// four); heads of 256 hold too many registers for it.
+// four); heads of 256 hold too many registers for it, and for two workgroups a CU:
+// split for the 256 that run at once, one sequence of 60,000 tokens and 2 kv heads
+// takes 40.5 us and 16 of 16,000 take 37.8; split for 512, 65.0 and 50.5.
 struct Plan {
   int rows;      // a tile's
   int waves;     // of the streaming kernel's workgroup; 0: attend_shared_kernel
@@ -934,7 +936,7 @@ struct Plan {
 };
 Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
   const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  if (rows <= 16) return (int64_t)n_seq * hkv < 64 && D < 256 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
+  if (rows <= 16) return D == 256 ? Plan{16, 4, 256, 4, 18} : (int64_t)n_seq * hkv < 64 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
   if (rows <= 64) return {64, 0, 512, 10, 14};
   return {128, 0, D == 256 ? 256 : 512, 30, 32};
 }
