@@ -19,6 +19,7 @@ from . import _binding as B
 _HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "draftlayer.h")
 PAGES = (32, 64, 128, 256)     # tokens a page may hold
 HEAD_DIMS = (64, 128, 256)
+WORKSPACE_ZERO_BYTES = 6144    # DL_WORKSPACE_ZERO_BYTES
 
 _lib = None
 
@@ -234,10 +235,12 @@ def draft_layer_workspace_bytes(rows: int, n_seq: int, hq: int, hkv: int, d: int
 
 
 def draft_layer_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: int, device):
-    """A device workspace for draft_layer_attend (zero-filled once; the library
-    keeps the part that must start at zero at zero)."""
+    """A device workspace for draft_layer_attend (the part that must start at
+    zero is cleared here; the library keeps it at zero)."""
     import torch
-    return torch.zeros(draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d), dtype=torch.uint8, device=device)
+    t = torch.empty(draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d), dtype=torch.uint8, device=device)
+    t[:WORKSPACE_ZERO_BYTES].zero_()
+    return t
 
 
 def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, scale: float | None = None, window: int = 0,

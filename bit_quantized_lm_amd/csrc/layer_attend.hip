@@ -60,7 +60,8 @@ template <int R>
 constexpr int kMaxParts = kJoinPairs<R> / R;
 template <int R, int kThreads>
 constexpr int kJoinFloats = 2 * kJoinPairs<R> + 4 * kThreads;
-constexpr size_t kArrivedBytes = (kMaxSlots * sizeof(uint32_t) + 255) / 256 * 256;
+constexpr size_t kArrivedBytes = DL_WORKSPACE_ZERO_BYTES;
+static_assert(kArrivedBytes >= kMaxSlots * sizeof(uint32_t) && kArrivedBytes % 256 == 0, "a counter a slot, the parts aligned");
 
 struct Range {   // groups of 32 tokens a tile sees: first `ns` groups, then g0 .. g0 + n - ns - 1
   int ns, g0, n;

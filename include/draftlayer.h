@@ -59,6 +59,7 @@ extern "C" {
 #define DL_MAX_ROWS (1 << 22)
 #define DL_MAX_SEQS 4096
 #define DL_MAX_POSITIONS (1 << 30)
+#define DL_WORKSPACE_ZERO_BYTES 6144   /* the start of a workspace that has to be zero before its first use */
 
 /*
  * HOST.  cos and sin of the rotary angles: out[p][i] = (m cos(p f_i),
@@ -126,9 +127,10 @@ int draft_layer_read(const uint8_t* k_codes, const uint8_t* v_codes, const float
 
 /*
  * Bytes of device workspace draft_layer_attend needs for T rows of n_seq
- * sequences.  A workspace must be zero before its first use; the calls leave
- * the part that has to be zero at zero, so one workspace serves any number of
- * calls of any sizes it is large enough for, in order (one stream).
+ * sequences.  Its first DL_WORKSPACE_ZERO_BYTES must be zero before its first
+ * use, the rest may hold anything; the calls leave those bytes at zero, so one
+ * workspace serves any number of calls of any sizes it is large enough for, in
+ * order (one stream).
  * Errors: DH_EINVAL (null pointer), DH_ESHAPE, DH_EUNSUP.
  */
 int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t* bytes);

@@ -534,3 +534,15 @@ def test_example_runs(dev, window, sinks):
     a, b = mod.run(**kw), mod.run(**kw)
     assert a.shape == (2, 3, 4) and int(a.min()) >= 0 and int(a.max()) < 3000
     assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("lens,d", [([(1, 9000)], 128), ([(9, 4000)] * 3, 128), ([(700, 4000), (100, 100)], 64), ([(1, 300 * i + 1) for i in range(30)], 256)])
+def test_workspace_may_hold_anything_after_its_counters(dev, lens, d):
+    """Parts are read only where this call wrote them."""
+    c = Case(dev, lens, 8, 2, d, 64, seed=23).upload()
+    ws = torch.full((L.draft_layer_workspace_bytes(c.rows, len(lens), 8, 2, d),), 255, dtype=torch.uint8, device=dev)   # NaN as fp32
+    ws[:L.WORKSPACE_ZERO_BYTES] = 0
+    for _ in range(2):
+        check_attend(c, 0, 0, workspace=ws)
+        assert not ws[:L.WORKSPACE_ZERO_BYTES].any()
+        ws[L.WORKSPACE_ZERO_BYTES:] = 255

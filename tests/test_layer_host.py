@@ -162,3 +162,15 @@ def test_binding_refuses_host_tensors():
         L.DraftCache(4, 2, 96, device="cpu")
     with pytest.raises(ValueError):
         L.DraftCache(4, 2, 64, page=48, device="cpu")
+
+
+def test_workspace_clears_its_counters_alone(lib, monkeypatch):
+    """A new workspace costs the clearing of its counters, whatever its size."""
+    torch = pytest.importorskip("torch")
+    with open(L._HEADER) as f:
+        assert f"#define DL_WORKSPACE_ZERO_BYTES {L.WORKSPACE_ZERO_BYTES} " in f.read()
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, **kw: empty(*a, **kw).fill_(255))
+    ws = L.draft_layer_workspace(72, 8, 40, 8, 128, "cpu")
+    assert ws.numel() == L.draft_layer_workspace_bytes(72, 8, 40, 8, 128) > 1 << 20
+    assert not ws[:L.WORKSPACE_ZERO_BYTES].any() and bool((ws[L.WORKSPACE_ZERO_BYTES:] == 255).all())
