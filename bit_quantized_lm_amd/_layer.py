@@ -227,7 +227,8 @@ def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table,
 
 
 def draft_layer_workspace_bytes(rows: int, n_seq: int, hq: int, hkv: int, d: int) -> int:
-    """Device workspace bytes draft_layer_attend needs for `rows` rows of n_seq sequences."""
+    """Device workspace bytes draft_layer_attend needs at most for calls of up to
+    `rows` rows of up to n_seq sequences."""
     lib = _load()
     out = ctypes.c_size_t()
     B._check(lib.draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d, ctypes.byref(out)))

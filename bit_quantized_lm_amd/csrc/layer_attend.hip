@@ -935,11 +935,14 @@ struct Plan {
   int min_run;   // least groups of a part: one a wave, or as many steps as its beginning takes
   int alone;     // most groups of a tile that joining parts would not make faster (4 us and more)
 };
-Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
-  const int64_t rows = ((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq;
-  if (rows <= 16) return D == 256 ? Plan{16, 4, 256, 4, 18} : (int64_t)n_seq * hkv < 64 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
-  if (rows <= 64) return {64, 0, 512, 10, 14};
+constexpr int kStreamRows = 16, kSmallRows = 64;   // most rows a sequence of the streaming kernel and of tiles of 64
+Plan plan_of(int64_t rows, int n_seq, int hkv, int D) {
+  if (rows <= kStreamRows) return D == 256 ? Plan{16, 4, 256, 4, 18} : (int64_t)n_seq * hkv < 64 ? Plan{16, 8, 256, 8, 36} : Plan{16, 4, 512, 4, 18};
+  if (rows <= kSmallRows) return {64, 0, 512, 10, 14};
   return {128, 0, D == 256 ? 256 : 512, 30, 32};
+}
+Plan plan_for(int T, int n_seq, int hq, int hkv, int D) {
+  return plan_of(((int64_t)T * (hq / hkv) + n_seq - 1) / n_seq, n_seq, hkv, D);
 }
 
 int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }
@@ -947,6 +950,17 @@ int target_items(int blocks, int hkv) { return std::max(1, blocks / hkv); }
 size_t workspace_bytes(const Plan& p, int hkv, int D) {
   const size_t slots = 2 * (size_t)target_items(p.blocks, hkv) * hkv;
   return kArrivedBytes + slots * p.rows * (D + 2) * sizeof(float);
+}
+
+// What any call of up to T rows of up to n_seq sequences needs: fewer sequences
+// have more rows each, up to all T in one, and any fewer, so every plan up to that
+// one's is within reach (few rows: more sequences take no fewer workgroups).
+size_t workspace_bound(int T, int n_seq, int hq, int hkv, int D) {
+  const int64_t most = (int64_t)T * (hq / hkv);
+  size_t bytes = workspace_bytes(plan_of(0, n_seq, hkv, D), hkv, D);
+  if (most > kStreamRows) bytes = std::max(bytes, workspace_bytes(plan_of(kSmallRows, n_seq, hkv, D), hkv, D));
+  if (most > kSmallRows) bytes = std::max(bytes, workspace_bytes(plan_of(kSmallRows + 1, n_seq, hkv, D), hkv, D));
+  return bytes;
 }
 
 template <int D, int NQ, int W>
@@ -996,7 +1010,7 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
   int rc = check_heads("workspace_bytes", hq, hkv, D);
   if (rc) return rc;
   if ((rc = check_rows("workspace_bytes", T, n_seq))) return rc;
-  *bytes = workspace_bytes(plan_for(T, n_seq, hq, hkv, D), hkv, D);
+  *bytes = workspace_bound(T, n_seq, hq, hkv, D);
   return dh::ok();
 }
 

@@ -63,8 +63,7 @@ def run(seqs=8, prompt=700, slots=9, rounds=2, hidden=1024, vocab=16384, hq=10, 
     rng = torch.Generator().manual_seed(seed)
     lengths = [prompt - i * (prompt // (2 * seqs)) for i in range(seqs)]          # prompts of several lengths
     table = torch.randperm(seqs * per_seq, generator=rng).view(seqs, per_seq).to(torch.int32).to(dev)
-    workspace = draft_layer_workspace(sum(lengths), seqs, hq, hkv, d, dev)
-    workspace_one = draft_layer_workspace(seqs, seqs, hq, hkv, d, dev)
+    workspace = draft_layer_workspace(sum(lengths), seqs, hq, hkv, d, dev)       # for the prompts, and for every smaller batch
 
     def ints(x):
         return torch.tensor(x, dtype=torch.int32, device=dev)
@@ -84,7 +83,7 @@ def run(seqs=8, prompt=700, slots=9, rounds=2, hidden=1024, vocab=16384, hq=10, 
     for r in range(rounds):
         got, token = [], last
         for i in range(slots):
-            x = layer(token, one, kept + (i + 1), table, workspace_one, window, sinks)
+            x = layer(token, one, kept + (i + 1), table, workspace, window, sinks)
             token = head_tokens(x)
             got.append(token)
         drafts.append(torch.stack(got, 1))

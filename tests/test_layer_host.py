@@ -3,6 +3,7 @@ oracle, the stored byte order, and every refusal (all arguments are checked
 before any HIP call, so none needs a GPU)."""
 import ctypes
 import math
+import re
 
 import numpy as np
 import pytest
@@ -174,3 +175,30 @@ def test_workspace_clears_its_counters_alone(lib, monkeypatch):
     ws = L.draft_layer_workspace(72, 8, 40, 8, 128, "cpu")
     assert ws.numel() == L.draft_layer_workspace_bytes(72, 8, 40, 8, 128) > 1 << 20
     assert not ws[:L.WORKSPACE_ZERO_BYTES].any() and bool((ws[L.WORKSPACE_ZERO_BYTES:] == 255).all())
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(40, 8, 128), (7, 7, 256), (16, 2, 256), (8, 1, 64), (56, 8, 64), (256, 1, 128), (200, 200, 64)])
+def test_workspace_of_the_largest_batch_serves_smaller_ones(lib, hq, hkv, d):
+    """The size never falls as rows or sequences grow."""
+    rows = [0, 1, 2, 3, 4, 8, 12, 13, 16, 17, 32, 63, 64, 65, 72, 100, 128, 500, 512, 513, 1024, 4096, 70000, 1 << 22]
+    seqs = [1, 2, 3, 7, 8, 9, 16, 31, 32, 33, 63, 64, 65, 100, 128, 512, 4096]
+    size = {(t, n): L.draft_layer_workspace_bytes(t, n, hq, hkv, d) for t in rows for n in seqs}
+    for at, here in (((i, j), size[t, n]) for i, t in enumerate(rows) for j, n in enumerate(seqs)):
+        i, j = at
+        assert i == 0 or here >= size[rows[i - 1], seqs[j]], at
+        assert j == 0 or here >= size[rows[i], seqs[j - 1]], at
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(40, 8, 128), (7, 7, 256), (16, 1, 64)])
+@pytest.mark.parametrize("most_rows,most_seqs", [(512, 64), (4096, 1), (64, 64), (20, 4)])
+def test_attend_takes_the_largest_batchs_workspace(lib, hq, hkv, d, most_rows, most_seqs):
+    """No smaller call asks for more than the size for the largest batch (what a
+    call asks for is in its refusal of a workspace of 16 bytes)."""
+    given = L.draft_layer_workspace_bytes(most_rows, most_seqs, hq, hkv, d)
+    for t in (1, 2, 5, 17, 64, 65, 500, 512, 4096):
+        for n in (1, 2, 3, 8, 63, 64):
+            if t <= most_rows and n <= most_seqs:
+                _refused(lib, lib.draft_layer_attend, ATTEND,
+                         dict(T=t, n_seq=n, hq=hq, hkv=hkv, D=d, ldq=hq * d, bytes=16), B.DH_EINVAL, b"attend")
+                need = int(re.search(rb"below the (\d+) needed", lib.draft_head_last_error()).group(1))
+                assert 16 < need <= given, (t, n)
