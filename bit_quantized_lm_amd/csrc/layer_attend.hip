@@ -275,7 +275,7 @@ __device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bo
 // largest is just under 2^16), and one keeps its 11 bits down to 2^-21 of the
 // largest.
 constexpr float kHead = 7.0f, kFit = 15.0f, kMost = 0x1p15f;
-constexpr float kLowest = -1e30f;   // m before the first visible token; finite, so no inf - inf arises
+constexpr float kLowest = -0x1p127f;   // m before the first visible token; finite, so no inf - inf arises
 
 // --------------------------------------------------------------- split parts
 // Partial results pass between workgroups, perhaps on different XCDs, through
@@ -472,6 +472,15 @@ struct Weights {
     }
   }
 
+  // A score's exponent, rounded as a reference is. form() does not round the product:
+  // a reference of 2^28 may be 16 off it, and a weight from such a difference is
+  // anything from 0 to infinity.
+  static __device__ __forceinline__ float rounded(float x, float c, float lv) {
+#pragma clang fp contract(off)
+    const float z = x * c;
+    return z + lv;
+  }
+
   // weights `from` .. `to` - 1 of the 8 N
   __device__ __forceinline__ void form(const Group& g, const f32x4 (&x)[N][2], const float (&m)[N], int from = 0, int to = 8 * N) {
 #pragma unroll
@@ -494,7 +503,7 @@ struct Weights {
         float top = x[t][0][0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = fmaxf(top, x[t][j >> 2][j & 3]);
-        top = fmaf(top, c[t], g.lv);
+        top = rounded(top, c[t], g.lv);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32));
         // by each row's own maximum, whichever row asked: rows do not touch each other's bits
@@ -504,7 +513,12 @@ struct Weights {
 #pragma unroll
         for (int i = 0; i < C; ++i) o[t][i] *= down;
       }
-      form(g, x, m);
+#pragma unroll
+      for (int t = 0; t < N; ++t) {
+        sum[t] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[t] += p[t][j] = __builtin_amdgcn_exp2f(rounded(x[t][j >> 2][j & 3], c[t], g.lv - m[t]));
+      }
     }
 #pragma unroll
     for (int t = 0; t < N; ++t) {

@@ -546,3 +546,29 @@ def test_workspace_may_hold_anything_after_its_counters(dev, lens, d):
         check_attend(c, 0, 0, workspace=ws)
         assert not ws[:L.WORKSPACE_ZERO_BYTES].any()
         ws[L.WORKSPACE_ZERO_BYTES:] = 255
+
+
+@pytest.mark.parametrize("new,d", [(1, 64), (9, 128), (40, 64), (200, 128), (30, 256)])
+@pytest.mark.parametrize("power", [10, 28, 31, 60, 100])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attend_large_scores(dev, new, d, power, sign):
+    """Scores of 2^power, past what fp32 holds to a unit: one token stands out by a
+    quarter of them, far more than their rounding, so every row is that token's
+    value; lower than all of -1e30, scores are still scores."""
+    c = Case(dev, [(new, 700)], 4, 2, d, 64, seed=24)
+    signs = c.rng.choice([-1.0, 1.0], d)
+    far = 100 if sign > 0 else -80         # codes along the signs: the others', and the winner's 25% to 40% above
+    win = 127 if sign > 0 else -40
+    for t in range(700):
+        code = (128 + signs * (win if t == 130 else far)).astype(np.uint8)
+        c.kc[c.table[0, t // 64]].reshape(2, -1)[:, O.key_byte(np.full(d, t % 64), np.arange(d), d)] = code
+    c.ks[:] = 2.0 ** (power // 2)
+    c.q = torch.from_numpy(np.tile(signs * 2.0 ** (power - power // 2 - 6), (new, 4, 1)).astype(np.float32)).to(torch.bfloat16)
+    c.upload()
+    out, lse = check_attend(c, 0, 0, scale=1.0 / d)
+    _, vn = c.naturals()
+    pid = c.table[0, 2]
+    want = np.repeat(vn[pid, :, 130 % 64] * c.vs[pid].astype(np.float64)[:, None], 2, axis=0)
+    assert np.all(np.abs(out - want) <= half_ulp(want) + 2.0 ** -11 * np.abs(want))
+    z = 2.0 ** (power - 6) * win
+    assert np.all(np.abs(lse - z) <= (d + 16) * U * abs(z))
