@@ -240,7 +240,8 @@ __device__ __forceinline__ u32x4 load_codes(const uint8_t* at, int f) {
 // A row's query fragments, lane (hi, lo) holding elements 64 f + 16 hi ..
 // + 15 of the tile's row lo, as fp16 scaled by 2^-e so that the row's largest
 // element is in [2^14, 2^15).  Returns scale_log2 * 2^e.  A zero row keeps 1;
-// an infinite or NaN element makes its own row NaN and no other.
+// an infinite or NaN element makes its own row NaN and no other, through what is
+// returned: infinite scores of one sign alone would be a row that sees nothing.
 template <int D>
 __device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bool valid, float scale_log2, half8 (&frag)[D / 32]) {
   const int hi = (threadIdx.x & 63) >> 4;
@@ -263,7 +264,7 @@ __device__ __forceinline__ float load_query(const uint16_t* __restrict__ row, bo
       frag[f][2 * i] = (_Float16)(bf16_lo(raw[f][i]) * up);
       frag[f][2 * i + 1] = (_Float16)(bf16_hi(raw[f][i]) * up);
     }
-  return __builtin_ldexpf(scale_log2, e);
+  return top >= 0x7F80u ? __builtin_nanf("") : __builtin_ldexpf(scale_log2, e);
 }
 
 // Online softmax of one row: weights are 2^(x - m) with x = z log2(e) +

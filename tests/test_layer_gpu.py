@@ -572,3 +572,20 @@ def test_attend_large_scores(dev, new, d, power, sign):
     assert np.all(np.abs(out - want) <= half_ulp(want) + 2.0 ** -11 * np.abs(want))
     z = 2.0 ** (power - 6) * win
     assert np.all(np.abs(lse - z) <= (d + 16) * U * abs(z))
+
+
+@pytest.mark.parametrize("new,d", [(3, 64), (9, 128), (40, 64), (200, 128), (30, 256)])
+def test_attend_infinite_query_is_nan(dev, new, d):
+    """An infinite element makes the row NaN even where every score is -inf."""
+    c = Case(dev, [(new, 700)], 4, 2, d, 64, seed=25)
+    c.kc[:] = np.minimum(c.kc, 127)                      # negative codes alone
+    c.upload()
+    out, lse = check_attend(c, 0, 0)
+    q = c.q.clone()
+    q[1, 2, :] = 0.0
+    q[1, 2, 5] = float("inf")
+    got, glse = (t.double().cpu().numpy() for t in L.draft_layer_attend(q.to(dev), *c.cache, *c.batch))
+    bad = np.zeros((new, 4), bool)
+    bad[1, 2] = True
+    assert np.isnan(got[bad]).all() and np.isnan(glse[bad]).all()
+    assert np.array_equal(got[~bad], out[~bad]) and np.array_equal(glse[~bad], lse[~bad])
