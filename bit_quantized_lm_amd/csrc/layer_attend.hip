@@ -433,6 +433,17 @@ __device__ __forceinline__ void join_parts(const AttendArgs& A, const Segment& w
   }
 }
 
+// What the scores take of a page's two scales.  One that is not finite makes the
+// key scale NaN, and with it the scores of the rows that see the page; a hidden
+// token's weight is formed from the value scale's logarithm, which stays finite.
+struct PageScales {
+  float ks, lv, rv;   // key scale, log2(value scale), 1 / (value scale)
+};
+__device__ __forceinline__ PageScales page_scales(float ks, float vs) {
+  const float nan_if_not_finite = (ks - ks) + (vs - vs), v = fminf(fmaxf(vs, kMinScale), 0x1p126f);
+  return {ks + nan_if_not_finite, __builtin_amdgcn_logf(v), __builtin_amdgcn_rcpf(v)};
+}
+
 // Whether some row at p_first .. p_last does not see some of the tokens first .. first + 31.
 __device__ __forceinline__ bool hides(const AttendArgs& A, int first, int p_first, int p_last) {
   return first + 31 > p_first || (A.window > 0 && first <= p_last - A.window && first + 31 >= A.sinks);
@@ -569,16 +580,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel
 
     // lane i: page and scales of the wave's i-th group from `base`, 64 at a time
     int base = from + wave, id_mine;
-    float ks_mine, lv_mine, rv_mine;
+    PageScales mine_scales;
     auto group_at = [&](int n) { return n < see.ns ? n : n - see.ns + see.g0; };
     auto look = [&] {
       const int n = base + lane * W;
       id_mine = n < to ? page_id(A.b, A.c.n_pages, w.seq, group_at(n) >> (A.c.page_shift - 5)) : -1;
       const size_t at = (size_t)max(id_mine, 0) * A.c.hkv + head;
-      const float vs = id_mine < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
-      ks_mine = A.c.ks[at];
-      lv_mine = __builtin_amdgcn_logf(vs);
-      rv_mine = __builtin_amdgcn_rcpf(vs);
+      mine_scales = page_scales(A.c.ks[at], A.c.vs[at]);   // of one that is not there page 0's, which step() hides
     };
     auto load = [&](int i, Bytes<F>& b) {   // of a group that is not there page 0's bytes, which step() hides
       const size_t off = ((size_t)max(__builtin_amdgcn_readlane(id_mine, i), 0) * A.c.hkv + head) * page_bytes +
@@ -608,9 +616,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel
     }
     auto step = [&](int i, const Bytes<F>& b) {
       const int first = group_at(base + i * W) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
-      const Group group{id, first, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ks_mine), i)),
-                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv_mine), i)),
-                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(rv_mine), i)),
+      const Group group{id, first, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.ks), i)),
+                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.lv), i)),
+                        __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.rv), i)),
                         id < 0 || hides(A, first, p_first, p_last)};
       f32x4 s[1][2] = {{{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}}};
 #pragma unroll
@@ -756,11 +764,10 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
       const int i = max(n + tid, from), g = group_at(i);
       const int id = i < to ? page_id(A.b, A.c.n_pages, w.seq, g >> (A.c.page_shift - 5)) : -1;
       const size_t at = (size_t)max(id, 0) * A.c.hkv + head;
-      const float ks = A.c.ks[at], vs = id < 0 ? 1.0f : fmaxf(A.c.vs[at], kMinScale);   // page 0's own may be anything
+      const PageScales scales = page_scales(A.c.ks[at], A.c.vs[at]);   // of one that is not there page 0's, hidden later
       const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
       __syncthreads();
-      table[tid] = u32x4{(uint32_t)where, __float_as_uint(ks), __float_as_uint(__builtin_amdgcn_logf(vs)),
-                         __float_as_uint(__builtin_amdgcn_rcpf(vs))};
+      table[tid] = u32x4{(uint32_t)where, __float_as_uint(scales.ks), __float_as_uint(scales.lv), __float_as_uint(scales.rv)};
       table_at = n;
       __syncthreads();
     };

@@ -589,3 +589,27 @@ def test_attend_infinite_query_is_nan(dev, new, d):
     bad[1, 2] = True
     assert np.isnan(got[bad]).all() and np.isnan(glse[bad]).all()
     assert np.array_equal(got[~bad], out[~bad]) and np.array_equal(glse[~bad], lse[~bad])
+
+
+@pytest.mark.parametrize("new,length,d,window,sinks", [(5, 130, 64, 0, 0), (40, 600, 128, 0, 0), (260, 600, 64, 0, 0), (40, 600, 256, 100, 4),
+                                                       (1, 5000, 128, 0, 0), (9, 5000, 64, 0, 0)])
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_attend_scale_not_finite(dev, new, length, d, window, sinks, which, value):
+    """A page whose scale is not finite makes the rows that see it NaN, and no other row."""
+    page = 32
+    c = Case(dev, [(new, length)], 4, 2, d, page, seed=26).upload()
+    out, lse = check_attend(c, window, sinks)
+    pos = np.arange(length - new, length)
+    for j in {(length - 1) // page, (length - new) // page, 2, 0}:
+        c.upload()
+        c.cache[2 if which == "k" else 3][int(c.table[0, j]), 1] = value
+        got, glse = (t.double().cpu().numpy() for t in L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch, window=window, sinks=sinks))
+        t = np.arange(j * page, min(j * page + page, length))[None, :]
+        seen = t <= pos[:, None]
+        if window:
+            seen &= (t > pos[:, None] - window) | (t < sinks)
+        bad = np.zeros((new, 4), bool)
+        bad[:, 2:] = seen.any(axis=1)[:, None]
+        assert np.isnan(got[bad]).all() and np.isnan(glse[bad]).all(), j
+        assert np.array_equal(got[~bad], out[~bad]) and np.array_equal(glse[~bad], lse[~bad]), j
