@@ -16,6 +16,7 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr float kMinScale = 0x1p-40f;   // smallest scale of a page
+constexpr uint32_t kNotFinite = 0x7F800000u;   // fp32 magnitudes from here on are infinity and NaN
 
 struct Batch {
   const int32_t* q_start;
@@ -88,6 +89,15 @@ template <int kControl, int kRows>
 __device__ __forceinline__ float max_moved(float x) {
   const int v = (int)__float_as_uint(x);
   return fmaxf(x, __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(v, v, kControl, kRows, 0xf, false)));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = max(x, (uint32_t)moved<0x111, 0xf>((int)x));
+  x = max(x, (uint32_t)moved<0x112, 0xf>((int)x));
+  x = max(x, (uint32_t)moved<0x114, 0xf>((int)x));
+  x = max(x, (uint32_t)moved<0x118, 0xf>((int)x));
+  x = max(x, (uint32_t)moved<0x142, 0xa>((int)x));
+  x = max(x, (uint32_t)moved<0x143, 0xc>((int)x));
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
 }
 __device__ __forceinline__ float wave_max(float x) {
   x = max_moved<0x111, 0xf>(x);

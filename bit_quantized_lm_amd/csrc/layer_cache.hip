@@ -132,6 +132,11 @@ __device__ __forceinline__ void rotate_queries(const AppendArgs& A) {
 // here without a race, and only where the scale rose.  Values that a thread has
 // read for the scale it keeps for the codes, as far as its registers go; a
 // larger page's are read again.
+//
+// largest() gives the largest magnitude's bits: magnitudes compare as integers,
+// infinity above all numbers and NaN above it, so none is lost on the way. A page
+// that takes one of them gets the scale NaN, whatever the codes: its tokens' values
+// are NaN from then on, and no number is made of what is none.
 struct Page {
   const uint16_t* x;   // token 0's head (tokens before t0 are not there)
   int64_t ld;
@@ -149,12 +154,12 @@ struct KeyCodes {
     const uint16_t* at = g.x + t * g.ld;
     return make_unit(load8(at + p.d0), load8(at + p.d1), p.turned ? load_turn(A.rope, g.p0 + t, A.rot, u) : Turn{}, p);
   }
-  __device__ __forceinline__ float largest(const AppendArgs& A, const Page& g) {
+  __device__ __forceinline__ uint32_t largest(const AppendArgs& A, const Page& g) {
     const int units = (g.t1 - g.t0) * (D / 16);
-    float top = 0.0f;
+    uint32_t top = 0u;
     auto take = [&](const Unit& x) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) top = fmaxf(top, fabsf(x.x[j]));
+      for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(x.x[j]) & 0x7FFFFFFFu);
     };
 #pragma unroll
     for (int k = 0; k < kKept; ++k) {
@@ -206,9 +211,9 @@ struct ValueCodes {
     for (int k = 0; k < 4; ++k) f.x[k] = t + k >= g.t0 && t + k < g.t1 ? load8(g.x + (t + k) * g.ld + e) : u32x4{0u, 0u, 0u, 0u};
     return f;
   }
-  __device__ __forceinline__ float largest(const AppendArgs&, const Page& g) {
+  __device__ __forceinline__ uint32_t largest(const AppendArgs&, const Page& g) {
     const int n = quads(g);
-    uint32_t top = 0u;   // bf16 magnitudes compare as integers
+    uint32_t top = 0u;
     auto take = [&](const Four& f) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
@@ -221,7 +226,7 @@ struct ValueCodes {
       if (i < n) take(kept[k] = four(g, i));
     }
     for (int i = threadIdx.x + kKept * kThreads; i < n; i += kThreads) take(four(g, i));
-    return __uint_as_float(top << 16);
+    return top << 16;
   }
   __device__ __forceinline__ void write(const AppendArgs&, const Page& g, float inv, uint8_t* lds) const {
     const int n = quads(g);
@@ -250,7 +255,7 @@ template <int D, class Codes>
 __device__ __forceinline__ void write_page(const AppendArgs& A, int s, int page_no, int head, const uint16_t* x, int64_t ld,
                                            uint8_t* codes_base, float* scale_base, uint8_t* lds) {
 #pragma clang fp contract(off)
-  __shared__ float wave_top[kThreads / 64];
+  __shared__ uint32_t wave_top[kThreads / 64];
   const int tid = threadIdx.x, page = 1 << A.c.page_shift;
   const int id = page_id(A.b, A.c.n_pages, s, page_no);
   if (id < 0) return;
@@ -264,14 +269,15 @@ __device__ __forceinline__ void write_page(const AppendArgs& A, int s, int page_
   float* scale = scale_base + (size_t)id * A.c.hkv + head;
   u32x4* codes = reinterpret_cast<u32x4*>(codes_base + ((size_t)id * A.c.hkv + head) * ((size_t)page * D));
   Codes values;
-  float top = wave_max(values.largest(A, g));
+  uint32_t top = wave_max(values.largest(A, g));
   if ((tid & 63) == 0) wave_top[tid >> 6] = top;
   const float before = *scale;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kThreads / 64; ++w) top = fmaxf(top, wave_top[w]);
-  float step = fmaxf(top / 127.0f, kMinScale);
+  for (int w = 0; w < kThreads / 64; ++w) top = max(top, wave_top[w]);
+  float step = fmaxf(__uint_as_float(top) / 127.0f, kMinScale);
   if (g.t0 > 0) step = fmaxf(step, before);
+  if (top >= kNotFinite || (g.t0 > 0 && (__float_as_uint(before) & 0x7FFFFFFFu) >= kNotFinite)) step = __builtin_nanf("");
   const float ratio = before / step;
   const bool raised = g.t0 > 0 && step > before;
   values.write(A, g, 1.0f / step, lds);

@@ -95,6 +95,9 @@ int draft_layer_rope_table(int positions, int rot, double base, double factor, i
  *          the present scale if the page holds older tokens of the sequence;
  *   where that raises the scale, an older code c becomes rne(c * (old / step));
  *   a new code is rne(x * (1 / step)) clamped to -127..127; scale = step.
+ * A new value that is infinite or NaN (in a key: after the rotation) makes its
+ * page's and head's scale NaN, whatever the codes: all tokens of that page read
+ * back as NaN, and so is every row that sees one, until the page starts afresh.
  * A page whose first new token is its token 0 starts afresh, whatever its
  * scale and codes held, so rejected tokens are dropped by writing over them.
  *   q        device, bf16, row r head h at q + r*ldq + h*D; may be NULL with
@@ -104,7 +107,7 @@ int draft_layer_rope_table(int positions, int rot, double base, double factor, i
  *   q_out    out, bf16 [T][hq][D] without gaps; may be q itself if ldq = hq*D
  * Row strides are in elements, multiples of 8 and at least the heads' D each;
  * q, k, v, q_out and rope are 16-byte aligned.  Two sequences of one call
- * must not write the same page.  Values must be finite with |x| < 2^60.
+ * must not write the same page.
  * Limits: rot a multiple of 16 in 0..D (0: nothing is rotated, rope unused).
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */

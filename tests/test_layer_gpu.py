@@ -613,3 +613,64 @@ def test_attend_scale_not_finite(dev, new, length, d, window, sinks, which, valu
         bad[:, 2:] = seen.any(axis=1)[:, None]
         assert np.isnan(got[bad]).all() and np.isnan(glse[bad]).all(), j
         assert np.array_equal(got[~bad], out[~bad]) and np.array_equal(glse[~bad], lse[~bad]), j
+
+
+@pytest.mark.parametrize("new,length,d,page", [(3, 40, 64, 32), (9, 100, 128, 64), (200, 230, 64, 64), (300, 300, 256, 256)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+def test_append_not_finite(dev, new, length, d, page, value):
+    """A new value that is no number makes its page and head NaN, reading and
+    attention say so, tokens that follow there do not undo it, a fresh start does."""
+    rope = torch.from_numpy(L.draft_layer_rope_table(-(-length // page) * page + 2 * page, d)).to(dev)
+    for which in ("k", "v"):
+        c = Case(dev, [(new, length)], 4, 2, d, page, seed=27).upload()
+        kv = {x: bf16(c.rng, new, 2, d).to(dev) for x in "kv"}
+        begin, at = length - new, new - 2
+        pid = int(c.table[0, (begin + at) // page])
+        L.draft_layer_append(None, kv["k"], kv["v"], rope, *c.cache, *c.batch)
+        clean = [t.clone() for t in c.cache]
+        clean_kv = L.draft_layer_read(*c.cache, *c.batch, new)
+        before = L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch)
+        c.upload()
+        kv[which][at, 1, d // 2 + 3] = value
+        L.draft_layer_append(None, kv["k"], kv["v"], rope, *c.cache, *c.batch)
+        scale, other = (c.cache[2], c.cache[3]) if which == "k" else (c.cache[3], c.cache[2])
+        want = (clean[2] if which == "k" else clean[3]).clone()
+        want[pid, 1] = float("nan")
+        assert torch.equal(scale.isnan(), want.isnan()) and torch.equal(scale.nan_to_num(), want.nan_to_num())
+        assert torch.equal(other, clean[3] if which == "k" else clean[2])
+        got_kv = L.draft_layer_read(*c.cache, *c.batch, new)
+        on_page = torch.arange(begin, length, device=dev) // page == (begin + at) // page
+        for x, got, was in (("k", got_kv[0], clean_kv[0]), ("v", got_kv[1], clean_kv[1])):
+            nan = torch.zeros_like(got, dtype=torch.bool)
+            if x == which:
+                nan[on_page, 1] = True
+            assert torch.equal(got.isnan(), nan) and torch.equal(got[~nan], was[~nan])
+        out, lse = L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch)
+        see = torch.arange(begin, length, device=dev) >= (begin + at) // page * page
+        nan = torch.zeros_like(lse, dtype=torch.bool)
+        nan[:, 2:] = see[:, None]
+        assert torch.equal(lse.isnan(), nan) and bool(out[nan].isnan().all())
+        assert torch.equal(out[~nan], before[0][~nan]) and torch.equal(lse[~nan], before[1][~nan])
+        # one more token of the page: still NaN; the page's own start: no longer
+        one = torch.tensor([0, 1], dtype=torch.int32, device=dev)
+        fine = {x: bf16(c.rng, 1, 2, d).to(dev) for x in "kv"}
+        first = (begin + at) // page * page
+        for position, still in ((first + 1, True), (first, False)):
+            L.draft_layer_append(None, fine["k"], fine["v"], rope, *c.cache, one, torch.tensor([position + 1], dtype=torch.int32, device=dev), c.batch[2])
+            assert bool(scale[pid, 1].isnan()) == still and not bool(scale[pid, 0].isnan())
+
+
+def test_append_not_finite_in_queries_alone(dev):
+    """The queries' own NaN and infinity stay in their rows and heads and out of the cache."""
+    c = Case(dev, [(9, 100)], 4, 2, 64, 32, seed=28).upload()
+    rope = torch.from_numpy(L.draft_layer_rope_table(160, 64)).to(dev)
+    k, v = bf16(c.rng, 9, 2, 64).to(dev), bf16(c.rng, 9, 2, 64).to(dev)
+    q = c.q.to(dev)
+    clean = L.draft_layer_append(q, k, v, rope, *c.cache, *c.batch)
+    kept = [t.clone() for t in c.cache]
+    q[4, 3, 7], q[6, 0, 1] = float("nan"), float("inf")
+    got = L.draft_layer_append(q, k, v, rope, *c.upload().cache, *c.batch)
+    nan = torch.zeros((9, 4), dtype=torch.bool, device=dev)
+    nan[4, 3] = nan[6, 0] = True
+    assert torch.equal(got[~nan], clean[~nan]) and not bool(torch.isfinite(got[nan]).all(dim=1).any())
+    assert all(torch.equal(a, b) for a, b in zip(kept, c.cache))
