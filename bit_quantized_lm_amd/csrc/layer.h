@@ -190,6 +190,14 @@ inline int check_stride(const char* who, const char* what, const void* p, int64_
   return DH_OK;
 }
 
+// Lets `kernel` take `bytes` of dynamic LDS on the current device.
+inline hipError_t allow_lds(dh::OncePerDevice& once, const void* kernel, size_t bytes) {
+  int device = 0;
+  const hipError_t e = hipGetDevice(&device);
+  if (e != hipSuccess) return e;
+  return once.run(device, hipSuccess, [&] { return hipFuncSetAttribute(kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes); });
+}
+
 inline int launched(const char* what) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return dh::fail(DH_EHIP, "%s: %s", what, hipGetErrorString(e));

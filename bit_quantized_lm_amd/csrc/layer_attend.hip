@@ -988,13 +988,9 @@ size_t workspace_bound(int T, int n_seq, int hq, int hkv, int D) {
 template <int D, int NQ, int W>
 hipError_t launch_shared(const AttendArgs& A, dim3 grid, hipStream_t s) {
   using S = Shared<D, NQ, W>;
-  static bool attr_set = false;
-  if (!attr_set) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&attend_shared_kernel<D, NQ, W>),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)S::kLds);
-    if (e != hipSuccess) return e;
-    attr_set = true;
-  }
+  static dh::OncePerDevice once;
+  const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&attend_shared_kernel<D, NQ, W>), S::kLds);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL((attend_shared_kernel<D, NQ, W>), grid, dim3(S::kThreads), S::kLds, s, A);
   return hipSuccess;
 }

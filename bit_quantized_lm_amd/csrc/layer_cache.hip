@@ -458,13 +458,9 @@ int draft_layer_append(const void* q, int64_t ldq, const void* k, int64_t ldk, c
     case 64: hipLaunchKernelGGL(append_kernel<64>, dim3((unsigned)grid), dim3(kThreads), lds, st, A); break;
     case 128: hipLaunchKernelGGL(append_kernel<128>, dim3((unsigned)grid), dim3(kThreads), lds, st, A); break;
     default: {
-      static bool attr_set = false;   // 64 KiB and the wave maxima: above the default limit
-      if (!attr_set) {
-        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&append_kernel<256>),
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, 256 * 256);
-        if (e != hipSuccess) return dh::fail(DH_EHIP, "append_kernel: %s", hipGetErrorString(e));
-        attr_set = true;
-      }
+      static dh::OncePerDevice once;   // 64 KiB and the wave maxima: above the default limit
+      const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&append_kernel<256>), 256 * 256);
+      if (e != hipSuccess) return dh::fail(DH_EHIP, "append_kernel: %s", hipGetErrorString(e));
       hipLaunchKernelGGL(append_kernel<256>, dim3((unsigned)grid), dim3(kThreads), lds, st, A);
     }
   }

@@ -3,7 +3,9 @@ oracle, the stored byte order, and every refusal (all arguments are checked
 before any HIP call, so none needs a GPU)."""
 import ctypes
 import math
+import os
 import re
+import subprocess
 
 import numpy as np
 import pytest
@@ -202,3 +204,38 @@ def test_attend_takes_the_largest_batchs_workspace(lib, hq, hkv, d, most_rows, m
                          dict(T=t, n_seq=n, hq=hq, hkv=hkv, D=d, ldq=hq * d, bytes=16), B.DH_EINVAL, b"attend")
                 need = int(re.search(rb"below the (\d+) needed", lib.draft_head_last_error()).group(1))
                 assert 16 < need <= given, (t, n)
+
+
+def test_kernel_attributes_are_set_on_every_device(tmp_path):
+    """A kernel's LDS limit is set once a device, from any number of threads, and
+    again after a failure (the helper alone, with counters in the runtime's place)."""
+    csrc = os.path.join(os.path.dirname(B.__file__), "csrc")
+    src = tmp_path / "once.cpp"
+    src.write_text(r"""
+#include <cstdio>
+#include <thread>
+#include <vector>
+#include "common.h"
+int main() {
+  dh::OncePerDevice once;
+  std::atomic<int> calls[80] = {};
+  auto on = [&](int device, int result) { return once.run(device, 0, [&] { ++calls[device]; return result; }); };
+  if (on(0, 7) != 7 || on(0, 7) != 7 || calls[0] != 2) return 1;     // failed: tried again
+  for (int i = 0; i < 3; ++i)
+    for (int d : {0, 1, 63}) if (on(d, 0) != 0) return 2;
+  if (calls[0] != 3 || calls[1] != 1 || calls[63] != 1) return 3;    // once each
+  for (int i = 0; i < 3; ++i) on(64, 0);
+  if (calls[64] != 3) return 4;                                      // more devices than it remembers
+  std::vector<std::thread> pool;
+  for (int t = 0; t < 8; ++t) pool.emplace_back([&] { for (int i = 0; i < 1000; ++i) on(i % 32 + 2, 0); });
+  for (auto& t : pool) t.join();
+  for (int d = 2; d < 34; ++d) if (calls[d] < 1 || calls[d] > 8) return 5;
+  return 0;
+}
+""")
+    exe = tmp_path / "once"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", "-I", csrc, str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
+    for name in ("layer_attend.hip", "layer_cache.hip"):
+        with open(os.path.join(csrc, name)) as f:
+            assert "hipFuncSetAttribute" not in f.read()     # through the helper alone
