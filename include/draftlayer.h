@@ -107,7 +107,9 @@ int draft_layer_rope_table(int positions, int rot, double base, double factor, i
  *   q_out    out, bf16 [T][hq][D] without gaps; may be q itself if ldq = hq*D
  * Row strides are in elements, multiples of 8 and at least the heads' D each;
  * q, k, v, q_out and rope are 16-byte aligned.  Two sequences of one call
- * must not write the same page.
+ * must not write the same page.  Values (of q, k and v) below 2^60 in magnitude
+ * and rope entries below 4 leave rotated elements below 2^63 and scales below
+ * 2^57, which is what draft_layer_attend takes.
  * Limits: rot a multiple of 16 in 0..D (0: nothing is rotated, rope unused).
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */
@@ -156,8 +158,11 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
  *   q  device, bf16, row r head h at q + r*ldq + h*D, 16-byte aligned, ldq a
  *      multiple of 8, at least hq*D
  *   workspace  16-byte aligned, of draft_layer_workspace_bytes() bytes
- * Limits: scale finite and > 0, window >= 0, sinks >= 0; scales of seen pages
- * as draft_layer_append leaves them (finite, at least 2^-40, below 2^53).
+ * A row with an infinite or NaN element of q, or that sees a page whose key or
+ * value scale is infinite or NaN, is NaN (out and lse), and no other row is.
+ * Limits: scale finite and > 0, window >= 0, sinks >= 0.  Results hold for q
+ * below 2^64 in magnitude, scales of seen pages in 2^-40 .. 2^57 and scores z_j
+ * below 2^120 in magnitude (from 2^24 on fp32 holds no fractions of them).
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */
 int draft_layer_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const uint8_t* v_codes,

@@ -674,3 +674,36 @@ def test_append_not_finite_in_queries_alone(dev):
     nan[4, 3] = nan[6, 0] = True
     assert torch.equal(got[~nan], clean[~nan]) and not bool(torch.isfinite(got[nan]).all(dim=1).any())
     assert all(torch.equal(a, b) for a, b in zip(kept, c.cache))
+
+
+@pytest.mark.parametrize("new", [3, 60])
+def test_append_limits_are_attends(dev, new):
+    """The largest values that append takes, rotated by the largest entries, next
+    to pages of the smallest scale: attend holds over what append leaves."""
+    d, page, length = 128, 32, 200
+    c = Case(dev, [(length, length)], 4, 2, d, page, seed=29)
+    c.upload()
+    rope = L.draft_layer_rope_table(c.max_pages * page, d, mscale=3.99)
+    assert np.abs(rope).max() < 4
+    big = 2.0 ** 60 * (1 - 2.0 ** -8)
+    k, v = (torch.from_numpy(c.rng.choice([-big, big], (length, 2, d)).astype(np.float32)).to(torch.bfloat16) for _ in range(2))
+    k[32:64], v[64:96] = 0.0, 0.0
+    before = c.naturals()
+    q = torch.from_numpy(c.rng.choice([-big, big], (length, 4, d)).astype(np.float32)).to(torch.bfloat16)
+    c.q = q
+    got = L.draft_layer_append(q.to(dev), k.to(dev), v.to(dev), torch.from_numpy(rope).to(dev), *c.cache, *c.batch)
+    check_append(c, None, rope, False, k, v, before, with_q=False)
+    want, _ = O.append(q.float().numpy(), k.float().numpy(), v.float().numpy(), rope, *before, c.ks, c.vs, c.q_start, c.kv_len, c.table, False)
+    assert np.all(np.abs(got.double().cpu().numpy() - want) <= half_ulp(want) + 4 * 8 * U * big)      # entries of 4 instead of 1
+    assert 2.0 ** 62 < float(got.float().abs().max()) < 2.0 ** 63
+    c.kc, c.vc, c.ks, c.vs = (t.cpu().numpy() for t in c.cache)
+    used = c.table[0, :-(-length // page)]
+    assert c.ks[used].max() > 2.0 ** 55 and max(c.ks[used].max(), c.vs[used].max()) < 2.0 ** 57
+    assert c.ks[used].min() == c.vs[used].min() == 2.0 ** -40
+    # rows whose scores stay in single figures, then the rotated queries themselves
+    c.q_start[1] = c.rows = new
+    c.q = (got.float() * 2.0 ** -126)[length - new:].to(torch.bfloat16).cpu()
+    c.upload()
+    check_attend(c, 0, 0)
+    c.q = got[length - new:].cpu()
+    check_attend(c, 0, 0, scale=2.0 ** -14)
