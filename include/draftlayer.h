@@ -99,7 +99,10 @@ int draft_layer_rope_table(int positions, int rot, double base, double factor, i
  * page's and head's scale NaN, whatever the codes: all tokens of that page read
  * back as NaN, and so is every row that sees one, until the page starts afresh.
  * A page whose first new token is its token 0 starts afresh, whatever its
- * scale and codes held, so rejected tokens are dropped by writing over them.
+ * scale and codes held.  Rejected tokens are dropped by writing over them; what
+ * one has done to a page that also holds accepted tokens stays: where it raised
+ * the scale, the accepted codes are re-rounded to the larger step, and the scale
+ * keeps it until the page starts afresh.
  *   q        device, bf16, row r head h at q + r*ldq + h*D; may be NULL with
  *            q_out (keys and values only)
  *   k, v     device, bf16, row strides ldk, ldv

@@ -707,3 +707,37 @@ def test_append_limits_are_attends(dev, new):
     check_attend(c, 0, 0)
     c.q = got[length - new:].cpu()
     check_attend(c, 0, 0, scale=2.0 ** -14)
+
+
+def test_append_rejected_outlier(dev):
+    """A rejected token far larger than its page's: written over, it is gone, but the
+    step that it raised stays with the page's accepted tokens and with those that
+    follow there; pages before it, and its own once it starts afresh, are as if it
+    had never been."""
+    d, page = 64, 32
+    c = Case(dev, [(1, 1)], 1, 1, d, page, seed=30, max_pages=3, spare=4)
+    c.table[0] = [0, 1, 2]
+    c.upload()
+    one = lambda n: torch.tensor([n], dtype=torch.int32, device=dev)  # noqa: E731
+    start = lambda n: torch.tensor([0, n], dtype=torch.int32, device=dev)  # noqa: E731
+    put = lambda x, end: L.draft_layer_append(None, x.to(dev), x.to(dev), None, *c.cache, start(len(x)), one(end), c.batch[2])  # noqa: E731
+    x = bf16(c.rng, 48, 1, d)
+    put(x[:42], 42)                                          # positions 0..41: ten accepted tokens on page 1
+    own = c.cache[3][:2, 0].clone()
+    first = L.draft_layer_read(*c.cache, start(42), one(42), c.batch[2], 42)[1]
+    put(x[42:43] * 100.0, 43)                                # an outlier, rejected
+    raised = float(c.cache[3][1, 0])
+    assert raised > 20 * float(own[1]) and c.cache[3][0, 0] == own[0]
+    put(x[42:48], 48)                                        # what took its place
+    assert float(c.cache[3][1, 0]) == raised
+    got = L.draft_layer_read(*c.cache, start(48), one(48), c.batch[2], 48)[1]
+    assert torch.equal(got[:32], first[:32])                 # the page before
+    err = (got.float().cpu() - x.float()).abs().flatten(1).max(dim=1).values
+    read = float(half_ulp(8.0))                              # what is read back is below 8
+    lim = torch.full((48,), (0.5 + 2.0 ** -12) * raised + read)
+    lim[32:42] += 0.5 * float(own[1])                        # rounded twice
+    assert bool((err[32:] <= lim[32:]).all())
+    put(x[32:48], 48)                                        # from its token 0 on
+    again = L.draft_layer_read(*c.cache, start(48), one(48), c.batch[2], 48)[1]
+    assert float(c.cache[3][1, 0]) == np.float32(x[32:48].float().abs().max().item()) / np.float32(127)
+    assert float((again.float().cpu() - x.float()).abs().max()) <= (0.5 + 2.0 ** -12) * float(c.cache[3][:2].max()) + read
