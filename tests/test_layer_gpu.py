@@ -741,3 +741,12 @@ def test_append_rejected_outlier(dev):
     again = L.draft_layer_read(*c.cache, start(48), one(48), c.batch[2], 48)[1]
     assert float(c.cache[3][1, 0]) == np.float32(x[32:48].float().abs().max().item()) / np.float32(127)
     assert float((again.float().cpu() - x.float()).abs().max()) <= (0.5 + 2.0 ** -12) * float(c.cache[3][:2].max()) + read
+
+
+@pytest.mark.parametrize("hkv,new,seqs,window", [(8, 1, 30, 0), (2, 1, 30, 0), (2, 3, 100, 0), (8, 2, 70, 500), (1, 1, 3, 0), (7, 1, 40, 0)])
+def test_attend_large_heads_of_few_rows(dev, hkv, new, seqs, window):
+    """The streaming kernel at heads of 256 over several sequences, whose fewer
+    workgroups take other runs and parts: lengths far apart, in each plan."""
+    lens = [(new if i % 7 else 0, new + 3 + (95 * i) % 2500) for i in range(seqs)]
+    lens[1] = (new, 5000)
+    check_attend(Case(dev, lens, hkv * 2, hkv, 256, 64, seed=31 + hkv).upload(), window, 4 if window else 0)
