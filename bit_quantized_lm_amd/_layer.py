@@ -212,7 +212,7 @@ def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_star
 def draft_layer_read(k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, rows: int, k_out=None, v_out=None, stream=None):
     """The last tokens of each sequence out of the cache: sequence s's
     q_start[s+1] - q_start[s] last ones, `rows` in all.  Returns (k, v), bf16
-    [rows][hkv][D]."""
+    [rows][hkv][D]; rows from q_start[-1] on are not written."""
     lib = _device_lib()
     dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
     n_seq, max_pages = _batch(q_start, kv_len, table, dev)
@@ -251,7 +251,8 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     q: CUDA bf16 [T][hq][D], rows with gaps allowed; scale: None for
     1/sqrt(D); window > 0: a row sees the last `window` tokens up to its own and
     the first `sinks`; workspace: from draft_layer_workspace (allocated when
-    None).  Returns (out bf16 [T][hq][D], lse fp32 [T][hq])."""
+    None).  Returns (out bf16 [T][hq][D], lse fp32 [T][hq]); rows from
+    q_start[-1] on are not written."""
     lib = _device_lib()
     dev, n_pages, hkv, page, d = _cache(k_codes, v_codes, k_scale, v_scale)
     n_seq, max_pages = _batch(q_start, kv_len, table, dev)

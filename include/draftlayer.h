@@ -25,6 +25,9 @@
  *   kv_len   device, int32 [n_seq]: tokens of sequence s in the cache, its new
  *            ones included; row i of s is the token at position
  *            kv_len[s] - n_s + i.  Rows of negative positions have no token.
+ *            Rows from q_start[n_seq] on belong to no sequence: draft_layer_read
+ *            and draft_layer_attend leave their outputs as they are, and what
+ *            draft_layer_append puts into their q_out is of no use.
  *   table    device, int32 [n_seq][max_pages]: page ids, page j of a sequence
  *            holding positions j*page .. j*page + page - 1.  Entries beyond a
  *            sequence's length are not used.  Positions from max_pages*page
@@ -157,7 +160,7 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
  * scaled by a power of two to its largest element (elements 2^-28 below it
  * lose bits), and a token's weight times its value scale is rounded once to 11
  * bits (to fewer below 2^-21 of the row's largest); the statistics stay in
- * fp32.  Rows of the batch that no sequence covers are not written.
+ * fp32.
  *   q  device, bf16, row r head h at q + r*ldq + h*D, 16-byte aligned, ldq a
  *      multiple of 8, at least hq*D
  *   workspace  16-byte aligned, of draft_layer_workspace_bytes() bytes

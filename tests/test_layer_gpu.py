@@ -750,3 +750,30 @@ def test_attend_large_heads_of_few_rows(dev, hkv, new, seqs, window):
     lens = [(new if i % 7 else 0, new + 3 + (95 * i) % 2500) for i in range(seqs)]
     lens[1] = (new, 5000)
     check_attend(Case(dev, lens, hkv * 2, hkv, 256, 64, seed=31 + hkv).upload(), window, 4 if window else 0)
+
+
+@pytest.mark.parametrize("lens", [[(9, 100), (1, 40)], [(80, 200)]])
+def test_rows_of_no_sequence_are_left_alone(dev, lens):
+    """A batch with more rows than its sequences have: the others' outputs stay as
+    they are, and the covered ones' are those of the batch without them."""
+    c = Case(dev, lens, 4, 2, 64, 32, seed=32).upload()
+    n, extra = c.rows, 50
+    want = L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch)
+    q = torch.cat([c.q, torch.full((extra, 4, 64), float("nan"), dtype=torch.bfloat16)]).to(dev)
+    out = torch.full((n + extra, 4, 64), 7.0, dtype=torch.bfloat16, device=dev)
+    lse = torch.full((n + extra, 4), 7.0, device=dev)
+    L.draft_layer_attend(q, *c.cache, *c.batch, out=out, lse=lse)
+    assert bool((out[n:] == 7).all()) and bool((lse[n:] == 7).all())
+    assert torch.allclose(out[:n].float(), want[0].float(), rtol=2.0 ** -7, atol=2.0 ** -8)     # perhaps in tiles of another height
+    assert torch.allclose(lse[:n], want[1], rtol=0, atol=2.0 ** -12)
+    read = L.draft_layer_read(*c.cache, *c.batch, n)
+    k, v = (torch.full((n + extra, 2, 64), 7.0, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    L.draft_layer_read(*c.cache, *c.batch, n + extra, k_out=k, v_out=v)
+    assert all(torch.equal(a[:n], b) and bool((a[n:] == 7).all()) for a, b in ((k, read[0]), (v, read[1])))
+    # append: the rows without a sequence write nothing to the cache
+    kk, vv = (torch.cat([bf16(c.rng, n, 2, 64), torch.full((extra, 2, 64), float("nan"), dtype=torch.bfloat16)]).to(dev) for _ in range(2))
+    rope = torch.from_numpy(L.draft_layer_rope_table(c.max_pages * 32, 64)).to(dev)
+    first = L.draft_layer_append(q[:n], kk[:n], vv[:n], rope, *c.cache, *c.batch)
+    kept = [t.clone() for t in c.cache]
+    both = L.draft_layer_append(q, kk, vv, rope, *c.upload().cache, *c.batch)
+    assert torch.equal(both[:n], first) and all(torch.equal(a, b) for a, b in zip(kept, c.cache))
