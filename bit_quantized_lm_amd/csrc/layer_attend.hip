@@ -38,7 +38,8 @@ struct AttendArgs {
 // fills the card:
 //   twice the target or more, or up to the target and short or much the same
 //     length, or a prompt whose first tiles see so much less than its last that
-//     those set the pace: a tile a workgroup, the longest first;
+//     those set the pace: a tile a workgroup, the sequences in the batch's order,
+//     in the shared kernel a sequence's tiles from the one that sees most;
 //   a quarter of the target or fewer: each tile cut into equal parts of about the
 //     same length for all, a part a workgroup;
 //   else the tiles' visible tokens, as groups of 32, are laid end to end and cut
@@ -50,6 +51,9 @@ struct AttendArgs {
 // tile a workgroup.  A windowed batch of equal lengths (32, 32): 54.6 us in runs,
 // 49.5 by tiles.  72 slots (7, 64): 34 us in runs, 29 in parts.  A prompt of 512
 // rows (20, 64): 34 us in runs, 23 by tiles; of 2,048 (80, 64): 94 in runs, 67.
+// From twice the target on the longest tile is not looked at: one sequence of
+// 131,072 tokens among 126 of 500 (8 kv heads) takes 82 us in runs, among 127 of
+// them 966, a workgroup a head walking it alone.
 constexpr int kMaxBlocks = 512;          // most workgroups that a plan takes to fill the card
 constexpr int kMaxSlots = 2 * (kMaxBlocks + DL_MAX_HEADS);
 // Pairs of a row and a part that a tile's joining holds in LDS: what bounds the
@@ -718,12 +722,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void attend_stream_kernel
 // places: while one is read, the next one's codes are converted into the other and
 // the one after that is on its way from memory in registers; one barrier a step.
 //
-// Bound by instruction issue, at the clock that the matrix cores leave: a prompt
-// of 4096 rows, 40 on 8 heads of 128, takes 190 to 200 us (860 to 900 TFLOP/s
-// against 1,240 for a large bf16 matrix product).  Per group and wave 32 matrix
-// instructions (512 cycles) and about 115 vector ones (650 cycles: four each, an
-// exponential sixteen), 38% of the matrix cycles with a vector instruction beside
-// them; with products and exponentials in blocks that was 19%, and 212 us.
+// A prompt of 4096 rows, 40 on 8 heads of 128, takes 190 to 200 us (860 to 900
+// TFLOP/s against 1,240 for a large bf16 matrix product).  Neither kind of unit is
+// full: of a SIMD's busy cycles 40% have a matrix instruction and about half a
+// vector one (per group and wave 32 matrix instructions, 512 cycles, and about 115
+// vector ones, 650 cycles: four each, an exponential sixteen), 38% of the matrix
+// cycles with a vector instruction beside them; with products and exponentials in
+// blocks that was 19%, and 212 us.  What is left is overlap.
 template <int D, int NQ, int W>
 struct Shared {
   static constexpr int R = 16 * NQ * W, F = D / 32, kThreads = 64 * W;
@@ -943,13 +948,16 @@ __global__ __launch_bounds__(64 * W, 2) void attend_shared_kernel(AttendArgs A) 
 }
 
 // ------------------------------------------------------------------- launch
-// The launch's kernel, by the rows that an average sequence has for one kv head,
-// and for few rows by the tiles: under 64 of them, which are split anyway, eight
+// The launch's kernel, by the rows that an average sequence has for one kv head
+// (those without rows count; one prompt of 2,048 rows and 63 single tokens over 6,000,
+// 225 us in tiles of 128, take 66 and 126 apart; one of 100 rows with them, 207 in
+// tiles of 16, 13 and 126), and for few rows by the tiles: under 64 of them, which are split anyway, eight
 // waves a workgroup leave half the parts to join (4 sequences of 8,000 tokens, 2 kv
 // heads: 13.8 us instead of 16.2; 16 of 4,000, 8 heads: 36 instead of 31.7 with
 // four); heads of 256 hold too many registers for it, and for two workgroups a CU:
 // split for the 256 that run at once, one sequence of 60,000 tokens and 2 kv heads
-// takes 40.5 us and 16 of 16,000 take 37.8; split for 512, 65.0 and 50.5.
+// takes 40.5 us and 16 of 16,000 take 37.8; split for 512, 65.0 and 50.5 (four of
+// 2,000 and 8 kv heads lose: 15.3 against 14.8).
 struct Plan {
   int rows;      // a tile's
   int waves;     // of the streaming kernel's workgroup; 0: attend_shared_kernel

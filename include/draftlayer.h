@@ -164,6 +164,13 @@ int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t
  *   q  device, bf16, row r head h at q + r*ldq + h*D, 16-byte aligned, ldq a
  *      multiple of 8, at least hq*D
  *   workspace  16-byte aligned, of draft_layer_workspace_bytes() bytes
+ * How the work is divided goes by the batch's averages (the results hold for any
+ * batch): rows a sequence, those without rows included, choose one kernel for the
+ * call, so long prompts and single tokens are faster in calls of their own (one of
+ * 2,048 rows and 63 single tokens over 6,000: 225 us together, 66 and 126 apart);
+ * and a batch of about 1024/hkv sequences of few rows and more (512/hkv at D =
+ * 256) does not split a long context among workgroups: one of 131,072 tokens among
+ * 127 of 500 and 8 kv heads takes 966 us, among 126 of them 82.
  * A row with an infinite or NaN element of q, or that sees a page whose key or
  * value scale is infinite or NaN, is NaN (out and lse), and no other row is.
  * Limits: scale finite and > 0, window >= 0, sinks >= 0.  Results hold for q
