@@ -241,7 +241,8 @@ def draft_layer_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: int, devi
     library keeps it at zero)."""
     import torch
     size = draft_layer_workspace_bytes(rows, n_seq, hq, hkv, d)
-    if size <= 16 << 20:     # a few rows' 8.5 MB: clearing all of it, 3 us on the GPU, hides behind the host's call (17.4 us, 18.8 with a view)
+    if size <= 16 << 20:
+        # few rows (8.5 MB): clearing all hides behind the host's call, 17.3 us, which a view of the counters makes 18.6
         return torch.zeros(size, dtype=torch.uint8, device=device)
     t = torch.empty(size, dtype=torch.uint8, device=device)
     t.narrow(0, 0, WORKSPACE_ZERO_BYTES).zero_()

@@ -139,10 +139,10 @@ int draft_layer_read(const uint8_t* k_codes, const uint8_t* v_codes, const float
 /*
  * Bytes of device workspace that draft_layer_attend needs at most for calls of
  * up to T rows of up to n_seq sequences with these heads: one size, asked for
- * the largest batch, serves them all.  Its first DL_WORKSPACE_ZERO_BYTES must be zero before its first
- * use, the rest may hold anything; the calls leave those bytes at zero, so one
- * workspace serves any number of calls in order (one stream), with other heads
- * too where it is large enough for them.
+ * the largest batch, serves them all.  Its first DL_WORKSPACE_ZERO_BYTES must
+ * be zero before its first use, the rest may hold anything; the calls leave those
+ * bytes at zero, so one workspace serves any number of calls in order (one
+ * stream), with other heads too where it is large enough for them.
  * Errors: DH_EINVAL (null pointer), DH_ESHAPE, DH_EUNSUP.
  */
 int draft_layer_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t* bytes);
