@@ -7,7 +7,9 @@ argmax token.  All per-call steps run in hand-written HIP kernels behind a
 C ABI (include/drafthead.h); `_binding` is a thin ctypes layer over it.  The
 draft layer's attention before the head (include/draftlayer.h: rotary append to
 an 8-bit paged cache, its reading back, attention over it) is in the same
-library, bound by `_layer`.
+library, bound by `_layer`, and so is what several branches of one context need
+(include/draftbranch.h: pages forked and drawn together, log probabilities),
+bound by `_branch`.
 
 Importing the package loads nothing native: the binding's names are resolved
 on first attribute access, and the native library is loaded on first call
@@ -24,7 +26,12 @@ _LAYER_NAMES = (
     "draft_layer_workspace_bytes", "draft_layer_workspace", "DraftCache",
 )
 
-__all__ = list(_BINDING_NAMES + _LAYER_NAMES)
+_BRANCH_NAMES = (
+    "draft_branch_fork", "draft_branch_compact", "draft_branch_pages_workspace_bytes", "draft_branch_pages_workspace",
+    "draft_branch_logprobs", "draft_branch_logprobs_workspace_bytes", "draft_branch_logprobs_workspace",
+)
+
+__all__ = list(_BINDING_NAMES + _LAYER_NAMES + _BRANCH_NAMES)
 
 
 def __getattr__(name):
@@ -32,6 +39,8 @@ def __getattr__(name):
         from . import _binding as home
     elif name in _LAYER_NAMES:
         from . import _layer as home
+    elif name in _BRANCH_NAMES:
+        from . import _branch as home
     else:
         raise AttributeError(name)
     value = globals()[name] = getattr(home, name)   # found here from now on

@@ -528,6 +528,17 @@ class DraftHead:
         return draft_head_forward_row(x, self.tiled, self.pairs, self.w, self.N, self.kcand, self.R, topk_only,
                                       out=out, row=row, workspace=workspace, stream=stream)
 
+    def logprobs(self, x, tokens=None, top=0, scale=1.0, scales=None, topk_only=False, stream=None, workspace=None):
+        """One call, the row, and the log probabilities of `tokens` (int32
+        [M][any], or None) with entropy and the `top` best alternatives
+        under it; returns the forward outputs with "row", "logprob", "top_id",
+        "top_logprob", "lse" and "entropy" added (draft_branch_logprobs)."""
+        from ._branch import draft_branch_logprobs
+        out = self.logits_row(x, topk_only=topk_only, stream=stream, workspace=workspace)
+        got = draft_branch_logprobs(out["row"], tokens, top=top, scale=scale, scales=scales, stream=stream)
+        out.update(zip(("logprob", "top_id", "top_logprob", "lse", "entropy"), got))
+        return out
+
     def logits_row_staged(self, x, topk_only=False, stream=None):
         """The same row from the fp32 coarse row: a forward with coarse_out,
         then draft_head_logits_row."""

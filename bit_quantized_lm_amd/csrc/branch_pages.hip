@@ -1,0 +1,471 @@
+// The pages of several branches on gfx950: the next batch's table from the
+// present one, and the pool drawn together (draft_branch_fork,
+// draft_branch_compact).
+//
+// All is decided on the device, since the lengths are there: the host knows
+// none of them, waits for nothing, and a call can be captured.  Free pages are
+// given out by rank (the r-th free page to the r-th entry that asks), which needs
+// two sums over everything before an entry: the entries that ask in the rows
+// before it, and the free pages below an id.  The first launch makes both, a
+// number a row and a number a chunk of 2,048 pages; in the second every workgroup
+// sums the few numbers before its own place, so no workgroup waits for another.
+#include <algorithm>
+
+#include "../../include/draftbranch.h"
+#include "layer.h"
+
+namespace {
+
+using namespace dl;
+
+constexpr int kThreads = 256;
+constexpr int kChunk = 2048;         // pages a count is made of: eight a thread
+constexpr int kSlice = 16 << 10;     // bytes of a page that a workgroup copies: four loads of 16 bytes a thread
+
+struct PoolArgs {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int n_pages, hkv, n_chunks;
+  int64_t page_bytes;   // of one page's keys, all heads
+  int slices;           // of a page's keys and values
+  const int32_t* uses;
+  const int32_t* table;
+  int32_t* uses_out;
+  int32_t* table_out;
+  int32_t* status;
+  int rows, wide;       // present table
+  int32_t* counts;      // [n_chunks] free pages (fork) or pages in use (compact)
+};
+
+struct ForkArgs {
+  PoolArgs p;
+  const int32_t *kv_len, *parents, *need;
+  int n_new, page_shift;
+  int32_t* asked;       // [n_new] free pages that a row takes
+};
+
+struct CompactArgs {
+  PoolArgs p;
+  int32_t *src, *dst;   // [n_pages / 2 + 1] the moves
+  int32_t* number;      // [n_pages] of a page that moves: which move
+};
+
+// ---------------------------------------------------------------- block sums
+// Sum over the workgroup of the threads before this one; `total` of all.
+__device__ __forceinline__ int block_before(int x, int& total, int* lds) {
+  const int wave = threadIdx.x >> 6, sum = wave_inclusive_sum(x);
+  if ((threadIdx.x & 63) == 63) lds[wave] = sum;
+  __syncthreads();
+  int before = sum - x;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    before += w < wave ? lds[w] : 0;
+    total += lds[w];
+  }
+  __syncthreads();
+  return before;
+}
+__device__ __forceinline__ int block_sum(int x, int* lds) {
+  int total;
+  block_before(x, total, lds);
+  return total;
+}
+
+// The thread's eight counts of uses from its chunk (pages past the pool: `none`).
+struct Eight {
+  int32_t u[8];
+};
+__device__ __forceinline__ Eight load_uses(const PoolArgs& A, int chunk, int none) {
+  Eight e;
+  const int first = chunk * kChunk + threadIdx.x * 8;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) e.u[i] = first + i < A.n_pages ? A.uses[first + i] : none;
+  return e;
+}
+
+// A chunk's part of the first launch: the copy of its counts, and how many of
+// its pages are free (or in use).
+template <bool kFree>
+__device__ __forceinline__ void survey_chunk(const PoolArgs& A, int chunk, int* lds) {
+  const Eight e = load_uses(A, chunk, kFree ? 1 : 0);
+  const int first = chunk * kChunk + threadIdx.x * 8;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if (first + i < A.n_pages) A.uses_out[first + i] = max(e.u[i], 0);
+    n += kFree ? e.u[i] <= 0 : e.u[i] > 0;
+  }
+  n = block_sum(n, lds);
+  if (threadIdx.x == 0) A.counts[chunk] = n;
+}
+
+// ---------------------------------------------------------------------- fork
+struct Row {
+  int parent, len, full, last;
+  bool eldest;              // the first row with its parent
+  const int32_t* old;       // the parent's entries
+};
+
+__device__ __forceinline__ Row row_of(const ForkArgs& A, int s) {
+  Row r;
+  const int p = A.parents[s], page = 1 << A.page_shift, cap = A.p.wide << A.page_shift;
+  const bool has = (unsigned)p < (unsigned)A.p.rows;
+  r.parent = has ? p : -1;
+  r.old = A.p.table + (size_t)(has ? p : 0) * A.p.wide;
+  r.len = has ? min(max(A.kv_len[p], 0), cap) : 0;
+  r.full = r.len >> A.page_shift;
+  r.last = (int)(((int64_t)min(max(A.need[s], r.len), cap) + page - 1) >> A.page_shift);
+  int before = 0;
+  for (int i = threadIdx.x; has && i < s; i += kThreads) before |= A.parents[i] == p;
+  r.eldest = !__syncthreads_or(before) && has;
+  return r;
+}
+
+// The page that the parent's entry j names, or -1.
+__device__ __forceinline__ int named(const ForkArgs& A, const Row& r, int j) {
+  if (r.parent < 0 || j >= A.p.wide) return -1;
+  const int id = r.old[j];
+  return (unsigned)id < (unsigned)A.p.n_pages ? id : -1;
+}
+__device__ __forceinline__ bool stays(const ForkArgs& A, const Row& r, int id) { return r.eldest && id >= 0 && A.p.uses[id] == 1; }
+
+__global__ __launch_bounds__(kThreads) void fork_survey_kernel(ForkArgs A) {
+  __shared__ int lds[kThreads / 64];
+  if ((int)blockIdx.x < A.p.n_chunks) {
+    survey_chunk<true>(A.p, blockIdx.x, lds);
+    if (blockIdx.x == 0 && threadIdx.x < 2) A.p.status[threadIdx.x] = 0;
+    return;
+  }
+  const int s = blockIdx.x - A.p.n_chunks;
+  const Row r = row_of(A, s);
+  int n = 0;
+  for (int j = r.full + threadIdx.x; j < r.last; j += kThreads) n += !stays(A, r, named(A, r, j));
+  n = block_sum(n, lds);
+  if (threadIdx.x == 0) A.asked[s] = n;
+}
+
+// The free pages of ranks rank .. rank + n - 1 (n at most kThreads) to list[0 ..
+// n - 1]: the chunks that hold them by the sums of the chunks' counts, then those
+// chunks' pages themselves.
+struct Finder {
+  int sums[kThreads / 64], start[kThreads], first, last, list[kThreads];
+};
+__device__ __forceinline__ void free_pages(const PoolArgs& A, int rank, int n, Finder& f) {
+  const int tid = threadIdx.x;
+  int at = 0;
+  for (int base = 0; base < A.n_chunks && at < rank + n; base += kThreads) {
+    const int c = base + tid < A.n_chunks ? A.counts[base + tid] : 0;
+    int total;
+    const int begin = at + block_before(c, total, f.sums);
+    f.start[tid] = begin;
+    if (tid == 0) f.first = kThreads, f.last = -1;
+    __syncthreads();
+    if (begin < rank + n && begin + c > rank) {
+      atomicMin(&f.first, tid);
+      atomicMax(&f.last, tid);
+    }
+    __syncthreads();
+    const int first = f.first, last = f.last;
+    for (int i = first; i <= last; ++i) {
+      const Eight e = load_uses(A, base + i, 1);
+      int mine = 0, all;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) mine += e.u[k] <= 0;
+      int r = f.start[i] + block_before(mine, all, f.sums) - rank;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (e.u[k] <= 0) {
+          if ((unsigned)r < (unsigned)n) f.list[r] = (base + i) * kChunk + tid * 8 + k;
+          ++r;
+        }
+    }
+    at += total;
+    __syncthreads();
+  }
+}
+
+// Part `slice` of page `from` over page `to`; scales with the first.
+__device__ __forceinline__ void copy_page(const PoolArgs& A, int from, int to, int slice) {
+  const int64_t units = A.page_bytes / 16, all = 2 * units;   // keys, then values
+  const int64_t a = all * slice / A.slices, b = all * (slice + 1) / A.slices;
+  auto at = [&](int page, int64_t u) {
+    return reinterpret_cast<u32x4*>((u < units ? A.k : A.v) + (size_t)page * A.page_bytes) + (u < units ? u : u - units);
+  };
+  for (int64_t u0 = a + threadIdx.x; u0 < b; u0 += 4 * kThreads) {
+    u32x4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (u0 + i * kThreads < b) x[i] = *at(from, u0 + i * kThreads);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (u0 + i * kThreads < b) *at(to, u0 + i * kThreads) = x[i];
+  }
+  if (slice == 0)
+    for (int h = threadIdx.x; h < A.hkv; h += kThreads) {
+      A.ks[(size_t)to * A.hkv + h] = A.ks[(size_t)from * A.hkv + h];
+      A.vs[(size_t)to * A.hkv + h] = A.vs[(size_t)from * A.hkv + h];
+    }
+}
+
+// Grid: n_new * slices workgroups for the new rows (the first of a row writes
+// its entries, all copy their part of its page), then one for each present row.
+__global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
+  __shared__ Finder f;
+  const int tid = threadIdx.x, made = A.n_new * A.p.slices;
+  const bool old_row = (int)blockIdx.x >= made;
+  const int s = old_row ? 0 : blockIdx.x / A.p.slices, slice = old_row ? 0 : blockIdx.x % A.p.slices;
+  Row r{};
+  int partial = -1;   // the page whose tokens have to be copied
+  if (old_row) {
+    const int p = blockIdx.x - made;
+    int has_heir = 0;
+    for (int i = tid; i < A.n_new; i += kThreads) has_heir |= A.parents[i] == p;
+    if (__syncthreads_or(has_heir)) return;
+    r.old = A.p.table + (size_t)p * A.p.wide;
+    r.parent = p;
+  } else {
+    r = row_of(A, s);
+    if (r.len & ((1 << A.page_shift) - 1)) {
+      partial = named(A, r, r.full);
+      if (stays(A, r, partial)) partial = -1;
+    }
+    if (slice > 0 && partial < 0) return;
+  }
+  // what is free, what is asked for, and by the rows before this one
+  int free = 0, asked = 0, before = 0;
+  for (int i = tid; i < A.p.n_chunks; i += kThreads) free += A.p.counts[i];
+  for (int i = tid; i < A.n_new; i += kThreads) {
+    const int n = A.asked[i];
+    asked += n;
+    before += i < s ? n : 0;
+  }
+  free = block_sum(free, f.sums);
+  asked = block_sum(asked, f.sums);
+  before = block_sum(before, f.sums);
+  const bool done = asked <= free;
+  if (blockIdx.x == 0 && tid == 0) {
+    atomicAdd(A.p.status, done ? free - asked : free);
+    A.p.status[1] = max(asked - free, 0);
+  }
+  int freed = 0;
+  auto give_up = [&](int id) { freed += atomicSub(A.p.uses_out + id, 1) == 1; };
+  if (old_row) {
+    if (done)
+      for (int j = tid; j < A.p.wide; j += kThreads)
+        if (const int id = named(A, r, j); id >= 0) give_up(id);
+  } else if (slice == 0) {
+    int rank = before;
+    for (int j0 = 0; j0 < A.p.wide; j0 += kThreads) {
+      const int j = j0 + tid, id = named(A, r, j);
+      const bool asks = j >= r.full && j < r.last, keeps = asks && stays(A, r, id), takes = asks && !keeps;
+      int entry = j < r.full || keeps ? id : -1, n = 0;
+      if (j0 < r.last && j0 + kThreads > r.full) {
+        const int at = block_before(takes && done, n, f.sums);
+        if (n > 0) {
+          free_pages(A.p, rank, n, f);
+          // an id is looked at before it is written through: counts that change meanwhile fault nothing
+          if (takes) entry = (unsigned)f.list[at] < (unsigned)A.p.n_pages ? f.list[at] : -1;
+          __syncthreads();
+        }
+        rank += n;
+      }
+      if (j >= A.p.wide) continue;
+      A.p.table_out[(size_t)s * A.p.wide + j] = done ? entry : -1;
+      if (!done) continue;
+      // the eldest takes over what its parent's entries counted for
+      if (entry >= 0 && (takes || !r.eldest)) atomicAdd(A.p.uses_out + entry, 1);
+      if (r.eldest && id >= 0 && j >= r.full && !keeps) give_up(id);
+    }
+  }
+  if (!old_row && partial >= 0 && done) {
+    free_pages(A.p, before, 1, f);
+    if ((unsigned)f.list[0] < (unsigned)A.p.n_pages) copy_page(A.p, partial, f.list[0], slice);
+  }
+  freed = wave_inclusive_sum(freed);
+  if ((tid & 63) == 63 && freed > 0) atomicAdd(A.p.status, freed);
+}
+
+// ------------------------------------------------------------------- compact
+__global__ __launch_bounds__(kThreads) void compact_survey_kernel(CompactArgs A) {
+  __shared__ int lds[kThreads / 64];
+  survey_chunk<false>(A.p, blockIdx.x, lds);
+}
+
+// Numbers the moves: page i in use behind the first `used` is move (pages in use
+// before it) - (those among the first `used`), a free one before them takes move
+// (free pages before it).
+__global__ __launch_bounds__(kThreads) void compact_number_kernel(CompactArgs A) {
+  __shared__ int lds[kThreads / 64];
+  const int tid = threadIdx.x, chunk = blockIdx.x;
+  int used = 0, before = 0;
+  for (int i = tid; i < A.p.n_chunks; i += kThreads) {
+    const int n = A.p.counts[i];
+    used += n;
+    before += i < chunk ? n : 0;
+  }
+  used = block_sum(used, lds);
+  before = block_sum(before, lds);
+  // pages in use among the first `used`: whole chunks, and a part of one
+  const int part = used / kChunk;
+  int front = 0;
+  for (int i = tid; i < part; i += kThreads) front += A.p.counts[i];
+  if (part < A.p.n_chunks) {
+    const Eight e = load_uses(A.p, part, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) front += e.u[i] > 0 && part * kChunk + tid * 8 + i < used;
+  }
+  front = block_sum(front, lds);
+  if (chunk == 0 && tid == 0) {
+    A.p.status[0] = used;
+    A.p.status[1] = used - front;
+  }
+  const Eight e = load_uses(A.p, chunk, 0);
+  int mine = 0, all;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mine += e.u[i] > 0;
+  int rank = before + block_before(mine, all, lds);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = chunk * kChunk + tid * 8 + k;
+    const bool taken = e.u[k] > 0;
+    if (taken && i >= used) {
+      A.src[rank - front] = i;
+      A.number[i] = rank - front;
+    } else if (!taken && i < used) {
+      A.dst[i - rank] = i;
+    }
+    rank += taken;
+  }
+}
+
+// Grid: `movers` workgroups that take turns at the moves' parts, then those for
+// the table's entries.
+__global__ __launch_bounds__(kThreads) void compact_move_kernel(CompactArgs A, int movers) {
+  const int tid = threadIdx.x, used = A.p.status[0], moves = A.p.status[1];
+  if ((int)blockIdx.x < movers) {
+    const int64_t parts = (int64_t)moves * A.p.slices;
+    for (int64_t i = blockIdx.x; i < parts; i += movers) {
+      const int m = (int)(i / A.p.slices), slice = (int)(i % A.p.slices), from = A.src[m], to = A.dst[m];
+      if ((unsigned)from >= (unsigned)A.p.n_pages || (unsigned)to >= (unsigned)A.p.n_pages) continue;
+      copy_page(A.p, from, to, slice);
+      if (slice == 0 && tid == 0) {
+        A.p.uses_out[to] = A.p.uses[from];
+        A.p.uses_out[from] = 0;
+      }
+    }
+    return;
+  }
+  const int64_t entries = (int64_t)A.p.rows * A.p.wide;
+  for (int64_t i = (int64_t)(blockIdx.x - movers) * kThreads + tid; i < entries; i += (int64_t)(gridDim.x - movers) * kThreads) {
+    int id = A.p.table[i];
+    if (id >= used && id < A.p.n_pages && A.p.uses[id] > 0) id = A.dst[A.number[id]];
+    A.p.table_out[i] = id;
+  }
+}
+
+// -------------------------------------------------------------------- checks
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+int chunks_of(int n_pages) { return (n_pages + kChunk - 1) / kChunk; }
+size_t counts_bytes(int n_pages) { return rounded((size_t)chunks_of(n_pages) * 4); }
+size_t moves_bytes(int n_pages) { return rounded(((size_t)n_pages / 2 + 1) * 4); }
+size_t fork_bytes(int n_pages, int n_new) { return counts_bytes(n_pages) + (size_t)n_new * 4; }
+size_t compact_bytes(int n_pages) { return counts_bytes(n_pages) + 2 * moves_bytes(n_pages) + (size_t)n_pages * 4; }
+
+bool overlap(const void* a, size_t n, const void* b, size_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + m && y < x + n;
+}
+
+int check_pool(const char* who, int n_pages, int rows, const char* rows_name) {
+  if (n_pages < 1 || n_pages > DB_MAX_PAGES)
+    return dh::fail(DH_ESHAPE, "%s: n_pages must be in 1..%d (got %d)", who, DB_MAX_PAGES, n_pages);
+  if (rows < 1 || rows > DL_MAX_SEQS) return dh::fail(DH_ESHAPE, "%s: %s must be in 1..%d (got %d)", who, rows_name, DL_MAX_SEQS, rows);
+  return DH_OK;
+}
+
+// What fork and compact have in common; `made` is the new table's rows.
+int check_pages(const char* who, PoolArgs& A, int page, int D, int made, const char* rows_name, void* workspace, size_t given, size_t need) {
+  int rc = check_heads(who, A.hkv, A.hkv, D);
+  if (rc) return rc;
+  if ((rc = check_pool(who, A.n_pages, A.rows, rows_name))) return rc;
+  // the table stands in for the row starts and lengths, which these calls do not have
+  const Batch b{A.table, A.table, A.table, A.rows, A.wide, 0};
+  if ((rc = check_cache(who, Cache{A.k, A.v, A.ks, A.vs, A.n_pages, page_shift_of(page), A.hkv}, page, b))) return rc;
+  if (!A.uses || !A.uses_out || !A.table_out || !A.status) return dh::fail(DH_EINVAL, "%s: null pointer", who);
+  if (!aligned(A.uses, 4) || !aligned(A.uses_out, 4) || !aligned(A.table_out, 4) || !aligned(A.status, 4))
+    return dh::fail(DH_EINVAL, "%s: counts, tables and status must be 4-byte aligned", who);
+  const size_t counts = (size_t)A.n_pages * 4, old = (size_t)A.rows * A.wide * 4, made_bytes = (size_t)made * A.wide * 4;
+  const struct { const void* p; size_t n; } in[] = {{A.uses, counts}, {A.table, old}}, out[] = {{A.uses_out, counts}, {A.table_out, made_bytes}, {A.status, 8}};
+  for (const auto& o : out)
+    for (const auto& i : in)
+      if (overlap(o.p, o.n, i.p, i.n)) return dh::fail(DH_EINVAL, "%s: the new counts, table and status must not overlap the present ones", who);
+  if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "%s: workspace must be a 16-byte aligned pointer", who);
+  if (given < need) return dh::fail(DH_EINVAL, "%s: workspace of %zu bytes is below the %zu needed", who, given, need);
+  A.n_chunks = chunks_of(A.n_pages);
+  A.page_bytes = (int64_t)A.hkv * page * D;
+  A.slices = (int)std::min<int64_t>(std::max<int64_t>(2 * A.page_bytes / kSlice, 1), 128);
+  A.counts = static_cast<int32_t*>(workspace);
+  return DH_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int draft_branch_pages_workspace_bytes(int n_pages, int n_new, size_t* bytes) {
+  if (!bytes) return dh::fail(DH_EINVAL, "pages_workspace_bytes: null pointer");
+  const int rc = check_pool("pages_workspace_bytes", n_pages, n_new, "n_new");
+  if (rc) return rc;
+  *bytes = std::max(fork_bytes(n_pages, n_new), compact_bytes(n_pages));
+  return dh::ok();
+}
+
+int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page, int hkv,
+                      int D, const int32_t* uses, const int32_t* table, const int32_t* kv_len, int n_seq,
+                      const int32_t* parents, const int32_t* need, int n_new, int max_pages, int32_t* uses_out,
+                      int32_t* table_out, int32_t* status, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* who = "fork";
+  ForkArgs A{};
+  A.p = PoolArgs{k_codes, v_codes, k_scale, v_scale, n_pages, hkv, 0, 0, 0, uses, table, uses_out, table_out, status, n_seq, max_pages, nullptr};
+  int rc = check_pool(who, n_pages, n_new, "n_new");
+  if (rc) return rc;
+  if ((rc = check_pages(who, A.p, page, D, n_new, "n_seq", workspace, workspace_bytes, fork_bytes(n_pages, n_new)))) return rc;
+  if (!kv_len || !parents || !need) return dh::fail(DH_EINVAL, "fork: null pointer");
+  if (!aligned(kv_len, 4) || !aligned(parents, 4) || !aligned(need, 4))
+    return dh::fail(DH_EINVAL, "fork: kv_len, parents and need must be 4-byte aligned");
+  A.kv_len = kv_len;
+  A.parents = parents;
+  A.need = need;
+  A.n_new = n_new;
+  A.page_shift = page_shift_of(page);
+  A.asked = A.p.counts + counts_bytes(n_pages) / 4;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(fork_survey_kernel, dim3(A.p.n_chunks + n_new), dim3(kThreads), 0, st, A);
+  hipLaunchKernelGGL(fork_kernel, dim3(n_new * A.p.slices + n_seq), dim3(kThreads), 0, st, A);
+  return launched("fork_kernel");
+}
+
+int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page,
+                         int hkv, int D, const int32_t* uses, const int32_t* table, int n_rows, int max_pages,
+                         int32_t* uses_out, int32_t* table_out, int32_t* status, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  const char* who = "compact";
+  CompactArgs A{};
+  A.p = PoolArgs{k_codes, v_codes, k_scale, v_scale, n_pages, hkv, 0, 0, 0, uses, table, uses_out, table_out, status, n_rows, max_pages, nullptr};
+  const int rc = check_pages(who, A.p, page, D, n_rows, "n_rows", workspace, workspace_bytes, compact_bytes(n_pages));
+  if (rc) return rc;
+  A.src = A.p.counts + counts_bytes(n_pages) / 4;
+  A.dst = A.src + moves_bytes(n_pages) / 4;
+  A.number = A.dst + moves_bytes(n_pages) / 4;
+  const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  hipLaunchKernelGGL(compact_survey_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
+  hipLaunchKernelGGL(compact_number_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
+  // eight workgroups a CU, or a move at most for every second page
+  const int movers = (int)std::min<int64_t>(2048, std::max<int64_t>((int64_t)(n_pages / 2) * A.p.slices, 1));
+  const int entries = (int)std::min<int64_t>(256, ((int64_t)n_rows * max_pages + kThreads - 1) / kThreads);
+  hipLaunchKernelGGL(compact_move_kernel, dim3(movers + entries), dim3(kThreads), 0, st, A, movers);
+  return launched("compact_move_kernel");
+}
+
+}  // extern "C"

@@ -1,0 +1,154 @@
+/*
+ * draftbranch.h -- C ABI for several branches of one context (drafts, samples,
+ * beams) on MI355X (gfx950), in the same library as the draft head
+ * (drafthead.h) and the draft layer's attention (draftlayer.h).
+ *
+ * Branches share the pages of what they have in common.  Between two steps the
+ * next batch's page table is made from the present one (draft_branch_fork): a
+ * sequence goes on as one branch, as several or as none, full pages are shared,
+ * a partly filled one is copied, pages for the coming tokens are taken.  What
+ * the head says of their tokens is scored (draft_branch_logprobs).  A pool that
+ * has become sparse is drawn together (draft_branch_compact).
+ *
+ * The conventions are drafthead.h's: DH_OK or a negative DH_E* code, nothing
+ * thrown, every argument checked before any HIP call, the caller owns every
+ * buffer, device functions enqueue on `stream` and return without waiting,
+ * draft_head_last_error() describes the last error of the calling thread.  The
+ * cache and a batch are draftlayer.h's.
+ *
+ * The pages' counts: uses, device int32 [n_pages], says how many table entries
+ * name each page (and holds one more for whatever else the caller keeps a page
+ * for); a page with none is free, a count below 0 is taken as 0 and left as 0.
+ * A table entry outside 0 .. n_pages - 1 names no page.  No input is written
+ * except the pages of the pool that are said to be: both functions leave the new
+ * table and counts in buffers of their own, so a call can be repeated, and the
+ * caller then goes on with the new ones.
+ *
+ * Workspaces of this header need no initial contents and hold nothing between
+ * calls; calls that share one must be ordered (one stream).
+ */
+#ifndef DRAFTBRANCH_H
+#define DRAFTBRANCH_H
+
+#include "draftlayer.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define DB_MAX_PAGES (1 << 24)
+#define DB_MAX_TOP 64
+#define DB_MAX_TOKENS 64
+#define DB_MAX_VOCAB (1 << 24)
+#define DB_BF16 0
+#define DB_FP32 1
+
+/*
+ * Bytes of device workspace for draft_branch_fork (to at most n_new rows) and
+ * draft_branch_compact over a pool of n_pages: one size serves both, and every
+ * smaller pool and batch.
+ * Errors: DH_EINVAL (null pointer), DH_ESHAPE.
+ */
+int draft_branch_pages_workspace_bytes(int n_pages, int n_new, size_t* bytes);
+
+/*
+ * DEVICE.  The next batch's page table from the present one.  Row s of the new
+ * table goes on from the present sequence p = parents[s] with its len =
+ * kv_len[p] tokens (0 .. max_pages*page); a parent outside 0 .. n_seq - 1 is
+ * none: the row starts empty (len = 0).  It gets pages for `need[s]` positions
+ * (at least len, at most max_pages*page).  With full = len / page and last =
+ * ceil(max(need, len) / page), entry j of row s is
+ *   j < full           the parent's entry, shared (-1 where that names no page)
+ *   full <= j < last   the parent's entry, where it names a page that nothing
+ *                      else names (uses = 1) and s is the first row with this
+ *                      parent; else a free page
+ *   j >= last          -1
+ * The free pages are those with uses = 0 before the call (a page that the call
+ * frees is free from the next call on); the lowest ids come first, to entries in
+ * the order of (s, j).  Where tokens stand in the parent's page j = full (len no
+ * multiple of page) and a free page takes its place, codes and scales of the
+ * whole page are copied.  The counts give up every entry of the present table
+ * and take on every entry of the new one: a present sequence that no row goes on
+ * from is freed.
+ * If fewer pages are free than asked for, nothing is done: no page is written,
+ * uses_out is uses, and table_out is -1 throughout.
+ *   k_codes .. v_scale  the pool, whose free pages take the copies
+ *   table      int32 [n_seq][max_pages], kv_len int32 [n_seq]
+ *   parents, need  int32 [n_new]
+ *   uses_out   out, int32 [n_pages];  table_out  out, int32 [n_new][max_pages];
+ *              neither may overlap uses or table
+ *   status     out, int32 [2]: free pages after the call; pages that were lacking
+ * Limits: 1 <= n_seq, n_new <= DL_MAX_SEQS, n_pages <= DB_MAX_PAGES, D, page,
+ * heads and max_pages as in draftlayer.h.
+ * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
+ */
+int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page, int hkv,
+                      int D, const int32_t* uses, const int32_t* table, const int32_t* kv_len, int n_seq,
+                      const int32_t* parents, const int32_t* need, int n_new, int max_pages, int32_t* uses_out,
+                      int32_t* table_out, int32_t* status, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * DEVICE.  Moves the pages in use (uses > 0) to the front of the pool: with
+ * `used` of them, the k-th page in use at or behind `used` (in ascending order)
+ * goes to the k-th free page before it, codes, scales and count.  The places
+ * that pages leave keep their codes and have the count 0; pages from `used` on
+ * are free then.  Entries of `table` that name a moved page name its new place,
+ * all others stay as they are; it has to hold every row that names a page of
+ * the pool, n_rows of them with max_pages entries each.
+ *   uses_out  out, int32 [n_pages];  table_out  out, int32 [n_rows][max_pages];
+ *             neither may overlap uses or table
+ *   status    out, int32 [2]: pages in use; pages moved
+ * Limits: as draft_branch_fork's, n_rows in 1..DL_MAX_SEQS.
+ * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
+ */
+int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page,
+                         int hkv, int D, const int32_t* uses, const int32_t* table, int n_rows, int max_pages,
+                         int32_t* uses_out, int32_t* table_out, int32_t* status, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of device workspace for draft_branch_logprobs' calls of up to M rows of
+ * up to N logits with up to `top` alternatives.
+ * Errors: DH_EINVAL (null pointer), DH_ESHAPE, DH_EUNSUP.
+ */
+int draft_branch_logprobs_workspace_bytes(int M, int N, int top, size_t* bytes);
+
+/*
+ * DEVICE.  Log probabilities under the softmax of rows of logits, such as
+ * draft_head_forward_row's bf16 rows or draft_head_coarse's fp32 ones.  With
+ * z_j = f x_j, f = scale * (scales ? scales[m] : 1), of row m:
+ *   lse         = ln sum_j exp(z_j)
+ *   logprob[t]  = z_tok - lse for each of the row's n_tok given tokens; -inf for
+ *                 a token outside 0 .. N - 1 (another shard's)
+ *   entropy     = sum_j p_j (lse - z_j), p_j = exp(z_j - lse)
+ *   top_id, top_logprob  the `top` largest x_j of those above -inf, the larger
+ *                 first, of equal ones the lower id first, and their log
+ *                 probabilities; id -1 and -inf where the row has no more
+ * A row without an element above -inf gets lse, logprob and top_logprob -inf,
+ * entropy 0 and ids -1.  A row with a NaN or +inf element, or whose f is not
+ * finite and > 0, gets NaN in lse, logprob, entropy and top_logprob, and ids -1.
+ * The shards of one vocabulary join by their lse: with L = ln sum_r exp(lse_r),
+ * log probabilities fall by L - lse_r, and the entropy is
+ * L - sum_r exp(lse_r - L) (lse_r - entropy_r).
+ * Sums are fp32 under the running maximum; x is taken as it is, differences to
+ * the maximum are rounded once, so rows at the type's lowest value are rows too.
+ *   logits    device, bf16 (type DB_BF16) or fp32 (DB_FP32), row m at logits +
+ *             m*ld elements, ld >= N; aligned to its element alone
+ *   scales    device, fp32 [M], or NULL
+ *   tokens    device, int32 [M][n_tok]; n_tok = 0: tokens and logprob unused
+ *   logprob fp32 [M][n_tok], lse and entropy fp32 [M], top_id int32 [M][top],
+ *             top_logprob fp32 [M][top]: out; top = 0: the last two unused
+ *   workspace 16-byte aligned; may be NULL where the size asked for is 0
+ * Limits: 0 <= M <= DL_MAX_ROWS (M = 0 does nothing), 1 <= N <= DB_MAX_VOCAB,
+ * 0 <= top <= DB_MAX_TOP, 0 <= n_tok <= DB_MAX_TOKENS, scale finite and > 0.
+ * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
+ */
+int draft_branch_logprobs(const void* logits, int type, int64_t ld, int M, int N, float scale, const float* scales,
+                          const int32_t* tokens, int n_tok, int top, float* logprob, float* lse, float* entropy,
+                          int32_t* top_id, float* top_logprob, void* workspace, size_t workspace_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* DRAFTBRANCH_H */

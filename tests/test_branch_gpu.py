@@ -1,0 +1,414 @@
+"""The operators on several branches on the GPU against the oracle.
+
+Pages are moved, not computed: tables, counts and every byte of the pool are
+compared as they are.
+
+Log probabilities, from the arithmetic (u = 2^-24, one fp32 rounding; d = z - max z
+of an element, E the mean under the row's probabilities):
+  exponent       f log2(e) is two roundings (its constant's and the product's), x - max
+                 one, their product one: 4 u |d|
+  weight         that, and 2^-22 for the exponential
+  sums           of positive terms, each through at most N/2048 + 8 additions a lane, 8 over
+                 the lanes, 3 over the waves and one a part (each joining rounds its weight
+                 too): A = (N/2048 + 3 * (20 + parts)) u relative, beside the weights' own
+  lse            4 u E|d| + 2^-22 + A, u |f max| for f max, and u |lse|, 2 u ln(sum) for the logarithm
+  logprob        3 u |d_token| and lse's without f max
+  entropy        ln(sum)'s as lse's; s/l: (2^-22 + A) E|d| twice (s and l), 4 u E d^2 and 8 u E|d|
+"""
+import numpy as np
+import pytest
+
+from bit_quantized_lm_amd import _binding as B
+from bit_quantized_lm_amd import _branch as R
+from bit_quantized_lm_amd import _layer as L
+from oracle import branch as O
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU visible")
+    B.load_library()
+    return torch.device("cuda:0")
+
+
+def ints(x, dev):
+    return torch.from_numpy(np.ascontiguousarray(x, np.int32)).to(dev)
+
+
+# --------------------------------------------------------------------- pages
+class Pool:
+    """A pool of random contents, some of it in use by the sequences of a table."""
+
+    def __init__(self, dev, lens, n_pages, hkv, d, page, seed, reserve=0, shared=0, wide=None):
+        """shared: every second sequence has that many full pages from the one before it."""
+        rng = self.rng = np.random.default_rng(seed)
+        self.dev, self.page, self.n_pages = dev, page, n_pages
+        self.kv_len = np.array(lens, np.int32)
+        held = [-(-(n + reserve) // page) for n in lens]
+        self.wide = wide or max(max(held), 1) + 1
+        self.table = np.full((len(lens), self.wide), -1, np.int32)
+        order, at = rng.permutation(n_pages), 0
+        for s, n in enumerate(held):
+            k = min(shared, lens[s] // page, lens[s - 1] // page) if s % 2 else 0
+            self.table[s, :k] = self.table[s - 1, :k]
+            self.table[s, k:n] = order[at:at + n - k]
+            at += n - k
+        self.uses = np.bincount(self.table[self.table >= 0], minlength=n_pages).astype(np.int32)
+        g = torch.Generator(device=dev).manual_seed(seed)
+        shape = (n_pages, hkv, page, d)
+        self.cache = [torch.randint(0, 256, shape, dtype=torch.uint8, generator=g, device=dev) for _ in range(2)]
+        self.cache += [torch.rand(shape[:2], generator=g, device=dev) for _ in range(2)]
+
+    def fork(self, parents, need, **kw):
+        before = [t.clone() for t in self.cache]
+        got = R.draft_branch_fork(*self.cache, ints(self.uses, self.dev), ints(self.table, self.dev), ints(self.kv_len, self.dev),
+                                  ints(parents, self.dev), ints(need, self.dev), **kw)
+        torch.cuda.synchronize()
+        table, uses, status, copies = O.fork(self.uses, self.table, self.kv_len, parents, need, self.page)
+        assert np.array_equal(got[2].cpu().numpy(), status)
+        assert np.array_equal(got[1].cpu().numpy(), uses) and np.array_equal(got[0].cpu().numpy(), table)
+        self.moved(before, copies)
+        return table, uses, status, copies
+
+    def compact(self, **kw):
+        before = [t.clone() for t in self.cache]
+        got = R.draft_branch_compact(*self.cache, ints(self.uses, self.dev), ints(self.table, self.dev), **kw)
+        torch.cuda.synchronize()
+        table, uses, status, moves = O.compact(self.uses, self.table)
+        assert np.array_equal(got[2].cpu().numpy(), status)
+        assert np.array_equal(got[1].cpu().numpy(), uses) and np.array_equal(got[0].cpu().numpy(), table)
+        self.moved(before, moves)
+        return table, uses, status, moves
+
+    def moved(self, before, moves):
+        for was, now in zip(before, self.cache):
+            for a, b in moves:
+                was[b].copy_(was[a])
+            assert torch.equal(was, now)
+
+
+FORKS = [
+    # lens, new rows' parents, tokens more, pages, hkv, d, page, reserve, shared
+    ([1], [0], 1, 3, 1, 64, 32, 0, 0),
+    ([33], [0, 0, 0], 9, 20, 8, 128, 64, 9, 0),
+    ([100, 64, 7], [0, 0, 1, 1, 2], 1, 30, 2, 128, 64, 1, 0),            # one ends on a page's last token
+    ([100, 64, 7], [2, -1, 0, 2, 99, 0], 40, 60, 3, 64, 32, 0, 0),       # none, in no order, outside
+    ([500, 500, 300], [1, 1], 5, 80, 2, 256, 32, 16, 7),                 # two end; pages shared with one that does not go on
+    ([0, 5], [0, 1, 0], 0, 6, 1, 64, 32, 0, 0),                          # an empty sequence; nothing needed
+    ([256 * 3 + 1] * 5, [4, 3, 2, 1, 0, 0, 1], 300, 60, 1, 256, 256, 255, 2),
+    ([31 * (i % 9) + 1 for i in range(90)], [i // 3 for i in range(200)], 12, 2500, 1, 64, 32, 6, 1),
+]
+
+
+@pytest.mark.parametrize("lens,parents,more,n_pages,hkv,d,page,reserve,shared", FORKS)
+def test_fork(dev, lens, parents, more, n_pages, hkv, d, page, reserve, shared):
+    p = Pool(dev, lens, n_pages, hkv, d, page, seed=len(parents) + d, reserve=reserve, shared=shared, wide=max(lens) // page + more // page + 4)
+    need = [lens[q] + more if 0 <= q < len(lens) else more + 3 for q in parents]
+    _, _, status, _ = p.fork(parents, need)
+    assert status[1] == 0
+    p.fork(parents, need, workspace=torch.full((R.draft_branch_pages_workspace_bytes(n_pages, len(parents)),), 255, dtype=torch.uint8, device=dev))
+
+
+def test_fork_long_rows(dev):
+    """Rows of more entries than a workgroup has threads, all fresh, kept or shared, over several chunks of counts."""
+    p = Pool(dev, [32 * 700 + 5, 40], 6100, 1, 64, 32, seed=3, reserve=32 * 400, wide=1500)
+    _, _, status, copies = p.fork([0, 0, -1, 1], [32 * 1400, 32 * 1100, 32 * 1500, 32 * 600])
+    assert status[1] == 0 and len(copies) == 1
+
+
+def test_fork_many_rows(dev):
+    """As many rows as a table may have."""
+    rng = np.random.default_rng(4)
+    lens = [int(n) for n in rng.integers(0, 90, 4096)]
+    p = Pool(dev, lens, 30000, 1, 64, 32, seed=4, reserve=3, wide=5)
+    parents = rng.integers(-1, 4096, 4096)
+    _, _, status, copies = p.fork(parents, [lens[q] + 4 if q >= 0 else 20 for q in parents])
+    assert status[1] == 0 and len(copies) > 500
+
+
+def test_fork_lacking_pages_does_nothing(dev):
+    p = Pool(dev, [100, 40], 9, 2, 64, 32, seed=5, reserve=1)
+    table, uses, status, copies = p.fork([0, 0, 1, 1], [130, 130, 60, 60])
+    assert status[1] == 1 and status[0] == 3 and not copies and (table == -1).all() and np.array_equal(uses, p.uses)
+    p.fork([0, 1, 1], [104, 60, 60])       # what is left suffices for this
+
+
+def test_fork_odd_numbers(dev):
+    """Lengths, needs, ids and counts that no caller should have: taken as the header says."""
+    p = Pool(dev, [100, 64, 90, 20], 60, 1, 64, 32, seed=6, wide=5)
+    p.kv_len[:] = [-5, 1 << 30, 90, 20]
+    p.table[1, 2:] = [-7, 60, 1 << 30]     # no page
+    p.table[2, 2] = -1                     # the partial page is missing
+    p.uses[p.table[3, 0]] = 3              # something else keeps it
+    p.uses[p.uses == 0] = np.where(np.arange((p.uses == 0).sum()) % 3 == 0, -2, 0)
+    p.fork([0, 1, 2, 2, 3, 3, 4, -(1 << 31), (1 << 31) - 1], [-9, 1 << 30, 95, 0, 21, 200, 33, -1, (1 << 31) - 1])
+
+
+def test_fork_keeps_no_page_that_is_shared(dev):
+    """A page that a sequence has from another is copied before it is written, for its first row too."""
+    p = Pool(dev, [64, 64], 12, 1, 64, 32, seed=7, shared=2)
+    p.kv_len[:] = [40, 64]                 # the first went back behind what the second has from it
+    _, _, _, copies = p.fork([0, 1], [60, 70])
+    assert [a for a, _ in copies] == [p.table[0, 1]]
+
+
+@pytest.mark.parametrize("n_pages,hkv,d,page,lens", [
+    (1, 1, 64, 32, [1]), (7, 1, 64, 32, [5, 60]), (60, 3, 128, 64, [500, 64, 1, 700]), (60, 2, 256, 256, [1000, 2000, 30]),
+    (2048, 1, 64, 32, [100 * i for i in range(20)]), (5000, 1, 64, 32, [2000 + 300 * (i % 7) for i in range(40)])])
+def test_compact(dev, n_pages, hkv, d, page, lens):
+    p = Pool(dev, lens, n_pages, hkv, d, page, seed=n_pages, shared=1)
+    table, uses, status, moves = p.compact()
+    assert (uses[:status[0]] > 0).all() and not uses[status[0]:].any()
+    # drawn together already: nothing moves
+    p.uses, p.table = uses, table
+    assert not p.compact()[3]
+
+
+def test_compact_all_or_none_in_use(dev):
+    p = Pool(dev, [100], 30, 1, 64, 32, seed=8, wide=30)
+    p.uses[:] = 1
+    assert not p.compact()[3]
+    p.uses[:] = 0
+    assert not p.compact()[3]
+    p.uses[:15], p.uses[15:] = -1, 2
+    assert len(p.compact()[3]) == 15
+    p.table[0, :3] = [-9, 30, 1 << 30]     # no page: left as they are
+    p.compact()
+
+
+def test_pages_of_a_large_pool(dev):
+    """More chunks of counts than a workgroup has threads."""
+    n = 2048 * 260 + 3
+    p = Pool(dev, [40], 8, 1, 64, 32, seed=9, wide=8)
+    cache = [torch.zeros((n, 1, 32, 64), dtype=torch.uint8, device=dev) for _ in range(2)]
+    cache += [torch.zeros((n, 1), dtype=torch.float32, device=dev) for _ in range(2)]
+    uses = (p.rng.random(n) < 0.6).astype(np.int32)
+    uses[:2048 * 258] = 1                  # the free ones stand at the end
+    used = np.nonzero(uses)[0]
+    table = used[p.rng.integers(0, len(used), (3, 50))].astype(np.int32)
+    kv_len = np.array([40 * 32 + 3, 20, 0], np.int32)
+    args = (ints(uses, dev), ints(table, dev))
+    cache[0][torch.from_numpy(table[0, 40:41]).long().to(dev)] = 7
+    got = R.draft_branch_fork(*cache, *args, ints(kv_len, dev), ints([0, 0, -1], dev), ints([1400, 1500, 64], dev))
+    want = O.fork(uses, table, kv_len, [0, 0, -1], [1400, 1500, 64], 32)
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+    assert want[3] and all(bool((cache[0][b] == 7).all()) for _, b in want[3])
+    got = R.draft_branch_compact(*cache, *args)
+    want = O.compact(uses, table)
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want)) and len(want[3]) > 500
+
+
+def test_pages_refuse_overlaps(dev):
+    p = Pool(dev, [40, 70], 20, 1, 64, 32, seed=10)
+    uses, table = ints(p.uses, dev), ints(p.table, dev)
+    two = ints([0, 1], dev)
+    with pytest.raises(ValueError):
+        R.draft_branch_fork(*p.cache, uses, table, ints(p.kv_len, dev), two, two, uses_out=uses)
+    with pytest.raises(ValueError):
+        R.draft_branch_fork(*p.cache, uses, table, ints(p.kv_len, dev), two, two, table_out=table)
+    with pytest.raises(ValueError):
+        R.draft_branch_compact(*p.cache, uses, table, table_out=table)
+    with pytest.raises(ValueError):
+        R.draft_branch_fork(*p.cache, uses, table, ints(p.kv_len, dev), two, ints([1], dev))
+    with pytest.raises(ValueError):
+        R.draft_branch_fork(*p.cache, uses, table.long(), ints(p.kv_len, dev), two, two)
+
+
+def test_pages_on_another_stream_and_in_a_graph(dev):
+    p = Pool(dev, [100, 500, 64, 7], 90, 2, 128, 32, seed=11, reserve=5)
+    parents, need = [0, 1, 1, 2, 3, 3], [110, 530, 520, 70, 40, 40]
+    args = [ints(x, dev) for x in (p.uses, p.table, p.kv_len, parents, need)]
+    want = O.fork(p.uses, p.table, p.kv_len, parents, need, 32)
+    packed = O.compact(p.uses, p.table)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = R.draft_branch_fork(*p.cache, *args, stream=side)
+    side.synchronize()
+    assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+    ws = R.draft_branch_pages_workspace(90, 6, dev)
+    outs = [torch.empty_like(t) for t in got]
+    more = [torch.empty_like(args[1]), torch.empty_like(args[0]), torch.empty_like(outs[2])]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        R.draft_branch_fork(*p.cache, *args, table_out=outs[0], uses_out=outs[1], status=outs[2], workspace=ws)
+        R.draft_branch_compact(*p.cache, args[0], args[1], table_out=more[0], uses_out=more[1], status=more[2], workspace=ws)
+    for i in range(3):
+        for t in outs + more:
+            t.fill_(77)
+        ws.fill_(i)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(outs, want))
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(more, packed))
+
+
+# ---------------------------------------------------------- log probabilities
+def rows_of(rng, m, n, kind):
+    x = rng.standard_normal((m, n)).astype(np.float32) * 2
+    if kind == "kept":
+        x[rng.random((m, n)) > min(1.0, 30.0 / n)] = -np.inf
+    elif kind == "equal":
+        x[:] = 0.25
+    elif kind == "few values":
+        x = np.rint(x)
+    elif kind == "rising":
+        x = np.sort(x, axis=1)
+    elif kind == "falling":
+        x = -np.sort(x, axis=1)
+    elif kind == "peaked":
+        x[np.arange(m), rng.integers(0, n, m)] = 40.0
+    elif kind == "far":
+        x = x * 60 - 5000
+    elif kind == "lowest":
+        x[:, ::3] = -3.3895313892515355e38      # bf16's lowest
+    return x
+
+
+def check_logprobs(dev, x, tokens, top, scale=1.0, scales=None, gap=0, dtype=None, **kw):
+    m, n = x.shape
+    dtype = dtype or torch.bfloat16
+    wide = torch.full((m, n + gap), 99.0, dtype=dtype, device=dev)
+    wide[:, :n] = torch.from_numpy(np.ascontiguousarray(x)).to(dtype).to(dev)
+    x = wide[:, :n].float().cpu().numpy()
+    given = None if scales is None else torch.from_numpy(np.asarray(scales, np.float32)).to(dev)
+    got = R.draft_branch_logprobs(wide[:, :n], ints(tokens, dev), top=top, scale=scale, scales=given, **kw)
+    torch.cuda.synchronize()
+    factor = np.full(m, np.float32(scale)) * (np.ones(m, np.float32) if scales is None else np.asarray(scales, np.float32))
+    want = O.logprobs(x, tokens, top, factor)
+    logprob, top_id, top_logprob, lse, entropy = (t.cpu().numpy() for t in got)
+    assert np.array_equal(top_id, want["top_id"])
+    for name, t in (("logprob", logprob), ("top_logprob", top_logprob), ("lse", lse), ("entropy", entropy)):
+        w = want[name]
+        assert np.array_equal(np.isnan(t), np.isnan(w)) and np.array_equal(np.isneginf(t), np.isneginf(w)), name
+    A = (n / 2048 + 3 * (20 + 256)) * U
+    far, far2, peak = want["far"], want["far2"], want["max"]
+    with np.errstate(invalid="ignore"):
+        lnl = want["lse"] - peak
+        ln_err = 4 * U * far + 2.0 ** -22 + A + 2 * U * np.abs(lnl)
+        lims = {"lse": ln_err + U * np.abs(peak) + U * np.abs(want["lse"]),
+                "entropy": ln_err + (2 * (2.0 ** -22 + A) + 8 * U) * far + 4 * U * far2 + U * want["entropy"]}
+        for name in ("logprob", "top_logprob"):
+            lims[name] = ln_err[:, None] + 3 * U * np.abs(want[name] + lnl[:, None]) + U * np.abs(want[name])
+        for name, t in (("logprob", logprob), ("top_logprob", top_logprob), ("lse", lse), ("entropy", entropy)):
+            fine = np.isfinite(want[name])
+            err = np.abs(t.astype(np.float64) - want[name])
+            assert np.all(err[fine] <= lims[name][fine]), (name, (err - lims[name])[fine].max())
+    return got
+
+
+KINDS = ["plain", "kept", "equal", "few values", "rising", "falling", "peaked", "far", "lowest"]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("m,n,top,n_tok,gap", [(1, 1, 1, 1, 0), (3, 5, 8, 2, 3), (2, 2047, 64, 1, 1), (1, 9001, 20, 3, 0), (5, 30011, 64, 2, 7),
+                                               (600, 4099, 8, 1, 0)])
+def test_logprobs(dev, kind, m, n, top, n_tok, gap):
+    rng = np.random.default_rng(n + top)
+    x = rows_of(rng, m, n, kind)
+    tokens = rng.integers(-1, n + 1, (m, n_tok))
+    for dtype in (torch.bfloat16, torch.float32):
+        check_logprobs(dev, x, tokens, top, scale=0.7, gap=gap, dtype=dtype)
+
+
+@pytest.mark.parametrize("m", [1, 9, 72, 128])
+def test_logprobs_of_the_heads_row(dev, m):
+    """The head's vocabulary shard, as many rows as it takes at once."""
+    rng = np.random.default_rng(m)
+    check_logprobs(dev, rows_of(rng, m, 124160, "plain"), rng.integers(0, 124160, (m, 1)), 8)
+
+
+def test_logprobs_without_tokens_or_alternatives(dev):
+    rng = np.random.default_rng(1)
+    x = rows_of(rng, 4, 20000, "plain")
+    check_logprobs(dev, x, np.zeros((4, 0), np.int32), 5)
+    check_logprobs(dev, x, rng.integers(0, 20000, (4, 64)), 0)
+    got = R.draft_branch_logprobs(torch.from_numpy(x).to(dev))
+    assert got[0].shape == (4, 0) and got[1].shape == (4, 0) and bool(torch.isfinite(got[3]).all())
+    none = R.draft_branch_logprobs(torch.empty((0, 100), device=dev), top=3)
+    assert none[1].shape == (0, 3)
+
+
+@pytest.mark.parametrize("m,n", [(4, 700), (4, 50000), (700, 700)])
+def test_logprobs_of_rows_that_are_no_numbers(dev, m, n):
+    """NaN, +inf, nothing but -inf, one element alone, factors that are none: each row for itself."""
+    rng = np.random.default_rng(n)
+    x = rows_of(rng, m, n, "plain")
+    x[0, n // 2] = np.nan
+    x[1] = -np.inf
+    x[2, n - 1] = np.inf
+    x[3] = -np.inf
+    x[3, 17] = -4.0
+    tokens = np.array([[3, n]] * (m - 1) + [[17, -5]])
+    check_logprobs(dev, x, tokens, 4, dtype=torch.float32)
+    check_logprobs(dev, x, tokens, 4)
+    x[0, n // 2], x[2, n - 1] = 1.0, 2.0
+    check_logprobs(dev, x, tokens, 4, scales=[0.5, 1.0, 2.0, 1e30] + [1.5] * (m - 4), scale=2.0)
+    check_logprobs(dev, x, tokens, 4, scales=[0.0, -1.0, np.nan, np.inf] + [1.0] * (m - 4))
+    x[0] = np.nan
+    check_logprobs(dev, x, tokens, 4)
+
+
+def test_logprobs_of_bits_and_shards(dev):
+    """int16 rows are bf16 bits; two shards join by their lse."""
+    rng = np.random.default_rng(2)
+    x = torch.from_numpy(rows_of(rng, 7, 6000, "plain")).to(torch.bfloat16).to(dev)
+    tokens = ints(rng.integers(0, 6000, (7, 2)), dev)
+    whole = R.draft_branch_logprobs(x, tokens, top=9)
+    bits = R.draft_branch_logprobs(x.view(torch.int16), tokens, top=9)
+    assert all(torch.equal(a, b) for a, b in zip(whole, bits))
+    parts = [R.draft_branch_logprobs(x[:, a:b], tokens - a, top=9) for a, b in ((0, 2500), (2500, 6000))]
+    lses = torch.stack([p[3] for p in parts]).double()
+    lse = torch.logsumexp(lses, 0)
+    entropy = lse - sum(torch.exp(p[3].double() - lse) * (p[3] - p[4]).double() for p in parts)
+    logprob = torch.maximum(*(p[0].double() + (p[3].double() - lse)[:, None] for p in parts))
+    for a, b in ((lse, whole[3]), (entropy, whole[4]), (logprob, whole[0])):
+        assert float((a - b).abs().max()) < 1e-5
+
+
+def test_logprobs_repeat_to_the_bit_on_another_stream_and_in_a_graph(dev):
+    rng = np.random.default_rng(3)
+    for m, n in ((1, 124160), (40, 9001), (900, 3001)):
+        x = torch.from_numpy(rows_of(rng, m, n, "few values")).to(torch.bfloat16).to(dev)
+        tokens = ints(rng.integers(0, n, (m, 1)), dev)
+        want = R.draft_branch_logprobs(x, tokens, top=20)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = R.draft_branch_logprobs(x, tokens, top=20, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        ws = torch.full((R.draft_branch_logprobs_workspace_bytes(m, n, 20),), 255, dtype=torch.uint8, device=dev)
+        names = ("logprob", "top_id", "top_logprob", "lse", "entropy")
+        outs = {k: torch.empty_like(t) for k, t in zip(names, want)}
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            R.draft_branch_logprobs(x, tokens, top=20, workspace=ws, **outs)
+        for i in range(3):
+            for t in outs.values():
+                t.fill_(3)
+            ws.fill_(i)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(outs[k], t) for k, t in zip(names, want))
+
+
+def test_head_scores_its_tokens(dev):
+    """The head's own call: its row's log probabilities, for a full and a top-k row."""
+    from bit_quantized_lm_amd import workload
+    n, k, m = 4000, 1024, 5
+    head = B.DraftHead.from_weight(workload.gen_weight(n, k, seed=3), device=dev)
+    x = torch.from_numpy(workload.gen_x(m, k, seed=4).view(np.int16)).to(dev)
+    for topk_only in (False, True):
+        first = head.logits_row(x, topk_only=topk_only)
+        tokens = first["out_id"][:, None].contiguous()
+        got = head.logprobs(x, tokens, top=3, scale=0.8, topk_only=topk_only)
+        assert torch.equal(got["row"], first["row"]) and torch.equal(got["top_id"][:, 0], got["top_id"][:, 0].clamp(0, n - 1))
+        want = O.logprobs(first["row"].view(torch.bfloat16).double().cpu().numpy(), tokens.cpu().numpy(), 3, np.full(m, np.float32(0.8)))
+        assert np.array_equal(got["top_id"].cpu().numpy(), want["top_id"])
+        assert np.abs(got["logprob"].cpu().numpy() - want["logprob"]).max() < 1e-4 and np.abs(got["entropy"].cpu().numpy() - want["entropy"]).max() < 1e-4
