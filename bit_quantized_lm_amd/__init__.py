@@ -8,8 +8,8 @@ C ABI (include/drafthead.h); `_binding` is a thin ctypes layer over it.  The
 draft layer's attention before the head (include/draftlayer.h: rotary append to
 an 8-bit paged cache, its reading back, attention over it) is in the same
 library, bound by `_layer`, and so is what several branches of one context need
-(include/draftbranch.h: pages forked and drawn together, log probabilities),
-bound by `_branch`.
+(include/draftbranch.h: pages forked and drawn together, attention over shared
+prefixes, log probabilities), bound by `_branch`.
 
 Importing the package loads nothing native: the binding's names are resolved
 on first attribute access, and the native library is loaded on first call
@@ -28,6 +28,7 @@ _LAYER_NAMES = (
 
 _BRANCH_NAMES = (
     "draft_branch_fork", "draft_branch_compact", "draft_branch_pages_workspace_bytes", "draft_branch_pages_workspace",
+    "draft_branch_attend", "draft_branch_attend_workspace_bytes", "draft_branch_attend_workspace",
     "draft_branch_logprobs", "draft_branch_logprobs_workspace_bytes", "draft_branch_logprobs_workspace",
 )
 

@@ -8,6 +8,7 @@ ValueError (an argument) or DraftHeadError (the runtime).
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import re
 
@@ -31,6 +32,9 @@ def _load():
                 ("draft_branch_pages_workspace_bytes", [i32, i32, ctypes.POINTER(sz)]),
                 ("draft_branch_fork", [P, P, P, P, i32, i32, i32, i32, P, P, P, i32, P, P, i32, i32, P, P, P, P, sz, P]),
                 ("draft_branch_compact", [P, P, P, P, i32, i32, i32, i32, P, P, i32, i32, P, P, P, P, sz, P]),
+                ("draft_branch_attend_workspace_bytes", [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]),
+                ("draft_branch_attend", [P, i64, P, P, P, P, i32, i32, P, P, P, i32, i32, P, P, i32, i32, i32, i32, i32, f32, i32, i32, P,
+                                         P, P, sz, P]),
                 ("draft_branch_logprobs_workspace_bytes", [i32, i32, i32, ctypes.POINTER(sz)]),
                 ("draft_branch_logprobs", [P, i32, i64, i32, i32, f32, P, P, i32, i32, P, P, P, P, P, P, sz, P])):
             f = getattr(lib, name)
@@ -139,6 +143,48 @@ def draft_branch_compact(k_codes, v_codes, k_scale, v_scale, uses, table, uses_o
         *pool, uses.data_ptr(), table.data_ptr(), table.shape[0], table.shape[1], uses_out.data_ptr(), table_out.data_ptr(),
         status.data_ptr(), at, size, L._raw_stream(stream, dev)))
     return table_out, uses_out, status
+
+
+# ----------------------------------------------------------------- attention
+def draft_branch_attend_workspace_bytes(rows: int, n_seq: int, hq: int, hkv: int, d: int) -> int:
+    """Device workspace bytes of draft_branch_attend's calls of up to `rows` rows
+    of up to n_seq sequences."""
+    return _size(_load().draft_branch_attend_workspace_bytes, rows, n_seq, hq, hkv, d)
+
+
+def draft_branch_attend_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: int, device):
+    """A device workspace for them; it may hold anything."""
+    import torch
+    return torch.empty(draft_branch_attend_workspace_bytes(rows, n_seq, hq, hkv, d), dtype=torch.uint8, device=device)
+
+
+def draft_branch_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, group_start, prefix_len, scale: float | None = None,
+                        window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
+    """draft_layer_attend for sequences that share prefixes, each read once.
+
+    group_start: CUDA int32 [groups + 1]: sequences group_start[g] ..
+    group_start[g+1] - 1 share the tokens of the positions below prefix_len[g]
+    (int32 [groups]), which are read from the pages of the first one's table row.
+    The rest as draft_layer_attend.  Returns (out bf16 [T][hq][D], lse fp32
+    [T][hq]); rows from q_start[-1] on are not written."""
+    lib = _device_lib()
+    dev, n_pages, hkv, page, d = L._cache(k_codes, v_codes, k_scale, v_scale)
+    n_seq, max_pages = L._batch(q_start, kv_len, table, dev)
+    n_groups = prefix_len.shape[0] if len(prefix_len.shape) == 1 else 0
+    if not (L._is(group_start, L._I32, (n_groups + 1,), dev) and L._is(prefix_len, L._I32, (n_groups,), dev)):
+        _ints("prefix_len", prefix_len, (n_groups,), dev)
+        _ints("group_start", group_start, (n_groups + 1,), dev)
+    ldq = L._rows3("q", q, dev, None, d)
+    rows, hq = q.shape[0], q.shape[1]
+    out = L._out(out, "out", q, (rows, hq, d), L._BF16, dev, stream)
+    lse = L._out(lse, "lse", k_scale, (rows, hq), L._F32, dev, stream)
+    at, size, _held = _workspace(workspace, lambda: draft_branch_attend_workspace_bytes(rows, n_seq, hq, hkv, d), dev, stream)
+    B._check(lib.draft_branch_attend(
+        q.data_ptr(), ldq, k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page,
+        q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), n_seq, max_pages, group_start.data_ptr(), prefix_len.data_ptr(), n_groups,
+        rows, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else scale, window, sinks, out.data_ptr(), lse.data_ptr(), at, size,
+        L._raw_stream(stream, dev)))
+    return out, lse
 
 
 # ---------------------------------------------------------- log probabilities

@@ -308,6 +308,12 @@ class DraftCache:
         return draft_layer_attend(q, *self.tensors, q_start, kv_len, table, scale=scale, window=window, sinks=sinks, out=out,
                                   lse=lse, workspace=workspace, stream=stream)
 
+    def attend_branches(self, q, q_start, kv_len, table, group_start, prefix_len, scale=None, window=0, sinks=0, out=None, lse=None,
+                        workspace=None, stream=None):
+        from ._branch import draft_branch_attend
+        return draft_branch_attend(q, *self.tensors, q_start, kv_len, table, group_start, prefix_len, scale=scale, window=window,
+                                   sinks=sinks, out=out, lse=lse, workspace=workspace, stream=stream)
+
     def fork(self, uses, table, kv_len, parents, need, uses_out=None, table_out=None, status=None, workspace=None, stream=None):
         from ._branch import draft_branch_fork
         return draft_branch_fork(*self.tensors, uses, table, kv_len, parents, need, uses_out=uses_out, table_out=table_out,

@@ -17,7 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libdrafthead.so")
 HOST = ("host.cpp", "layer_host.cpp")
-DEVICE = ("device.hip", "layer_attend.hip", "layer_cache.hip", "branch_pages.hip", "branch_logprobs.hip")
+DEVICE = ("device.hip", "layer_attend.hip", "layer_cache.hip", "branch_attend.hip", "branch_pages.hip",
+          "branch_logprobs.hip")
 ARCH = os.environ.get("DRAFTHEAD_OFFLOAD_ARCH", "gfx950")
 
 

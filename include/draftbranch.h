@@ -6,9 +6,11 @@
  * Branches share the pages of what they have in common.  Between two steps the
  * next batch's page table is made from the present one (draft_branch_fork): a
  * sequence goes on as one branch, as several or as none, full pages are shared,
- * a partly filled one is copied, pages for the coming tokens are taken.  What
- * the head says of their tokens is scored (draft_branch_logprobs).  A pool that
- * has become sparse is drawn together (draft_branch_compact).
+ * a partly filled one is copied, pages for the coming tokens are taken.  The
+ * step's attention reads a shared prefix once for all its branches
+ * (draft_branch_attend), and what the head says of their tokens is scored
+ * (draft_branch_logprobs).  A pool that has become sparse is drawn together
+ * (draft_branch_compact).
  *
  * The conventions are drafthead.h's: DH_OK or a negative DH_E* code, nothing
  * thrown, every argument checked before any HIP call, the caller owns every
@@ -105,6 +107,40 @@ int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, flo
                          int hkv, int D, const int32_t* uses, const int32_t* table, int n_rows, int max_pages,
                          int32_t* uses_out, int32_t* table_out, int32_t* status, void* workspace,
                          size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of device workspace for draft_branch_attend's calls of up to T rows of
+ * up to n_seq sequences with these heads.
+ * Errors: DH_EINVAL (null pointer), DH_ESHAPE, DH_EUNSUP.
+ */
+int draft_branch_attend_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t* bytes);
+
+/*
+ * DEVICE.  draft_layer_attend for a batch whose sequences share prefixes, each
+ * read once for all that share it.  The sequences group_start[g] ..
+ * group_start[g+1] - 1 are a group and have the tokens of the positions 0 ..
+ * prefix_len[g] - 1 in common: these are read from the pages that the first
+ * sequence's table row names (group members' entries for whole pages of them
+ * need not be there), those from prefix_len[g] on from each one's own.  A row
+ * sees what it sees in draft_layer_attend, by its position, window and sinks,
+ * whichever row the page is taken from; a token at a position that it does not
+ * see stays unseen in a prefix too.  Sequences from group_start[n_groups] on have
+ * no prefix.  Where the members' table rows name the pages of one prefix, as
+ * draft_branch_fork leaves them, the result is draft_layer_attend's of the same
+ * batch up to rounding.
+ *   group_start  device, int32 [n_groups + 1], not decreasing, 0 first, at most n_seq
+ *   prefix_len   device, int32 [n_groups], any number of tokens (a negative one is 0)
+ *   the other arguments, their limits, what is said of rows without a token to
+ *   see, of values that are not finite, and the precision: as draft_layer_attend's
+ * Limits: 1 <= n_groups <= n_seq.
+ * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
+ */
+int draft_branch_attend(const void* q, int64_t ldq, const uint8_t* k_codes, const uint8_t* v_codes,
+                        const float* k_scale, const float* v_scale, int n_pages, int page, const int32_t* q_start,
+                        const int32_t* kv_len, const int32_t* table, int n_seq, int max_pages,
+                        const int32_t* group_start, const int32_t* prefix_len, int n_groups, int T, int hq, int hkv,
+                        int D, float scale, int window, int sinks, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /*
  * Bytes of device workspace for draft_branch_logprobs' calls of up to M rows of

@@ -57,6 +57,49 @@ def compact(uses, table):
     return np.array([[to.get(int(i), int(i)) for i in line] for line in table], np.int32), out, np.array([used, len(moves)], np.int32), moves
 
 
+def attend(q, kc, vc, ks, vs, q_start, kv_len, table, group_start, prefix_len, scale, window, sinks):
+    """(out, lse, spread, absqk) as oracle.layer.attend gives them; kc, vc: signed
+    codes token by element."""
+    rows, hq, d = q.shape
+    n_pages, hkv, page = kc.shape[0], kc.shape[1], kc.shape[2]
+    group, cap = hq // hkv, table.shape[1] * page
+    out, spread = np.zeros((rows, hq, d)), np.zeros((rows, hq, d))
+    lse, absqk = np.full((rows, hq), -np.inf), np.zeros((rows, hq))
+    leader, shared = np.arange(len(kv_len)), np.zeros(len(kv_len), np.int64)
+    for g, p in enumerate(prefix_len):
+        for s in range(group_start[g], group_start[g + 1]):
+            leader[s], shared[s] = group_start[g], max(int(p), 0)
+    for s in range(len(kv_len)):
+        n = int(q_start[s + 1] - q_start[s])
+        length = int(min(max(kv_len[s], 0), cap))
+        if n == 0 or length == 0:
+            continue
+        j = np.arange(length)
+        ids = np.where(j < shared[s], table[leader[s], j // page], table[s, j // page])     # every token's page
+        there = (ids >= 0) & (ids < n_pages)
+        ids = np.where(there, ids, 0)
+        p = (int(kv_len[s]) - n + np.arange(n))[:, None]
+        seen = (j[None, :] <= p) & there[None, :]
+        if window:
+            seen &= (j[None, :] > p - window) | (j[None, :] < sinks)
+        r = slice(int(q_start[s]), int(q_start[s + 1]))
+        for h in range(hkv):
+            k = np.where(there[:, None], kc[ids, h, j % page] * ks[ids, h].astype(np.float64)[:, None], 0.0)
+            v = np.where(there[:, None], vc[ids, h, j % page] * vs[ids, h].astype(np.float64)[:, None], 0.0)
+            for m in range(h * group, (h + 1) * group):
+                x = q[r, m].astype(np.float64)
+                z = np.where(seen, scale * (x @ k.T), -np.inf)
+                top = z.max(axis=1, keepdims=True)
+                some = np.isfinite(top[:, 0])
+                e = np.exp(z - np.where(some[:, None], top, 0.0))
+                total = e.sum(axis=1, keepdims=True)
+                w = e / np.where(total == 0, 1.0, total)
+                out[r, m], spread[r, m] = w @ v, w @ np.abs(v)
+                lse[r, m] = np.where(some, top[:, 0] + np.log(np.where(some, total[:, 0], 1.0)), -np.inf)
+                absqk[r, m] = np.where(seen, scale * (np.abs(x) @ np.abs(k).T), 0.0).max(axis=1)
+    return out, lse, spread, absqk
+
+
 def logprobs(x, tokens, top, factor):
     """x [M][N], factor [M]: dict of float64 results, and what tolerances are made
     of: far = mean of |z - max z|, far2 = mean of its square."""

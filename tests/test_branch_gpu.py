@@ -1,5 +1,8 @@
 """The operators on several branches on the GPU against the oracle.
 
+Attention: the tolerances of draft_layer_attend's tests (z's products and sums, weights of
+11 bits, bf16's half ulp; their 2^-18 and 2^-20 hold the joining of the parts too).
+
 Pages are moved, not computed: tables, counts and every byte of the pool are
 compared as they are.
 
@@ -22,6 +25,7 @@ from bit_quantized_lm_amd import _binding as B
 from bit_quantized_lm_amd import _branch as R
 from bit_quantized_lm_amd import _layer as L
 from oracle import branch as O
+from oracle import layer as OL
 
 pytestmark = pytest.mark.gpu
 
@@ -247,6 +251,240 @@ def test_pages_on_another_stream_and_in_a_graph(dev):
         torch.cuda.synchronize()
         assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(outs, want))
         assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(more, packed))
+
+
+# ----------------------------------------------------------------- attention
+def half_ulp(x):
+    """Half a bf16 ulp at x, with room for a neighbour one binade up."""
+    return 2.0 ** (np.floor(np.log2(np.maximum(np.abs(x), 2.0 ** -120) * (1 + 2.0 ** -8))) - 8)
+
+
+class Branches:
+    """A cache with random contents and a batch whose groups share prefixes.
+    groups: [(prefix, [(new, tokens from the prefix's end on)])]; loose: [(new, tokens)]."""
+
+    def __init__(self, dev, groups, loose, hq, hkv, d, page, seed, max_pages=None, members_know=True):
+        rng = self.rng = np.random.default_rng(seed)
+        self.dev, self.hq, self.hkv, self.d, self.page = dev, hq, hkv, d, page
+        lens = [(n, p + t, p, i == 0) for p, m in groups for i, (n, t) in enumerate(m)] + [(n, t, 0, True) for n, t in loose]
+        reach = max([t for _, t, _, _ in lens] + [p for p, _ in groups] + [1])
+        self.max_pages = max_pages or -(-reach // page) + 1
+        n_pages = sum(-(-max(t, p) // page) for _, t, p, _ in lens) + 3
+        order, at = rng.permutation(n_pages), 0
+        self.table = np.full((len(lens), self.max_pages), -7, np.int32)
+        for s, (_, total, prefix, first) in enumerate(lens):
+            if first:
+                leader, k = s, 0
+            else:      # whole pages of the prefix are the first's, its last part is not
+                k = min(prefix // page, self.max_pages)
+                if members_know:
+                    self.table[s, :k] = self.table[leader, :k]
+            n = min(-(-max(total, prefix if first else 0) // page), self.max_pages)
+            if n > k:
+                self.table[s, k:n] = order[at:at + n - k]
+                at += n - k
+        self.q_start = np.concatenate([[0], np.cumsum([n for n, _, _, _ in lens])]).astype(np.int32)
+        self.kv_len = np.array([t for _, t, _, _ in lens], np.int32)
+        self.group_start = np.concatenate([[0], np.cumsum([len(m) for _, m in groups])]).astype(np.int32)
+        self.prefix_len = np.array([p for p, _ in groups], np.int32)
+        self.rows = int(self.q_start[-1])
+        shape = (n_pages, hkv, page, d)
+        self.codes = [(np.clip(np.rint(rng.standard_normal(shape) * 33), -127, 127) + 128).astype(np.uint8) for _ in range(2)]
+        self.scales = [rng.uniform(0.01, 0.06, shape[:2]).astype(np.float32) for _ in range(2)]
+        self.q = torch.from_numpy(rng.standard_normal((self.rows, hq, d)).astype(np.float32)).to(torch.bfloat16)
+
+    def upload(self):
+        self.cache = [torch.from_numpy(a).to(self.dev) for a in (*self.codes, *self.scales)]
+        self.batch = [ints(a, self.dev) for a in (self.q_start, self.kv_len, self.table, self.group_start, self.prefix_len)]
+        return self
+
+    def check(self, window=0, sinks=0, q=None, scale=None, **kw):
+        self.upload()
+        qd = self.q.to(self.dev) if q is None else q
+        scale = 1.0 / np.sqrt(self.d) if scale is None else scale
+        out, lse = R.draft_branch_attend(qd, *self.cache, *self.batch, scale=scale, window=window, sinks=sinks, **kw)
+        torch.cuda.synchronize()
+        rows = self.rows
+        want, lwant, spread, absqk = O.attend(self.q.float().numpy(), OL.natural(self.codes[0], OL.key_byte), OL.natural(self.codes[1], OL.value_byte),
+                                              *self.scales, self.q_start, self.kv_len, self.table, self.group_start, self.prefix_len, scale, window, sinks)
+        got, lgot = out[:rows].double().cpu().numpy(), lse[:rows].double().cpu().numpy()
+        dz = (self.d + 16) * U * absqk
+        none = np.isneginf(lwant)
+        assert np.array_equal(np.isneginf(lgot), none) and not np.isnan(lgot).any()
+        assert np.all(np.abs(lgot - lwant)[~none] <= (dz + 2.0 ** -20 + 4 * U * np.abs(lwant))[~none])
+        err, lim = np.abs(got - want), half_ulp(want) + (2.0 ** -11 + 2 * dz[..., None] + 2.0 ** -18) * spread
+        assert np.all(err <= lim), (err - lim).max()
+        assert not got[none].any()
+        return out, lse
+
+
+ATTENDS = [
+    # groups, loose, hq, hkv, d, page, window, sinks
+    ([(1, [(1, 1)])], [], 1, 1, 64, 32, 0, 0),
+    ([(64, [(1, 1), (1, 5), (1, 70)])], [], 5, 1, 128, 64, 0, 0),
+    ([(960, [(1, 30)] * 4)], [], 40, 8, 128, 64, 0, 0),
+    ([(5000, [(1, 20 + 3 * i) for i in range(9)])], [], 16, 2, 256, 128, 0, 0),
+    ([(333, [(1, 40), (0, 9), (2, 2), (1, 300)]), (77, [(1, 1)]), (100, [(1, 600), (1, 2)])], [(1, 90), (2, 2)], 10, 2, 128, 64, 0, 0),
+    ([(700, [(9, 20), (3, 3), (9, 100)])], [(4, 50)], 21, 3, 64, 32, 0, 0),              # the prefix ends inside a page
+    ([(200, [(40, 40), (77, 300), (100, 101)])], [], 12, 3, 128, 32, 0, 0),
+    ([(300, [(150, 150), (200, 450)]), (64, [(130, 130)])], [], 8, 2, 64, 64, 0, 0),
+    ([(250, [(100, 120), (90, 90)])], [(30, 60)], 8, 1, 256, 64, 0, 0),
+    ([(500, [(2, 30)] * 3)], [(5, 600)], 8, 1, 256, 128, 0, 0),                          # tiles of 64 and of 16 rows, heads of 256
+    ([(400, [(70, 70)] * 2)], [(1, 30)] * 9, 2, 1, 128, 64, 0, 0),                        # groups of many rows, sequences of few
+    ([(0, [(1, 40), (1, 7)])], [], 4, 2, 64, 32, 0, 0),                                  # no prefix
+    ([(100, [(6, -40), (1, 3), (3, -100), (5, 2), (2, -96)])], [], 4, 2, 64, 32, 0, 0),  # rows within the prefix, rows that see nothing
+    ([(500, [(1, 300), (1, 20)])], [(1, 50)], 4, 2, 64, 32, 100, 4),                     # a window that leaves the prefix out, or in part
+    ([(1000, [(9, 60), (4, 9), (1, 700)])], [], 5, 1, 128, 64, 200, 70),
+    ([(40, [(3, 200), (2, 30)])], [(2, 300)], 4, 2, 64, 32, 50, 100),                    # sinks past the prefix
+    ([(300, [(90, 100), (60, 61)])], [], 6, 2, 128, 64, 1, 0),                           # a row sees itself alone
+    ([(300, [(90, 100), (60, 61)])], [], 6, 2, 128, 64, 33, 3),
+    ([(700, [(40, 90), (64, 64)])], [(10, 90)], 8, 1, 256, 64, 100000, 4),               # a window past everything
+    ([(65, [(1, 1 + i) for i in range(90)])], [(1, 20)] * 5, 4, 1, 64, 32, 0, 0),         # more sequences than a wave has lanes
+    ([(40 + i, [(1, 3), (1, 1 + i)]) for i in range(70)], [(1, 9)], 2, 1, 64, 32, 0, 0),  # and more groups
+    ([(40 + i, [(1, -30 + i), (2, 1 + i)]) for i in range(70)], [(1, 9)], 2, 2, 64, 32, 45, 2),
+    ([(20000, [(1, 3)] * 3)], [], 8, 1, 64, 128, 0, 0),                                   # few rows over a long prefix: many parts
+]
+
+
+@pytest.mark.parametrize("groups,loose,hq,hkv,d,page,window,sinks", ATTENDS)
+def test_attend(dev, groups, loose, hq, hkv, d, page, window, sinks):
+    Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq + len(groups), members_know=len(groups) % 2 == 0).check(window, sinks)
+
+
+def test_attend_is_the_layers(dev):
+    """Where the rows name one prefix's pages, draft_layer_attend of the same batch says the same."""
+    c = Branches(dev, [(640, [(3, 50), (9, 70), (1, 1)]), (128, [(2, 30)] * 6)], [(4, 100)], 10, 2, 128, 64, seed=1)
+    out, lse = c.check()
+    want, lwant = L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch[:3])
+    assert float((lse - lwant).abs().max()) < 1e-4 and float((out.float() - want.float()).abs().max()) < 0.02
+
+
+def test_attend_leaves_other_rows_alone(dev):
+    """Rows behind the last sequence, and a row stride."""
+    c = Branches(dev, [(100, [(2, 20), (0, 3), (3, 9)])], [(1, 40)], 4, 2, 64, 32, seed=2)
+    q = torch.zeros((c.rows + 5, 7, 64), dtype=torch.bfloat16, device=dev)[:, :4]
+    q[:c.rows] = c.q.to(dev)
+    out, lse = torch.full((c.rows + 5, 4, 64), 7.0, dtype=torch.bfloat16, device=dev), torch.full((c.rows + 5, 4), 7.0, device=dev)
+    c.check(q=q, out=out, lse=lse)
+    assert bool((out[c.rows:] == 7).all()) and bool((lse[c.rows:] == 7).all())
+
+
+@pytest.mark.parametrize("new", [1, 30])
+def test_attend_missing_pages_and_the_tables_end(dev, new):
+    c = Branches(dev, [(300, [(new, new + 40), (new, new + 10)])], [(new, 200)], 4, 1, 64, 32, seed=3)
+    c.table[0, 3], c.table[1, 9], c.table[2, 2] = -1, 1 << 30, len(c.codes[0])
+    c.check()
+    for window, sinks in ((0, 0), (50, 3)):
+        Branches(dev, [(300, [(new, new + 40), (new, new + 10)])], [(new, 400)], 4, 1, 64, 32, seed=4, max_pages=10).check(window, sinks)
+
+
+def test_attend_of_values_that_are_no_numbers(dev):
+    """A page whose scale is none makes the rows that see it NaN, a query its own row; no others."""
+    for new in (1, 30):
+        c = Branches(dev, [(100, [(new, new + 10), (new, new + 40)]), (64, [(new, new), (new, new + 5)])], [], 4, 2, 64, 32, seed=5)
+        c.scales[0][c.table[0, 1], 0] = np.nan          # the first group's prefix, the first kv head
+        c.scales[1][c.table[3, 2 + (new + 4) // 32], 1] = np.inf      # a sequence's own last page, the second
+        c.upload()
+        q = c.q.to(dev)
+        q[c.q_start[2], 0, 3] = float("inf")
+        out, lse = R.draft_branch_attend(q, *c.cache, *c.batch)
+        bad = torch.isnan(lse).cpu().numpy()
+        want = np.zeros_like(bad)
+        want[:c.q_start[2], :2] = True
+        sees = np.arange(c.rows) >= c.q_start[3] + max(0, new - 1 - (new + 4) % 32)
+        want[:, 2:] |= (sees & (np.arange(c.rows) >= c.q_start[3]))[:, None]
+        want[c.q_start[2], 0] = True
+        assert np.array_equal(bad, want) and np.array_equal(torch.isnan(out.float()).any(-1).cpu().numpy(), want)
+
+
+def test_attend_groups_that_no_caller_should_have(dev):
+    """Row starts, groups and lengths that do not fit each other fault nothing and touch no row outside."""
+    c = Branches(dev, [(100, [(3, 20), (3, 9)]), (64, [(2, 9)])], [(1, 40)], 4, 2, 64, 32, seed=6).upload()
+    rng = np.random.default_rng(7)
+    for t in range(12):
+        start = ints(rng.integers(-5, 20, 5), dev)
+        groups, prefix = ints(rng.integers(-3, 8, 3), dev), ints(rng.integers(-100, 1 << 30, 2), dev)
+        out = torch.full((c.rows + 64, 4, 64), 7.0, dtype=torch.bfloat16, device=dev)
+        R.draft_branch_attend(c.q.to(dev), *c.cache, start, c.batch[1] * (t % 3) - 9, c.batch[2], groups, prefix, window=t % 2 * 40, out=out[:c.rows])
+        torch.cuda.synchronize()
+        assert bool((out[c.rows:] == 7).all())
+
+
+def test_attend_repeats_to_the_bit_on_another_stream_and_in_graphs(dev):
+    """Two graphs that share one workspace, replayed in turn with eager calls between."""
+    cases = [Branches(dev, [(900, [(1, 30)] * 9)], [(1, 50)], 10, 2, 128, 64, seed=8).upload(),
+             Branches(dev, [(300, [(20, 60), (50, 50)])], [], 8, 2, 64, 32, seed=9).upload()]
+    ws = torch.full((max(R.draft_branch_attend_workspace_bytes(c.rows, len(c.kv_len), c.hq, c.hkv, c.d) for c in cases),), 255, dtype=torch.uint8, device=dev)
+    graphs = []
+    for c in cases:
+        q = c.q.to(dev)
+        want = R.draft_branch_attend(q, *c.cache, *c.batch)
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        got = R.draft_branch_attend(q, *c.cache, *c.batch, stream=side)
+        side.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        outs = [torch.empty_like(t) for t in want]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            R.draft_branch_attend(q, *c.cache, *c.batch, out=outs[0], lse=outs[1], workspace=ws)
+        graphs.append((graph, outs, want, q, c))
+    for i in range(3):
+        for graph, outs, want, q, c in graphs:
+            for t in outs:
+                t.fill_(3)
+            ws.fill_(i * 100)
+            graph.replay()
+            eager = R.draft_branch_attend(q, *c.cache, *c.batch, workspace=ws)
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) and torch.equal(a, d) for a, b, d in zip(outs, want, eager))
+
+
+def test_fork_then_attend(dev):
+    """As they are used: prompts, their branches, a step of each branch over the shared pages, and the pool drawn together."""
+    hq, hkv, d, page, n_pages = 10, 2, 128, 64, 80
+    rng = np.random.default_rng(10)
+    cache = L.DraftCache(n_pages, hkv, d, page, device=dev)
+    lens = [300, 128, 77]
+    table = np.full((3, 8), -1, np.int32)
+    uses = torch.zeros(n_pages, dtype=torch.int32, device=dev)
+    none = torch.full((3,), -1, dtype=torch.int32, device=dev)
+    zero = torch.zeros(3, dtype=torch.int32, device=dev)
+    table, uses, status = cache.fork(uses, ints(table, dev), zero, none, ints(lens, dev))
+    assert status.tolist() == [n_pages - sum(-(-n // page) for n in lens), 0]
+
+    def made(rows):
+        return [torch.from_numpy(rng.standard_normal((rows, h, d)).astype(np.float32)).to(torch.bfloat16).to(dev) for h in (hq, hkv, hkv)]
+
+    q_start, kv_len = ints(np.concatenate([[0], np.cumsum(lens)]), dev), ints(lens, dev)
+    q, k, v = made(sum(lens))
+    cache.append(q, k, v, None, q_start, kv_len, table)
+    parents = [0, 0, 0, 0, 2, 2]                     # the second ends
+    branch_len = torch.tensor([lens[p] for p in parents], dtype=torch.int32, device=dev)
+    more, counts, status = cache.fork(uses, table, kv_len, ints(parents, dev), branch_len + 3)
+    assert int(status[1]) == 0 and int((counts > 0).sum()) == 4 + 4 + 1 + 2       # shared whole pages, and each branch's own
+    groups, prefix = ints([0, 4, 6], dev), ints([300 // page * page, 77 // page * page], dev)
+    for draw_together in (False, True):
+        if draw_together:
+            more, counts, status = cache.compact(counts, more)
+            assert int(status[0]) == 11 and not bool((counts[11:] != 0).any())
+        for step in range(3):
+            length = branch_len + step + 1
+            one = ints(list(range(7)), dev)
+            q, k, v = made(6)
+            cache.append(q, k, v, None, one, length, more)
+            got = cache.attend_branches(q, one, length, more, groups, prefix)
+            want = cache.attend(q, one, length, more)
+            assert float((got[1] - want[1]).abs().max()) < 1e-4
+            assert float((got[0].float() - want[0].float()).abs().max()) <= 2.0 ** -7 * float(want[0].float().abs().max())
+        first = cache.read(ints([0] + list(np.cumsum(branch_len.tolist())), dev), branch_len, more, int(branch_len.sum()))
+        own_ = cache.read(q_start, kv_len, table, sum(lens)) if not draw_together else own_
+        at = 0
+        for p, n in zip(parents, branch_len.tolist()):     # every branch still has its parent's whole pages as they were
+            whole = n // page * page
+            lo = sum(lens[:p])
+            assert all(torch.equal(a[at:at + whole], b[lo:lo + whole]) for a, b in zip(first, own_))
+            at += n
 
 
 # ---------------------------------------------------------- log probabilities

@@ -46,6 +46,10 @@ COMPACT = dict(kc=P, vc=P, ks=P, vs=P, n_pages=9, page=64, hkv=2, D=128, uses=P,
 LOGPROBS = dict(x=P, type=0, ld=1000, M=3, N=1000, scale=1.0, scales=None, tokens=P, n_tok=1, top=8, logprob=P, lse=P, entropy=P, top_id=P,
                 top_logprob=P, workspace=P, bytes=1 << 40, stream=None)
 
+ATTEND = dict(q=P, ldq=1024, kc=P, vc=P, ks=P, vs=P, n_pages=9, page=64, q_start=P, kv_len=P, table=P, n_seq=3, max_pages=10, group_start=P,
+              prefix_len=P, n_groups=2, T=5, hq=8, hkv=2, D=128, scale=0.1, window=0, sinks=0, out=P, lse=P, workspace=P, bytes=1 << 40,
+              stream=None)
+
 PAGES = [(dict(D=96), B.DH_EUNSUP), (dict(hkv=0), B.DH_ESHAPE), (dict(hkv=257), B.DH_ESHAPE), (dict(kc=None), B.DH_EINVAL),
          (dict(vc=None), B.DH_EINVAL), (dict(ks=None), B.DH_EINVAL), (dict(vs=None), B.DH_EINVAL), (dict(kc=P + 8), B.DH_EINVAL),
          (dict(vs=P + 2), B.DH_EINVAL), (dict(page=48), B.DH_EUNSUP), (dict(n_pages=0), B.DH_ESHAPE), (dict(n_pages=(1 << 24) + 1), B.DH_ESHAPE),
@@ -75,6 +79,38 @@ def test_compact_refuses(lib, change, want):
 
 
 @pytest.mark.parametrize("change,want", [
+    (dict(D=96), B.DH_EUNSUP), (dict(hkv=0), B.DH_ESHAPE), (dict(hq=7), B.DH_ESHAPE), (dict(hq=512), B.DH_ESHAPE), (dict(T=-1), B.DH_ESHAPE),
+    (dict(T=1 << 23), B.DH_ESHAPE), (dict(n_seq=0), B.DH_ESHAPE), (dict(n_seq=4097), B.DH_ESHAPE), (dict(n_groups=0), B.DH_ESHAPE),
+    (dict(n_groups=4), B.DH_ESHAPE), (dict(kc=None), B.DH_EINVAL), (dict(vc=P + 8), B.DH_EINVAL), (dict(ks=None), B.DH_EINVAL),
+    (dict(q_start=None), B.DH_EINVAL), (dict(kv_len=P + 2), B.DH_EINVAL), (dict(table=None), B.DH_EINVAL), (dict(page=16), B.DH_EUNSUP),
+    (dict(max_pages=0), B.DH_ESHAPE), (dict(max_pages=1 << 24), B.DH_ESHAPE), (dict(n_pages=0), B.DH_ESHAPE), (dict(group_start=None), B.DH_EINVAL),
+    (dict(prefix_len=None), B.DH_EINVAL), (dict(prefix_len=P + 1), B.DH_EINVAL), (dict(group_start=P + 2), B.DH_EINVAL), (dict(scale=0.0), B.DH_EINVAL),
+    (dict(scale=float("nan")), B.DH_EINVAL), (dict(window=-1), B.DH_EINVAL), (dict(sinks=-1), B.DH_EINVAL), (dict(q=None), B.DH_EINVAL),
+    (dict(q=P + 8), B.DH_EINVAL), (dict(ldq=1028), B.DH_EINVAL), (dict(ldq=1016), B.DH_EINVAL), (dict(out=None), B.DH_EINVAL),
+    (dict(out=P + 8), B.DH_EINVAL), (dict(lse=P + 2), B.DH_EINVAL), (dict(workspace=None), B.DH_EINVAL), (dict(workspace=P + 8), B.DH_EINVAL),
+    (dict(bytes=1000), B.DH_EINVAL)])
+def test_attend_refuses(lib, change, want):
+    _refused(lib, lib.draft_branch_attend, ATTEND, change, want, b"attend")
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(40, 8, 128), (7, 7, 256), (16, 1, 64), (16, 2, 256), (200, 200, 64), (256, 1, 128)])
+def test_attend_takes_the_largest_batchs_workspace(lib, hq, hkv, d):
+    """The size never falls as rows or sequences grow, and no smaller call asks for more."""
+    import re
+    rows, seqs = (0, 1, 2, 5, 16, 17, 64, 65, 500, 4096), (1, 2, 3, 8, 63, 64, 500)
+    size = {(t, n): R.draft_branch_attend_workspace_bytes(t, n, hq, hkv, d) for t in rows for n in seqs}
+    for (t, n), most in size.items():
+        assert all(most >= other for (u, m), other in size.items() if u <= t and m <= n)
+    for t in rows[1:]:
+        for n in seqs:
+            for g in {1, min(2, n), n // 2 or 1, n}:
+                _refused(lib, lib.draft_branch_attend, ATTEND, dict(T=t, n_seq=n, n_groups=g, hq=hq, hkv=hkv, D=d, ldq=hq * d, bytes=16),
+                         B.DH_EINVAL, b"attend")
+                need = int(re.search(rb"below the (\d+) needed", lib.draft_head_last_error()).group(1))
+                assert 16 < need <= size[t, n], (t, n, g)
+
+
+@pytest.mark.parametrize("change,want", [
     (dict(M=-1), B.DH_ESHAPE), (dict(M=(1 << 22) + 1), B.DH_ESHAPE), (dict(N=0), B.DH_ESHAPE), (dict(N=(1 << 24) + 1), B.DH_ESHAPE),
     (dict(top=-1), B.DH_EUNSUP), (dict(top=65), B.DH_EUNSUP), (dict(n_tok=-1), B.DH_EUNSUP), (dict(n_tok=65), B.DH_EUNSUP),
     (dict(type=2), B.DH_EUNSUP), (dict(ld=999), B.DH_EINVAL), (dict(scale=0.0), B.DH_EINVAL), (dict(scale=-1.0), B.DH_EINVAL),
@@ -89,6 +125,7 @@ def test_logprobs_refuses(lib, change, want):
 
 def test_no_rows_is_no_work(lib):
     assert lib.draft_branch_logprobs(*{**LOGPROBS, "M": 0, "x": None, "lse": None}.values()) == B.DH_OK
+    assert lib.draft_branch_attend(*{**ATTEND, "T": 0, "q": None}.values()) == B.DH_OK
 
 
 def test_workspace_bytes(lib):
@@ -143,5 +180,7 @@ def test_binding_refuses_host_tensors():
         R.draft_branch_fork(c, c, s, s, i, table, i[:1], i, i)
     with pytest.raises(ValueError):
         R.draft_branch_compact(c, c, s, s, i, table)
+    with pytest.raises(ValueError):
+        R.draft_branch_attend(torch.zeros((1, 1, 64), dtype=torch.bfloat16), c, c, s, s, i, i[:1], table, i, i[:1])
     with pytest.raises(ValueError):
         R.draft_branch_logprobs(torch.zeros((2, 5)), torch.zeros((2, 1), dtype=torch.int32))
