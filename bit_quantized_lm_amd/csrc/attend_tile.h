@@ -17,23 +17,30 @@ struct Range {   // groups of 32 tokens a tile sees: `ns` groups from s0 on, the
 
 // The tokens of one sequence that a tile's rows see, and where they are: the row
 // at position p those at j <= p, of these only j > p - window and j < sinks where
-// window > 0, and (kBetween) of these only lo .. hi - 1.
-template <bool kBetween>
+// window > 0.  kSplit: of two sequences' table rows, the positions below `split` (the
+// groups `shared` counts, which come first) from row `lead`, the others from row
+// `seq`; a group that holds positions of both comes twice.
+template <bool kSplit>
 struct Tokens {
   const Batch& b;
   const Cache& c;
   int seq, head;
   Range see;
   int window, sinks;
-  int lo = 0, hi = 0;
+  Range shared = {};
+  int lead = 0, split = 0;
 
-  __device__ __forceinline__ int group_at(int n) const { return n < see.ns ? n + see.s0 : n - see.ns + see.g0; }
-  // whether some row at p_first .. p_last does not see some of the tokens first .. first + 31
-  __device__ __forceinline__ bool hides(int first, int p_first, int p_last) const {
+  static __device__ __forceinline__ int at(const Range& r, int n) { return n < r.ns ? n + r.s0 : n - r.ns + r.g0; }
+  __device__ __forceinline__ bool before(int n) const { return kSplit && n < shared.n; }   // among the shared groups
+  __device__ __forceinline__ int group_at(int n) const { return before(n) ? at(shared, n) : at(see, kSplit ? n - shared.n : n); }
+  __device__ __forceinline__ int row_at(int n) const { return before(n) ? lead : seq; }
+  __device__ __forceinline__ int lo_at(int n) const { return kSplit && !before(n) ? split : 0; }
+  __device__ __forceinline__ int hi_at(int n) const { return before(n) ? split : INT32_MAX; }
+  // whether some row at p_first .. p_last does not see some of the tokens of group n, first .. first + 31
+  __device__ __forceinline__ bool hides(int n, int first, int p_first, int p_last) const {
     return first + 31 > p_first || (window > 0 && first <= p_last - window && first + 31 >= sinks) ||
-           (kBetween && (first < lo || first + 31 >= hi));
+           (kSplit && (first < lo_at(n) || first + 31 >= hi_at(n)));
   }
-  __device__ __forceinline__ bool between(int at) const { return !kBetween | ((at >= lo) & (at < hi)); }
 };
 
 // --------------------------------------------------------------- conversions
@@ -118,6 +125,7 @@ struct Group {
   int id, first;       // page (-1: nothing there), position of token 0
   float ks, lv, rv;    // key scale, log2(value scale), 1 / (value scale)
   bool edge;           // some row does not see some of its tokens
+  int lo, hi;          // only positions lo .. hi - 1 of it count (kSplit)
 };
 
 // A group's weights of all row tiles, from its scores x in code units.  In
@@ -130,8 +138,8 @@ template <int N>
 struct Weights {
   float c[N], p[N][8], sum[N];   // scale of x, weights, this lane's sum of them
 
-  template <bool kBetween>
-  __device__ __forceinline__ void hide(const Tokens<kBetween>& A, const Group& g, f32x4 (&x)[N][2], const float (&qs)[N], const int (&pos)[N]) {
+  template <bool kSplit>
+  __device__ __forceinline__ void hide(const Tokens<kSplit>& A, const Group& g, f32x4 (&x)[N][2], const float (&qs)[N], const int (&pos)[N]) {
 #pragma unroll
     for (int t = 0; t < N; ++t) c[t] = g.ks * qs[t];
     if (!g.edge) return;
@@ -142,7 +150,8 @@ struct Weights {
       for (int j = 0; j < 8; ++j) {
         const int at = g.first + hi * 4 + (j >> 2) * 16 + (j & 3);
         // & and |, not && and ||: selects, no branch a score
-        const bool seen = (g.id >= 0) & (at <= pos[t]) & ((A.window == 0) | (at > pos[t] - A.window) | (at < A.sinks)) & A.between(at);
+        const bool seen = (g.id >= 0) & (at <= pos[t]) & ((A.window == 0) | (at > pos[t] - A.window) | (at < A.sinks)) &
+                          (!kSplit | ((at >= g.lo) & (at < g.hi)));
         x[t][j >> 2][j & 3] = seen ? x[t][j >> 2][j & 3] * c[t] : -INFINITY;
       }
       c[t] = 1.0f;
@@ -224,15 +233,16 @@ struct Bytes {   // a lane's codes of one group
 };
 
 // Rows 0 .. rows - 1 of a tile against the groups from .. to - 1 of what they see
-// (positions p_first .. p_last), each wave its own of them.  place(r, pos) gives row
+// (positions p_first .. p_last), each of the W waves its own of them (W = 1: the wave
+// is alone with the tile).  place(r, pos) gives row
 // r's queries and position (-1 past the last row); finish(o, m, l) takes this wave's
 // share, within the function, so that o never leaves its registers (handed back as
 // an argument it spilled 19 of 256).
-template <int D, int W, int kPolicy, bool kBetween, class Place, class Finish>
-__device__ __forceinline__ void stream_tile(const Tokens<kBetween> A, int from, int to, int rows, int p_first, int p_last, float scale_log2,
+template <int D, int W, int kPolicy, bool kSplit, class Place, class Finish>
+__device__ __forceinline__ void stream_tile(const Tokens<kSplit> A, int from, int to, int rows, int p_first, int p_last, float scale_log2,
                                             const Place place, const Finish finish) {
   constexpr int F = D / 32, C = D / 16;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, lo = lane & 15;
+  const int wave = W == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, lo = lane & 15;
   const size_t page_bytes = (size_t)D << A.c.page_shift;
 
   // lane i: page and scales of the wave's i-th group from `base`, 64 at a time
@@ -240,7 +250,7 @@ __device__ __forceinline__ void stream_tile(const Tokens<kBetween> A, int from, 
   PageScales mine_scales;
   auto look = [&] {
     const int n = base + lane * W;
-    id_mine = n < to ? page_id(A.b, A.c.n_pages, A.seq, A.group_at(n) >> (A.c.page_shift - 5)) : -1;
+    id_mine = n < to ? page_id(A.b, A.c.n_pages, A.row_at(n), A.group_at(n) >> (A.c.page_shift - 5)) : -1;
     const size_t at = (size_t)max(id_mine, 0) * A.c.hkv + A.head;
     mine_scales = page_scales(A.c.ks[at], A.c.vs[at]);   // of one that is not there page 0's, which step() hides
   };
@@ -269,11 +279,11 @@ __device__ __forceinline__ void stream_tile(const Tokens<kBetween> A, int from, 
     for (int c = 0; c < C; ++c) o[0][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   }
   auto step = [&](int i, const Bytes<F>& b) {
-    const int first = A.group_at(base + i * W) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
+    const int n = base + i * W, first = A.group_at(n) * 32, id = __builtin_amdgcn_readlane(id_mine, i);
     const Group group{id, first, __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.ks), i)),
                       __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.lv), i)),
                       __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(mine_scales.rv), i)),
-                      id < 0 || A.hides(first, p_first, p_last)};
+                      id < 0 || A.hides(n, first, p_first, p_last), A.lo_at(n), A.hi_at(n)};
     f32x4 s[1][2] = {{{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}}};
 #pragma unroll
     for (int f = 0; f < F; ++f) {
@@ -343,8 +353,8 @@ struct Shared {
 // Rows 0 .. rows - 1 of a tile against the groups from .. to - 1 of what they see:
 // finish(o, m, l) takes those of this wave's rows (positions w_first .. w_last).  Every
 // thread of the workgroup calls it; `stage` is the workgroup's LDS, free before.
-template <int D, int NQ, int W, bool kBetween, class Place, class Finish>
-__device__ __forceinline__ void shared_tile(const Tokens<kBetween> A, int from, int to, int rows, int w_first, int w_last, float scale_log2,
+template <int D, int NQ, int W, bool kSplit, class Place, class Finish>
+__device__ __forceinline__ void shared_tile(const Tokens<kSplit> A, int from, int to, int rows, int w_first, int w_last, float scale_log2,
                                             const Place place, u32x4* stage, const Finish finish) {
   using S = Shared<D, NQ, W>;
   constexpr int F = S::F, C = D / 16;
@@ -356,7 +366,7 @@ __device__ __forceinline__ void shared_tile(const Tokens<kBetween> A, int from, 
   int table_at = 0;   // group of the table's first entry
   auto fill = [&](int n) {
     const int i = max(n + tid, from), g = A.group_at(i);
-    const int id = i < to ? page_id(A.b, A.c.n_pages, A.seq, g >> (A.c.page_shift - 5)) : -1;
+    const int id = i < to ? page_id(A.b, A.c.n_pages, A.row_at(i), g >> (A.c.page_shift - 5)) : -1;
     const size_t at = (size_t)max(id, 0) * A.c.hkv + A.head;
     const PageScales scales = page_scales(A.c.ks[at], A.c.vs[at]);   // of one that is not there page 0's, hidden later
     const int where = id < 0 ? -1 : (int)((at << (A.c.page_shift - 5)) + (g & in_page));
@@ -467,7 +477,7 @@ __device__ __forceinline__ void shared_tile(const Tokens<kBetween> A, int from, 
 #pragma unroll
       for (int i = 0; i < kRing; ++i) fetch(kf, i);
       const int first = A.group_at(n) * 32;
-      const Group group{id, first, ks, lv, rv, id < 0 || A.hides(first, w_first, w_last)};
+      const Group group{id, first, ks, lv, rv, id < 0 || A.hides(n, first, w_first, w_last), A.lo_at(n), A.hi_at(n)};
       Weights<NQ> weights;
       weights.hide(A, group, now, qs, pos);
       products(kf, vf, score(next), [&](int i) { weights.form(group, now, m, i * 8 * NQ / C, (i + 1) * 8 * NQ / C); });

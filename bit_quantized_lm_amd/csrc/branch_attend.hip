@@ -4,9 +4,9 @@
 // A group's rows against its prefix, and each sequence's rows against its own
 // tokens, are two kinds of items of one launch.  Both leave partial results (sums
 // of values, reference and sum of the weights, fp32); a second launch joins a row's
-// parts of both kinds.  The members' rows follow each other in memory, so a
-// prefix's tiles are packed from all of them as if they were one sequence's, and
-// each key and value of the prefix is loaded once for 16, 64 or 128 of them.
+// parts.  The members' rows follow each other in memory, so a prefix's tiles are
+// packed from all of them as if they were one sequence's, and each key and value of
+// the prefix is loaded once for up to 128 of them.
 #include <algorithm>
 #include <cmath>
 
@@ -19,11 +19,16 @@ using namespace dl;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kNoLimit = DL_MAX_POSITIONS;
+constexpr int kStreamRows = 16, kSmallRows = 64;
 
-struct Parts {        // of one kind of items
-  float* o;           // [hkv][rows + runs * tile rows][D]
-  float2* ml;         // [hkv][rows + runs * tile rows] reference, sum of weights
+// Partial results of one kind of items and of tiles: row x of a head from run r at
+// place x + r * (rows of a tile).  Runs that share a tile stand that far apart, so two
+// parts never meet: no part needs a number, and nothing has to be cleared or counted.
+struct Parts {
+  float* o;           // [hkv][places][D]
+  float2* ml;         // [hkv][places] reference, sum of weights
 };
+enum Line { kShared, kStream };   // tiles of a workgroup, tiles of a wave
 
 struct BranchArgs {
   Batch b;
@@ -38,60 +43,87 @@ struct BranchArgs {
   uint16_t* out;
   float* lse;
   int runs;           // workgroups a head
-  int min_run;        // least units of a run
-  int prefix_rows, own_rows;     // of a tile
-  int prefix_cost, own_cost;     // units of a group of 32 tokens against a tile
-  int64_t rows;       // T * group: rows of a kv head
-  Parts prefix, own;
-  int32_t* plan;      // units of a run, and from [4] on first unit and units a tile of each item
+  int64_t places[2];  // a head's, by line
+  Parts prefix[2], own[2];
+  int32_t* plan;      // left by the first launch for the second: units of a run by line, then 8 numbers an item
 };
 
 // ------------------------------------------------------------------ the work
-// Items: the groups' prefixes, then the sequences' own tokens.  An item's tiles
-// cost as many units as the last of them has groups of 32 tokens, times what such a
-// group costs; all tiles' units are laid end to end and cut into equal runs, one a
-// workgroup.  A run may hold the end of one tile, whole ones and the start of
-// another; what it has of a tile is a part.  Row x of a kv head (token row * group +
-// head) has its part from run r at place x + r * (rows of a tile): runs that share a
-// tile stand that far apart, and two parts never meet.  So no part needs a number,
-// and nothing has to be cleared or counted.
+// Items: the sequences' own tokens, then the groups' prefixes.  An item's rows (query
+// heads of one kv head, token after token) are cut into tiles of H = 128 (heads of
+// 256: 64) and a rest; up to 16 rows are one wave's (stream_tile), up to 64 and up to
+// H a workgroup's (shared_tile), whatever the other items have.  Where the members of
+// a group have H rows each on average, sharing saves no time (such tiles are bound by
+// the matrix units) and joining costs some, so the prefix's tokens are the
+// sequences' own then (16 prompts of 112 rows over 6,000 tokens: 345 us so, 517 apart).
+//
+// All tiles of a line are laid end to end, each as long as it is thought to take, and
+// cut into equal runs: a workgroup's, or a wave's, which walks its own segments and
+// waits for no other.  A run may hold the end of one tile, whole ones and the start of
+// another; what it has of a tile is a part.  The workgroups are divided between the
+// lines by what the lines take.
 struct Item {
-  int seq;               // whose table row names the pages
+  int seq, lead;         // whose table rows name the pages of the own and of the shared tokens
   int row0, n;           // token rows
-  int lo, hi;            // tokens at positions lo .. hi - 1
+  int split;             // positions below are the shared ones
+  int sees;              // 1: the own tokens, 2: the shared ones
   int p_first, p_last;   // the rows' positions
-  int tiles, units;      // units of a tile
+  int groups;            // of 32 tokens that a tile sees at most
 };
 
-struct Segment {
-  Item item;
-  bool prefix;
-  int tile, from, to, of, run;
+// Lengths of tiles in units of about 0.1 us of a workgroup (of a wave, for the
+// stream): what a tile's beginning and end take, and what a group of 32 tokens
+// takes: on a full card a tile of 128 rows with heads of 128 takes 1.2 us a group.
+template <int D>
+struct Cost {
+  static constexpr int kRows = D == 256 ? 64 : 128;     // H
+  static __host__ __device__ constexpr int per_group(int rows) {
+    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 7 : 12) * D / 128);
+  }
+  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 40 : 50; }
+  static __device__ __forceinline__ int of(int rows, int groups) { return groups == 0 ? 0 : begin(rows) + groups * per_group(rows); }
 };
 
-__device__ __forceinline__ Range visible(const BranchArgs& A, const Item& t, int p_first, int p_last) {
-  Range r{t.lo >> 5, 0, t.lo >> 5, 0};
-  const int cap = A.b.max_pages << A.c.page_shift, end = min(min(t.hi, p_last + 1), cap);
-  if (end <= t.lo) return r;
+// An item's tiles: `full` ones of H rows, then one of `rest`.
+template <int D>
+struct Shape {
+  int full, rest, each, last;    // tiles and their units
+  __device__ __forceinline__ Shape(int64_t rows, int groups, int shift) {
+    constexpr int H = Cost<D>::kRows;
+    full = (int)(rows / H);
+    rest = (int)(rows % H);
+    auto scaled = [&](int units) { return (int)(((int64_t)units + (1 << shift) - 1) >> shift); };
+    each = scaled(Cost<D>::of(H, groups));
+    last = rest == 0 ? 0 : scaled(Cost<D>::of(rest, groups));
+    if (groups == 0) full = rest = 0;
+  }
+  __device__ __forceinline__ bool streams() const { return rest <= kStreamRows; }
+  __device__ __forceinline__ int units(Line line) const {
+    return line == kStream ? (streams() ? last : 0) : full * each + (streams() ? 0 : last);
+  }
+};
+
+__device__ __forceinline__ Range visible(const BranchArgs& A, int lo, int hi, int p_first, int p_last) {
+  Range r{lo >> 5, 0, lo >> 5, 0};
+  const int cap = A.b.max_pages << A.c.page_shift, end = min(min(hi, p_last + 1), cap);
+  if (end <= lo) return r;
   const int top = (end + 31) >> 5;
   if (A.window > 0) {
     const int low = p_first - A.window + 1;
-    if (low > t.lo) r.g0 = min(low >> 5, top);
+    if (low > lo) r.g0 = min(low >> 5, top);
     r.ns = min(max(((min(A.sinks, cap) + 31) >> 5) - r.s0, 0), r.g0 - r.s0);
   }
   r.n = r.ns + top - r.g0;
   return r;
 }
-
-__device__ __forceinline__ int prefix_of_group(const BranchArgs& A, int g) { return min(max(A.prefix_len[g], 0), kNoLimit); }
-
-// First and past-the-last sequence of group g.
-__device__ __forceinline__ int2 members(const BranchArgs& A, int g) {
-  const int a = min(max(A.group_start[g], 0), A.b.n_seq), b = min(A.group_start[g + 1], A.b.n_seq);
-  return int2{a, max(a, b)};
+__device__ __forceinline__ Range visible_own(const BranchArgs& A, const Item& t, int p_first, int p_last) {
+  return t.sees & 1 ? visible(A, t.split, kNoLimit, p_first, p_last) : Range{};
+}
+__device__ __forceinline__ Range visible_shared(const BranchArgs& A, const Item& t, int p_first, int p_last) {
+  return t.sees & 2 ? visible(A, 0, t.split, p_first, p_last) : Range{};
 }
 
-// The group that sequence s (its own in each lane) is of, or -1.
+// The group that sequence s (its own in each lane; every lane calls it) is of, or -1.
 __device__ __forceinline__ int group_of(const BranchArgs& A, int s) {
   int g = -1;
   if (A.n_groups < 64) {
@@ -111,72 +143,130 @@ __device__ __forceinline__ int group_of(const BranchArgs& A, int s) {
   return g < A.n_groups ? g : -1;
 }
 
+struct Members {
+  int first, last;    // sequences first .. last - 1
+  int row0, n;        // token rows
+  int prefix;
+  bool whole;         // its prefix's tokens count as the sequences' own
+};
+template <int D>
+__device__ __forceinline__ Members members_of(const BranchArgs& A, int g) {
+  Members r;
+  r.first = min(max(A.group_start[g], 0), A.b.n_seq);
+  r.last = max(r.first, min(A.group_start[g + 1], A.b.n_seq));
+  r.row0 = min(max(A.b.q_start[r.first], 0), A.b.T);
+  r.n = max(min(A.b.q_start[r.last], A.b.T) - r.row0, 0);
+  r.prefix = min(max(A.prefix_len[g], 0), kNoLimit);
+  r.whole = (int64_t)r.n * A.group >= (int64_t)Cost<D>::kRows * (r.last - r.first);
+  return r;
+}
+
+__device__ __forceinline__ void write_lse(float* lse, size_t row, float ref, float sum) {
+  if (lse) lse[row] = sum == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+}
+
+struct Segment {
+  Item item;
+  Line line;
+  int tile, from, to, of, run;
+};
+
+template <int D>
 class Walk {
  public:
-  __device__ __forceinline__ void begin(const BranchArgs& A, int run) {
+  // The plan, which every wave computes alike from the lengths.
+  __device__ __forceinline__ void begin(const BranchArgs& A) {
     const int lane = threadIdx.x & 63;
-    run_ = run;
     // whether some row does not see the whole of its prefix: only then do the positions of a prefix's rows matter
     placed_ = A.window > 0;
-    for (int base = 0; base < A.b.n_seq && !placed_; base += 64) {
-      const Item t = own_item(A, min(base + lane, A.b.n_seq - 1));
-      placed_ = __any(t.n > 0 && t.p_first + 1 < t.lo);
-    }
-    float sum = 0.0f;
-    for (int base = 0; base < items(A); base += 64) {
-      const Item t = item_at(A, base + lane);
+    for (int base = 0; base < A.b.n_seq; base += 64) {
+      const Item t = own_item(A, base + lane);
       if (base == 0) first_ = t;
-      sum += (float)t.tiles * (float)t.units;
+      placed_ |= __any(t.n > 0 && t.p_first + 1 < t.split) != 0;
     }
-    sum = wave_sum(sum);
-    // units are counted in 2^shift, so that their sum fits 32 bits
-    shift_ = max(0, (int)((__float_as_uint(sum) >> 23) & 255u) - 127 - 27);
-    int total = 0;
+    if (lane >= A.b.n_seq && lane < items(A)) first_ = prefix_item(A, lane - A.b.n_seq);
+    float sum[2] = {0.0f, 0.0f};
     for (int base = 0; base < items(A); base += 64) {
-      const Item t = base == 0 ? first_ : item_at(A, base + lane);
-      total += __builtin_amdgcn_readlane(wave_inclusive_sum(t.tiles * scaled(t.units)), 63);
+      const Item t = block(A, base);
+      const Shape<D> s(rows_of(A, t), t.groups, 0);
+      sum[kShared] += (float)s.full * (float)s.each + (s.streams() ? 0.0f : (float)s.last);
+      sum[kStream] += s.streams() ? (float)s.last : 0.0f;
     }
-    per_ = max(max(1, A.min_run >> shift_), (total + A.runs - 1) / A.runs);
-    at_ = run * per_;
-    end_ = at_ + per_;
+    sum[0] = wave_sum(sum[0]);
+    sum[1] = wave_sum(sum[1]);
+    // lengths are counted in 2^shift units, so that their sums fit 32 bits
+    shift_ = max(0, (int)((__float_as_uint(fmaxf(sum[0], sum[1])) >> 23) & 255u) - 127 - 27);
+    int total[2] = {0, 0};
+    for (int base = 0; base < items(A); base += 64) {
+      const Item t = block(A, base);
+      const Shape<D> s(rows_of(A, t), t.groups, shift_);
+      for (int l = 0; l < 2; ++l) total[l] += __builtin_amdgcn_readlane(wave_inclusive_sum(s.units((Line)l)), 63);
+    }
+    const float by_wave = sum[kStream] * (1.0f / kWaves);
+    shared_ = sum[kShared] == 0.0f ? 0 : by_wave == 0.0f ? A.runs
+              : min(max((int)(A.runs * (sum[kShared] / (sum[kShared] + by_wave)) + 0.5f), 1), A.runs - 1);
+    shared_ = __builtin_amdgcn_readfirstlane(shared_);
+    const int runs[2] = {max(shared_, 1), max((A.runs - shared_) * kWaves, 1)};
+    // a part shorter than four groups' time costs more to begin and to join than it saves
+    for (int l = 0; l < 2; ++l) {
+      const int rows = l == kStream ? kStreamRows : kSmallRows;
+      per_[l] = max(max((Cost<D>::begin(rows) + 4 * Cost<D>::per_group(rows)) >> shift_, 1), (total[l] + runs[l] - 1) / runs[l]);
+    }
   }
 
-  // The plan, for the launch that joins the parts.
+  // Workgroup `number` of a head: which line it works on, and which run of it this wave has.
+  __device__ __forceinline__ Line take(int number) {
+    const Line line = number < shared_ ? kShared : kStream;
+    run_ = line == kShared ? number : (number - shared_) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    at_ = run_ * per_[line];
+    end_ = at_ + per_[line];
+    return line;
+  }
+
+  // What the launch that joins the parts has to know.
   __device__ __forceinline__ void write(const BranchArgs& A) const {
     const int lane = threadIdx.x & 63;
-    if (lane == 0) A.plan[0] = per_;
-    int before = 0;
+    if (lane == 0) *reinterpret_cast<int4*>(A.plan) = int4{per_[0], per_[1], shift_, 0};
+    int before[2] = {0, 0};
     for (int base = 0; base < items(A); base += 64) {
-      const Item t = base == 0 ? first_ : item_at(A, base + lane);
-      const int each = scaled(t.units), sum = wave_inclusive_sum(t.tiles * each);
-      if (base + lane < items(A)) {
-        A.plan[4 + 2 * (base + lane)] = before + sum - t.tiles * each;
-        A.plan[5 + 2 * (base + lane)] = each;
+      const Item t = block(A, base);
+      const Shape<D> s(rows_of(A, t), t.groups, shift_);
+      int at[2];
+      for (int l = 0; l < 2; ++l) {
+        const int mine = s.units((Line)l), sum = wave_inclusive_sum(mine);
+        at[l] = before[l] + sum - mine;
+        before[l] += __builtin_amdgcn_readlane(sum, 63);
       }
-      before += __builtin_amdgcn_readlane(sum, 63);
+      if (base + lane < items(A)) {
+        int4* to = reinterpret_cast<int4*>(A.plan + 8 + 8 * (base + lane));
+        to[0] = int4{at[0], at[1], t.groups, t.n};
+        to[1] = int4{t.row0, t.split == 0 || t.sees == 3, 0, 0};
+      }
     }
   }
 
   // The run's next segment; false past its last.
-  __device__ __forceinline__ bool next(const BranchArgs& A, Segment& g) {
+  __device__ __forceinline__ bool next(const BranchArgs& A, Line line, Segment& g) {
     if (at_ >= end_) return false;
     const int lane = threadIdx.x & 63;
     int at = at_;
     for (int base = 0; base < items(A); base += 64) {
-      const Item t = base == 0 ? first_ : item_at(A, base + lane);
-      const int each = scaled(t.units), mine = t.tiles * each, sum = wave_inclusive_sum(mine);
+      const Item t = block(A, base);
+      const Shape<D> s(rows_of(A, t), t.groups, shift_);
+      const int mine = s.units(line), sum = wave_inclusive_sum(mine);
       const int total = __builtin_amdgcn_readlane(sum, 63);
       if (at < total) {
         const int i = __builtin_ctzll(__ballot(sum > at));
         auto of = [&](int x) { return __builtin_amdgcn_readlane(x, i); };
-        g.item = Item{of(t.seq), of(t.row0), of(t.n), of(t.lo), of(t.hi), of(t.p_first), of(t.p_last), of(t.tiles), of(t.units)};
-        g.prefix = base + i < A.n_groups;
-        g.of = of(each);
-        const int start = of(sum) - of(mine);
-        g.tile = (at - start) / g.of;
-        g.from = at - start - g.tile * g.of;
-        g.to = min(g.of, g.from + end_ - at_);
+        g.item = Item{of(t.seq), of(t.lead), of(t.row0), of(t.n), of(t.split), of(t.sees), of(t.p_first), of(t.p_last), of(t.groups)};
+        const int full = of(s.full), each = of(s.each), last = of(s.last);
+        at -= of(sum) - of(mine);
+        g.line = line;
         g.run = run_;
+        g.tile = line == kStream ? full : min(at / each, full);
+        g.of = g.tile < full ? each : last;
+        g.from = at - (line == kStream ? 0 : g.tile * each);
+        g.to = min(g.of, g.from + end_ - at_);
         at_ += g.to - g.from;
         return true;
       }
@@ -188,89 +278,87 @@ class Walk {
 
   __device__ __forceinline__ bool placed() const { return placed_; }
 
+  static __device__ __forceinline__ int64_t rows_of(const BranchArgs& A, const Item& t) { return (int64_t)t.n * A.group; }
+
  private:
   Item first_;    // item `lane`
   bool placed_;
-  int shift_, per_, run_, at_, end_;
+  int shift_, per_[2], shared_, run_, at_, end_;   // shared_: workgroups a head of the shared line
 
   static __device__ __forceinline__ int items(const BranchArgs& A) { return A.n_groups + A.b.n_seq; }
-  __device__ __forceinline__ int scaled(int units) const { return (units + (1 << shift_) - 1) >> shift_; }
 
-  static __device__ __forceinline__ Item own_item(const BranchArgs& A, int s) {
+  static __device__ __forceinline__ Item own_item(const BranchArgs& A, int i) {
     Item t;
+    const int s = min(i, A.b.n_seq - 1);
     const Seq q = load_seq(A.b, s);
     const int g = group_of(A, s);
+    const Members group = members_of<D>(A, max(g, 0));
     t.seq = s;
+    t.lead = min(group.first, A.b.n_seq - 1);
     t.row0 = q.row0;
-    t.n = q.n;
-    t.lo = g < 0 ? 0 : prefix_of_group(A, max(g, 0));
-    t.hi = kNoLimit;
+    t.n = i < A.b.n_seq ? q.n : 0;
+    t.split = g < 0 ? 0 : group.prefix;
+    t.sees = g >= 0 && group.whole ? 3 : 1;
     t.p_first = q.begin;
     t.p_last = q.len - 1;
-    // a tile's rows at most, from the last on: how much it sees
-    const int rows = min(q.n, A.own_rows / A.group + 2);
-    t.tiles = (int)(((int64_t)q.n * A.group + A.own_rows - 1) / A.own_rows);
-    t.units = max(visible(A, t, q.len - rows, q.len - 1).n, A.window > 0 ? 1 : 0) * A.own_cost;   // a window may hide all from the last tile alone
+    // the last tile's rows at most: what they see is the longest; a window may hide all from that tile alone
+    const int first = q.len - min(q.n, Cost<D>::kRows / A.group + 2);
+    t.groups = q.n == 0 ? 0 : max(visible_own(A, t, first, t.p_last).n + visible_shared(A, t, first, t.p_last).n, A.window > 0 ? 1 : 0);
     return t;
   }
 
   __device__ __forceinline__ Item prefix_item(const BranchArgs& A, int g) const {
     Item t;
-    const int2 m = members(A, g);
-    t.seq = min(m.x, A.b.n_seq - 1);
-    t.row0 = min(max(A.b.q_start[m.x], 0), A.b.T);
-    t.n = max(min(A.b.q_start[m.y], A.b.T) - t.row0, 0);
-    t.lo = 0;
-    t.hi = prefix_of_group(A, g);
+    const Members group = members_of<D>(A, g);
+    t.seq = t.lead = min(group.first, A.b.n_seq - 1);
+    t.row0 = group.row0;
+    t.n = group.whole ? 0 : group.n;
+    t.split = group.prefix;
+    t.sees = 2;
     t.p_first = t.p_last = kNoLimit;   // behind the prefix
     if (placed_) {
       t.p_last = -1;
-      for (int s = m.x; s < m.y; ++s) {
+      for (int s = group.first; s < group.last; ++s) {
         const Seq q = load_seq(A.b, s);
         if (q.n == 0) continue;
         t.p_first = min(t.p_first, q.begin);
         t.p_last = max(t.p_last, q.len - 1);
       }
     }
-    t.tiles = (int)(((int64_t)t.n * A.group + A.prefix_rows - 1) / A.prefix_rows);
-    t.units = visible(A, t, t.p_first, t.p_last).n * A.prefix_cost;
+    t.groups = visible_shared(A, t, t.p_first, t.p_last).n;
     return t;
   }
 
-  __device__ __forceinline__ Item item_at(const BranchArgs& A, int i) const {
-    Item t = own_item(A, min(max(i - A.n_groups, 0), A.b.n_seq - 1));   // every lane: group_of is the wave's
-    if (i < A.n_groups) t = prefix_item(A, i);
-    if (i >= items(A)) t.tiles = t.units = 0;
+  // Items base .. base + 63, one a lane; those past the last have no rows.
+  __device__ __forceinline__ Item block(const BranchArgs& A, int base) const {
+    if (base == 0) return first_;
+    const int i = base + (threadIdx.x & 63);
+    Item t = own_item(A, i);   // in every lane: group_of is the wave's
+    if (i >= A.b.n_seq && i < items(A)) t = prefix_item(A, i - A.b.n_seq);
     return t;
   }
 };
 
 // ----------------------------------------------------------------- the parts
 template <int D, int R>
-struct Tile {
-  static constexpr bool kStream = R == 16;
-  static constexpr int kPer = kStream ? 1 : R / (16 * kWaves);   // tiles of 16 rows a wave
-  static constexpr size_t kJoin = (size_t)kWaves * R * (D + 4 + 2) * 4;   // a wave's sums, references and sums of weights
-  static constexpr size_t kLds = kStream ? kJoin : Shared<D, kPer, kWaves>::kLds;
-};
-
-template <int D, int R, bool kPrefix>
 __device__ __forceinline__ void attend_part(const BranchArgs& A, const Segment& w, bool placed, int head, u32x4* stage) {
   constexpr int C = D / 16;
   const Item& t = w.item;
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
-  const int x0 = w.tile * R, rows = (int)min((int64_t)R, (int64_t)t.n * A.group - x0);
+  const bool prefix = t.sees == 2;
+  const int lane = threadIdx.x & 63, hi = lane >> 4, lo = lane & 15;
+  const int x0 = w.tile * Cost<D>::kRows, rows = (int)min((int64_t)R, (int64_t)t.n * A.group - x0);
   // positions of rows a .. b of the tile: a sequence's follow each other, a group's are anywhere among its own
-  auto first_of = [&](int a) { return kPrefix ? t.p_first : t.p_first + (x0 + a) / A.group; };
-  auto last_of = [&](int b) { return kPrefix ? t.p_last : t.p_first + (x0 + b) / A.group; };
-  const Range see = visible(A, t, first_of(0), last_of(rows - 1));
-  const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.from / w.of));
-  const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)see.n * w.to / w.of));
+  auto first_of = [&](int a) { return prefix ? t.p_first : t.p_first + (x0 + a) / A.group; };
+  auto last_of = [&](int b) { return prefix ? t.p_last : t.p_first + (x0 + b) / A.group; };
+  const Range own = visible_own(A, t, first_of(0), last_of(rows - 1)), shared = visible_shared(A, t, first_of(0), last_of(rows - 1));
+  const int n = own.n + shared.n;
+  const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)n * w.from / w.of));
+  const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)n * w.to / w.of));
   auto place = [&](int r, int& pos) {
     const int x = x0 + r, row = t.row0 + x / A.group;
     pos = -1;
     if (r < rows) {
-      if (!kPrefix) {
+      if (!prefix) {
         pos = t.p_first + x / A.group;
       } else if (!placed) {
         pos = kNoLimit;
@@ -289,79 +377,73 @@ __device__ __forceinline__ void attend_part(const BranchArgs& A, const Segment& 
     }
     return A.q + (int64_t)row * A.ldq + (head * A.group + x % A.group) * D;
   };
-  const Tokens<true> tokens{A.b, A.c, t.seq, head, see, A.window, A.sinks, t.lo, t.hi};
-  const Parts& to_parts = kPrefix ? A.prefix : A.own;
-  const size_t part_row = (size_t)head * (A.rows + (int64_t)A.runs * R) + (size_t)t.row0 * A.group + x0 + (size_t)w.run * R;
-  __syncthreads();   // the LDS: the segment before this one
-  if constexpr (Tile<D, R>::kStream) {
-    // a prefix's codes are read by its other tiles too
-    stream_tile<D, kWaves, kPrefix ? 0 : kOnce>(tokens, from, to, rows, first_of(0), last_of(rows - 1), A.scale_log2, place,
-                                                [&](const f32x4 (&o)[1][C], const float (&m)[1], const float (&l)[1]) {
-      float* sums = reinterpret_cast<float*>(stage);                 // [kWaves][R][D + 4]
-      float* ref = sums + kWaves * R * (D + 4);                      // [kWaves][R]
-      float* weight = ref + kWaves * R;
+  const Tokens<true> tokens{A.b, A.c, t.seq, head, own, A.window, A.sinks, shared, t.lead, t.split};
+  // a tile's only part of rows that have no prefix apart is the result
+  const bool done = w.from == 0 && w.to == w.of && (t.sees == 3 || (t.sees == 1 && t.split == 0));
+  const Parts& to_parts = (prefix ? A.prefix : A.own)[w.line];
+  const size_t part_row = (size_t)head * A.places[w.line] + (size_t)t.row0 * A.group + x0 + (size_t)w.run * (R == kStreamRows ? R : Cost<D>::kRows);
+  auto put = [&](int r, const f32x4 (&o)[C], float ref, float sum) {   // row r, a lane's elements
+    if (r >= rows) return;
+    if (done) {
+      const int x = x0 + r;
+      const size_t row = (size_t)(t.row0 + x / A.group) * A.hq + head * A.group + x % A.group;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+        *reinterpret_cast<u32x2*>(A.out + row * D + c * 16 + hi * 4) = u32x2{bf16_pair(o[c][0] * inv, o[c][1] * inv), bf16_pair(o[c][2] * inv, o[c][3] * inv)};
+      if (hi == 0) write_lse(A.lse, row, ref, sum);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(to_parts.o + (part_row + r) * D + c * 16 + hi * 4) = o[c];
+      if (hi == 0) to_parts.ml[part_row + r] = float2{ref, sum};
+    }
+  };
+  if constexpr (R == kStreamRows) {
+    stream_tile<D, 1, kOnce>(tokens, from, to, rows, first_of(0), last_of(rows - 1), A.scale_log2, place,
+                             [&](const f32x4 (&o)[1][C], const float (&m)[1], const float (&l)[1]) {
       float sum = l[0];
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
-      if (hi == 0) {
-        ref[wave * R + lo] = m[0];
-        weight[wave * R + lo] = sum;
-      }
-#pragma unroll
-      for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(sums + (wave * R + lo) * (D + 4) + c * 16 + hi * 4) = o[0][c];
-      __syncthreads();
-      const int r = tid / (4 * kWaves);   // 16 threads a row
-      if (r < rows) {
-        float top = ref[r], all = 0.0f, share[kWaves];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) top = fmaxf(top, ref[v * R + r]);
-#pragma unroll
-        for (int v = 0; v < kWaves; ++v) {
-          share[v] = __builtin_amdgcn_exp2f(ref[v * R + r] - top);
-          all += weight[v * R + r] * share[v];
-        }
-#pragma unroll
-        for (int e = tid % 16 * 4; e < D; e += 64) {
-          f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int v = 0; v < kWaves; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(sums + (v * R + r) * (D + 4) + e);
-          *reinterpret_cast<f32x4*>(to_parts.o + (part_row + r) * D + e) = y;
-        }
-        if (tid % 16 == 0) to_parts.ml[part_row + r] = float2{top, all};
-      }
+      put(lo, o[0], m[0], sum);
     });
   } else {
-    constexpr int N = Tile<D, R>::kPer;
-    const int mine0 = wave * 16 * N;
+    constexpr int N = R / (16 * kWaves);
+    const int mine0 = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * 16 * N;
+    __syncthreads();   // the LDS: the segment before this one
     shared_tile<D, N, kWaves>(tokens, from, to, rows, first_of(mine0), last_of(min(rows, mine0 + 16 * N) - 1), A.scale_log2, place, stage,
                               [&](const f32x4 (&o)[N][C], const float (&m)[N], const float (&l)[N]) {
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        const int r = mine0 + u * 16 + lo;
         float sum = l[u];
         sum += __shfl_xor(sum, 16);
         sum += __shfl_xor(sum, 32);
-        if (r >= rows) continue;
-#pragma unroll
-        for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(to_parts.o + (part_row + r) * D + c * 16 + hi * 4) = o[u][c];
-        if (hi == 0) to_parts.ml[part_row + r] = float2{m[u], sum};
+        put(mine0 + u * 16 + lo, o[u], m[u], sum);
       }
     });
   }
 }
 
-template <int D, int RP, int RS>
-__global__ __launch_bounds__(kThreads, D == 256 && RS == 16 ? 1 : 2) void branch_parts_kernel(BranchArgs A) {
+template <int D>
+constexpr size_t kLds = std::max(Shared<D, 1, kWaves>::kLds, Shared<D, Cost<D>::kRows / (16 * kWaves), kWaves>::kLds);
+
+template <int D>
+__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void branch_parts_kernel(BranchArgs A) {
   extern __shared__ __align__(16) u32x4 stage[];
   const int head = blockIdx.x % A.c.hkv;
-  Walk walk;
-  walk.begin(A, blockIdx.x / A.c.hkv);
+  Walk<D> walk;
+  walk.begin(A);
   if (blockIdx.x == 0 && threadIdx.x < 64) walk.write(A);
-  for (Segment w; walk.next(A, w);) {
-    if (w.prefix)
-      attend_part<D, RP, true>(A, w, walk.placed(), head, stage);
-    else
-      attend_part<D, RS, false>(A, w, false, head, stage);
+  const Line line = walk.take(blockIdx.x / A.c.hkv);
+  for (Segment w; walk.next(A, line, w);) {
+    if (line == kStream) {
+      attend_part<D, kStreamRows>(A, w, walk.placed(), head, stage);
+    } else {
+      constexpr int H = Cost<D>::kRows;
+      if (H == kSmallRows || Walk<D>::rows_of(A, w.item) - (int64_t)w.tile * H <= kSmallRows)
+        attend_part<D, kSmallRows>(A, w, walk.placed(), head, stage);
+      else
+        attend_part<D, H>(A, w, walk.placed(), head, stage);
+    }
   }
 }
 
@@ -369,7 +451,7 @@ __global__ __launch_bounds__(kThreads, D == 256 && RS == 16 ? 1 : 2) void branch
 // A row of one query head: W waves take turns at its parts.
 template <int D, int W>
 __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
-  constexpr int E = D / 64;   // elements a lane
+  constexpr int E = D / 64, H = Cost<D>::kRows;   // elements a lane
   __shared__ float sums[kWaves][D], refs[kWaves], weights[kWaves];
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int turn = wave % W;
@@ -382,40 +464,49 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
     s += before;
     if (before < 64) break;
   }
-  const Seq q = load_seq(A.b, max(s, 0));
-  const bool there = s >= 0 && r < A.b.T && r >= q.row0 && r < q.row0 + q.n;
-  if (W == 1 && !there) return;   // more waves: all of them or none
   const int g = __builtin_amdgcn_readfirstlane(group_of(A, s));
+  const Seq q = load_seq(A.b, max(s, 0));
+  if (s < 0 || r >= A.b.T || r < q.row0 || r >= q.row0 + q.n) return;   // all waves of a row, which are a workgroup's, or the one
   const int64_t x = (int64_t)r * A.group + h % A.group;
-  const int per = A.plan[0];
-  auto parts_of = [&](int item, int row0, int rows, int R, int& first) {
-    if (r < row0 || r >= row0 + rows) return 0;   // groups and sequences that do not fit each other
-    const int units = A.plan[5 + 2 * item], at = A.plan[4 + 2 * item] + (int)((x - (int64_t)row0 * A.group) / R) * units;
-    first = at / per;
-    return units == 0 ? 0 : (at + units - 1) / per - first + 1;
+  const int4 plan = *reinterpret_cast<const int4*>(A.plan);
+  // an item's parts of this row: where the first is, how far apart they are, how many
+  struct Run {
+    const float* o;
+    const float2* ml;
+    int step, n;
+    bool alone;
   };
-  int first_prefix = 0, first_own = 0, n_prefix = 0, n_own = 0;
-  if (there) {
-    if (g >= 0) {
-      const int2 m = members(A, g);
-      const int row0 = min(max(A.b.q_start[m.x], 0), A.b.T);
-      n_prefix = parts_of(g, row0, min(A.b.q_start[m.y], A.b.T) - row0, A.prefix_rows, first_prefix);
-    }
-    n_own = parts_of(A.n_groups + s, q.row0, q.n, A.own_rows, first_own);
-  }
-  const int n = n_prefix + n_own;
-  const size_t prefix_at = (size_t)head * (A.rows + (int64_t)A.runs * A.prefix_rows) + x + (size_t)first_prefix * A.prefix_rows;
-  const size_t own_at = (size_t)head * (A.rows + (int64_t)A.runs * A.own_rows) + x + (size_t)first_own * A.own_rows;
+  auto parts_of = [&](int item, const Parts (&all)[2]) {
+    const int4* of = reinterpret_cast<const int4*>(A.plan + 8 + 8 * item);
+    const int4 a = of[0], b = of[1];
+    Run p{nullptr, nullptr, 0, 0, b.y != 0};
+    const int64_t y = x - (int64_t)b.x * A.group, rows = (int64_t)a.w * A.group;
+    if (y < 0 || y >= rows || a.z == 0) return p;   // nothing to see, or groups and sequences that do not fit each other
+    const Shape<D> shape(rows, a.z, plan.z);
+    const int tile = min((int)(y / H), shape.full);
+    const Line line = tile == shape.full && shape.streams() ? kStream : kShared;
+    const int length = tile < shape.full ? shape.each : shape.last, at = line == kStream ? a.y : a.x + tile * shape.each;
+    const int per = line == kStream ? plan.y : plan.x, first = at / per;
+    p.step = line == kStream ? kStreamRows : H;
+    p.n = (at + length - 1) / per - first + 1;
+    const size_t place = (size_t)head * A.places[line] + x + (size_t)first * p.step;
+    p.o = all[line].o + place * D;
+    p.ml = all[line].ml + place;
+    return p;
+  };
+  const Run own = parts_of(s, A.own);
+  Run prefix{nullptr, nullptr, 0, 0, false};
+  if (g >= 0) prefix = parts_of(A.b.n_seq + g, A.prefix);
+  if (own.alone && own.n == 1) return;   // the result already
+  const int n = prefix.n + own.n;
   float top = kLowest, sum = 0.0f, y[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) y[e] = 0.0f;
   for (int base = turn; base < n; base += 64 * W) {
     // lane k: part base + k W
     const int k = base + lane * W;
-    const bool of_prefix = k < n_prefix;
-    const size_t at = of_prefix ? prefix_at + (size_t)k * A.prefix_rows : own_at + (size_t)(k - n_prefix) * A.own_rows;
     float2 ml = {kLowest, 0.0f};
-    if (k < n) ml = (of_prefix ? A.prefix.ml : A.own.ml)[at];
+    if (k < n) ml = k < prefix.n ? prefix.ml[(size_t)k * prefix.step] : own.ml[(size_t)(k - prefix.n) * own.step];
     const float next = fmaxf(top, wave_max(ml.x)), share = __builtin_amdgcn_exp2f(ml.x - next), down = __builtin_amdgcn_exp2f(top - next);
     sum = sum * down + wave_sum(k < n ? share * ml.y : 0.0f);
     top = next;
@@ -423,19 +514,19 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
     for (int e = 0; e < E; ++e) y[e] *= down;
     const int count = min(64, (n - base + W - 1) / W);
     for (int j0 = 0; j0 < count; j0 += 8) {   // eight parts' loads under way together; past the last, that once more with no share
-      float x[8][E], w[8];
+      float v[8][E], by[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int at_j = min(j0 + j, count - 1), kj = base + at_j * W;
-        const float* o = kj < n_prefix ? A.prefix.o + (prefix_at + (size_t)kj * A.prefix_rows) * D : A.own.o + (own_at + (size_t)(kj - n_prefix) * A.own_rows) * D;
-        w[j] = j0 + j < count ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(share), at_j)) : 0.0f;
+        const float* o = kj < prefix.n ? prefix.o + (size_t)kj * prefix.step * D : own.o + (size_t)(kj - prefix.n) * own.step * D;
+        by[j] = j0 + j < count ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(share), at_j)) : 0.0f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[j][e] = o[lane * E + e];
+        for (int e = 0; e < E; ++e) v[j][e] = o[lane * E + e];
       }
 #pragma unroll
       for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(w[j], x[j][e], y[e]);
+        for (int e = 0; e < E; ++e) y[e] = fmaf(by[j], v[j][e], y[e]);
     }
   }
   if (W > 1) {
@@ -443,7 +534,7 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
     for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = y[e];
     if (lane == 0) refs[wave] = top, weights[wave] = sum;
     __syncthreads();
-    if (turn > 0 || !there) return;
+    if (turn > 0) return;
     float all = refs[wave];
 #pragma unroll
     for (int v = 1; v < W; ++v) all = fmaxf(all, refs[wave + v]);
@@ -460,56 +551,46 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
     top = all;
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  uint16_t* to = A.out + ((size_t)r * A.hq + h) * D + lane * E;
+  const size_t row = (size_t)r * A.hq + h;
+  uint16_t* to = A.out + row * D + lane * E;
   if constexpr (E == 1) {
     *to = (uint16_t)bf16_pair(y[0] * inv, 0.0f);
   } else {
 #pragma unroll
     for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(to + e) = bf16_pair(y[e] * inv, y[e + 1] * inv);
   }
-  if (lane == 0 && A.lse) A.lse[(size_t)r * A.hq + h] = sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
+  if (lane == 0) write_lse(A.lse, row, top, sum);
 }
 
 // ------------------------------------------------------------------- launch
-// Tiles by the rows that an average group (and an average sequence) has for one
-// kv head.
-int tile_rows(int64_t rows, int D) { return rows <= 16 ? 16 : rows <= 64 || D == 256 ? 64 : 128; }
-int runs_of(int hkv, int D) { return std::max(1, (D == 256 ? 256 : 512) / hkv); }
-// What 32 tokens cost a tile, as a multiple of what they cost one of 16 rows.
-int cost_of(int rows) { return rows == 16 ? 1 : rows == 64 ? 2 : 4; }
+// Workgroups that run at once, by head; two at least, so that both lines have one.
+int runs_of(int hkv, int D) { return std::max(2, (D == 256 ? 256 : 512) / hkv); }
+int rows_of_tall(int D) { return D == 256 ? 64 : 128; }
 
-constexpr size_t kAlign = 256;
-size_t rounded(size_t bytes) { return (bytes + kAlign - 1) / kAlign * kAlign; }
-size_t plan_bytes(int64_t items) { return rounded((4 + 2 * items) * 4); }
-size_t parts_rows(int64_t rows, int hkv, int D, int R) { return (size_t)hkv * (rows + (int64_t)runs_of(hkv, D) * R); }
-size_t workspace_bytes(int64_t rows, int64_t items, int hkv, int D, int RP, int RS) {
-  size_t bytes = plan_bytes(items);
-  for (int R : {RP, RS}) bytes += rounded(parts_rows(rows, hkv, D, R) * D * 4) + rounded(parts_rows(rows, hkv, D, R) * 8);
-  return bytes;
+size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
+size_t plan_bytes(int64_t items) { return rounded((8 + 8 * items) * 4); }
+// Places of a line: the rows, and a tile's height a run.
+int64_t places_of(int64_t rows, int hkv, int D, int line) {
+  if (line == kStream) return rows + (int64_t)runs_of(hkv, D) * kWaves * kStreamRows;
+  return rows <= kStreamRows ? 0 : rows + (int64_t)runs_of(hkv, D) * rows_of_tall(D);   // no tile has more than 16 rows
 }
-
-template <int D, int RP, int RS>
-int launch_parts(const BranchArgs& A, hipStream_t s) {
-  constexpr size_t kLds = std::max(Tile<D, RP>::kLds, Tile<D, RS>::kLds);
-  static dh::OncePerDevice once;
-  const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_parts_kernel<D, RP, RS>), kLds);
-  if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_parts_kernel: %s", hipGetErrorString(e));
-  hipLaunchKernelGGL((branch_parts_kernel<D, RP, RS>), dim3((unsigned)(A.runs * A.c.hkv)), dim3(kThreads), kLds, s, A);
-  return launched("branch_parts_kernel");
+size_t sums_bytes(int64_t places, int hkv, int D) { return rounded((size_t)places * hkv * D * 4); }
+size_t refs_bytes(int64_t places, int hkv) { return rounded((size_t)places * hkv * 8); }
+size_t workspace_bytes(int64_t rows, int64_t items, int hkv, int D) {
+  size_t bytes = plan_bytes(items);
+  for (int line = 0; line < 2; ++line) {
+    const int64_t places = places_of(rows, hkv, D, line);
+    bytes += 2 * (sums_bytes(places, hkv, D) + refs_bytes(places, hkv));
+  }
+  return bytes;
 }
 
 template <int D>
 int launch(const BranchArgs& A, hipStream_t s) {
-  int rc;
-  if (A.prefix_rows == 16)
-    rc = launch_parts<D, 16, 16>(A, s);
-  else if (A.prefix_rows == 64)
-    rc = A.own_rows == 16 ? launch_parts<D, 64, 16>(A, s) : launch_parts<D, 64, 64>(A, s);
-  else if constexpr (D == 256)
-    return dh::fail(DH_EUNSUP, "attend: no tile of %d rows", A.prefix_rows);
-  else
-    rc = A.own_rows == 16 ? launch_parts<D, 128, 16>(A, s) : A.own_rows == 64 ? launch_parts<D, 128, 64>(A, s) : launch_parts<D, 128, 128>(A, s);
-  if (rc) return rc;
+  static dh::OncePerDevice once;
+  const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_parts_kernel<D>), kLds<D>);
+  if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_parts_kernel: %s", hipGetErrorString(e));
+  hipLaunchKernelGGL((branch_parts_kernel<D>), dim3((unsigned)(A.runs * A.c.hkv)), dim3(kThreads), kLds<D>, s, A);
   const int64_t rows = (int64_t)A.b.T * A.hq;
   if (rows <= 2048)
     hipLaunchKernelGGL((branch_join_kernel<D, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, s, A);
@@ -527,10 +608,7 @@ int draft_branch_attend_workspace_bytes(int T, int n_seq, int hq, int hkv, int D
   int rc = check_heads("attend_workspace_bytes", hq, hkv, D);
   if (rc) return rc;
   if ((rc = check_rows("attend_workspace_bytes", T, n_seq))) return rc;
-  // fewer sequences or groups have more rows each, up to all T in one
-  const int64_t rows = (int64_t)T * (hq / hkv);
-  const int R = tile_rows(rows, D);
-  *bytes = workspace_bytes(rows, 2 * (int64_t)n_seq, hkv, D, R, R);
+  *bytes = workspace_bytes((int64_t)T * (hq / hkv), 2 * (int64_t)n_seq, hkv, D);
   return dh::ok();
 }
 
@@ -560,10 +638,8 @@ int draft_branch_attend(const void* q, int64_t ldq, const uint8_t* k_codes, cons
   if (lse && !aligned(lse, 4)) return dh::fail(DH_EINVAL, "attend: lse must be 4-byte aligned");
   if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "attend: workspace must be a 16-byte aligned pointer");
   A.group = hq / hkv;
-  A.rows = (int64_t)T * A.group;
-  A.prefix_rows = tile_rows((A.rows + n_groups - 1) / n_groups, D);
-  A.own_rows = tile_rows((A.rows + n_seq - 1) / n_seq, D);
-  const size_t need = workspace_bytes(A.rows, (int64_t)n_groups + n_seq, hkv, D, A.prefix_rows, A.own_rows);
+  const int64_t rows = (int64_t)T * A.group, items = (int64_t)n_groups + n_seq;
+  const size_t need = workspace_bytes(rows, items, hkv, D);
   if (workspace_bytes_given < need)
     return dh::fail(DH_EINVAL, "attend: workspace of %zu bytes is below the %zu needed", workspace_bytes_given, need);
   A.group_start = group_start;
@@ -578,20 +654,19 @@ int draft_branch_attend(const void* q, int64_t ldq, const uint8_t* k_codes, cons
   A.out = static_cast<uint16_t*>(out);
   A.lse = lse;
   A.runs = runs_of(hkv, D);
-  A.min_run = 8;
-  A.prefix_cost = cost_of(A.prefix_rows);
-  A.own_cost = cost_of(A.own_rows);
   unsigned char* at = static_cast<unsigned char*>(workspace);
   auto take = [&](size_t bytes) {
     unsigned char* p = at;
-    at += rounded(bytes);
+    at += bytes;
     return p;
   };
-  A.plan = reinterpret_cast<int32_t*>(take(plan_bytes((int64_t)n_groups + n_seq)));
-  for (Parts* p : {&A.prefix, &A.own}) {
-    const size_t rows = parts_rows(A.rows, hkv, D, p == &A.prefix ? A.prefix_rows : A.own_rows);
-    p->o = reinterpret_cast<float*>(take(rows * D * 4));
-    p->ml = reinterpret_cast<float2*>(take(rows * 8));
+  A.plan = reinterpret_cast<int32_t*>(take(plan_bytes(items)));
+  for (int line = 0; line < 2; ++line) {
+    A.places[line] = places_of(rows, hkv, D, line);
+    for (Parts* p : {&A.prefix[line], &A.own[line]}) {
+      p->o = reinterpret_cast<float*>(take(sums_bytes(A.places[line], hkv, D)));
+      p->ml = reinterpret_cast<float2*>(take(refs_bytes(A.places[line], hkv)));
+    }
   }
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   switch (D) {
