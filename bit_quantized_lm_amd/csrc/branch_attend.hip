@@ -9,6 +9,7 @@
 // the prefix is loaded once for up to 128 of them.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/draftbranch.h"
 #include "attend_tile.h"
@@ -45,7 +46,7 @@ struct BranchArgs {
   int runs;           // workgroups a head
   int64_t places[2];  // a head's, by line
   Parts prefix[2], own[2];
-  int32_t* plan;      // left by the first launch for the second: units of a run by line, then 8 numbers an item
+  int32_t* plan;      // a Plan, then a Record an item
 };
 
 // ------------------------------------------------------------------ the work
@@ -63,39 +64,42 @@ struct BranchArgs {
 // another; what it has of a tile is a part.  The workgroups are divided between the
 // lines by what the lines take.
 struct Item {
-  int seq, lead;         // whose table rows name the pages of the own and of the shared tokens
-  int row0, n;           // token rows
-  int split;             // positions below are the shared ones
-  int sees;              // 1: the own tokens, 2: the shared ones
-  int p_first, p_last;   // the rows' positions
   int groups;            // of 32 tokens that a tile sees at most
+  int n, row0;           // token rows
+  int sees;              // 1: the own tokens, 2: the shared ones
+  int split;             // positions below are the shared ones
+  int of;                // the sequence's group, -1: none
+  int seq, lead;         // whose table rows name the pages of the own and of the shared tokens
+  int p_first, p_last;   // the rows' positions
 };
 
 // Lengths of tiles in units of about 0.1 us of a workgroup (of a wave, for the
-// stream): what a tile's beginning and end take, and what a group of 32 tokens
-// takes: on a full card a tile of 128 rows with heads of 128 takes 1.2 us a group.
+// stream): what a tile's beginning and end take, and what a group of 32 tokens takes.
+// Measured with heads of 128 on a full card: 2.2 + 0.8 us a group for 64 rows, 3.0 +
+// 1.15 for 128, 2.0 + 1.6 for a wave's 16, and 1.4 to 3 us to set up and to leave.
 template <int D>
 struct Cost {
   static constexpr int kRows = D == 256 ? 64 : 128;     // H
   static __host__ __device__ constexpr int per_group(int rows) {
-    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 7 : 12) * D / 128);
+    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 8 : 12) * D / 128);
   }
-  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 40 : 50; }
+  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 35 : rows <= kSmallRows ? 45 : 60; }
   static __device__ __forceinline__ int of(int rows, int groups) { return groups == 0 ? 0 : begin(rows) + groups * per_group(rows); }
 };
 
-// An item's tiles: `full` ones of H rows, then one of `rest`.
+// An item's tiles: `full` ones of H rows, then one of `rest`, and their units, of
+// 2^shift (whole: 1 for the stream's).
 template <int D>
 struct Shape {
-  int full, rest, each, last;    // tiles and their units
-  __device__ __forceinline__ Shape(int64_t rows, int groups, int shift) {
+  int full, rest, each, last;
+  __device__ __forceinline__ Shape(int64_t rows, int groups, int shift, bool whole) {
     constexpr int H = Cost<D>::kRows;
+    if (groups == 0) rows = 0;
     full = (int)(rows / H);
     rest = (int)(rows % H);
     auto scaled = [&](int units) { return (int)(((int64_t)units + (1 << shift) - 1) >> shift); };
-    each = scaled(Cost<D>::of(H, groups));
-    last = rest == 0 ? 0 : scaled(Cost<D>::of(rest, groups));
-    if (groups == 0) full = rest = 0;
+    each = max(scaled(Cost<D>::of(H, groups)), 1);
+    last = rest == 0 ? 0 : whole && streams() ? 1 : scaled(Cost<D>::of(rest, groups));
   }
   __device__ __forceinline__ bool streams() const { return rest <= kStreamRows; }
   __device__ __forceinline__ int units(Line line) const {
@@ -123,40 +127,21 @@ __device__ __forceinline__ Range visible_shared(const BranchArgs& A, const Item&
   return t.sees & 2 ? visible(A, 0, t.split, p_first, p_last) : Range{};
 }
 
-// The group that sequence s (its own in each lane; every lane calls it) is of, or -1.
-__device__ __forceinline__ int group_of(const BranchArgs& A, int s) {
-  int g = -1;
-  if (A.n_groups < 64) {
-    const int lane = threadIdx.x & 63, mine = A.group_start[min(lane, A.n_groups)];
-    for (int i = 0; i <= A.n_groups; ++i) g += __builtin_amdgcn_readlane(mine, i) <= s;
-  } else {   // the last that starts at or before s
-    int lo = 0, hi = A.n_groups + 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (A.group_start[mid] <= s)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    g = lo - 1;
-  }
-  return g < A.n_groups ? g : -1;
-}
-
 struct Members {
   int first, last;    // sequences first .. last - 1
   int row0, n;        // token rows
   int prefix;
   bool whole;         // its prefix's tokens count as the sequences' own
 };
-template <int D>
-__device__ __forceinline__ Members members_of(const BranchArgs& A, int g) {
+// A group from its entries of the lists; rows_before(s) is q_start[s].
+template <int D, class Rows>
+__device__ __forceinline__ Members members_of(const BranchArgs& A, int2 group, int prefix, const Rows rows_before) {
   Members r;
-  r.first = min(max(A.group_start[g], 0), A.b.n_seq);
-  r.last = max(r.first, min(A.group_start[g + 1], A.b.n_seq));
-  r.row0 = min(max(A.b.q_start[r.first], 0), A.b.T);
-  r.n = max(min(A.b.q_start[r.last], A.b.T) - r.row0, 0);
-  r.prefix = min(max(A.prefix_len[g], 0), kNoLimit);
+  r.first = min(max(group.x, 0), A.b.n_seq);
+  r.last = max(r.first, min(group.y, A.b.n_seq));
+  r.row0 = min(max(rows_before(r.first), 0), A.b.T);
+  r.n = max(min(rows_before(r.last), A.b.T) - r.row0, 0);
+  r.prefix = min(max(prefix, 0), kNoLimit);
   r.whole = (int64_t)r.n * A.group >= (int64_t)Cost<D>::kRows * (r.last - r.first);
   return r;
 }
@@ -165,178 +150,302 @@ __device__ __forceinline__ void write_lse(float* lse, size_t row, float ref, flo
   if (lse) lse[row] = sum == 0.0f ? -INFINITY : (ref + __builtin_amdgcn_logf(sum)) * 0.693147180559945f;
 }
 
+// Sequence s with the group that it is of (g < 0: none).
+template <int D>
+__device__ __forceinline__ Item own_item(const BranchArgs& A, int s, const Seq& q, int g, const Members& group) {
+  Item t;
+  t.n = q.n;
+  t.row0 = q.row0;
+  t.sees = g >= 0 && group.whole ? 3 : 1;
+  t.split = g < 0 ? 0 : group.prefix;
+  t.of = g;
+  t.seq = s;
+  t.lead = min(group.first, A.b.n_seq - 1);
+  t.p_first = q.begin;
+  t.p_last = q.len - 1;
+  // the last tile's rows at most: what they see is the longest; a window may hide all from that tile alone
+  const int first = q.len - min(q.n, Cost<D>::kRows / A.group + 2);
+  t.groups = q.n == 0 ? 0 : max(visible_own(A, t, first, t.p_last).n + visible_shared(A, t, first, t.p_last).n, A.window > 0 ? 1 : 0);
+  return t;
+}
+
+// A group whose rows are at p_first .. p_last.
+__device__ __forceinline__ Item prefix_item(const BranchArgs& A, const Members& group, int p_first, int p_last) {
+  Item t;
+  t.n = group.whole ? 0 : group.n;
+  t.row0 = group.row0;
+  t.sees = 2;
+  t.split = group.prefix;
+  t.of = -1;
+  t.seq = t.lead = min(group.first, A.b.n_seq - 1);
+  t.p_first = p_first;
+  t.p_last = p_last;
+  t.groups = visible_shared(A, t, p_first, p_last).n;
+  return t;
+}
+
+// Whether the row at p_first does not see the whole of its prefix: only where some
+// row does not, or has a window, do the positions of a prefix's rows matter.
+__device__ __forceinline__ bool inside_prefix(const Item& t) { return t.n > 0 && t.p_first + 1 < t.split; }
+
+// ------------------------------------------------------------------ the plan
+// What every part and the joining go by, from the lengths.
+struct Plan {
+  int per[2];    // units of a run, by line
+  int shift;     // units are 2^shift, so that their sums fit 32 bits
+  int whole;     // the stream's tiles are a wave each
+  int shared;    // workgroups a head of the shared line
+  int placed;    // the positions of a prefix's rows matter
+  int unused[2];
+};
+struct Record {
+  int at[2];     // first unit, by line
+  Item item;
+};
+static_assert(sizeof(Plan) == 32 && sizeof(Record) == 48, "both are read 16 bytes at a time");
+
+struct Sums {    // of all items' tiles, in units
+  float units[2] = {0.0f, 0.0f}, tiles = 0.0f, longest = 0.0f;   // the last two: the stream's
+  template <int D>
+  __device__ __forceinline__ void add(const Shape<D>& s) {
+    const float stream = (float)s.units(kStream);
+    units[kShared] += (float)s.units(kShared);
+    units[kStream] += stream;
+    tiles += stream > 0.0f ? 1.0f : 0.0f;
+    longest = fmaxf(longest, stream);
+  }
+};
+
+// The lines' shares of the workgroups: by their work; or a wave a tile for the
+// stream, where both lines end as soon so.  Nothing ends before a part of four groups.
+template <int D>
+__device__ __forceinline__ void divide(const BranchArgs& A, const Sums& sum, Plan& p) {
+  const float shared = sum.units[kShared], stream = sum.units[kStream], runs = (float)A.runs;
+  const float even = (shared + stream * (1.0f / kWaves)) / runs;
+  const float end = fmaxf(even, (float)Cost<D>::of(kSmallRows, 4)) + (float)Cost<D>::begin(kStreamRows) * 0.5f;
+  const float rest = runs - ceilf(sum.tiles * (1.0f / kWaves));
+  p.whole = stream > 0.0f && sum.longest <= end && shared <= rest * end && rest >= 0.0f;
+  p.shared = (int)(p.whole ? rest : stream == 0.0f ? runs : shared == 0.0f ? 0.0f : fminf(fmaxf(rintf(shared / even), 1.0f), runs - 1.0f));
+  p.shift = max(0, (int)((__float_as_uint(fmaxf(shared, stream)) >> 23) & 255u) - 127 - 27);
+}
+
+// A part of fewer than four groups costs more to begin and to join than it saves.
+template <int D>
+__device__ __forceinline__ void cut(const BranchArgs& A, int shared_units, int stream_units, Plan& p) {
+  const int waves = max(A.runs - p.shared, 1) * kWaves;
+  p.per[kShared] = max(max((4 * Cost<D>::per_group(kSmallRows)) >> p.shift, 1), (shared_units + p.shared - 1) / max(p.shared, 1));
+  p.per[kStream] = p.whole ? 1 : max(max((4 * Cost<D>::per_group(kStreamRows)) >> p.shift, 1), (stream_units + waves - 1) / waves);
+}
+
+// Up to 64 sequences and groups: one wave, a sequence and a group a lane, the
+// lists' entries passed between the lanes.  Every workgroup makes the plan for itself.
+constexpr int kSmall = 64;
+template <int D>
+__device__ __forceinline__ void make_plan(const BranchArgs& A, Plan* plan, Record* records) {
+  const int lane = threadIdx.x & 63, s = min(lane, A.b.n_seq - 1), g = min(lane, A.n_groups - 1);
+  const int start = A.b.q_start[s], end = A.b.q_start[s + 1], length = A.b.kv_len[s];
+  const int2 group{A.group_start[g], A.group_start[g + 1]};
+  const int prefix = A.prefix_len[g];
+  const int all_rows = __builtin_amdgcn_readlane(end, A.b.n_seq - 1), all_seqs = __builtin_amdgcn_readlane(group.y, A.n_groups - 1);
+  auto rows_before = [&](int i) {
+    const int there = __shfl(start, i);   // by every lane: none is another's source else
+    return i < A.b.n_seq ? there : all_rows;
+  };
+  Seq q;
+  q.row0 = min(max(start, 0), A.b.T);
+  q.n = max(min(end, A.b.T) - q.row0, 0);
+  q.len = min(max(length, 0), DL_MAX_POSITIONS);
+  q.begin = q.len - q.n;
+  int of = -1;
+  for (int i = 0; i < A.n_groups; ++i) of += __builtin_amdgcn_readlane(group.x, i) <= s;
+  of = all_seqs <= s ? -1 : of;
+  const int from = max(of, 0);
+  const int group_prefix = __shfl(prefix, from);
+  const Members mine = members_of<D>(A, int2{__shfl(group.x, from), __shfl(group.y, from)}, group_prefix, rows_before);
+  const Members members = members_of<D>(A, group, prefix, rows_before);
+  Item own = own_item<D>(A, s, q, of, mine);
+  if (lane >= A.b.n_seq) own.n = 0;
+  Plan p{};
+  p.placed = A.window > 0 || __any(inside_prefix(own));
+  int p_first = kNoLimit, p_last = kNoLimit;   // behind every prefix
+  if (p.placed) {
+    p_last = -1;
+    for (int i = 0; i < A.b.n_seq; ++i) {
+      const int n = __builtin_amdgcn_readlane(q.n, i), len = __builtin_amdgcn_readlane(q.len, i);
+      if (n == 0 || i < members.first || i >= members.last) continue;
+      p_first = min(p_first, len - n);
+      p_last = max(p_last, len - 1);
+    }
+  }
+  Item shared = prefix_item(A, members, p_first, p_last);
+  if (lane >= A.n_groups) shared.n = 0;
+  const int64_t own_rows = (int64_t)own.n * A.group, shared_rows = (int64_t)shared.n * A.group;
+  Sums sum;
+  sum.add(Shape<D>(own_rows, own.groups, 0, false));
+  sum.add(Shape<D>(shared_rows, shared.groups, 0, false));
+  for (float& x : sum.units) x = wave_sum(x);
+  sum.tiles = wave_sum(sum.tiles);
+  sum.longest = wave_max(sum.longest);
+  divide<D>(A, sum, p);
+  const Shape<D> a(own_rows, own.groups, p.shift, p.whole), b(shared_rows, shared.groups, p.shift, p.whole);
+  Record r[2] = {{{0, 0}, own}, {{0, 0}, shared}};
+  int total[2];
+#pragma unroll
+  for (int l = 0; l < 2; ++l) {
+    const int x = a.units((Line)l), y = b.units((Line)l), to_x = wave_inclusive_sum(x), to_y = wave_inclusive_sum(y);
+    const int before = __builtin_amdgcn_readlane(to_x, 63);
+    r[0].at[l] = to_x - x;
+    r[1].at[l] = before + to_y - y;
+    total[l] = before + __builtin_amdgcn_readlane(to_y, 63);
+  }
+  cut<D>(A, total[kShared], total[kStream], p);
+  if (lane < A.b.n_seq) records[lane] = r[0];
+  if (lane < A.n_groups) records[A.b.n_seq + lane] = r[1];
+  if (lane == 0) *plan = p;
+}
+
+// More: a launch of its own makes it, one workgroup.
+constexpr int kPlanThreads = 1024;
+template <int D>
+__global__ __launch_bounds__(kPlanThreads) void branch_plan_kernel(BranchArgs A) {
+  __shared__ int first[DL_MAX_SEQS], last[DL_MAX_SEQS];   // positions of a group's rows
+  __shared__ float sums[4][kPlanThreads / 64];
+  __shared__ int totals[2][kPlanThreads / 64];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, items = A.b.n_seq + A.n_groups;
+  Plan* plan = reinterpret_cast<Plan*>(A.plan);
+  Record* records = reinterpret_cast<Record*>(plan + 1);
+  auto rows_before = [&](int i) { return A.b.q_start[i]; };
+  auto members = [&](int g) { return members_of<D>(A, int2{A.group_start[g], A.group_start[g + 1]}, A.prefix_len[g], rows_before); };
+  for (int g = tid; g < A.n_groups; g += kPlanThreads) first[g] = kNoLimit, last[g] = -1;
+  __syncthreads();
+  Sums sum;
+  bool inside = false;
+  for (int s = tid; s < A.b.n_seq; s += kPlanThreads) {
+    int g = 0;   // groups that start at or before s
+    for (int end = A.n_groups + 1; g < end;) {
+      const int mid = (g + end) >> 1;
+      if (A.group_start[mid] <= s)
+        g = mid + 1;
+      else
+        end = mid;
+    }
+    g = g - 1 < A.n_groups ? g - 1 : -1;
+    const Seq q = load_seq(A.b, s);
+    const Item t = own_item<D>(A, s, q, g, members(max(g, 0)));
+    inside |= inside_prefix(t);
+    if (g >= 0 && q.n > 0) {
+      atomicMin(&first[g], q.begin);
+      atomicMax(&last[g], q.len - 1);
+    }
+    sum.add(Shape<D>((int64_t)t.n * A.group, t.groups, 0, false));
+    records[s].item = t;
+  }
+  Plan p{};
+  p.placed = __syncthreads_or(inside) || A.window > 0;
+  for (int g = tid; g < A.n_groups; g += kPlanThreads) {
+    const Item t = prefix_item(A, members(g), p.placed ? first[g] : kNoLimit, p.placed ? last[g] : kNoLimit);
+    sum.add(Shape<D>((int64_t)t.n * A.group, t.groups, 0, false));
+    records[A.b.n_seq + g].item = t;
+  }
+  const float of_wave[4] = {wave_sum(sum.units[0]), wave_sum(sum.units[1]), wave_sum(sum.tiles), wave_max(sum.longest)};
+  if (lane == 0)
+    for (int i = 0; i < 4; ++i) sums[i][wave] = of_wave[i];
+  __syncthreads();
+  sum = Sums{};
+  for (int w = 0; w < kPlanThreads / 64; ++w) {
+    sum.units[0] += sums[0][w];
+    sum.units[1] += sums[1][w];
+    sum.tiles += sums[2][w];
+    sum.longest = fmaxf(sum.longest, sums[3][w]);
+  }
+  divide<D>(A, sum, p);
+  int before[2] = {0, 0};
+  for (int base = 0; base < items; base += kPlanThreads) {
+    const int i = base + tid;
+    const Shape<D> s(i < items ? (int64_t)records[i].item.n * A.group : 0, i < items ? records[i].item.groups : 0, p.shift, p.whole);
+    int to[2], mine[2];
+    __syncthreads();
+    for (int l = 0; l < 2; ++l) {
+      mine[l] = s.units((Line)l);
+      to[l] = wave_inclusive_sum(mine[l]);
+      if (lane == 63) totals[l][wave] = to[l];
+    }
+    __syncthreads();
+    for (int l = 0; l < 2; ++l) {
+      int all = 0, here = 0;
+      for (int w = 0; w < kPlanThreads / 64; ++w) {
+        here += w < wave ? totals[l][w] : 0;
+        all += totals[l][w];
+      }
+      if (i < items) records[i].at[l] = before[l] + here + to[l] - mine[l];
+      before[l] += all;
+    }
+  }
+  cut<D>(A, before[kShared], before[kStream], p);
+  if (tid == 0) *plan = p;
+}
+
+// The last of n ascending numbers that is at most x, by the whole wave: 64 at a look.
+template <class At>
+__device__ __forceinline__ int last_up_to(int n, int x, const At at) {
+  const int lane = threadIdx.x & 63;
+  int from = 0;
+  for (int span = n; span > 1;) {
+    const int step = (span + 63) >> 6;
+    const bool is = lane * step < span && at(from + min(lane * step, span - 1)) <= x;
+    const int up_to = (int)__popcll(__ballot(is));   // 0 where not even the first is
+    from += max(up_to - 1, 0) * step;
+    span = min(step, n - from);
+  }
+  return from;
+}
+
 struct Segment {
   Item item;
   Line line;
   int tile, from, to, of, run;
 };
 
+// The walk through one run's segments.
 template <int D>
 class Walk {
  public:
-  // The plan, which every wave computes alike from the lengths.
-  __device__ __forceinline__ void begin(const BranchArgs& A) {
-    const int lane = threadIdx.x & 63;
-    // whether some row does not see the whole of its prefix: only then do the positions of a prefix's rows matter
-    placed_ = A.window > 0;
-    for (int base = 0; base < A.b.n_seq; base += 64) {
-      const Item t = own_item(A, base + lane);
-      if (base == 0) first_ = t;
-      placed_ |= __any(t.n > 0 && t.p_first + 1 < t.split) != 0;
-    }
-    if (lane >= A.b.n_seq && lane < items(A)) first_ = prefix_item(A, lane - A.b.n_seq);
-    float sum[2] = {0.0f, 0.0f};
-    for (int base = 0; base < items(A); base += 64) {
-      const Item t = block(A, base);
-      const Shape<D> s(rows_of(A, t), t.groups, 0);
-      sum[kShared] += (float)s.full * (float)s.each + (s.streams() ? 0.0f : (float)s.last);
-      sum[kStream] += s.streams() ? (float)s.last : 0.0f;
-    }
-    sum[0] = wave_sum(sum[0]);
-    sum[1] = wave_sum(sum[1]);
-    // lengths are counted in 2^shift units, so that their sums fit 32 bits
-    shift_ = max(0, (int)((__float_as_uint(fmaxf(sum[0], sum[1])) >> 23) & 255u) - 127 - 27);
-    int total[2] = {0, 0};
-    for (int base = 0; base < items(A); base += 64) {
-      const Item t = block(A, base);
-      const Shape<D> s(rows_of(A, t), t.groups, shift_);
-      for (int l = 0; l < 2; ++l) total[l] += __builtin_amdgcn_readlane(wave_inclusive_sum(s.units((Line)l)), 63);
-    }
-    const float by_wave = sum[kStream] * (1.0f / kWaves);
-    shared_ = sum[kShared] == 0.0f ? 0 : by_wave == 0.0f ? A.runs
-              : min(max((int)(A.runs * (sum[kShared] / (sum[kShared] + by_wave)) + 0.5f), 1), A.runs - 1);
-    shared_ = __builtin_amdgcn_readfirstlane(shared_);
-    const int runs[2] = {max(shared_, 1), max((A.runs - shared_) * kWaves, 1)};
-    // a part shorter than four groups' time costs more to begin and to join than it saves
-    for (int l = 0; l < 2; ++l) {
-      const int rows = l == kStream ? kStreamRows : kSmallRows;
-      per_[l] = max(max((Cost<D>::begin(rows) + 4 * Cost<D>::per_group(rows)) >> shift_, 1), (total[l] + runs[l] - 1) / runs[l]);
-    }
+  // Workgroup `number` of a head works on one line, and each wave of the stream's has a run of its own.
+  __device__ __forceinline__ Walk(const Plan& p, int number) {
+    auto of = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    const int shared = of(p.shared), per[2] = {of(p.per[0]), of(p.per[1])};
+    line_ = number < shared ? kShared : kStream;
+    shift_ = of(p.shift);
+    whole_ = of(p.whole);
+    run_ = line_ == kShared ? number : (number - shared) * kWaves + of(threadIdx.x >> 6);
+    at_ = run_ * per[line_];
+    end_ = at_ + per[line_];
   }
-
-  // Workgroup `number` of a head: which line it works on, and which run of it this wave has.
-  __device__ __forceinline__ Line take(int number) {
-    const Line line = number < shared_ ? kShared : kStream;
-    run_ = line == kShared ? number : (number - shared_) * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    at_ = run_ * per_[line];
-    end_ = at_ + per_[line];
-    return line;
-  }
-
-  // What the launch that joins the parts has to know.
-  __device__ __forceinline__ void write(const BranchArgs& A) const {
-    const int lane = threadIdx.x & 63;
-    if (lane == 0) *reinterpret_cast<int4*>(A.plan) = int4{per_[0], per_[1], shift_, 0};
-    int before[2] = {0, 0};
-    for (int base = 0; base < items(A); base += 64) {
-      const Item t = block(A, base);
-      const Shape<D> s(rows_of(A, t), t.groups, shift_);
-      int at[2];
-      for (int l = 0; l < 2; ++l) {
-        const int mine = s.units((Line)l), sum = wave_inclusive_sum(mine);
-        at[l] = before[l] + sum - mine;
-        before[l] += __builtin_amdgcn_readlane(sum, 63);
-      }
-      if (base + lane < items(A)) {
-        int4* to = reinterpret_cast<int4*>(A.plan + 8 + 8 * (base + lane));
-        to[0] = int4{at[0], at[1], t.groups, t.n};
-        to[1] = int4{t.row0, t.split == 0 || t.sees == 3, 0, 0};
-      }
-    }
-  }
+  __device__ __forceinline__ Line line() const { return line_; }
 
   // The run's next segment; false past its last.
-  __device__ __forceinline__ bool next(const BranchArgs& A, Line line, Segment& g) {
+  __device__ __forceinline__ bool next(const BranchArgs& A, const Record* records, Segment& g) {
     if (at_ >= end_) return false;
-    const int lane = threadIdx.x & 63;
-    int at = at_;
-    for (int base = 0; base < items(A); base += 64) {
-      const Item t = block(A, base);
-      const Shape<D> s(rows_of(A, t), t.groups, shift_);
-      const int mine = s.units(line), sum = wave_inclusive_sum(mine);
-      const int total = __builtin_amdgcn_readlane(sum, 63);
-      if (at < total) {
-        const int i = __builtin_ctzll(__ballot(sum > at));
-        auto of = [&](int x) { return __builtin_amdgcn_readlane(x, i); };
-        g.item = Item{of(t.seq), of(t.lead), of(t.row0), of(t.n), of(t.split), of(t.sees), of(t.p_first), of(t.p_last), of(t.groups)};
-        const int full = of(s.full), each = of(s.each), last = of(s.last);
-        at -= of(sum) - of(mine);
-        g.line = line;
-        g.run = run_;
-        g.tile = line == kStream ? full : min(at / each, full);
-        g.of = g.tile < full ? each : last;
-        g.from = at - (line == kStream ? 0 : g.tile * each);
-        g.to = min(g.of, g.from + end_ - at_);
-        at_ += g.to - g.from;
-        return true;
-      }
-      at -= total;
-    }
-    at_ = end_;
-    return false;
+    const Record* r = records + last_up_to(A.b.n_seq + A.n_groups, at_, [&](int i) { return records[i].at[line_]; });
+    auto of = [&](int x) { return __builtin_amdgcn_readfirstlane(x); };
+    const Item& t = r->item;
+    g.item = Item{of(t.groups), of(t.n), of(t.row0), of(t.sees), of(t.split), of(t.of), of(t.seq), of(t.lead), of(t.p_first), of(t.p_last)};
+    const Shape<D> s((int64_t)g.item.n * A.group, g.item.groups, shift_, whole_);
+    const int at = at_ - of(r->at[line_]);
+    if (at >= s.units(line_)) return false;   // past the last item's
+    g.line = line_;
+    g.run = run_;
+    g.tile = line_ == kStream ? s.full : min(at / s.each, s.full);
+    g.of = g.tile < s.full ? s.each : s.last;
+    g.from = at - (line_ == kStream ? 0 : g.tile * s.each);
+    g.to = min(g.of, g.from + end_ - at_);
+    at_ += g.to - g.from;
+    return true;
   }
-
-  __device__ __forceinline__ bool placed() const { return placed_; }
-
-  static __device__ __forceinline__ int64_t rows_of(const BranchArgs& A, const Item& t) { return (int64_t)t.n * A.group; }
 
  private:
-  Item first_;    // item `lane`
-  bool placed_;
-  int shift_, per_[2], shared_, run_, at_, end_;   // shared_: workgroups a head of the shared line
-
-  static __device__ __forceinline__ int items(const BranchArgs& A) { return A.n_groups + A.b.n_seq; }
-
-  static __device__ __forceinline__ Item own_item(const BranchArgs& A, int i) {
-    Item t;
-    const int s = min(i, A.b.n_seq - 1);
-    const Seq q = load_seq(A.b, s);
-    const int g = group_of(A, s);
-    const Members group = members_of<D>(A, max(g, 0));
-    t.seq = s;
-    t.lead = min(group.first, A.b.n_seq - 1);
-    t.row0 = q.row0;
-    t.n = i < A.b.n_seq ? q.n : 0;
-    t.split = g < 0 ? 0 : group.prefix;
-    t.sees = g >= 0 && group.whole ? 3 : 1;
-    t.p_first = q.begin;
-    t.p_last = q.len - 1;
-    // the last tile's rows at most: what they see is the longest; a window may hide all from that tile alone
-    const int first = q.len - min(q.n, Cost<D>::kRows / A.group + 2);
-    t.groups = q.n == 0 ? 0 : max(visible_own(A, t, first, t.p_last).n + visible_shared(A, t, first, t.p_last).n, A.window > 0 ? 1 : 0);
-    return t;
-  }
-
-  __device__ __forceinline__ Item prefix_item(const BranchArgs& A, int g) const {
-    Item t;
-    const Members group = members_of<D>(A, g);
-    t.seq = t.lead = min(group.first, A.b.n_seq - 1);
-    t.row0 = group.row0;
-    t.n = group.whole ? 0 : group.n;
-    t.split = group.prefix;
-    t.sees = 2;
-    t.p_first = t.p_last = kNoLimit;   // behind the prefix
-    if (placed_) {
-      t.p_last = -1;
-      for (int s = group.first; s < group.last; ++s) {
-        const Seq q = load_seq(A.b, s);
-        if (q.n == 0) continue;
-        t.p_first = min(t.p_first, q.begin);
-        t.p_last = max(t.p_last, q.len - 1);
-      }
-    }
-    t.groups = visible_shared(A, t, t.p_first, t.p_last).n;
-    return t;
-  }
-
-  // Items base .. base + 63, one a lane; those past the last have no rows.
-  __device__ __forceinline__ Item block(const BranchArgs& A, int base) const {
-    if (base == 0) return first_;
-    const int i = base + (threadIdx.x & 63);
-    Item t = own_item(A, i);   // in every lane: group_of is the wave's
-    if (i >= A.b.n_seq && i < items(A)) t = prefix_item(A, i - A.b.n_seq);
-    return t;
-  }
+  Line line_;
+  int shift_, whole_, run_, at_, end_;
 };
 
 // ----------------------------------------------------------------- the parts
@@ -426,140 +535,147 @@ __device__ __forceinline__ void attend_part(const BranchArgs& A, const Segment& 
 template <int D>
 constexpr size_t kLds = std::max(Shared<D, 1, kWaves>::kLds, Shared<D, Cost<D>::kRows / (16 * kWaves), kWaves>::kLds);
 
-template <int D>
+template <int D, bool kSmallBatch>
 __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void branch_parts_kernel(BranchArgs A) {
   extern __shared__ __align__(16) u32x4 stage[];
+  __shared__ Plan plan_here;
+  __shared__ Record records_here[kSmallBatch ? 2 * kSmall : 1];
+  const Plan* plan = reinterpret_cast<const Plan*>(A.plan);
+  const Record* records = reinterpret_cast<const Record*>(plan + 1);
+  if (kSmallBatch) {
+    if (threadIdx.x < 64) make_plan<D>(A, &plan_here, records_here);
+    __syncthreads();
+    if (blockIdx.x == 0) {   // for the launch that joins the parts
+      for (int i = threadIdx.x; i < (A.b.n_seq + A.n_groups) * (int)(sizeof(Record) / 4); i += kThreads)
+        A.plan[sizeof(Plan) / 4 + i] = reinterpret_cast<const int*>(records_here)[i];
+      if (threadIdx.x < sizeof(Plan) / 4) A.plan[threadIdx.x] = reinterpret_cast<const int*>(&plan_here)[threadIdx.x];
+    }
+  }
   const int head = blockIdx.x % A.c.hkv;
-  Walk<D> walk;
-  walk.begin(A);
-  if (blockIdx.x == 0 && threadIdx.x < 64) walk.write(A);
-  const Line line = walk.take(blockIdx.x / A.c.hkv);
-  for (Segment w; walk.next(A, line, w);) {
-    if (line == kStream) {
-      attend_part<D, kStreamRows>(A, w, walk.placed(), head, stage);
+  const Plan& p = kSmallBatch ? plan_here : *plan;
+  const bool placed = __builtin_amdgcn_readfirstlane(p.placed);
+  Walk<D> walk(p, blockIdx.x / A.c.hkv);
+  for (Segment w; walk.next(A, kSmallBatch ? records_here : records, w);) {
+    if (walk.line() == kStream) {
+      attend_part<D, kStreamRows>(A, w, placed, head, stage);
     } else {
       constexpr int H = Cost<D>::kRows;
-      if (H == kSmallRows || Walk<D>::rows_of(A, w.item) - (int64_t)w.tile * H <= kSmallRows)
-        attend_part<D, kSmallRows>(A, w, walk.placed(), head, stage);
+      if (H == kSmallRows || (int64_t)w.item.n * A.group - (int64_t)w.tile * H <= kSmallRows)
+        attend_part<D, kSmallRows>(A, w, placed, head, stage);
       else
-        attend_part<D, H>(A, w, walk.placed(), head, stage);
+        attend_part<D, H>(A, w, placed, head, stage);
     }
   }
 }
 
 // ---------------------------------------------------------------- the joining
-// A row of one query head: W waves take turns at its parts.
+// D / 4 lanes a row of one query head.  With few rows W waves take turns at a row's
+// parts; with many (W = 1) a wave has `heads` query heads of a token row, because
+// finding the parts takes longer than joining them.
 template <int D, int W>
-__global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A) {
-  constexpr int E = D / 64, H = Cost<D>::kRows;   // elements a lane
-  __shared__ float sums[kWaves][D], refs[kWaves], weights[kWaves];
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
-  const int turn = wave % W;
-  const int64_t i = (int64_t)blockIdx.x * (kWaves / W) + wave / W;
-  const int r = (int)(i / A.hq), h = (int)(i % A.hq), head = h / A.group;
-  // the row's sequence: the last that starts at or before it, 64 a look
-  int s = -1;
-  for (int base = 0; base < A.b.n_seq; base += 64) {
-    const int before = __popcll(__ballot(base + lane < A.b.n_seq && A.b.q_start[min(base + lane, A.b.n_seq - 1)] <= r));
-    s += before;
-    if (before < 64) break;
-  }
-  const int g = __builtin_amdgcn_readfirstlane(group_of(A, s));
-  const Seq q = load_seq(A.b, max(s, 0));
-  if (s < 0 || r >= A.b.T || r < q.row0 || r >= q.row0 + q.n) return;   // all waves of a row, which are a workgroup's, or the one
-  const int64_t x = (int64_t)r * A.group + h % A.group;
-  const int4 plan = *reinterpret_cast<const int4*>(A.plan);
-  // an item's parts of this row: where the first is, how far apart they are, how many
+__global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int heads) {
+  constexpr int L = D / 4, P = 64 / L, H = Cost<D>::kRows;   // lanes a row, rows a pass
+  __shared__ f32x4 sums[W][64];
+  __shared__ float2 refs[W][P];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane % L;
+  const int turn = wave % W, chunks = (A.hq + heads - 1) / heads;
+  const int64_t unit = (int64_t)blockIdx.x * (kWaves / W) + wave / W;
+  const int r = (int)(unit / chunks), h0 = (int)(unit % chunks) * heads;
+  if (r >= A.b.T) return;   // W > 1: all waves, a workgroup has one unit
+  const int s = __builtin_amdgcn_readfirstlane(last_up_to(A.b.n_seq, r, [&](int i) { return A.b.q_start[i]; }));
+  const Seq q = load_seq(A.b, s);
+  if (r < q.row0 || r >= q.row0 + q.n) return;
+  const Plan plan = *reinterpret_cast<const Plan*>(A.plan);
+  const Record* records = reinterpret_cast<const Record*>(A.plan + sizeof(Plan) / 4);
+  const Record own_record = records[s], prefix_record = records[A.b.n_seq + max(own_record.item.of, 0)];
+  // an item's parts of a row: where the first is, how far apart they are, how many
   struct Run {
     const float* o;
     const float2* ml;
     int step, n;
-    bool alone;
   };
-  auto parts_of = [&](int item, const Parts (&all)[2]) {
-    const int4* of = reinterpret_cast<const int4*>(A.plan + 8 + 8 * item);
-    const int4 a = of[0], b = of[1];
-    Run p{nullptr, nullptr, 0, 0, b.y != 0};
-    const int64_t y = x - (int64_t)b.x * A.group, rows = (int64_t)a.w * A.group;
-    if (y < 0 || y >= rows || a.z == 0) return p;   // nothing to see, or groups and sequences that do not fit each other
-    const Shape<D> shape(rows, a.z, plan.z);
+  auto parts_of = [&](const Record& rec, const Parts (&all)[2], int h) {
+    Run p{all[kStream].o, all[kStream].ml, 0, 0};
+    const int64_t x = (int64_t)r * A.group + h % A.group, y = x - (int64_t)rec.item.row0 * A.group, rows = (int64_t)rec.item.n * A.group;
+    if (y < 0 || y >= rows || rec.item.groups == 0) return p;   // nothing to see, or groups and sequences that do not fit each other
+    const Shape<D> shape(rows, rec.item.groups, plan.shift, plan.whole);
     const int tile = min((int)(y / H), shape.full);
     const Line line = tile == shape.full && shape.streams() ? kStream : kShared;
-    const int length = tile < shape.full ? shape.each : shape.last, at = line == kStream ? a.y : a.x + tile * shape.each;
-    const int per = line == kStream ? plan.y : plan.x, first = at / per;
+    const int length = tile < shape.full ? shape.each : shape.last, at = line == kStream ? rec.at[kStream] : rec.at[kShared] + tile * shape.each;
+    const int first = at / plan.per[line];
     p.step = line == kStream ? kStreamRows : H;
-    p.n = (at + length - 1) / per - first + 1;
-    const size_t place = (size_t)head * A.places[line] + x + (size_t)first * p.step;
+    p.n = (at + length - 1) / plan.per[line] - first + 1;
+    const size_t place = (size_t)(h / A.group) * A.places[line] + x + (size_t)first * p.step;
     p.o = all[line].o + place * D;
     p.ml = all[line].ml + place;
     return p;
   };
-  const Run own = parts_of(s, A.own);
-  Run prefix{nullptr, nullptr, 0, 0, false};
-  if (g >= 0) prefix = parts_of(A.b.n_seq + g, A.prefix);
-  if (own.alone && own.n == 1) return;   // the result already
-  const int n = prefix.n + own.n;
-  float top = kLowest, sum = 0.0f, y[E];
+  const bool alone = own_record.item.split == 0 || own_record.item.sees == 3;
+  for (int pass = h0; pass < min(A.hq, h0 + heads); pass += P) {
+    const int h = pass + lane / L;
+    Run own = parts_of(own_record, A.own, min(h, A.hq - 1)), prefix = parts_of(prefix_record, A.prefix, min(h, A.hq - 1));
+    if (own_record.item.of < 0) prefix.n = 0;
+    const bool done = h >= min(A.hq, h0 + heads) || (alone && own.n == 1);   // or the result already
+    const int n = done ? 0 : prefix.n + own.n, most = (int)wave_max((uint32_t)n);
+    if (W == 1 && __all(done)) continue;
+    float top = kLowest, sum = 0.0f;
+    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int base = turn; base < most; base += L * W) {
+      // lane i of a row: part base + i W
+      const int part = base + l * W;
+      float2 ml = {kLowest, 0.0f};
+      if (part < n) ml = part < prefix.n ? prefix.ml[(size_t)part * prefix.step] : own.ml[(size_t)(part - prefix.n) * own.step];
+      float next = ml.x;
 #pragma unroll
-  for (int e = 0; e < E; ++e) y[e] = 0.0f;
-  for (int base = turn; base < n; base += 64 * W) {
-    // lane k: part base + k W
-    const int k = base + lane * W;
-    float2 ml = {kLowest, 0.0f};
-    if (k < n) ml = k < prefix.n ? prefix.ml[(size_t)k * prefix.step] : own.ml[(size_t)(k - prefix.n) * own.step];
-    const float next = fmaxf(top, wave_max(ml.x)), share = __builtin_amdgcn_exp2f(ml.x - next), down = __builtin_amdgcn_exp2f(top - next);
-    sum = sum * down + wave_sum(k < n ? share * ml.y : 0.0f);
-    top = next;
+      for (int i = 1; i < L; i *= 2) next = fmaxf(next, __shfl_xor(next, i));
+      next = fmaxf(next, top);
+      const float share = part < n ? __builtin_amdgcn_exp2f(ml.x - next) : 0.0f, down = __builtin_amdgcn_exp2f(top - next);
+      float weight = share * ml.y;
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] *= down;
-    const int count = min(64, (n - base + W - 1) / W);
-    for (int j0 = 0; j0 < count; j0 += 8) {   // eight parts' loads under way together; past the last, that once more with no share
-      float v[8][E], by[8];
+      for (int i = 1; i < L; i *= 2) weight += __shfl_xor(weight, i);
+      sum = fmaf(sum, down, weight);
+      top = next;
+      y *= down;
+      const int count = min(L, (most - base + W - 1) / W);
+      auto add = [&](auto at_once, int j0) {   // past a row's last part, that once more with no share
+        constexpr int K = decltype(at_once)::value;
+        f32x4 v[K];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int at_j = min(j0 + j, count - 1), kj = base + at_j * W;
-        const float* o = kj < prefix.n ? prefix.o + (size_t)kj * prefix.step * D : own.o + (size_t)(kj - prefix.n) * own.step * D;
-        by[j] = j0 + j < count ? __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(share), at_j)) : 0.0f;
+        for (int j = 0; j < K; ++j) {
+          const int at = max(min(base + (j0 + j) * W, n - 1), 0);
+          v[j] = *reinterpret_cast<const f32x4*>((at < prefix.n ? prefix.o + (size_t)at * prefix.step * D : own.o + (size_t)(at - prefix.n) * own.step * D) + l * 4);
+        }
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[j][e] = o[lane * E + e];
+        for (int j = 0; j < K; ++j) {
+          const float by = __shfl(share, lane - l + min(j0 + j, L - 1));
+          y += (j0 + j < L ? by : 0.0f) * v[j];
+        }
+      };
+      int j = 0;
+      for (; j + 4 < count; j += 8) add(std::integral_constant<int, 8>{}, j);
+      if (j < count) add(std::integral_constant<int, 4>{}, j);
+    }
+    if constexpr (W > 1) {   // one pass
+      sums[wave][lane] = y;
+      if (l == 0) refs[wave][lane / L] = float2{top, sum};
+      __syncthreads();
+      if (turn > 0) return;
+#pragma unroll
+      for (int v = 1; v < W; ++v) {
+        const float2 other = refs[v][lane / L];
+        const float next = fmaxf(top, other.x), down = __builtin_amdgcn_exp2f(top - next), share = __builtin_amdgcn_exp2f(other.x - next);
+        y = down * y + share * sums[v][lane];
+        sum = fmaf(sum, down, share * other.y);
+        top = next;
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < E; ++e) y[e] = fmaf(by[j], v[j][e], y[e]);
     }
+    if (done) continue;
+    if (n == 0) y = f32x4{0.0f, 0.0f, 0.0f, 0.0f};   // what was loaded for it is another row's
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const size_t row = (size_t)r * A.hq + h;
+    *reinterpret_cast<u32x2*>(A.out + row * D + l * 4) = u32x2{bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv)};
+    if (l == 0) write_lse(A.lse, row, top, sum);
   }
-  if (W > 1) {
-#pragma unroll
-    for (int e = 0; e < E; ++e) sums[wave][lane * E + e] = y[e];
-    if (lane == 0) refs[wave] = top, weights[wave] = sum;
-    __syncthreads();
-    if (turn > 0) return;
-    float all = refs[wave];
-#pragma unroll
-    for (int v = 1; v < W; ++v) all = fmaxf(all, refs[wave + v]);
-    sum = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = 0.0f;
-#pragma unroll
-    for (int v = 0; v < W; ++v) {
-      const float share = __builtin_amdgcn_exp2f(refs[wave + v] - all);
-      sum = fmaf(share, weights[wave + v], sum);
-#pragma unroll
-      for (int e = 0; e < E; ++e) y[e] = fmaf(share, sums[wave + v][lane * E + e], y[e]);
-    }
-    top = all;
-  }
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-  const size_t row = (size_t)r * A.hq + h;
-  uint16_t* to = A.out + row * D + lane * E;
-  if constexpr (E == 1) {
-    *to = (uint16_t)bf16_pair(y[0] * inv, 0.0f);
-  } else {
-#pragma unroll
-    for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(to + e) = bf16_pair(y[e] * inv, y[e + 1] * inv);
-  }
-  if (lane == 0) write_lse(A.lse, row, top, sum);
 }
 
 // ------------------------------------------------------------------- launch
@@ -568,7 +684,7 @@ int runs_of(int hkv, int D) { return std::max(2, (D == 256 ? 256 : 512) / hkv); 
 int rows_of_tall(int D) { return D == 256 ? 64 : 128; }
 
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
-size_t plan_bytes(int64_t items) { return rounded((8 + 8 * items) * 4); }
+size_t plan_bytes(int64_t items) { return rounded(sizeof(Plan) + items * sizeof(Record)); }
 // Places of a line: the rows, and a tile's height a run.
 int64_t places_of(int64_t rows, int hkv, int D, int line) {
   if (line == kStream) return rows + (int64_t)runs_of(hkv, D) * kWaves * kStreamRows;
@@ -585,17 +701,30 @@ size_t workspace_bytes(int64_t rows, int64_t items, int hkv, int D) {
   return bytes;
 }
 
+template <int D, bool kSmallBatch>
+int launch_parts(const BranchArgs& A, hipStream_t s) {
+  static dh::OncePerDevice once;
+  const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_parts_kernel<D, kSmallBatch>), kLds<D>);
+  if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_parts_kernel: %s", hipGetErrorString(e));
+  if (!kSmallBatch) hipLaunchKernelGGL((branch_plan_kernel<D>), dim3(1), dim3(kPlanThreads), 0, s, A);
+  hipLaunchKernelGGL((branch_parts_kernel<D, kSmallBatch>), dim3((unsigned)(A.runs * A.c.hkv)), dim3(kThreads), kLds<D>, s, A);
+  return launched("branch_parts_kernel");
+}
+
 template <int D>
 int launch(const BranchArgs& A, hipStream_t s) {
-  static dh::OncePerDevice once;
-  const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_parts_kernel<D>), kLds<D>);
-  if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_parts_kernel: %s", hipGetErrorString(e));
-  hipLaunchKernelGGL((branch_parts_kernel<D>), dim3((unsigned)(A.runs * A.c.hkv)), dim3(kThreads), kLds<D>, s, A);
+  const int rc = A.b.n_seq <= kSmall && A.n_groups <= kSmall ? launch_parts<D, true>(A, s) : launch_parts<D, false>(A, s);
+  if (rc) return rc;
+  constexpr int P = 256 / D;   // rows a pass
   const int64_t rows = (int64_t)A.b.T * A.hq;
-  if (rows <= 2048)
-    hipLaunchKernelGGL((branch_join_kernel<D, kWaves>), dim3((unsigned)rows), dim3(kThreads), 0, s, A);
-  else
-    hipLaunchKernelGGL((branch_join_kernel<D, 1>), dim3((unsigned)((rows + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, A);
+  if (rows <= 1024 * P) {
+    const int64_t units = A.b.T * (int64_t)((A.hq + P - 1) / P);
+    hipLaunchKernelGGL((branch_join_kernel<D, kWaves>), dim3((unsigned)units), dim3(kThreads), 0, s, A, P);
+  } else {   // up to 8192 waves, a card's
+    const int passes = (int)std::min<int64_t>((rows + 8192 * P - 1) / (8192 * P), (A.hq + P - 1) / P);
+    const int64_t units = A.b.T * (int64_t)((A.hq + passes * P - 1) / (passes * P));
+    hipLaunchKernelGGL((branch_join_kernel<D, 1>), dim3((unsigned)((units + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, A, passes * P);
+  }
   return launched("branch_join_kernel");
 }
 
