@@ -75,35 +75,43 @@ struct Item {
 
 // Lengths of tiles in units of about 0.1 us of a workgroup (of a wave, for the
 // stream): what a tile's beginning and end take, and what a group of 32 tokens takes.
-// Measured with heads of 128 on a full card: 2.2 + 0.8 us a group for 64 rows, 3.0 +
-// 1.15 for 128, 2.0 + 1.6 for a wave's 16, and 1.4 to 3 us to set up and to leave.
+// Measured with heads of 128 on a full card: 0.8 us a group for 64 rows (0.9 to 1.2
+// beside tiles of 128), 1.15 for 128, 1.6 for a wave's 16; a workgroup that goes on
+// from one tile to the next loses 8 to 10 us, of which 5 pass until the first product.
 template <int D>
 struct Cost {
   static constexpr int kRows = D == 256 ? 64 : 128;     // H
+  static constexpr bool kStreams = D != 256;
   static __host__ __device__ constexpr int per_group(int rows) {
-    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 8 : 12) * D / 128);
+    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 9 : 12) * D / 128);
   }
-  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 35 : rows <= kSmallRows ? 45 : 60; }
+  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 40 : 80; }
   static __device__ __forceinline__ int of(int rows, int groups) { return groups == 0 ? 0 : begin(rows) + groups * per_group(rows); }
 };
 
 // An item's tiles: `full` ones of H rows, then one of `rest`, and their units, of
-// 2^shift (whole: 1 for the stream's).
+// 2^shift (whole: 1 for the stream's).  A tile's first units are its beginning, `pad`
+// of them: its groups are in the others.
 template <int D>
 struct Shape {
-  int full, rest, each, last;
-  __device__ __forceinline__ Shape(int64_t rows, int groups, int shift, bool whole) {
+  int full, rest, each, last, whole, shift;
+  __device__ __forceinline__ Shape(int rows, int groups, int shift_, int whole_) : whole(whole_), shift(shift_) {
     constexpr int H = Cost<D>::kRows;
     if (groups == 0) rows = 0;
-    full = (int)(rows / H);
-    rest = (int)(rows % H);
-    auto scaled = [&](int units) { return (int)(((int64_t)units + (1 << shift) - 1) >> shift); };
-    each = max(scaled(Cost<D>::of(H, groups)), 1);
+    full = rows / H;
+    rest = rows % H;
+    each = scaled(Cost<D>::of(H, max(groups, 1)));
     last = rest == 0 ? 0 : whole && streams() ? 1 : scaled(Cost<D>::of(rest, groups));
   }
-  __device__ __forceinline__ bool streams() const { return rest <= kStreamRows; }
+  __device__ __forceinline__ int scaled(int units) const { return (units + (1 << shift) - 1) >> shift; }
+  __device__ __forceinline__ bool streams() const { return Cost<D>::kStreams && rest <= kStreamRows; }
   __device__ __forceinline__ int units(Line line) const {
     return line == kStream ? (streams() ? last : 0) : full * each + (streams() ? 0 : last);
+  }
+  // Of tile t of a line's
+  __device__ __forceinline__ int length(int t) const { return t < full ? each : last; }
+  __device__ __forceinline__ int pad(Line line, int t) const {
+    return line == kStream && whole ? 0 : min(Cost<D>::begin(line == kStream ? kStreamRows : kSmallRows) >> shift, length(t) - 1);
   }
 };
 
@@ -192,11 +200,12 @@ __device__ __forceinline__ bool inside_prefix(const Item& t) { return t.n > 0 &&
 // What every part and the joining go by, from the lengths.
 struct Plan {
   int per[2];    // units of a run, by line
+  int more;      // of the shared line's first `half` runs; the others have as many less
+  int half;
   int shift;     // units are 2^shift, so that their sums fit 32 bits
   int whole;     // the stream's tiles are a wave each
   int shared;    // workgroups a head of the shared line
   int placed;    // the positions of a prefix's rows matter
-  int unused[2];
 };
 struct Record {
   int at[2];     // first unit, by line
@@ -229,11 +238,30 @@ __device__ __forceinline__ void divide(const BranchArgs& A, const Sums& sum, Pla
   p.shift = max(0, (int)((__float_as_uint(fmaxf(shared, stream)) >> 23) & 255u) - 127 - 27);
 }
 
+// Two workgroups share a CU, and the one that came first is served first: of two
+// equal ones of 220 groups it ended after 232 us, the other after 283.  So on long
+// runs (100 us and more) those that come first, blocks 0 .. 255, have a share more:
+// 16 prompts of 112 rows over 6,000 tokens took 284 us with even runs, 274 so (0.2:
+// 282, 0.25: 287); on short ones it costs (16 slots of 9: 59.0 us, 61.5 with 0.08).
+constexpr float kFirst = 0.15f;
+// First unit of run r, and the run that has unit `at`.
+__device__ __forceinline__ int start_of(int r, int per, int more, int half) { return r * per + more * min(r, 2 * half - r); }
+__device__ __forceinline__ int run_at(int at, int per, int more, int half) {
+  const int before = half * (per + more);
+  return at < before ? at / (per + more) : half + (at - before) / (per - more);
+}
+
 // A part of fewer than four groups costs more to begin and to join than it saves.
 template <int D>
 __device__ __forceinline__ void cut(const BranchArgs& A, int shared_units, int stream_units, Plan& p) {
   const int waves = max(A.runs - p.shared, 1) * kWaves;
-  p.per[kShared] = max(max((4 * Cost<D>::per_group(kSmallRows)) >> p.shift, 1), (shared_units + p.shared - 1) / max(p.shared, 1));
+  const int least = max((4 * Cost<D>::per_group(kSmallRows)) >> p.shift, 1);
+  p.half = A.runs >> 1;
+  const float even = (float)shared_units / (float)max(p.shared, 1), first = (float)(2 * min(p.half, p.shared) - p.shared);
+  const bool full = even * (float)(1 << p.shift) >= 1000.0f;
+  // 0.1% more than the mean: float quotients may fall short
+  p.per[kShared] = max(least, (int)(1.001f * even / (1.0f + (full ? kFirst * first / (float)max(p.shared, 1) : 0.0f))) + 2);
+  p.more = full ? (int)(kFirst * (float)p.per[kShared]) : 0;
   p.per[kStream] = p.whole ? 1 : max(max((4 * Cost<D>::per_group(kStreamRows)) >> p.shift, 1), (stream_units + waves - 1) / waves);
 }
 
@@ -279,10 +307,10 @@ __device__ __forceinline__ void make_plan(const BranchArgs& A, Plan* plan, Recor
   }
   Item shared = prefix_item(A, members, p_first, p_last);
   if (lane >= A.n_groups) shared.n = 0;
-  const int64_t own_rows = (int64_t)own.n * A.group, shared_rows = (int64_t)shared.n * A.group;
+  const int own_rows = own.n * A.group, shared_rows = shared.n * A.group;   // up to 2^30
   Sums sum;
-  sum.add(Shape<D>(own_rows, own.groups, 0, false));
-  sum.add(Shape<D>(shared_rows, shared.groups, 0, false));
+  sum.add(Shape<D>(own_rows, own.groups, 0, 0));
+  sum.add(Shape<D>(shared_rows, shared.groups, 0, 0));
   for (float& x : sum.units) x = wave_sum(x);
   sum.tiles = wave_sum(sum.tiles);
   sum.longest = wave_max(sum.longest);
@@ -337,14 +365,14 @@ __global__ __launch_bounds__(kPlanThreads) void branch_plan_kernel(BranchArgs A)
       atomicMin(&first[g], q.begin);
       atomicMax(&last[g], q.len - 1);
     }
-    sum.add(Shape<D>((int64_t)t.n * A.group, t.groups, 0, false));
+    sum.add(Shape<D>(t.n * A.group, t.groups, 0, 0));
     records[s].item = t;
   }
   Plan p{};
   p.placed = __syncthreads_or(inside) || A.window > 0;
   for (int g = tid; g < A.n_groups; g += kPlanThreads) {
     const Item t = prefix_item(A, members(g), p.placed ? first[g] : kNoLimit, p.placed ? last[g] : kNoLimit);
-    sum.add(Shape<D>((int64_t)t.n * A.group, t.groups, 0, false));
+    sum.add(Shape<D>(t.n * A.group, t.groups, 0, 0));
     records[A.b.n_seq + g].item = t;
   }
   const float of_wave[4] = {wave_sum(sum.units[0]), wave_sum(sum.units[1]), wave_sum(sum.tiles), wave_max(sum.longest)};
@@ -362,7 +390,7 @@ __global__ __launch_bounds__(kPlanThreads) void branch_plan_kernel(BranchArgs A)
   int before[2] = {0, 0};
   for (int base = 0; base < items; base += kPlanThreads) {
     const int i = base + tid;
-    const Shape<D> s(i < items ? (int64_t)records[i].item.n * A.group : 0, i < items ? records[i].item.groups : 0, p.shift, p.whole);
+    const Shape<D> s(i < items ? records[i].item.n * A.group : 0, i < items ? records[i].item.groups : 0, p.shift, p.whole);
     int to[2], mine[2];
     __syncthreads();
     for (int l = 0; l < 2; ++l) {
@@ -413,34 +441,39 @@ class Walk {
   // Workgroup `number` of a head works on one line, and each wave of the stream's has a run of its own.
   __device__ __forceinline__ Walk(const Plan& p, int number) {
     auto of = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
-    const int shared = of(p.shared), per[2] = {of(p.per[0]), of(p.per[1])};
+    const int shared = of(p.shared);
     line_ = number < shared ? kShared : kStream;
     shift_ = of(p.shift);
     whole_ = of(p.whole);
     run_ = line_ == kShared ? number : (number - shared) * kWaves + of(threadIdx.x >> 6);
-    at_ = run_ * per[line_];
-    end_ = at_ + per[line_];
+    const int per = of(p.per[line_]), more = line_ == kShared ? of(p.more) : 0, half = of(p.half);
+    at_ = start_of(run_, per, more, half);
+    end_ = start_of(run_ + 1, per, more, half);
   }
   __device__ __forceinline__ Line line() const { return line_; }
 
   // The run's next segment; false past its last.
   __device__ __forceinline__ bool next(const BranchArgs& A, const Record* records, Segment& g) {
-    if (at_ >= end_) return false;
-    const Record* r = records + last_up_to(A.b.n_seq + A.n_groups, at_, [&](int i) { return records[i].at[line_]; });
-    auto of = [&](int x) { return __builtin_amdgcn_readfirstlane(x); };
-    const Item& t = r->item;
-    g.item = Item{of(t.groups), of(t.n), of(t.row0), of(t.sees), of(t.split), of(t.of), of(t.seq), of(t.lead), of(t.p_first), of(t.p_last)};
-    const Shape<D> s((int64_t)g.item.n * A.group, g.item.groups, shift_, whole_);
-    const int at = at_ - of(r->at[line_]);
-    if (at >= s.units(line_)) return false;   // past the last item's
-    g.line = line_;
-    g.run = run_;
-    g.tile = line_ == kStream ? s.full : min(at / s.each, s.full);
-    g.of = g.tile < s.full ? s.each : s.last;
-    g.from = at - (line_ == kStream ? 0 : g.tile * s.each);
-    g.to = min(g.of, g.from + end_ - at_);
-    at_ += g.to - g.from;
-    return true;
+    while (at_ < end_) {
+      const Record* r = records + last_up_to(A.b.n_seq + A.n_groups, at_, [&](int i) { return records[i].at[line_]; });
+      auto of = [&](int x) { return __builtin_amdgcn_readfirstlane(x); };
+      const Item& t = r->item;
+      g.item = Item{of(t.groups), of(t.n), of(t.row0), of(t.sees), of(t.split), of(t.of), of(t.seq), of(t.lead), of(t.p_first), of(t.p_last)};
+      const Shape<D> s(g.item.n * A.group, g.item.groups, shift_, whole_);
+      const int at = at_ - of(r->at[line_]);
+      if (at >= s.units(line_)) return false;   // past the last item's
+      g.line = line_;
+      g.run = run_;
+      g.tile = line_ == kStream ? s.full : min(at / s.each, s.full);
+      const int in_tile = at - (line_ == kStream ? 0 : g.tile * s.each), pad = s.pad(line_, g.tile), length = s.length(g.tile);
+      const int to = min(length, in_tile + end_ - at_);
+      at_ += to - in_tile;
+      g.of = length - pad;
+      g.from = max(in_tile - pad, 0);
+      g.to = to - pad;
+      if (g.to > 0) return true;   // else the run ends in the tile's beginning
+    }
+    return false;
   }
 
  private:
@@ -455,14 +488,15 @@ __device__ __forceinline__ void attend_part(const BranchArgs& A, const Segment& 
   const Item& t = w.item;
   const bool prefix = t.sees == 2;
   const int lane = threadIdx.x & 63, hi = lane >> 4, lo = lane & 15;
-  const int x0 = w.tile * Cost<D>::kRows, rows = (int)min((int64_t)R, (int64_t)t.n * A.group - x0);
+  const int x0 = w.tile * Cost<D>::kRows, rows = min(R, t.n * A.group - x0);
   // positions of rows a .. b of the tile: a sequence's follow each other, a group's are anywhere among its own
   auto first_of = [&](int a) { return prefix ? t.p_first : t.p_first + (x0 + a) / A.group; };
   auto last_of = [&](int b) { return prefix ? t.p_last : t.p_first + (x0 + b) / A.group; };
   const Range own = visible_own(A, t, first_of(0), last_of(rows - 1)), shared = visible_shared(A, t, first_of(0), last_of(rows - 1));
   const int n = own.n + shared.n;
-  const int from = __builtin_amdgcn_readfirstlane((int)((int64_t)n * w.from / w.of));
-  const int to = __builtin_amdgcn_readfirstlane((int)((int64_t)n * w.to / w.of));
+  // unit u's group: a float division is monotone too, so parts meet, and the ends are exact
+  auto group_at = [&](int u) { return u == w.of ? n : min(n, (int)((float)n * ((float)u / (float)w.of))); };
+  const int from = __builtin_amdgcn_readfirstlane(group_at(w.from)), to = __builtin_amdgcn_readfirstlane(group_at(w.to));
   auto place = [&](int r, int& pos) {
     const int x = x0 + r, row = t.row0 + x / A.group;
     pos = -1;
@@ -536,7 +570,7 @@ template <int D>
 constexpr size_t kLds = std::max(Shared<D, 1, kWaves>::kLds, Shared<D, Cost<D>::kRows / (16 * kWaves), kWaves>::kLds);
 
 template <int D, bool kSmallBatch>
-__global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void branch_parts_kernel(BranchArgs A) {
+__global__ __launch_bounds__(kThreads, 2) void branch_parts_kernel(BranchArgs A) {
   extern __shared__ __align__(16) u32x4 stage[];
   __shared__ Plan plan_here;
   __shared__ Record records_here[kSmallBatch ? 2 * kSmall : 1];
@@ -556,11 +590,11 @@ __global__ __launch_bounds__(kThreads, D == 256 ? 1 : 2) void branch_parts_kerne
   const bool placed = __builtin_amdgcn_readfirstlane(p.placed);
   Walk<D> walk(p, blockIdx.x / A.c.hkv);
   for (Segment w; walk.next(A, kSmallBatch ? records_here : records, w);) {
-    if (walk.line() == kStream) {
-      attend_part<D, kStreamRows>(A, w, placed, head, stage);
+    constexpr int H = Cost<D>::kRows;
+    if (Cost<D>::kStreams && walk.line() == kStream) {
+      if constexpr (Cost<D>::kStreams) attend_part<D, kStreamRows>(A, w, placed, head, stage);
     } else {
-      constexpr int H = Cost<D>::kRows;
-      if (H == kSmallRows || (int64_t)w.item.n * A.group - (int64_t)w.tile * H <= kSmallRows)
+      if (H == kSmallRows || w.item.n * A.group - w.tile * H <= kSmallRows)
         attend_part<D, kSmallRows>(A, w, placed, head, stage);
       else
         attend_part<D, H>(A, w, placed, head, stage);
@@ -595,16 +629,17 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
     int step, n;
   };
   auto parts_of = [&](const Record& rec, const Parts (&all)[2], int h) {
-    Run p{all[kStream].o, all[kStream].ml, 0, 0};
-    const int64_t x = (int64_t)r * A.group + h % A.group, y = x - (int64_t)rec.item.row0 * A.group, rows = (int64_t)rec.item.n * A.group;
+    constexpr Line any = Cost<D>::kStreams ? kStream : kShared;   // of which there are places
+    Run p{all[any].o, all[any].ml, 0, 0};
+    const int x = r * A.group + h % A.group, y = x - rec.item.row0 * A.group, rows = rec.item.n * A.group;
     if (y < 0 || y >= rows || rec.item.groups == 0) return p;   // nothing to see, or groups and sequences that do not fit each other
     const Shape<D> shape(rows, rec.item.groups, plan.shift, plan.whole);
-    const int tile = min((int)(y / H), shape.full);
+    const int tile = min(y / H, shape.full);
     const Line line = tile == shape.full && shape.streams() ? kStream : kShared;
-    const int length = tile < shape.full ? shape.each : shape.last, at = line == kStream ? rec.at[kStream] : rec.at[kShared] + tile * shape.each;
-    const int first = at / plan.per[line];
+    const int at = line == kStream ? rec.at[kStream] : rec.at[kShared] + tile * shape.each;
+    const int more = line == kStream ? 0 : plan.more, first = run_at(at + shape.pad(line, tile), plan.per[line], more, plan.half);
     p.step = line == kStream ? kStreamRows : H;
-    p.n = (at + length - 1) / plan.per[line] - first + 1;
+    p.n = run_at(at + shape.length(tile) - 1, plan.per[line], more, plan.half) - first + 1;
     const size_t place = (size_t)(h / A.group) * A.places[line] + x + (size_t)first * p.step;
     p.o = all[line].o + place * D;
     p.ml = all[line].ml + place;
@@ -680,15 +715,16 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
 
 // ------------------------------------------------------------------- launch
 // Workgroups that run at once, by head; two at least, so that both lines have one.
-int runs_of(int hkv, int D) { return std::max(2, (D == 256 ? 256 : 512) / hkv); }
+int runs_of(int hkv) { return std::max(2, 512 / hkv); }
+bool streams(int D) { return D != 256; }
 int rows_of_tall(int D) { return D == 256 ? 64 : 128; }
 
 size_t rounded(size_t bytes) { return (bytes + 255) / 256 * 256; }
 size_t plan_bytes(int64_t items) { return rounded(sizeof(Plan) + items * sizeof(Record)); }
 // Places of a line: the rows, and a tile's height a run.
 int64_t places_of(int64_t rows, int hkv, int D, int line) {
-  if (line == kStream) return rows + (int64_t)runs_of(hkv, D) * kWaves * kStreamRows;
-  return rows <= kStreamRows ? 0 : rows + (int64_t)runs_of(hkv, D) * rows_of_tall(D);   // no tile has more than 16 rows
+  if (line == kStream) return streams(D) ? rows + (int64_t)runs_of(hkv) * kWaves * kStreamRows : 0;
+  return streams(D) && rows <= kStreamRows ? 0 : rows + (int64_t)runs_of(hkv) * rows_of_tall(D);   // no tile has more than 16 rows
 }
 size_t sums_bytes(int64_t places, int hkv, int D) { return rounded((size_t)places * hkv * D * 4); }
 size_t refs_bytes(int64_t places, int hkv) { return rounded((size_t)places * hkv * 8); }
@@ -782,7 +818,7 @@ int draft_branch_attend(const void* q, int64_t ldq, const uint8_t* k_codes, cons
   A.sinks = std::min(sinks, DL_MAX_POSITIONS);
   A.out = static_cast<uint16_t*>(out);
   A.lse = lse;
-  A.runs = runs_of(hkv, D);
+  A.runs = runs_of(hkv);
   unsigned char* at = static_cast<unsigned char*>(workspace);
   auto take = [&](size_t bytes) {
     unsigned char* p = at;
