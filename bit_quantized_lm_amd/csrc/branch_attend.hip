@@ -265,11 +265,14 @@ __device__ __forceinline__ void cut(const BranchArgs& A, int shared_units, int s
   p.per[kStream] = p.whole ? 1 : max(max((4 * Cost<D>::per_group(kStreamRows)) >> p.shift, 1), (stream_units + waves - 1) / waves);
 }
 
+// LDS accesses before stay before those after, in a wave that is alone with them.
+__device__ __forceinline__ void wave_fence() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
 // Up to 64 sequences and groups: one wave, a sequence and a group a lane, the
 // lists' entries passed between the lanes.  Every workgroup makes the plan for itself.
 constexpr int kSmall = 64;
 template <int D>
-__device__ __forceinline__ void make_plan(const BranchArgs& A, Plan* plan, Record* records) {
+__device__ __forceinline__ void make_plan(const BranchArgs& A, int (&first)[kSmall], int (&last)[kSmall], Plan* plan, Record* records) {
   const int lane = threadIdx.x & 63, s = min(lane, A.b.n_seq - 1), g = min(lane, A.n_groups - 1);
   const int start = A.b.q_start[s], end = A.b.q_start[s + 1], length = A.b.kv_len[s];
   const int2 group{A.group_start[g], A.group_start[g + 1]};
@@ -297,13 +300,16 @@ __device__ __forceinline__ void make_plan(const BranchArgs& A, Plan* plan, Recor
   p.placed = A.window > 0 || __any(inside_prefix(own));
   int p_first = kNoLimit, p_last = kNoLimit;   // behind every prefix
   if (p.placed) {
-    p_last = -1;
-    for (int i = 0; i < A.b.n_seq; ++i) {
-      const int n = __builtin_amdgcn_readlane(q.n, i), len = __builtin_amdgcn_readlane(q.len, i);
-      if (n == 0 || i < members.first || i >= members.last) continue;
-      p_first = min(p_first, len - n);
-      p_last = max(p_last, len - 1);
+    first[lane] = kNoLimit;
+    last[lane] = -1;
+    wave_fence();
+    if (own.n > 0 && of >= 0) {
+      atomicMin(&first[of], q.begin);
+      atomicMax(&last[of], q.len - 1);
     }
+    wave_fence();
+    p_first = first[g];
+    p_last = last[g];
   }
   Item shared = prefix_item(A, members, p_first, p_last);
   if (lane >= A.n_groups) shared.n = 0;
@@ -574,10 +580,11 @@ __global__ __launch_bounds__(kThreads, 2) void branch_parts_kernel(BranchArgs A)
   extern __shared__ __align__(16) u32x4 stage[];
   __shared__ Plan plan_here;
   __shared__ Record records_here[kSmallBatch ? 2 * kSmall : 1];
+  __shared__ int first[kSmallBatch ? kSmall : 1], last[kSmallBatch ? kSmall : 1];   // positions of a group's rows
   const Plan* plan = reinterpret_cast<const Plan*>(A.plan);
   const Record* records = reinterpret_cast<const Record*>(plan + 1);
-  if (kSmallBatch) {
-    if (threadIdx.x < 64) make_plan<D>(A, &plan_here, records_here);
+  if constexpr (kSmallBatch) {
+    if (threadIdx.x < 64) make_plan<D>(A, first, last, &plan_here, records_here);
     __syncthreads();
     if (blockIdx.x == 0) {   // for the launch that joins the parts
       for (int i = threadIdx.x; i < (A.b.n_seq + A.n_groups) * (int)(sizeof(Record) / 4); i += kThreads)
@@ -616,12 +623,27 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
   const int64_t unit = (int64_t)blockIdx.x * (kWaves / W) + wave / W;
   const int r = (int)(unit / chunks), h0 = (int)(unit % chunks) * heads;
   if (r >= A.b.T) return;   // W > 1: all waves, a workgroup has one unit
-  const int s = __builtin_amdgcn_readfirstlane(last_up_to(A.b.n_seq, r, [&](int i) { return A.b.q_start[i]; }));
-  const Seq q = load_seq(A.b, s);
-  if (r < q.row0 || r >= q.row0 + q.n) return;
   const Plan plan = *reinterpret_cast<const Plan*>(A.plan);
   const Record* records = reinterpret_cast<const Record*>(A.plan + sizeof(Plan) / 4);
-  const Record own_record = records[s], prefix_record = records[A.b.n_seq + max(own_record.item.of, 0)];
+  // the row's sequence and its records: of up to 64 items each lane has one, loaded at once
+  Record own_record, prefix_record;
+  if (const int items = A.b.n_seq + A.n_groups; items <= 64) {
+    const int start = A.b.q_start[min(lane, A.b.n_seq - 1)];
+    const Record mine = records[min(lane, items - 1)];
+    auto of_lane = [&](int i, Record& to) {
+      const int* from = reinterpret_cast<const int*>(&mine);
+#pragma unroll
+      for (int k = 0; k < (int)(sizeof(Record) / 4); ++k) reinterpret_cast<int*>(&to)[k] = __builtin_amdgcn_readlane(from[k], i);
+    };
+    const int up_to = (int)__popcll(__ballot(lane < A.b.n_seq && start <= r));
+    of_lane(max(up_to - 1, 0), own_record);
+    of_lane(A.b.n_seq + max(own_record.item.of, 0), prefix_record);
+  } else {
+    const int s = __builtin_amdgcn_readfirstlane(last_up_to(A.b.n_seq, r, [&](int i) { return A.b.q_start[i]; }));
+    own_record = records[s];
+    prefix_record = records[A.b.n_seq + max(own_record.item.of, 0)];
+  }
+  if (r < own_record.item.row0 || r >= own_record.item.row0 + own_record.item.n) return;
   // an item's parts of a row: where the first is, how far apart they are, how many
   struct Run {
     const float* o;
