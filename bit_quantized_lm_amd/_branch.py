@@ -8,6 +8,7 @@ ValueError (an argument) or DraftHeadError (the runtime).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import re
@@ -58,9 +59,10 @@ def branch_header_functions() -> list[str]:
         return re.findall(r"^int (draft_branch_\w+)\s*\(", f.read(), flags=re.M)
 
 
-def _size(f, *args) -> int:
+@functools.lru_cache(maxsize=256, typed=True)
+def _size(name, *args) -> int:
     out = ctypes.c_size_t()
-    B._check(f(*args, ctypes.byref(out)))
+    B._check(getattr(_load(), name)(*args, ctypes.byref(out)))
     return out.value
 
 
@@ -84,7 +86,7 @@ def _ints(name, t, shape, dev):
 def draft_branch_pages_workspace_bytes(n_pages: int, n_new: int) -> int:
     """Device workspace bytes of draft_branch_fork (to at most n_new rows) and
     draft_branch_compact over a pool of n_pages."""
-    return _size(_load().draft_branch_pages_workspace_bytes, n_pages, n_new)
+    return _size("draft_branch_pages_workspace_bytes", n_pages, n_new)
 
 
 def draft_branch_pages_workspace(n_pages: int, n_new: int, device):
@@ -100,9 +102,15 @@ def _pages(k_codes, v_codes, k_scale, v_scale, uses, table, made, uses_out, tabl
         raise ValueError("table must be [sequences][pages]")
     _ints("table", table, table.shape, dev)
     _ints("uses", uses, (n_pages,), dev)
-    uses_out = L._out(uses_out, "uses_out", uses, (n_pages,), L._I32, dev, stream)
-    table_out = L._out(table_out, "table_out", table, (made, table.shape[1]), L._I32, dev, stream)
-    status = L._out(status, "status", uses, (2,), L._I32, dev, stream)
+    wide = table.shape[1]
+    if uses_out is None and table_out is None and status is None:      # one allocation, 1.4 us of the host's time each
+        uses_out, table_out, status = L._out(None, "", uses, (n_pages + made * wide + 2,), L._I32, dev, stream).split_with_sizes(
+            (n_pages, made * wide, 2))
+        table_out = table_out.view(made, wide)
+    else:
+        uses_out = L._out(uses_out, "uses_out", uses, (n_pages,), L._I32, dev, stream)
+        table_out = L._out(table_out, "table_out", table, (made, wide), L._I32, dev, stream)
+        status = L._out(status, "status", uses, (2,), L._I32, dev, stream)
     return dev, (k_codes.data_ptr(), v_codes.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), n_pages, page, hkv, d), uses_out, table_out, status
 
 
@@ -149,7 +157,7 @@ def draft_branch_compact(k_codes, v_codes, k_scale, v_scale, uses, table, uses_o
 def draft_branch_attend_workspace_bytes(rows: int, n_seq: int, hq: int, hkv: int, d: int) -> int:
     """Device workspace bytes of draft_branch_attend's calls of up to `rows` rows
     of up to n_seq sequences."""
-    return _size(_load().draft_branch_attend_workspace_bytes, rows, n_seq, hq, hkv, d)
+    return _size("draft_branch_attend_workspace_bytes", rows, n_seq, hq, hkv, d)
 
 
 def draft_branch_attend_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: int, device):
@@ -191,7 +199,7 @@ def draft_branch_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, 
 def draft_branch_logprobs_workspace_bytes(rows: int, vocab: int, top: int = 0) -> int:
     """Device workspace bytes of draft_branch_logprobs' calls of up to `rows`
     rows of up to `vocab` logits with up to `top` alternatives."""
-    return _size(_load().draft_branch_logprobs_workspace_bytes, rows, vocab, top)
+    return _size("draft_branch_logprobs_workspace_bytes", rows, vocab, top)
 
 
 def draft_branch_logprobs_workspace(rows: int, vocab: int, top: int, device):
@@ -230,11 +238,16 @@ def draft_branch_logprobs(logits, tokens=None, top: int = 0, scale: float = 1.0,
         _ints("tokens", tokens, (rows, n_tok), dev)
     L._need(top >= 0, "top must be >= 0")
     like = logits
-    logprob = L._out(logprob, "logprob", like, (rows, n_tok), L._F32, dev, stream)
+    if logprob is None and top_logprob is None and lse is None and entropy is None:      # one allocation, 1.4 us of the host's time each
+        logprob, top_logprob, lse, entropy = L._out(None, "", like, (rows * (n_tok + top + 2),), L._F32, dev, stream).split_with_sizes(
+            (rows * n_tok, rows * top, rows, rows))
+        logprob, top_logprob = logprob.view(rows, n_tok), top_logprob.view(rows, top)
+    else:
+        logprob = L._out(logprob, "logprob", like, (rows, n_tok), L._F32, dev, stream)
+        top_logprob = L._out(top_logprob, "top_logprob", like, (rows, top), L._F32, dev, stream)
+        lse = L._out(lse, "lse", like, (rows,), L._F32, dev, stream)
+        entropy = L._out(entropy, "entropy", like, (rows,), L._F32, dev, stream)
     top_id = L._out(top_id, "top_id", like, (rows, top), L._I32, dev, stream)
-    top_logprob = L._out(top_logprob, "top_logprob", like, (rows, top), L._F32, dev, stream)
-    lse = L._out(lse, "lse", like, (rows,), L._F32, dev, stream)
-    entropy = L._out(entropy, "entropy", like, (rows,), L._F32, dev, stream)
     at, size, _held = _workspace(workspace, lambda: draft_branch_logprobs_workspace_bytes(rows, n, top), dev, stream)
     B._check(lib.draft_branch_logprobs(
         logits.data_ptr(), kind, ld, rows, n, scale, None if scales is None else scales.data_ptr(), None if tokens is None else tokens.data_ptr(),

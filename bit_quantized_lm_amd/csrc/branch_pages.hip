@@ -41,7 +41,7 @@ struct ForkArgs {
   PoolArgs p;
   const int32_t *kv_len, *parents, *need;
   int n_new, page_shift;
-  int32_t* asked;       // [n_new] free pages that a row takes
+  int32_t* asked;       // [n_new] free pages that a row takes, and kEldest
 };
 
 struct CompactArgs {
@@ -101,13 +101,14 @@ __device__ __forceinline__ void survey_chunk(const PoolArgs& A, int chunk, int* 
 }
 
 // ---------------------------------------------------------------------- fork
+constexpr int kEldest = 1 << 30;   // the first row with its parent
 struct Row {
   int parent, len, full, last;
   bool eldest;              // the first row with its parent
   const int32_t* old;       // the parent's entries
 };
 
-__device__ __forceinline__ Row row_of(const ForkArgs& A, int s) {
+__device__ __forceinline__ Row row_of(const ForkArgs& A, int s, bool eldest) {
   Row r;
   const int p = A.parents[s], page = 1 << A.page_shift, cap = A.p.wide << A.page_shift;
   const bool has = (unsigned)p < (unsigned)A.p.rows;
@@ -116,9 +117,7 @@ __device__ __forceinline__ Row row_of(const ForkArgs& A, int s) {
   r.len = has ? min(max(A.kv_len[p], 0), cap) : 0;
   r.full = r.len >> A.page_shift;
   r.last = (int)(((int64_t)min(max(A.need[s], r.len), cap) + page - 1) >> A.page_shift);
-  int before = 0;
-  for (int i = threadIdx.x; has && i < s; i += kThreads) before |= A.parents[i] == p;
-  r.eldest = !__syncthreads_or(before) && has;
+  r.eldest = eldest;
   return r;
 }
 
@@ -138,11 +137,16 @@ __global__ __launch_bounds__(kThreads) void fork_survey_kernel(ForkArgs A) {
     return;
   }
   const int s = blockIdx.x - A.p.n_chunks;
-  const Row r = row_of(A, s);
+  const int p = A.parents[s];
+  const bool has = (unsigned)p < (unsigned)A.p.rows;
+  int before = 0;
+  for (int i = threadIdx.x; has && i < s; i += kThreads) before |= A.parents[i] == p;
+  const bool eldest = !__syncthreads_or(before) && has;
+  const Row r = row_of(A, s, eldest);
   int n = 0;
   for (int j = r.full + threadIdx.x; j < r.last; j += kThreads) n += !stays(A, r, named(A, r, j));
   n = block_sum(n, lds);
-  if (threadIdx.x == 0) A.asked[s] = n;
+  if (threadIdx.x == 0) A.asked[s] = n | (eldest ? kEldest : 0);
 }
 
 // The free pages of ranks rank .. rank + n - 1 (n at most kThreads) to list[0 ..
@@ -151,13 +155,18 @@ __global__ __launch_bounds__(kThreads) void fork_survey_kernel(ForkArgs A) {
 struct Finder {
   int sums[kThreads / 64], start[kThreads], first, last, list[kThreads];
 };
-__device__ __forceinline__ void free_pages(const PoolArgs& A, int rank, int n, Finder& f) {
+struct Counted {   // of the first kThreads chunks: the thread's, the free pages before it, and in all of them
+  int c, begin, total;
+};
+__device__ __forceinline__ void free_pages(const PoolArgs& A, const Counted& head, int rank, int n, Finder& f) {
   const int tid = threadIdx.x;
   int at = 0;
   for (int base = 0; base < A.n_chunks && at < rank + n; base += kThreads) {
-    const int c = base + tid < A.n_chunks ? A.counts[base + tid] : 0;
-    int total;
-    const int begin = at + block_before(c, total, f.sums);
+    int c = head.c, begin = head.begin, total = head.total;
+    if (base > 0) {
+      c = base + tid < A.n_chunks ? A.counts[base + tid] : 0;
+      begin = at + block_before(c, total, f.sums);
+    }
     f.start[tid] = begin;
     if (tid == 0) f.first = kThreads, f.last = -1;
     __syncthreads();
@@ -225,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
     r.old = A.p.table + (size_t)p * A.p.wide;
     r.parent = p;
   } else {
-    r = row_of(A, s);
+    r = row_of(A, s, (A.asked[s] & kEldest) != 0);
     if (r.len & ((1 << A.page_shift) - 1)) {
       partial = named(A, r, r.full);
       if (stays(A, r, partial)) partial = -1;
@@ -233,16 +242,34 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
     if (slice > 0 && partial < 0) return;
   }
   // what is free, what is asked for, and by the rows before this one
+  Counted head;
   int free = 0, asked = 0, before = 0;
-  for (int i = tid; i < A.p.n_chunks; i += kThreads) free += A.p.counts[i];
+  head.c = tid < A.p.n_chunks ? A.p.counts[tid] : 0;
+  for (int i = kThreads + tid; i < A.p.n_chunks; i += kThreads) free += A.p.counts[i];
   for (int i = tid; i < A.n_new; i += kThreads) {
-    const int n = A.asked[i];
+    const int n = A.asked[i] & ~kEldest;
     asked += n;
     before += i < s ? n : 0;
   }
-  free = block_sum(free, f.sums);
-  asked = block_sum(asked, f.sums);
-  before = block_sum(before, f.sums);
+  __shared__ int4 of_wave[kThreads / 64];
+  const int up_to = wave_inclusive_sum(head.c);
+  free = wave_inclusive_sum(free);
+  asked = wave_inclusive_sum(asked);
+  before = wave_inclusive_sum(before);
+  if ((tid & 63) == 63) of_wave[tid >> 6] = int4{up_to, free, asked, before};
+  __syncthreads();
+  head.begin = up_to - head.c;
+  head.total = free = asked = before = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 64; ++w) {
+    const int4 x = of_wave[w];
+    head.begin += w < tid >> 6 ? x.x : 0;
+    head.total += x.x;
+    free += x.y;
+    asked += x.z;
+    before += x.w;
+  }
+  free += head.total;
   const bool done = asked <= free;
   if (blockIdx.x == 0 && tid == 0) {
     atomicAdd(A.p.status, done ? free - asked : free);
@@ -263,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
       if (j0 < r.last && j0 + kThreads > r.full) {
         const int at = block_before(takes && done, n, f.sums);
         if (n > 0) {
-          free_pages(A.p, rank, n, f);
+          free_pages(A.p, head, rank, n, f);
           // an id is looked at before it is written through: counts that change meanwhile fault nothing
           if (takes) entry = (unsigned)f.list[at] < (unsigned)A.p.n_pages ? f.list[at] : -1;
           __syncthreads();
@@ -279,7 +306,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
     }
   }
   if (!old_row && partial >= 0 && done) {
-    free_pages(A.p, before, 1, f);
+    free_pages(A.p, head, before, 1, f);
     if ((unsigned)f.list[0] < (unsigned)A.p.n_pages) copy_page(A.p, partial, f.list[0], slice);
   }
   freed = wave_inclusive_sum(freed);
@@ -287,6 +314,11 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
 }
 
 // ------------------------------------------------------------------- compact
+// A pool of one chunk is numbered by every workgroup that moves pages, in LDS, in the
+// one launch; a larger one by launches of their own (a launch is 3 us of the host's
+// time: a third of 700 pages of 64 tokens on 8 heads of 128, 18.8 us in three, 12.3 in
+// one; four chunks counted by every workgroup that numbers them, without the first
+// launch, cost what that one takes: 116 us for 8,192 pages, 113 in three).
 __global__ __launch_bounds__(kThreads) void compact_survey_kernel(CompactArgs A) {
   __shared__ int lds[kThreads / 64];
   survey_chunk<false>(A.p, blockIdx.x, lds);
@@ -360,6 +392,61 @@ __global__ __launch_bounds__(kThreads) void compact_move_kernel(CompactArgs A, i
   for (int64_t i = (int64_t)(blockIdx.x - movers) * kThreads + tid; i < entries; i += (int64_t)(gridDim.x - movers) * kThreads) {
     int id = A.p.table[i];
     if (id >= used && id < A.p.n_pages && A.p.uses[id] > 0) id = A.dst[A.number[id]];
+    A.p.table_out[i] = id;
+  }
+}
+
+// All of it, of one chunk.  Grid as the one above; the first workgroup for the
+// table's entries writes counts and status too.
+__global__ __launch_bounds__(kThreads) void compact_chunk_kernel(CompactArgs A, int movers) {
+  __shared__ int lds[kThreads / 64];
+  __shared__ int16_t src[kChunk / 2 + 1], dst[kChunk / 2 + 1], number[kChunk];
+  const int tid = threadIdx.x;
+  const Eight e = load_uses(A.p, 0, 0);
+  int mine = 0, used;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) mine += e.u[k] > 0;
+  const int before = block_before(mine, used, lds);
+  int front = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) front += e.u[k] > 0 && tid * 8 + k < used;
+  front = block_sum(front, lds);
+  int rank = before;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = tid * 8 + k;
+    const bool taken = e.u[k] > 0;
+    number[i] = -1;
+    if (taken && i >= used)
+      src[rank - front] = i, number[i] = rank - front;
+    else if (!taken && i < used)
+      dst[i - rank] = i;
+    rank += taken;
+  }
+  __syncthreads();
+  const int moves = used - front;
+  if ((int)blockIdx.x < movers) {
+    for (int i = blockIdx.x; i < moves * A.p.slices; i += movers) copy_page(A.p, src[i / A.p.slices], dst[i / A.p.slices], i % A.p.slices);
+    return;
+  }
+  if ((int)blockIdx.x == movers) {
+    rank = before;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = tid * 8 + k;
+      const bool taken = e.u[k] > 0;
+      if (i < A.p.n_pages) A.p.uses_out[i] = i >= used ? 0 : taken ? e.u[k] : A.p.uses[src[i - rank]];
+      rank += taken;
+    }
+    if (tid == 0) {
+      A.p.status[0] = used;
+      A.p.status[1] = moves;
+    }
+  }
+  const int64_t entries = (int64_t)A.p.rows * A.p.wide;
+  for (int64_t i = (int64_t)(blockIdx.x - movers) * kThreads + tid; i < entries; i += (int64_t)(gridDim.x - movers) * kThreads) {
+    int id = A.p.table[i];
+    if ((unsigned)id < (unsigned)A.p.n_pages && number[id] >= 0) id = dst[number[id]];
     A.p.table_out[i] = id;
   }
 }
@@ -459,11 +546,15 @@ int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, flo
   A.dst = A.src + moves_bytes(n_pages) / 4;
   A.number = A.dst + moves_bytes(n_pages) / 4;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  hipLaunchKernelGGL(compact_survey_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
-  hipLaunchKernelGGL(compact_number_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
   // eight workgroups a CU, or a move at most for every second page
   const int movers = (int)std::min<int64_t>(2048, std::max<int64_t>((int64_t)(n_pages / 2) * A.p.slices, 1));
   const int entries = (int)std::min<int64_t>(256, ((int64_t)n_rows * max_pages + kThreads - 1) / kThreads);
+  if (A.p.n_chunks == 1) {
+    hipLaunchKernelGGL(compact_chunk_kernel, dim3(movers + entries), dim3(kThreads), 0, st, A, movers);
+    return launched("compact_chunk_kernel");
+  }
+  hipLaunchKernelGGL(compact_survey_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
+  hipLaunchKernelGGL(compact_number_kernel, dim3(A.p.n_chunks), dim3(kThreads), 0, st, A);
   hipLaunchKernelGGL(compact_move_kernel, dim3(movers + entries), dim3(kThreads), 0, st, A, movers);
   return launched("compact_move_kernel");
 }
