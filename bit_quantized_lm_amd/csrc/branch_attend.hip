@@ -735,6 +735,83 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
   }
 }
 
+// ------------------------------------------------------------------ short ones
+// Contexts that are short by the table's width, and few rows: a tile of 16 rows a
+// workgroup, whose waves take turns at what it sees, the prefix's tokens and its own.
+// Nothing is shared but through the caches, nothing planned or joined, in one launch
+// (3 us of the host's time, and 5 of the card's).  Heads of 128, 40 on 8, one row of
+// each of 4 sequences over 500, 1,000, 2,000 and 4,000 tokens: 8.3, 10.1, 14.0 and
+// 21.6 us so, 15.8, 16.0, 16.7 and 18.0 planned; 9 rows of each of 16: 16.3, 20.3,
+// 28.4 and 46.0, planned 30.8, 33.6, 38.4 and 44.2; 100 of each of 4, 1,032 tiles:
+// 32.4, 40.8, 56.5 and 90.9, planned 42.9, 47.5, 57.3 and 72.5.  Heads of 256, 16 on
+// 2, one row of each of 4 over 500, 1,000 and 2,000: 11.4, 16.2 and 25.0, planned 17.7,
+// 17.9 and 17.8.
+template <int D>
+constexpr int kShortWaves = D == 256 ? 4 : 8;   // heads of 256: a wave a SIMD
+template <int D>
+constexpr size_t kShortLds = (size_t)kShortWaves<D> * kStreamRows * (D + 4 + 2) * 4;   // a wave's sums, references and sums of weights
+
+template <int D>
+__global__ __launch_bounds__(64 * kShortWaves<D>, D == 256 ? 1 : 2) void branch_short_kernel(BranchArgs A) {
+  extern __shared__ __align__(16) u32x4 stage[];
+  constexpr int C = D / 16, W = kShortWaves<D>, R = kStreamRows;
+  const int head = blockIdx.x % A.c.hkv, tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, hi = lane >> 4, lo = lane & 15;
+  int s, tile;
+  if (!find_item(A.b, blockIdx.x / A.c.hkv, [&](const Seq& q) { return (q.n * A.group + R - 1) / R; }, s, tile)) return;
+  const Seq q = load_seq(A.b, s);
+  const int g = __builtin_amdgcn_readfirstlane(A.group_start[0] <= s ? last_up_to(A.n_groups + 1, s, [&](int i) { return A.group_start[i]; }) : -1);
+  const bool grouped = g >= 0 && g < A.n_groups;
+  Item t{};
+  t.sees = grouped ? 3 : 1;
+  t.split = grouped ? min(max(A.prefix_len[g], 0), kNoLimit) : 0;
+  const int lead = grouped ? min(max(A.group_start[g], 0), A.b.n_seq - 1) : s;
+  const int x0 = tile * R, rows = min(R, q.n * A.group - x0);
+  const int p_first = q.begin + x0 / A.group, p_last = q.begin + (x0 + rows - 1) / A.group;
+  const Range own = visible_own(A, t, p_first, p_last), shared = visible_shared(A, t, p_first, p_last);
+  auto place = [&](int r, int& pos) {
+    const int x = x0 + r, row = q.row0 + x / A.group;
+    pos = r < rows ? q.begin + x / A.group : -1;
+    return A.q + (int64_t)row * A.ldq + (head * A.group + x % A.group) * D;
+  };
+  const Tokens<true> tokens{A.b, A.c, s, head, own, A.window, A.sinks, shared, lead, t.split};
+  stream_tile<D, W, 0>(tokens, 0, own.n + shared.n, rows, p_first, p_last, A.scale_log2, place,
+                       [&](const f32x4 (&o)[1][C], const float (&m)[1], const float (&l)[1]) {
+    float* sums = reinterpret_cast<float*>(stage);   // [W][R][D + 4]
+    float* ref = sums + W * R * (D + 4);              // [W][R]
+    float* weight = ref + W * R;
+    float sum = l[0];
+    sum += __shfl_xor(sum, 16);
+    sum += __shfl_xor(sum, 32);
+    if (hi == 0) {
+      ref[wave * R + lo] = m[0];
+      weight[wave * R + lo] = sum;
+    }
+#pragma unroll
+    for (int c = 0; c < C; ++c) *reinterpret_cast<f32x4*>(sums + (wave * R + lo) * (D + 4) + c * 16 + hi * 4) = o[0][c];
+    __syncthreads();
+    const int r = tid / (4 * W);   // 4 W threads a row
+    if (r >= rows) return;
+    float top = ref[r], all = 0.0f, share[W];
+#pragma unroll
+    for (int v = 1; v < W; ++v) top = fmaxf(top, ref[v * R + r]);
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      share[v] = __builtin_amdgcn_exp2f(ref[v * R + r] - top);
+      all = fmaf(weight[v * R + r], share[v], all);
+    }
+    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+    const size_t row = (size_t)(q.row0 + (x0 + r) / A.group) * A.hq + head * A.group + (x0 + r) % A.group;
+#pragma unroll
+    for (int e = tid % (4 * W) * 4; e < D; e += 16 * W) {
+      f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int v = 0; v < W; ++v) y += share[v] * *reinterpret_cast<const f32x4*>(sums + (v * R + r) * (D + 4) + e);
+      *reinterpret_cast<u32x2*>(A.out + row * D + e) = u32x2{bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv)};
+    }
+    if (tid % (4 * W) == 0) write_lse(A.lse, row, top, all);
+  });
+}
+
 // ------------------------------------------------------------------- launch
 // Workgroups that run at once, by head; two at least, so that both lines have one.
 int runs_of(int hkv) { return std::max(2, 512 / hkv); }
@@ -769,8 +846,20 @@ int launch_parts(const BranchArgs& A, hipStream_t s) {
   return launched("branch_parts_kernel");
 }
 
+// The short ones: tokens that the table has room for, and tiles, two rounds of a card's workgroups.
+int short_tokens(int D) { return D == 256 ? 1024 : 2048; }
+constexpr int kShortTiles = 1024;
+
 template <int D>
 int launch(const BranchArgs& A, hipStream_t s) {
+  const int64_t short_tiles = ((int64_t)A.b.T * A.group / kStreamRows + A.b.n_seq) * A.c.hkv;   // at least as many as there are
+  if (((int64_t)A.b.max_pages << A.c.page_shift) <= short_tokens(D) && short_tiles <= kShortTiles) {
+    static dh::OncePerDevice once;
+    const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_short_kernel<D>), kShortLds<D>);
+    if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_short_kernel: %s", hipGetErrorString(e));
+    hipLaunchKernelGGL(branch_short_kernel<D>, dim3((unsigned)short_tiles), dim3(64 * kShortWaves<D>), kShortLds<D>, s, A);
+    return launched("branch_short_kernel");
+  }
   const int rc = A.b.n_seq <= kSmall && A.n_groups <= kSmall ? launch_parts<D, true>(A, s) : launch_parts<D, false>(A, s);
   if (rc) return rc;
   constexpr int P = 256 / D;   // rows a pass

@@ -263,12 +263,13 @@ class Branches:
     """A cache with random contents and a batch whose groups share prefixes.
     groups: [(prefix, [(new, tokens from the prefix's end on)])]; loose: [(new, tokens)]."""
 
-    def __init__(self, dev, groups, loose, hq, hkv, d, page, seed, max_pages=None, members_know=True):
+    def __init__(self, dev, groups, loose, hq, hkv, d, page, seed, max_pages=None, members_know=True, wide=False, quick=False):
+        """wide: a table with room for more tokens than what is short; quick: codes that are all alike likely."""
         rng = self.rng = np.random.default_rng(seed)
         self.dev, self.hq, self.hkv, self.d, self.page = dev, hq, hkv, d, page
         lens = [(n, p + t, p, i == 0) for p, m in groups for i, (n, t) in enumerate(m)] + [(n, t, 0, True) for n, t in loose]
         reach = max([t for _, t, _, _ in lens] + [p for p, _ in groups] + [1])
-        self.max_pages = max_pages or -(-reach // page) + 1
+        self.max_pages = max_pages or max(-(-reach // page) + 1, (2048 // page + 3) * wide)
         n_pages = sum(-(-max(t, p) // page) for _, t, p, _ in lens) + 3
         order, at = rng.permutation(n_pages), 0
         self.table = np.full((len(lens), self.max_pages), -7, np.int32)
@@ -289,7 +290,8 @@ class Branches:
         self.prefix_len = np.array([p for p, _ in groups], np.int32)
         self.rows = int(self.q_start[-1])
         shape = (n_pages, hkv, page, d)
-        self.codes = [(np.clip(np.rint(rng.standard_normal(shape) * 33), -127, 127) + 128).astype(np.uint8) for _ in range(2)]
+        self.codes = [rng.integers(1, 256, shape, dtype=np.uint8) if quick else
+                      (np.clip(np.rint(rng.standard_normal(shape) * 33), -127, 127) + 128).astype(np.uint8) for _ in range(2)]
         self.scales = [rng.uniform(0.01, 0.06, shape[:2]).astype(np.float32) for _ in range(2)]
         self.q = torch.from_numpy(rng.standard_normal((self.rows, hq, d)).astype(np.float32)).to(torch.bfloat16)
 
@@ -346,22 +348,62 @@ ATTENDS = [
 ]
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("groups,loose,hq,hkv,d,page,window,sinks", ATTENDS)
-def test_attend(dev, groups, loose, hq, hkv, d, page, window, sinks):
-    Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq + len(groups), members_know=len(groups) % 2 == 0).check(window, sinks)
+def test_attend(dev, groups, loose, hq, hkv, d, page, window, sinks, wide):
+    Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq + len(groups), members_know=len(groups) % 2 == 0, wide=wide).check(window, sinks)
 
 
-def test_attend_is_the_layers(dev):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_is_the_layers(dev, wide):
     """Where the rows name one prefix's pages, draft_layer_attend of the same batch says the same."""
-    c = Branches(dev, [(640, [(3, 50), (9, 70), (1, 1)]), (128, [(2, 30)] * 6)], [(4, 100)], 10, 2, 128, 64, seed=1)
+    c = Branches(dev, [(640, [(3, 50), (9, 70), (1, 1)]), (128, [(2, 30)] * 6)], [(4, 100)], 10, 2, 128, 64, seed=1, wide=wide)
     out, lse = c.check()
     want, lwant = L.draft_layer_attend(c.q.to(dev), *c.cache, *c.batch[:3])
     assert float((lse - lwant).abs().max()) < 1e-4 and float((out.float() - want.float()).abs().max()) < 0.02
 
 
-def test_attend_leaves_other_rows_alone(dev):
+@pytest.mark.parametrize("groups,loose,hq,hkv,d,window", [
+    ([(20000, [(9, 60), (5, 40), (9, 10), (0, 5)]), (12000, [(9, 60)] * 4)], [], 40, 8, 128, 0),       # runs that hold several tiles
+    ([(30000, [(100, 100), (70, 300)])], [], 64, 64, 64, 0),                                         # long runs, shares that are not even
+    ([(3000, [(150 - i, 150) for i in range(12)])], [(200, 700)], 40, 8, 128, 0),                    # members with their prefix in them
+    ([(700, [(1, 20 + i) for i in range(150)]), (2400, [(1, 9), (3, 90)] * 75)], [(2, 900)] * 9, 8, 2, 128, 0),      # many sequences
+    ([(40 * i + 30, [(2, 3 + i)] * 2) for i in range(90)], [(1, 5)], 4, 2, 64, 0),                   # many groups
+    ([(3000, [(4, 100)] * 20)], [(4, 2500)], 16, 2, 256, 0),
+    ([(9000, [(4, 300)] * 12)], [(4, 5000)] * 2, 16, 2, 256, 2048),
+    ([(2500, [(1, 3000 + i) for i in range(20)])], [], 8, 1, 64, 0),                                 # few rows over many tokens of their own
+    ([(2500, [(1, 3000 + i) for i in range(20)])], [], 6, 3, 128, 3500),
+    ([(60000, [(1, 1)])], [], 1, 1, 128, 0),
+])
+def test_attend_of_large_batches_is_the_layers(dev, groups, loose, hq, hkv, d, window):
+    """Both attend to the same values: a difference is their rounding to bf16, of what is up to the largest of them."""
+    c = Branches(dev, groups, loose, hq, hkv, d, 64, seed=hq + d, quick=True, wide=True).upload()
+    c.table[c.table < 0] = 0      # a member's entry for the prefix's last page: the layer's call reads its own
+    for g, (prefix, m) in enumerate(groups):
+        for i in range(1, len(m)):
+            s, j = int(c.group_start[g]) + i, prefix // 64
+            if prefix % 64 and j < c.max_pages:      # the same tokens there
+                a, b = c.table[int(c.group_start[g]), j], c.table[s, j]
+                for x, byte in zip(c.cache[:2], (OL.key_byte, OL.value_byte)):
+                    at = torch.tensor([byte(t, e, d) for t in range(prefix % 64) for e in range(d)], device=dev)
+                    flat = x.view(x.shape[0], hkv, -1)
+                    flat[int(b)][:, at] = flat[int(a)][:, at]
+                for x in c.cache[2:]:
+                    x[int(b)] = x[int(a)]
+    c.batch[2] = ints(c.table, dev)
+    q = c.q.to(dev)
+    got = R.draft_branch_attend(q, *c.cache, *c.batch, window=window, sinks=4)
+    want = L.draft_layer_attend(q, *c.cache, *c.batch[:3], window=window, sinks=4)
+    again = R.draft_branch_attend(q, *c.cache, *c.batch, window=window, sinks=4)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+    assert float((got[1] - want[1]).abs().max()) < 1e-4
+    assert float((got[0].float() - want[0].float()).abs().max()) <= 2.0 ** -7 * float(want[0].float().abs().max())
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_leaves_other_rows_alone(dev, wide):
     """Rows behind the last sequence, and a row stride."""
-    c = Branches(dev, [(100, [(2, 20), (0, 3), (3, 9)])], [(1, 40)], 4, 2, 64, 32, seed=2)
+    c = Branches(dev, [(100, [(2, 20), (0, 3), (3, 9)])], [(1, 40)], 4, 2, 64, 32, seed=2, wide=wide)
     q = torch.zeros((c.rows + 5, 7, 64), dtype=torch.bfloat16, device=dev)[:, :4]
     q[:c.rows] = c.q.to(dev)
     out, lse = torch.full((c.rows + 5, 4, 64), 7.0, dtype=torch.bfloat16, device=dev), torch.full((c.rows + 5, 4), 7.0, device=dev)
@@ -369,19 +411,22 @@ def test_attend_leaves_other_rows_alone(dev):
     assert bool((out[c.rows:] == 7).all()) and bool((lse[c.rows:] == 7).all())
 
 
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("new", [1, 30])
-def test_attend_missing_pages_and_the_tables_end(dev, new):
-    c = Branches(dev, [(300, [(new, new + 40), (new, new + 10)])], [(new, 200)], 4, 1, 64, 32, seed=3)
+def test_attend_missing_pages_and_the_tables_end(dev, new, wide):
+    c = Branches(dev, [(300, [(new, new + 40), (new, new + 10)])], [(new, 200)], 4, 1, 64, 32, seed=3, wide=wide)
     c.table[0, 3], c.table[1, 9], c.table[2, 2] = -1, 1 << 30, len(c.codes[0])
     c.check()
     for window, sinks in ((0, 0), (50, 3)):
         Branches(dev, [(300, [(new, new + 40), (new, new + 10)])], [(new, 400)], 4, 1, 64, 32, seed=4, max_pages=10).check(window, sinks)
+        Branches(dev, [(2000, [(new, new + 200), (new, new + 60)])], [(new, 2300)], 4, 1, 64, 32, seed=4, max_pages=65).check(window, sinks)
 
 
-def test_attend_of_values_that_are_no_numbers(dev):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_of_values_that_are_no_numbers(dev, wide):
     """A page whose scale is none makes the rows that see it NaN, a query its own row; no others."""
     for new in (1, 30):
-        c = Branches(dev, [(100, [(new, new + 10), (new, new + 40)]), (64, [(new, new), (new, new + 5)])], [], 4, 2, 64, 32, seed=5)
+        c = Branches(dev, [(100, [(new, new + 10), (new, new + 40)]), (64, [(new, new), (new, new + 5)])], [], 4, 2, 64, 32, seed=5, wide=wide)
         c.scales[0][c.table[0, 1], 0] = np.nan          # the first group's prefix, the first kv head
         c.scales[1][c.table[3, 2 + (new + 4) // 32], 1] = np.inf      # a sequence's own last page, the second
         c.upload()
@@ -397,9 +442,10 @@ def test_attend_of_values_that_are_no_numbers(dev):
         assert np.array_equal(bad, want) and np.array_equal(torch.isnan(out.float()).any(-1).cpu().numpy(), want)
 
 
-def test_attend_groups_that_no_caller_should_have(dev):
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_groups_that_no_caller_should_have(dev, wide):
     """Row starts, groups and lengths that do not fit each other fault nothing and touch no row outside."""
-    c = Branches(dev, [(100, [(3, 20), (3, 9)]), (64, [(2, 9)])], [(1, 40)], 4, 2, 64, 32, seed=6).upload()
+    c = Branches(dev, [(100, [(3, 20), (3, 9)]), (64, [(2, 9)])], [(1, 40)], 4, 2, 64, 32, seed=6, wide=wide).upload()
     rng = np.random.default_rng(7)
     for t in range(12):
         start = ints(rng.integers(-5, 20, 5), dev)
@@ -410,10 +456,12 @@ def test_attend_groups_that_no_caller_should_have(dev):
         assert bool((out[c.rows:] == 7).all())
 
 
-def test_attend_repeats_to_the_bit_on_another_stream_and_in_graphs(dev):
-    """Two graphs that share one workspace, replayed in turn with eager calls between."""
-    cases = [Branches(dev, [(900, [(1, 30)] * 9)], [(1, 50)], 10, 2, 128, 64, seed=8).upload(),
-             Branches(dev, [(300, [(20, 60), (50, 50)])], [], 8, 2, 64, 32, seed=9).upload()]
+@pytest.mark.parametrize("wide", [False, True])
+def test_attend_repeats_to_the_bit_on_another_stream_and_in_graphs(dev, wide):
+    """Graphs that share one workspace, replayed in turn with eager calls between."""
+    cases = [Branches(dev, [(900, [(1, 30)] * 9)], [(1, 50)], 10, 2, 128, 64, seed=8, wide=wide).upload(),
+             Branches(dev, [(300, [(20, 60), (50, 50)])], [], 8, 2, 64, 32, seed=9, wide=wide).upload(),
+             Branches(dev, [(300, [(1, 60)] * 70)], [], 8, 2, 64, 32, seed=9, wide=wide).upload()]
     ws = torch.full((max(R.draft_branch_attend_workspace_bytes(c.rows, len(c.kv_len), c.hq, c.hkv, c.d) for c in cases),), 255, dtype=torch.uint8, device=dev)
     graphs = []
     for c in cases:
@@ -553,6 +601,30 @@ def test_logprobs(dev, kind, m, n, top, n_tok, gap):
     tokens = rng.integers(-1, n + 1, (m, n_tok))
     for dtype in (torch.bfloat16, torch.float32):
         check_logprobs(dev, x, tokens, top, scale=0.7, gap=gap, dtype=dtype)
+
+
+LONG = [(kind, *sizes) for kind in ("plain", "few values", "rising", "falling", "equal", "peaked", "kept")
+        for sizes in ((2, 140001, 64, 3), (3, 124160, 20, 0), (1, 1200007, 64, 0))] + [(kind, 1030, 20011, 20, 1) for kind in ("plain", "rising")]
+
+
+@pytest.mark.parametrize("kind,m,n,top,gap", LONG)
+def test_logprobs_of_long_rows(dev, kind, m, n, top, gap):
+    """Rows of many steps: bounds that are raised on the way, more elements above them than are put down."""
+    rng = np.random.default_rng(n + top + m)
+    x = rows_of(rng, m, n, kind)
+    for dtype in (torch.bfloat16, torch.float32):
+        check_logprobs(dev, x, rng.integers(0, n, (m, 1)), top, gap=gap, dtype=dtype)
+
+
+def test_logprobs_alternatives_at_the_edges(dev):
+    """The best stand before the first 16 bytes' boundary and behind the last one; rows of few elements, at every alignment."""
+    rng = np.random.default_rng(5)
+    for n in (1, 2, 6, 7, 8, 9, 15, 16, 17, 23, 100, 4096, 4103, 9000):
+        x = rows_of(rng, 9, n, "plain")
+        x[:, 0] += 20
+        x[:, -1] += 21
+        for dtype in (torch.bfloat16, torch.float32):
+            check_logprobs(dev, x, np.stack([np.zeros(9, np.int64), np.full(9, n - 1)], 1), 5, gap=1, dtype=dtype)
 
 
 @pytest.mark.parametrize("m", [1, 9, 72, 128])
