@@ -313,6 +313,125 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
   if ((tid & 63) == 63 && freed > 0) atomicAdd(A.p.status, freed);
 }
 
+// All of it, of one chunk and few rows: every workgroup counts and gives out for
+// itself, in LDS; the first makes the table and the counts, the others copy pages.  A
+// launch less is 3 us of the host's time: 32 rows of 8 sequences over 1,500 tokens, 880
+// entries in both tables, take 12.7 us in a loop of calls, 16.0 in two launches.  On the
+// card 8.5 and 12.1; 1,760 entries 11.2 and 14.2, 3,600 19.1 and 21.3, 4,480 13.9 and 11.9,
+// 8,448 26.9 and 21.5.
+constexpr int kFewRows = kThreads, kFewEntries = 4096;
+constexpr int kFewTaken = 8;   // entries that a first row's own thread goes through; of more all threads do
+
+__global__ __launch_bounds__(kThreads) void fork_chunk_kernel(ForkArgs A) {
+  __shared__ int uses[kChunk], counts[kChunk], first[kThreads], takes_from[kThreads], many[kThreads], n_many, lds[kThreads / 64];
+  __shared__ int16_t list[kChunk];   // the free pages
+  const int tid = threadIdx.x;
+  const Eight e = load_uses(A.p, 0, 1);
+  const int p = tid < A.n_new ? A.parents[tid] : -1;
+  const bool has = (unsigned)p < (unsigned)A.p.rows;
+  int mine = 0, free, asked;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    uses[tid * 8 + k] = e.u[k];
+    counts[tid * 8 + k] = max(e.u[k], 0);
+    mine += e.u[k] <= 0;
+  }
+  first[tid] = kThreads;
+  if (tid == 0) n_many = 0;
+  int at = block_before(mine, free, lds);   // its barriers are first's and uses' too
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (e.u[k] <= 0) list[at++] = tid * 8 + k;
+  if (has) atomicMin(&first[p], tid);
+  __syncthreads();
+  auto kept = [&](bool eldest, int id) { return eldest && id >= 0 && uses[id] == 1; };
+  Row r{};
+  int n = 0;
+  if (tid < A.n_new) {
+    r = row_of(A, tid, has && first[p] == tid);
+    n = r.last - r.full;
+    if (r.eldest && n > kFewTaken)
+      many[atomicAdd(&n_many, 1)] = tid;
+    else
+      for (int j = r.full; r.eldest && j < r.last; ++j) n -= kept(true, named(A, r, j));
+  }
+  __syncthreads();
+  for (int i = 0; i < n_many; ++i) {
+    const Row row = row_of(A, many[i], true);
+    int stay = 0;
+    for (int j = row.full + tid; j < row.last; j += kThreads) stay += kept(true, named(A, row, j));
+    stay = block_sum(stay, lds);
+    if (tid == many[i]) n -= stay;
+  }
+  takes_from[tid] = block_before(n, asked, lds);
+  __syncthreads();
+  const bool done = asked <= free;
+  if (blockIdx.x > 0) {
+    const int s = (blockIdx.x - 1) / A.p.slices, parent = A.parents[s];
+    const Row row = row_of(A, s, (unsigned)parent < (unsigned)A.p.rows && first[parent] == s);
+    if (!done || !(row.len & ((1 << A.page_shift) - 1))) return;
+    const int from = named(A, row, row.full);
+    if (from >= 0 && !kept(row.eldest, from)) copy_page(A.p, from, list[takes_from[s]], (blockIdx.x - 1) % A.p.slices);
+    return;
+  }
+  const int wide = A.p.wide;
+  for (int i = tid; i < A.n_new * wide; i += kThreads) {
+    const int s = i / wide, j = i % wide, parent = A.parents[s];
+    const Row row = row_of(A, s, (unsigned)parent < (unsigned)A.p.rows && first[parent] == s);
+    const bool asks = j >= row.full && j < row.last;
+    if (done && asks && row.eldest) continue;   // below, in order
+    const int id = named(A, row, j), entry = j < row.full ? id : asks && done ? list[takes_from[s] + j - row.full] : -1;
+    A.p.table_out[i] = done ? entry : -1;
+    if (!done) continue;
+    if (entry >= 0 && !row.eldest) atomicAdd(&counts[entry], 1);
+    if (row.eldest && id >= 0 && j >= row.last) atomicSub(&counts[id], 1);
+  }
+  if (done) {
+    auto put = [&](int s, int j, int id, int taken) {   // taken: -1 where the entry stays
+      A.p.table_out[(size_t)s * wide + j] = taken < 0 ? id : taken;
+      if (taken < 0) return;
+      atomicAdd(&counts[taken], 1);
+      if (id >= 0) atomicSub(&counts[id], 1);
+    };
+    if (r.eldest && r.last - r.full <= kFewTaken) {
+      int next = takes_from[tid];
+      for (int j = r.full; j < r.last; ++j) {
+        const int id = named(A, r, j);
+        put(tid, j, id, kept(true, id) ? -1 : list[next++]);
+      }
+    }
+    for (int i = 0; i < n_many; ++i) {
+      const Row row = row_of(A, many[i], true);
+      int next = takes_from[many[i]];
+      for (int j0 = row.full; j0 < row.last; j0 += kThreads) {
+        const int j = j0 + tid, id = j < row.last ? named(A, row, j) : -1;
+        const bool takes = j < row.last && !kept(true, id);
+        int all;
+        const int rank = block_before(takes, all, lds);
+        if (j < row.last) put(many[i], j, id, takes ? list[next + rank] : -1);
+        next += all;
+      }
+    }
+    for (int i = tid; i < A.p.rows * wide; i += kThreads)   // of sequences that no row goes on from
+      if (first[i / wide] == kThreads)
+        if (const int id = A.p.table[i]; (unsigned)id < (unsigned)A.p.n_pages) atomicSub(&counts[id], 1);
+  }
+  __syncthreads();
+  int left = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int i = tid * 8 + k;
+    if (i >= A.p.n_pages) continue;
+    A.p.uses_out[i] = counts[i];
+    left += counts[i] <= 0;
+  }
+  left = block_sum(left, lds);
+  if (tid == 0) {
+    A.p.status[0] = left;
+    A.p.status[1] = max(asked - free, 0);
+  }
+}
+
 // ------------------------------------------------------------------- compact
 // A pool of one chunk is numbered by every workgroup that moves pages, in LDS, in the
 // one launch; a larger one by launches of their own (a launch is 3 us of the host's
@@ -528,6 +647,10 @@ int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float*
   A.page_shift = page_shift_of(page);
   A.asked = A.p.counts + counts_bytes(n_pages) / 4;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (A.p.n_chunks == 1 && n_new <= kFewRows && n_seq <= kFewRows && (int64_t)(n_new + n_seq) * max_pages <= kFewEntries) {
+    hipLaunchKernelGGL(fork_chunk_kernel, dim3(1 + n_new * A.p.slices), dim3(kThreads), 0, st, A);
+    return launched("fork_chunk_kernel");
+  }
   hipLaunchKernelGGL(fork_survey_kernel, dim3(A.p.n_chunks + n_new), dim3(kThreads), 0, st, A);
   hipLaunchKernelGGL(fork_kernel, dim3(n_new * A.p.slices + n_seq), dim3(kThreads), 0, st, A);
   return launched("fork_kernel");

@@ -108,11 +108,15 @@ FORKS = [
     ([0, 5], [0, 1, 0], 0, 6, 1, 64, 32, 0, 0),                          # an empty sequence; nothing needed
     ([256 * 3 + 1] * 5, [4, 3, 2, 1, 0, 0, 1], 300, 60, 1, 256, 256, 255, 2),
     ([31 * (i % 9) + 1 for i in range(90)], [i // 3 for i in range(200)], 12, 2500, 1, 64, 32, 6, 1),
+    ([70, 200, 40], [0, 0, 1, -1, 1], 900, 300, 1, 64, 32, 500, 2),      # many pages kept, many taken
+    ([20 * (i % 9) + 1 for i in range(90)], [i // 3 for i in range(250)], 7, 2048, 1, 64, 32, 6, 1),
 ]
 
 
+@pytest.mark.parametrize("spare", [0, 2500])      # one chunk of counts and several
 @pytest.mark.parametrize("lens,parents,more,n_pages,hkv,d,page,reserve,shared", FORKS)
-def test_fork(dev, lens, parents, more, n_pages, hkv, d, page, reserve, shared):
+def test_fork(dev, lens, parents, more, n_pages, hkv, d, page, reserve, shared, spare):
+    n_pages += spare
     p = Pool(dev, lens, n_pages, hkv, d, page, seed=len(parents) + d, reserve=reserve, shared=shared, wide=max(lens) // page + more // page + 4)
     need = [lens[q] + more if 0 <= q < len(lens) else more + 3 for q in parents]
     _, _, status, _ = p.fork(parents, need)
@@ -137,27 +141,31 @@ def test_fork_many_rows(dev):
     assert status[1] == 0 and len(copies) > 500
 
 
-def test_fork_lacking_pages_does_nothing(dev):
-    p = Pool(dev, [100, 40], 9, 2, 64, 32, seed=5, reserve=1)
+@pytest.mark.parametrize("spare", [0, 2500])
+def test_fork_lacking_pages_does_nothing(dev, spare):
+    p = Pool(dev, [100, 40], 9 + spare, 2, 64, 32, seed=5, reserve=1)
+    p.uses[np.nonzero(p.uses == 0)[0][3:]] = 2
     table, uses, status, copies = p.fork([0, 0, 1, 1], [130, 130, 60, 60])
     assert status[1] == 1 and status[0] == 3 and not copies and (table == -1).all() and np.array_equal(uses, p.uses)
     p.fork([0, 1, 1], [104, 60, 60])       # what is left suffices for this
 
 
-def test_fork_odd_numbers(dev):
+@pytest.mark.parametrize("spare", [0, 2500])
+def test_fork_odd_numbers(dev, spare):
     """Lengths, needs, ids and counts that no caller should have: taken as the header says."""
-    p = Pool(dev, [100, 64, 90, 20], 60, 1, 64, 32, seed=6, wide=5)
+    p = Pool(dev, [100, 64, 90, 20], 60 + spare, 1, 64, 32, seed=6, wide=5)
     p.kv_len[:] = [-5, 1 << 30, 90, 20]
-    p.table[1, 2:] = [-7, 60, 1 << 30]     # no page
+    p.table[1, 2:] = [-7, 60 + spare, 1 << 30]     # no page
     p.table[2, 2] = -1                     # the partial page is missing
     p.uses[p.table[3, 0]] = 3              # something else keeps it
     p.uses[p.uses == 0] = np.where(np.arange((p.uses == 0).sum()) % 3 == 0, -2, 0)
     p.fork([0, 1, 2, 2, 3, 3, 4, -(1 << 31), (1 << 31) - 1], [-9, 1 << 30, 95, 0, 21, 200, 33, -1, (1 << 31) - 1])
 
 
-def test_fork_keeps_no_page_that_is_shared(dev):
+@pytest.mark.parametrize("spare", [0, 2500])
+def test_fork_keeps_no_page_that_is_shared(dev, spare):
     """A page that a sequence has from another is copied before it is written, for its first row too."""
-    p = Pool(dev, [64, 64], 12, 1, 64, 32, seed=7, shared=2)
+    p = Pool(dev, [64, 64], 12 + spare, 1, 64, 32, seed=7, shared=2)
     p.kv_len[:] = [40, 64]                 # the first went back behind what the second has from it
     _, _, _, copies = p.fork([0, 1], [60, 70])
     assert [a for a, _ in copies] == [p.table[0, 1]]
@@ -175,15 +183,16 @@ def test_compact(dev, n_pages, hkv, d, page, lens):
     assert not p.compact()[3]
 
 
-def test_compact_all_or_none_in_use(dev):
-    p = Pool(dev, [100], 30, 1, 64, 32, seed=8, wide=30)
+@pytest.mark.parametrize("n", [30, 2048, 5000])
+def test_compact_all_or_none_in_use(dev, n):
+    p = Pool(dev, [100], n, 1, 64, 32, seed=8, wide=30)
     p.uses[:] = 1
     assert not p.compact()[3]
     p.uses[:] = 0
     assert not p.compact()[3]
-    p.uses[:15], p.uses[15:] = -1, 2
-    assert len(p.compact()[3]) == 15
-    p.table[0, :3] = [-9, 30, 1 << 30]     # no page: left as they are
+    p.uses[:n // 2], p.uses[n // 2:] = -1, 2
+    assert len(p.compact()[3]) == n // 2
+    p.table[0, :3] = [-9, n, 1 << 30]     # no page: left as they are
     p.compact()
 
 
@@ -225,8 +234,9 @@ def test_pages_refuse_overlaps(dev):
         R.draft_branch_fork(*p.cache, uses, table.long(), ints(p.kv_len, dev), two, two)
 
 
-def test_pages_on_another_stream_and_in_a_graph(dev):
-    p = Pool(dev, [100, 500, 64, 7], 90, 2, 128, 32, seed=11, reserve=5)
+@pytest.mark.parametrize("n_pages", [90, 4200])
+def test_pages_on_another_stream_and_in_a_graph(dev, n_pages):
+    p = Pool(dev, [100, 500, 64, 7], n_pages, 2, 128, 32, seed=11, reserve=5)
     parents, need = [0, 1, 1, 2, 3, 3], [110, 530, 520, 70, 40, 40]
     args = [ints(x, dev) for x in (p.uses, p.table, p.kv_len, parents, need)]
     want = O.fork(p.uses, p.table, p.kv_len, parents, need, 32)
@@ -236,7 +246,7 @@ def test_pages_on_another_stream_and_in_a_graph(dev):
     got = R.draft_branch_fork(*p.cache, *args, stream=side)
     side.synchronize()
     assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
-    ws = R.draft_branch_pages_workspace(90, 6, dev)
+    ws = R.draft_branch_pages_workspace(n_pages, 6, dev)
     outs = [torch.empty_like(t) for t in got]
     more = [torch.empty_like(args[1]), torch.empty_like(args[0]), torch.empty_like(outs[2])]
     graph = torch.cuda.CUDAGraph()
