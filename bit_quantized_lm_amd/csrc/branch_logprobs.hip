@@ -89,7 +89,8 @@ struct RowOf {
   static __device__ __forceinline__ void expand(u32x4 w, float (&e)[kPer]);
   static __device__ __forceinline__ u32x4 packed(const float (&e)[kPer]);   // expand's input again
   __device__ __forceinline__ float at(int i) const { return number(x[i]); }
-  __device__ __forceinline__ u32x4 raw(int v) const { return reinterpret_cast<const u32x4*>(x + head)[v]; }
+  __device__ __forceinline__ const u32x4* at_vector(int v) const { return reinterpret_cast<const u32x4*>(x + head) + v; }
+  __device__ __forceinline__ u32x4 raw(int v) const { return *at_vector(v); }
   __device__ __forceinline__ int index(int v, int k) const { return head + v * kPer + k; }
   // the elements beside the vectors: edge i of head + tail
   __device__ __forceinline__ int edge(int i) const { return i < head ? i : n - tail + i - head; }
@@ -293,7 +294,9 @@ __device__ __forceinline__ Sum sum_of_all(Sum t, float c, Sum (&of_wave)[kWaves]
   return t;
 }
 
-template <class T>
+// kOnce: rows of many steps, whose loads go past the caches (2,048 rows of 124,160: 102 us
+// so, 107 through them); a row's parts are looked at again.
+template <class T, bool kOnce>
 __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
   __shared__ Shared lds;
   constexpr int kPer = RowOf<T>::kPer, kStep = kAtOnce * kThreads;
@@ -305,15 +308,16 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
   const int edges = part == 0 ? row.head + row.tail : 0;   // a lane's each
   if (tid == 0) lds.n_list = lds.n_kept = 0;
   u32x4 next[kAtOnce];
+  auto load = [&](int v) { return kOnce ? __builtin_nontemporal_load(row.at_vector(v)) : *row.at_vector(v); };
   auto fetch = [&](int base) {
     if (base + kStep <= v1) {
 #pragma unroll
-      for (int u = 0; u < kAtOnce; ++u) next[u] = row.raw(base + tid + u * kThreads);
+      for (int u = 0; u < kAtOnce; ++u) next[u] = load(base + tid + u * kThreads);
     } else {
 #pragma unroll
       for (int u = 0; u < kAtOnce; ++u) {
         next[u] = RowOf<T>::nothing();
-        if (base + tid + u * kThreads < v1) next[u] = row.raw(base + tid + u * kThreads);
+        if (base + tid + u * kThreads < v1) next[u] = load(base + tid + u * kThreads);
       }
     }
   };
@@ -517,8 +521,12 @@ int check_logits(const char* who, int M, int N, int top) {
 
 template <class T>
 void launch(const LogprobArgs& A, hipStream_t s) {
-  hipLaunchKernelGGL(logprobs_kernel<T>, dim3((unsigned)A.M * A.parts), dim3(kThreads), 0, s, A);
-  if (A.parts > 1) hipLaunchKernelGGL(logprobs_join_kernel<T>, dim3(A.M), dim3(kThreads), 0, s, A);
+  if (A.parts == 1) {
+    hipLaunchKernelGGL((logprobs_kernel<T, true>), dim3((unsigned)A.M), dim3(kThreads), 0, s, A);
+  } else {
+    hipLaunchKernelGGL((logprobs_kernel<T, false>), dim3((unsigned)A.M * A.parts), dim3(kThreads), 0, s, A);
+    hipLaunchKernelGGL(logprobs_join_kernel<T>, dim3(A.M), dim3(kThreads), 0, s, A);
+  }
 }
 
 }  // namespace

@@ -194,7 +194,10 @@ __device__ __forceinline__ void free_pages(const PoolArgs& A, const Counted& hea
   }
 }
 
-// Part `slice` of page `from` over page `to`; scales with the first.
+// Part `slice` of page `from` over page `to`; scales with the first.  kOnce: past the
+// caches, for pages that nobody reads soon (3,400 pages, 505 MB in and out: 104.4 us so,
+// 113.1 through them, 108.2 with the stores alone past them).
+template <bool kOnce>
 __device__ __forceinline__ void copy_page(const PoolArgs& A, int from, int to, int slice) {
   const int64_t units = A.page_bytes / 16, all = 2 * units;   // keys, then values
   const int64_t a = all * slice / A.slices, b = all * (slice + 1) / A.slices;
@@ -205,10 +208,15 @@ __device__ __forceinline__ void copy_page(const PoolArgs& A, int from, int to, i
     u32x4 x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (u0 + i * kThreads < b) x[i] = *at(from, u0 + i * kThreads);
+      if (u0 + i * kThreads < b) x[i] = kOnce ? __builtin_nontemporal_load(at(from, u0 + i * kThreads)) : *at(from, u0 + i * kThreads);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (u0 + i * kThreads < b) *at(to, u0 + i * kThreads) = x[i];
+      if (u0 + i * kThreads < b) {
+        if (kOnce)
+          __builtin_nontemporal_store(x[i], at(to, u0 + i * kThreads));
+        else
+          *at(to, u0 + i * kThreads) = x[i];
+      }
   }
   if (slice == 0)
     for (int h = threadIdx.x; h < A.hkv; h += kThreads) {
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
   }
   if (!old_row && partial >= 0 && done) {
     free_pages(A.p, head, before, 1, f);
-    if ((unsigned)f.list[0] < (unsigned)A.p.n_pages) copy_page(A.p, partial, f.list[0], slice);
+    if ((unsigned)f.list[0] < (unsigned)A.p.n_pages) copy_page<false>(A.p, partial, f.list[0], slice);
   }
   freed = wave_inclusive_sum(freed);
   if ((tid & 63) == 63 && freed > 0) atomicAdd(A.p.status, freed);
@@ -371,7 +379,7 @@ __global__ __launch_bounds__(kThreads) void fork_chunk_kernel(ForkArgs A) {
     const Row row = row_of(A, s, (unsigned)parent < (unsigned)A.p.rows && first[parent] == s);
     if (!done || !(row.len & ((1 << A.page_shift) - 1))) return;
     const int from = named(A, row, row.full);
-    if (from >= 0 && !kept(row.eldest, from)) copy_page(A.p, from, list[takes_from[s]], (blockIdx.x - 1) % A.p.slices);
+    if (from >= 0 && !kept(row.eldest, from)) copy_page<false>(A.p, from, list[takes_from[s]], (blockIdx.x - 1) % A.p.slices);
     return;
   }
   const int wide = A.p.wide;
@@ -499,7 +507,7 @@ __global__ __launch_bounds__(kThreads) void compact_move_kernel(CompactArgs A, i
     for (int64_t i = blockIdx.x; i < parts; i += movers) {
       const int m = (int)(i / A.p.slices), slice = (int)(i % A.p.slices), from = A.src[m], to = A.dst[m];
       if ((unsigned)from >= (unsigned)A.p.n_pages || (unsigned)to >= (unsigned)A.p.n_pages) continue;
-      copy_page(A.p, from, to, slice);
+      copy_page<true>(A.p, from, to, slice);
       if (slice == 0 && tid == 0) {
         A.p.uses_out[to] = A.p.uses[from];
         A.p.uses_out[from] = 0;
@@ -545,7 +553,7 @@ __global__ __launch_bounds__(kThreads) void compact_chunk_kernel(CompactArgs A, 
   __syncthreads();
   const int moves = used - front;
   if ((int)blockIdx.x < movers) {
-    for (int i = blockIdx.x; i < moves * A.p.slices; i += movers) copy_page(A.p, src[i / A.p.slices], dst[i / A.p.slices], i % A.p.slices);
+    for (int i = blockIdx.x; i < moves * A.p.slices; i += movers) copy_page<true>(A.p, src[i / A.p.slices], dst[i / A.p.slices], i % A.p.slices);
     return;
   }
   if ((int)blockIdx.x == movers) {
@@ -669,8 +677,11 @@ int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, flo
   A.dst = A.src + moves_bytes(n_pages) / 4;
   A.number = A.dst + moves_bytes(n_pages) / 4;
   const hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  // eight workgroups a CU, or a move at most for every second page
-  const int movers = (int)std::min<int64_t>(2048, std::max<int64_t>((int64_t)(n_pages / 2) * A.p.slices, 1));
+  // eight rounds of a card's workgroups, so that those that get on faster take more (3,400
+  // pages: 2,048 workgroups 104.5 us, 4,096 100.9, 8,192 96.7, 16,384 93.4, 32,768 95.5); one round where each numbers
+  // the moves for itself; a move at most for every second page
+  const int64_t parts = std::max<int64_t>((int64_t)(n_pages / 2) * A.p.slices, 1);
+  const int movers = (int)std::min<int64_t>(A.p.n_chunks == 1 ? 2048 : 16384, parts);
   const int entries = (int)std::min<int64_t>(256, ((int64_t)n_rows * max_pages + kThreads - 1) / kThreads);
   if (A.p.n_chunks == 1) {
     hipLaunchKernelGGL(compact_chunk_kernel, dim3(movers + entries), dim3(kThreads), 0, st, A, movers);
