@@ -244,13 +244,8 @@ __device__ __forceinline__ void divide(const BranchArgs& A, const Sums& sum, Pla
 // 16 prompts of 112 rows over 6,000 tokens took 284 us with even runs, 274 so (0.2:
 // 282, 0.25: 287); on short ones it costs (16 slots of 9: 59.0 us, 61.5 with 0.08).
 constexpr float kFirst = 0.15f;
-// First unit of run r, and the run that has unit `at`.
+// First unit of run r.
 __device__ __forceinline__ int start_of(int r, int per, int more, int half) { return r * per + more * min(r, 2 * half - r); }
-__device__ __forceinline__ int run_at(int at, int per, int more, int half) {
-  const int before = half * (per + more);
-  return at < before ? at / (per + more) : half + (at - before) / (per - more);
-}
-
 // A part of fewer than four groups costs more to begin and to join than it saves.
 template <int D>
 __device__ __forceinline__ void cut(const BranchArgs& A, int shared_units, int stream_units, Plan& p) {
@@ -650,28 +645,42 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
     const float2* ml;
     int step, n;
   };
-  auto parts_of = [&](const Record& rec, const Parts (&all)[2], int h) {
+  // The run that has a unit: fewer than 2^12 runs, so the quotient from a reciprocal is at most one off.
+  const int units[3] = {plan.per[kStream], plan.per[kShared] + plan.more, plan.per[kShared] - plan.more}, before = plan.half * units[1];
+  const float inverse[3] = {1.0f / (float)units[0], 1.0f / (float)units[1], 1.0f / (float)units[2]};
+  auto run_at = [&](Line line, int unit) {
+    const bool stream = line == kStream, rest = !stream && unit >= before;
+    const int d = stream ? units[0] : rest ? units[2] : units[1], x = rest ? unit - before : unit;
+    int q = (int)((float)x * (stream ? inverse[0] : rest ? inverse[2] : inverse[1]));
+    const int r = x - q * d;
+    q += (r >= d) - (r < 0);
+    return rest ? plan.half + q : q;
+  };
+  auto parts_of = [&](const Record& rec, const Parts (&all)[2], int head, int in_group) {
     constexpr Line any = Cost<D>::kStreams ? kStream : kShared;   // of which there are places
     Run p{all[any].o, all[any].ml, 0, 0};
-    const int x = r * A.group + h % A.group, y = x - rec.item.row0 * A.group, rows = rec.item.n * A.group;
+    const int x = r * A.group + in_group, y = x - rec.item.row0 * A.group, rows = rec.item.n * A.group;
     if (y < 0 || y >= rows || rec.item.groups == 0) return p;   // nothing to see, or groups and sequences that do not fit each other
     const Shape<D> shape(rows, rec.item.groups, plan.shift, plan.whole);
     const int tile = min(y / H, shape.full);
     const Line line = tile == shape.full && shape.streams() ? kStream : kShared;
     const int at = line == kStream ? rec.at[kStream] : rec.at[kShared] + tile * shape.each;
-    const int more = line == kStream ? 0 : plan.more, first = run_at(at + shape.pad(line, tile), plan.per[line], more, plan.half);
+    const int first = run_at(line, at + shape.pad(line, tile));
     p.step = line == kStream ? kStreamRows : H;
-    p.n = run_at(at + shape.length(tile) - 1, plan.per[line], more, plan.half) - first + 1;
-    const size_t place = (size_t)(h / A.group) * A.places[line] + x + (size_t)first * p.step;
+    p.n = run_at(line, at + shape.length(tile) - 1) - first + 1;
+    const size_t place = (size_t)head * A.places[line] + x + (size_t)first * p.step;
     p.o = all[line].o + place * D;
     p.ml = all[line].ml + place;
     return p;
   };
   const bool alone = own_record.item.split == 0 || own_record.item.sees == 3;
+  int head = (h0 + lane / L) / A.group, in_group = (h0 + lane / L) % A.group;
   for (int pass = h0; pass < min(A.hq, h0 + heads); pass += P) {
-    const int h = pass + lane / L;
-    Run own = parts_of(own_record, A.own, min(h, A.hq - 1)), prefix = parts_of(prefix_record, A.prefix, min(h, A.hq - 1));
-    if (own_record.item.of < 0) prefix.n = 0;
+    const int h = pass + lane / L;   // past the last head: the last one's places
+    const Run own = parts_of(own_record, A.own, min(head, A.c.hkv - 1), in_group);
+    Run prefix{own.o, own.ml, 0, 0};
+    if (own_record.item.of >= 0 && !alone) prefix = parts_of(prefix_record, A.prefix, min(head, A.c.hkv - 1), in_group);
+    for (in_group += P; in_group >= A.group; ++head) in_group -= A.group;
     const bool done = h >= min(A.hq, h0 + heads) || (alone && own.n == 1);   // or the result already
     const int n = done ? 0 : prefix.n + own.n, most = (int)wave_max((uint32_t)n);
     if (W == 1 && __all(done)) continue;
@@ -681,7 +690,7 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
       // lane i of a row: part base + i W
       const int part = base + l * W;
       float2 ml = {kLowest, 0.0f};
-      if (part < n) ml = part < prefix.n ? prefix.ml[(size_t)part * prefix.step] : own.ml[(size_t)(part - prefix.n) * own.step];
+      if (part < n) ml = part < prefix.n ? prefix.ml[part * prefix.step] : own.ml[(part - prefix.n) * own.step];
       float next = ml.x;
 #pragma unroll
       for (int i = 1; i < L; i *= 2) next = fmaxf(next, __shfl_xor(next, i));
@@ -700,7 +709,8 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
 #pragma unroll
         for (int j = 0; j < K; ++j) {
           const int at = max(min(base + (j0 + j) * W, n - 1), 0);
-          v[j] = *reinterpret_cast<const f32x4*>((at < prefix.n ? prefix.o + (size_t)at * prefix.step * D : own.o + (size_t)(at - prefix.n) * own.step * D) + l * 4);
+          const bool of_prefix = at < prefix.n;   // a run's distance is below 2^28 floats
+          v[j] = *reinterpret_cast<const f32x4*>((of_prefix ? prefix.o : own.o) + (of_prefix ? at : at - prefix.n) * (of_prefix ? prefix.step : own.step) * D + l * 4);
         }
 #pragma unroll
         for (int j = 0; j < K; ++j) {
@@ -710,7 +720,10 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
       };
       int j = 0;
       for (; j + 4 < count; j += 8) add(std::integral_constant<int, 8>{}, j);
-      if (j < count) add(std::integral_constant<int, 4>{}, j);
+      if (j + 2 < count)
+        add(std::integral_constant<int, 4>{}, j);
+      else if (j < count)
+        add(std::integral_constant<int, 2>{}, j);
     }
     if constexpr (W > 1) {   // one pass
       sums[wave][lane] = y;
