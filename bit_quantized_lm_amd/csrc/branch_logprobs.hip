@@ -28,8 +28,6 @@ constexpr int kAtOnce = 2;                  // vectors of a lane a step; the nex
 constexpr int kFirstSteps = 4, kMoreSteps = 16;   // before the first bound, and before a closer one
 constexpr float kLog2e = 1.44269504088896f, kLn2 = 0.693147180559945f;
 constexpr float kLowest = -3.4028234663852886e38f;   // m of nothing: finite, so no inf - inf arises
-constexpr float kAhead = 4.0f;              // exponents that a reference may lie below the maximum
-constexpr float kFar = 1e37f;               // a reference from here on: no difference to a product is taken
 constexpr float kLeast = -200.0f;           // exponents below give a weight of 0 anyway; keeps 0 * inf out of s
 
 struct LogprobArgs {
@@ -187,35 +185,23 @@ struct Shared {
   int n_list, n_kept;
 };
 
-// A lane's sums while it passes over the row: weights are 2^(x c - ref), the product
-// not rounded, and the reference moves only where the maximum passes it by kAhead, so
-// that most steps have an exponential an element and none beside.  Where x c is
-// past what fp32 holds, weights are 2^((x - at) c), from the reference's element.
+// A lane's sums while it passes over the row, under the largest element so far: its
+// weight is 1 exactly, which a peaked row's small results need.
 struct Running {
-  float most = -INFINITY, ref = -3e38f, at = 0.0f, l = 0.0f, s = 0.0f;
-  __device__ __forceinline__ bool far() const { return !(fabsf(ref) < kFar); }
-  __device__ __forceinline__ float exponent(float x, float c) const { return far() ? (x - at) * c : fmaf(x, c, -ref); }
+  float most = -INFINITY, at = kLowest, l = 0.0f, s = 0.0f;   // at: most, finite
   __device__ __forceinline__ void see(float x, float c) {   // the largest element of a step
     if (!(x > most)) return;
-    most = x;
-    if (!far() && fmaf(x, c, -ref) <= kAhead) return;
-    const float next = x * c, down = far() || !(fabsf(next) < kFar) ? (at - x) * c : ref - next;
-    const float d = fminf(fmaxf(down, kLeast), 0.0f), w = __builtin_amdgcn_exp2f(d);
+    const float d = fmaxf((at - x) * c, kLeast), w = __builtin_amdgcn_exp2f(d);
     s = (s + l * d) * w;
     l *= w;
-    ref = next;
-    at = x;
+    most = at = x;
   }
   __device__ __forceinline__ void add(float x, float c) {
-    const float d = exponent(x, c), w = __builtin_amdgcn_exp2f(d);
+    const float d = (x - at) * c, w = __builtin_amdgcn_exp2f(d);
     l += w;
     s = fmaf(w, fmaxf(d, kLeast), s);
   }
-  // under the maximum
-  __device__ __forceinline__ Sum sum(float c) const {
-    const float d = -exponent(most, c), w = __builtin_amdgcn_exp2f(d);
-    return l == 0.0f ? Sum{kLowest, 0.0f, 0.0f} : Sum{most, l * w, (s + l * d) * w};
-  }
+  __device__ __forceinline__ Sum sum() const { return {at, l, s}; }
 };
 
 __device__ __forceinline__ float factor_of(const LogprobArgs& A, int m) { return A.scales ? A.scale * A.scales[m] : A.scale; }
@@ -396,7 +382,7 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
         float l = 0.0f, s = 0.0f;   // the vector's own first: eight times fewer roundings at the size of the whole sum
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-          const float d = fmaf(e[u][k], c, -t.ref), w = __builtin_amdgcn_exp2f(d);
+          const float d = (e[u][k] - t.at) * c, w = __builtin_amdgcn_exp2f(d);
           l += w;
           s = fmaf(w, decltype(clean)::value ? d : fmaxf(d, kLeast), s);
         }
@@ -404,19 +390,10 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
         t.s += s;
       }
     };
-    if (__all(!t.far() && fmaf(low, c, -t.ref) > -kFar)) {
+    if (__all((low - t.at) * c > kLowest))
       add(std::true_type{});
-    } else if (!__any(t.far() && t.most > -INFINITY)) {
+    else
       add(std::false_type{});
-    } else {
-#pragma unroll 1
-      for (int i = 0; i < kAtOnce * kPer; ++i) {
-        float x = e[0][0];
-#pragma unroll
-        for (int k = 1; k < kAtOnce * kPer; ++k) x = i == k ? e[k / kPer][k % kPer] : x;
-        t.add(x, c);
-      }
-    }
   }
   if (A.top > 0) {
     raise(step <= kFirstSteps, v1);   // after more steps, what reaches this bound has reached the first and is put down
@@ -446,7 +423,7 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
     else
       pick_one_by_one(row, v0, v1, edges, A.top, lds);
   }
-  const Sum all = sum_of_all(t.sum(c), c, lds.sums);
+  const Sum all = sum_of_all(t.sum(), c, lds.sums);
   if (A.parts == 1) {
     finish(A, m, row, all, f, lds.out);
     return;

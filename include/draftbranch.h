@@ -167,9 +167,8 @@ int draft_branch_logprobs_workspace_bytes(int M, int N, int top, size_t* bytes);
  * The shards of one vocabulary join by their lse: with L = ln sum_r exp(lse_r),
  * log probabilities fall by L - lse_r, and the entropy is
  * L - sum_r exp(lse_r - L) (lse_r - entropy_r).
- * Sums are fp32 under the running maximum, or up to 2^4 below it; x is taken as it
- * is and an exponent rounded once (two roundings where f x is past 1e37), so rows
- * at the type's lowest value are rows too.
+ * Sums are fp32 under the running maximum; x is taken as it is, differences to
+ * the maximum are rounded once, so rows at the type's lowest value are rows too.
  *   logits    device, bf16 (type DB_BF16) or fp32 (DB_FP32), row m at logits +
  *             m*ld elements, ld >= N; aligned to its element alone
  *   scales    device, fp32 [M], or NULL
