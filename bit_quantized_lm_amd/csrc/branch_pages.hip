@@ -79,8 +79,14 @@ struct Eight {
 __device__ __forceinline__ Eight load_uses(const PoolArgs& A, int chunk, int none) {
   Eight e;
   const int first = chunk * kChunk + threadIdx.x * 8;
+  if ((reinterpret_cast<uintptr_t>(A.uses) & 15) == 0 && first + 8 <= A.n_pages) {
+    const int4* at = reinterpret_cast<const int4*>(A.uses + first);
+    const int4 a = at[0], b = at[1];
+    e = Eight{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+  } else {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e.u[i] = first + i < A.n_pages ? A.uses[first + i] : none;
+    for (int i = 0; i < 8; ++i) e.u[i] = first + i < A.n_pages ? A.uses[first + i] : none;
+  }
   return e;
 }
 
@@ -283,7 +289,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
     atomicAdd(A.p.status, done ? free - asked : free);
     A.p.status[1] = max(asked - free, 0);
   }
-  int freed = 0;
+  int freed = 0, to = -1;   // to: where the partial page goes, the first that the row takes
   auto give_up = [&](int id) { freed += atomicSub(A.p.uses_out + id, 1) == 1; };
   if (old_row) {
     if (done)
@@ -301,6 +307,7 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
           free_pages(A.p, head, rank, n, f);
           // an id is looked at before it is written through: counts that change meanwhile fault nothing
           if (takes) entry = (unsigned)f.list[at] < (unsigned)A.p.n_pages ? f.list[at] : -1;
+          if (rank == before) to = f.list[0];
           __syncthreads();
         }
         rank += n;
@@ -314,8 +321,11 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
     }
   }
   if (!old_row && partial >= 0 && done) {
-    free_pages(A.p, head, before, 1, f);
-    if ((unsigned)f.list[0] < (unsigned)A.p.n_pages) copy_page<false>(A.p, partial, f.list[0], slice);
+    if (slice > 0) {
+      free_pages(A.p, head, before, 1, f);
+      to = f.list[0];
+    }
+    if ((unsigned)to < (unsigned)A.p.n_pages) copy_page<false>(A.p, partial, to, slice);
   }
   freed = wave_inclusive_sum(freed);
   if ((tid & 63) == 63 && freed > 0) atomicAdd(A.p.status, freed);

@@ -218,6 +218,21 @@ def test_pages_of_a_large_pool(dev):
     assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want)) and len(want[3]) > 500
 
 
+@pytest.mark.parametrize("n_pages", [60, 2500])
+def test_pages_with_counts_at_any_alignment(dev, n_pages):
+    p = Pool(dev, [100, 64, 300], n_pages, 1, 64, 32, seed=13, reserve=3)
+    parents, need = [0, 0, 2, 1, 2], [110, 120, 310, 70, 340]
+    want, packed = O.fork(p.uses, p.table, p.kv_len, parents, need, 32), O.compact(p.uses, p.table)
+    for off in range(1, 4):
+        uses = torch.zeros(n_pages + off, dtype=torch.int32, device=dev)[off:]
+        uses.copy_(ints(p.uses, dev))
+        cache = [t.clone() for t in p.cache]
+        got = R.draft_branch_fork(*cache, uses, ints(p.table, dev), ints(p.kv_len, dev), ints(parents, dev), ints(need, dev))
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, want))
+        got = R.draft_branch_compact(*cache, uses, ints(p.table, dev))
+        assert all(np.array_equal(a.cpu().numpy(), b) for a, b in zip(got, packed))
+
+
 def test_pages_refuse_overlaps(dev):
     p = Pool(dev, [40, 70], 20, 1, 64, 32, seed=10)
     uses, table = ints(p.uses, dev), ints(p.table, dev)
