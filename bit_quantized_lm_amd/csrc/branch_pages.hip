@@ -334,8 +334,8 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
 // All of it, of one chunk and few rows: every workgroup counts and gives out for
 // itself, in LDS; the first makes the table and the counts, the others copy pages.  A
 // launch less is 3 us of the host's time: 32 rows of 8 sequences over 1,500 tokens, 880
-// entries in both tables, take 12.7 us in a loop of calls, 16.0 in two launches.  On the
-// card 8.5 and 12.1; 1,760 entries 11.2 and 14.2, 3,600 19.1 and 21.3, 4,480 13.9 and 11.9,
+// entries in both tables, take 12.5 us in a loop of calls, 16.0 in two launches.  On the
+// card 6.4 and 12.1 (8.5 with the workgroups that have nothing to copy); 1,760 entries 11.2 and 14.2, 3,600 19.1 and 21.3, 4,480 13.9 and 11.9,
 // 8,448 26.9 and 21.5.
 constexpr int kFewRows = kThreads, kFewEntries = 4096;
 constexpr int kFewTaken = 8;   // entries that a first row's own thread goes through; of more all threads do
@@ -344,6 +344,10 @@ __global__ __launch_bounds__(kThreads) void fork_chunk_kernel(ForkArgs A) {
   __shared__ int uses[kChunk], counts[kChunk], first[kThreads], takes_from[kThreads], many[kThreads], n_many, lds[kThreads / 64];
   __shared__ int16_t list[kChunk];   // the free pages
   const int tid = threadIdx.x;
+  if (blockIdx.x > 0) {   // nothing to copy: the parent's tokens end with a page
+    const int parent = A.parents[(blockIdx.x - 1) / A.p.slices];
+    if ((unsigned)parent >= (unsigned)A.p.rows || (A.kv_len[parent] & ((1 << A.page_shift) - 1)) == 0) return;
+  }
   const Eight e = load_uses(A.p, 0, 1);
   const int p = tid < A.n_new ? A.parents[tid] : -1;
   const bool has = (unsigned)p < (unsigned)A.p.rows;
