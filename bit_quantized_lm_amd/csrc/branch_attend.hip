@@ -12,7 +12,7 @@
 //
 // 40 heads on 8 of 128: 64 samples of a prompt of 8,192 tokens 40.5 us, 16 sequences of
 // 9 slots over four prefixes of up to 20,000 51.8, 16 prompts of 112 rows over 6,000
-// tokens 273 (812 TFLOP/s).  Of the first two's 34 and 47 us on the card before the
+// tokens 263 (843 TFLOP/s).  Of the first two's 34 and 47 us on the card before the
 // joining (8), the tiles take 16 and 36; the rest begins (plan 2.6, segment 1, queries
 // and first codes 4) and leaves (2).
 #include <algorithm>
@@ -613,13 +613,14 @@ __global__ __launch_bounds__(kThreads, 2) void branch_parts_kernel(BranchArgs A)
 }
 
 // ---------------------------------------------------------------- the joining
-// D / 4 lanes a row of one query head.  With few rows W waves take turns at a row's
-// parts; with many (W = 1) a wave has `heads` query heads of a token row, because
-// finding the parts takes longer than joining them.
+// D / 8 lanes a row of one query head, so that a pass takes four heads of 128 (16 prompts
+// 263 us; with D / 4 lanes and half as many rows a pass 269, the other sizes the same).
+// With few rows W waves take turns at a row's parts; with many (W = 1) a wave has `heads`
+// query heads of a token row, because finding the parts takes longer than joining them.
 template <int D, int W>
 __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int heads) {
-  constexpr int L = D / 4, P = 64 / L, H = Cost<D>::kRows;   // lanes a row, rows a pass
-  __shared__ f32x4 sums[W][64];
+  constexpr int L = D / 8, P = 64 / L, H = Cost<D>::kRows;   // lanes a row, rows a pass
+  __shared__ f32x4 sums[W][2][64];
   __shared__ float2 refs[W][P];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, l = lane % L;
   const int turn = wave % W, chunks = (A.hq + heads - 1) / heads;
@@ -693,7 +694,7 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
     const int n = done ? 0 : prefix.n + own.n, most = (int)wave_max((uint32_t)n);
     if (W == 1 && __all(done)) continue;
     float top = kLowest, sum = 0.0f;
-    f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 y[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};   // four elements of each half
     for (int base = turn; base < most; base += L * W) {
       // lane i of a row: part base + i W
       const int part = base + l * W;
@@ -709,32 +710,38 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
       for (int i = 1; i < L; i *= 2) weight += __shfl_xor(weight, i);
       sum = fmaf(sum, down, weight);
       top = next;
-      y *= down;
+      y[0] *= down;
+      y[1] *= down;
       const int count = min(L, (most - base + W - 1) / W);
       auto add = [&](auto at_once, int j0) {   // past a row's last part, that once more with no share
         constexpr int K = decltype(at_once)::value;
-        f32x4 v[K];
+        f32x4 v[K][2];
 #pragma unroll
         for (int j = 0; j < K; ++j) {
           const int at = max(min(base + (j0 + j) * W, n - 1), 0);
           const bool of_prefix = at < prefix.n;   // a run's distance is below 2^28 floats
-          v[j] = *reinterpret_cast<const f32x4*>((of_prefix ? prefix.o : own.o) + (of_prefix ? at : at - prefix.n) * (of_prefix ? prefix.step : own.step) * D + l * 4);
+          const float* o = (of_prefix ? prefix.o : own.o) + (of_prefix ? at : at - prefix.n) * (of_prefix ? prefix.step : own.step) * D + l * 4;
+          v[j][0] = *reinterpret_cast<const f32x4*>(o);
+          v[j][1] = *reinterpret_cast<const f32x4*>(o + D / 2);
         }
 #pragma unroll
         for (int j = 0; j < K; ++j) {
           const float by = __shfl(share, lane - l + min(j0 + j, L - 1));
-          y += (j0 + j < L ? by : 0.0f) * v[j];
+          const float w = j0 + j < L ? by : 0.0f;
+          y[0] += w * v[j][0];
+          y[1] += w * v[j][1];
         }
       };
       int j = 0;
-      for (; j + 4 < count; j += 8) add(std::integral_constant<int, 8>{}, j);
+      for (; j + 4 < count; j += 4) add(std::integral_constant<int, 4>{}, j);
       if (j + 2 < count)
         add(std::integral_constant<int, 4>{}, j);
       else if (j < count)
         add(std::integral_constant<int, 2>{}, j);
     }
     if constexpr (W > 1) {   // one pass
-      sums[wave][lane] = y;
+      sums[wave][0][lane] = y[0];
+      sums[wave][1][lane] = y[1];
       if (l == 0) refs[wave][lane / L] = float2{top, sum};
       __syncthreads();
       if (turn > 0) return;
@@ -742,16 +749,19 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
       for (int v = 1; v < W; ++v) {
         const float2 other = refs[v][lane / L];
         const float next = fmaxf(top, other.x), down = __builtin_amdgcn_exp2f(top - next), share = __builtin_amdgcn_exp2f(other.x - next);
-        y = down * y + share * sums[v][lane];
+        y[0] = down * y[0] + share * sums[v][0][lane];
+        y[1] = down * y[1] + share * sums[v][1][lane];
         sum = fmaf(sum, down, share * other.y);
         top = next;
       }
     }
     if (done) continue;
-    if (n == 0) y = f32x4{0.0f, 0.0f, 0.0f, 0.0f};   // what was loaded for it is another row's
+    if (n == 0) y[0] = y[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};   // what was loaded for it is another row's
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const size_t row = (size_t)r * A.hq + h;
-    *reinterpret_cast<u32x2*>(A.out + row * D + l * 4) = u32x2{bf16_pair(y[0] * inv, y[1] * inv), bf16_pair(y[2] * inv, y[3] * inv)};
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<u32x2*>(A.out + row * D + i * (D / 2) + l * 4) = u32x2{bf16_pair(y[i][0] * inv, y[i][1] * inv), bf16_pair(y[i][2] * inv, y[i][3] * inv)};
     if (l == 0) write_lse(A.lse, row, top, sum);
   }
 }
@@ -883,7 +893,7 @@ int launch(const BranchArgs& A, hipStream_t s) {
   }
   const int rc = A.b.n_seq <= kSmall && A.n_groups <= kSmall ? launch_parts<D, true>(A, s) : launch_parts<D, false>(A, s);
   if (rc) return rc;
-  constexpr int P = 256 / D;   // rows a pass
+  constexpr int P = 512 / D;   // rows a pass
   const int64_t rows = (int64_t)A.b.T * A.hq;
   if (rows <= 1024 * P) {
     const int64_t units = A.b.T * (int64_t)((A.hq + P - 1) / P);

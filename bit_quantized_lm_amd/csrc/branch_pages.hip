@@ -335,8 +335,8 @@ __global__ __launch_bounds__(kThreads) void fork_kernel(ForkArgs A) {
 // itself, in LDS; the first makes the table and the counts, the others copy pages.  A
 // launch less is 3 us of the host's time: 32 rows of 8 sequences over 1,500 tokens, 880
 // entries in both tables, take 12.5 us in a loop of calls, 16.0 in two launches.  On the
-// card 6.4 and 12.1 (8.5 with the workgroups that have nothing to copy); 1,760 entries 11.2 and 14.2, 3,600 19.1 and 21.3, 4,480 13.9 and 11.9,
-// 8,448 26.9 and 21.5.
+// card 6.4 and 12.1 (8.5 where the workgroups without a page to copy count too); 1,760
+// entries 11.2 and 14.2, 3,600 19.1 and 21.3, 4,480 13.9 and 11.9, 8,448 26.9 and 21.5.
 constexpr int kFewRows = kThreads, kFewEntries = 4096;
 constexpr int kFewTaken = 8;   // entries that a first row's own thread goes through; of more all threads do
 
