@@ -125,6 +125,7 @@ def draft_branch_fork(k_codes, v_codes, k_scale, v_scale, uses, table, kv_len, p
     [rows][max_pages], uses_out, status int32 [2]: free pages after the call,
     pages that were lacking, with nothing done where that is not 0)."""
     lib = _device_lib()
+    L._need(len(parents.shape) == 1, "parents must be [rows]")
     made = parents.shape[0]
     dev, pool, uses_out, table_out, status = _pages(k_codes, v_codes, k_scale, v_scale, uses, table, made, uses_out, table_out, status, stream)
     n_seq, wide = table.shape

@@ -600,9 +600,13 @@ size_t moves_bytes(int n_pages) { return rounded(((size_t)n_pages / 2 + 1) * 4);
 size_t fork_bytes(int n_pages, int n_new) { return counts_bytes(n_pages) + (size_t)n_new * 4; }
 size_t compact_bytes(int n_pages) { return counts_bytes(n_pages) + 2 * moves_bytes(n_pages) + (size_t)n_pages * 4; }
 
-bool overlap(const void* a, size_t n, const void* b, size_t m) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + m && y < x + n;
+struct Span {
+  const void* p;
+  size_t n;
+};
+bool overlap(const Span& a, const Span& b) {   // none with nothing
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
 }
 
 int check_pool(const char* who, int n_pages, int rows, const char* rows_name) {
@@ -612,8 +616,9 @@ int check_pool(const char* who, int n_pages, int rows, const char* rows_name) {
   return DH_OK;
 }
 
-// What fork and compact have in common; `made` is the new table's rows.
-int check_pages(const char* who, PoolArgs& A, int page, int D, int made, const char* rows_name, void* workspace, size_t given, size_t need) {
+// What fork and compact have in common; `made` is the new table's rows, `lists` what else is read.
+int check_pages(const char* who, PoolArgs& A, int page, int D, int made, const char* rows_name, const Span (&lists)[3], void* workspace,
+                size_t given, size_t need) {
   int rc = check_heads(who, A.hkv, A.hkv, D);
   if (rc) return rc;
   if ((rc = check_pool(who, A.n_pages, A.rows, rows_name))) return rc;
@@ -624,10 +629,13 @@ int check_pages(const char* who, PoolArgs& A, int page, int D, int made, const c
   if (!aligned(A.uses, 4) || !aligned(A.uses_out, 4) || !aligned(A.table_out, 4) || !aligned(A.status, 4))
     return dh::fail(DH_EINVAL, "%s: counts, tables and status must be 4-byte aligned", who);
   const size_t counts = (size_t)A.n_pages * 4, old = (size_t)A.rows * A.wide * 4, made_bytes = (size_t)made * A.wide * 4;
-  const struct { const void* p; size_t n; } in[] = {{A.uses, counts}, {A.table, old}}, out[] = {{A.uses_out, counts}, {A.table_out, made_bytes}, {A.status, 8}};
-  for (const auto& o : out)
-    for (const auto& i : in)
-      if (overlap(o.p, o.n, i.p, i.n)) return dh::fail(DH_EINVAL, "%s: the new counts, table and status must not overlap the present ones", who);
+  // the kernels go by what they have left in them, and by the inputs, in more than one launch
+  const Span present[] = {{A.uses, counts}, {A.table, old}, lists[0], lists[1], lists[2]}, out[] = {{A.uses_out, counts}, {A.table_out, made_bytes}, {A.status, 8}};
+  for (int o = 0; o < 3; ++o) {
+    for (const Span& i : present)
+      if (overlap(out[o], i)) return dh::fail(DH_EINVAL, "%s: the new counts, table and status must not overlap the inputs", who);
+    if (overlap(out[o], out[(o + 1) % 3])) return dh::fail(DH_EINVAL, "%s: the new counts, table and status must not overlap each other", who);
+  }
   if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "%s: workspace must be a 16-byte aligned pointer", who);
   if (given < need) return dh::fail(DH_EINVAL, "%s: workspace of %zu bytes is below the %zu needed", who, given, need);
   A.n_chunks = chunks_of(A.n_pages);
@@ -658,7 +666,10 @@ int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float*
   A.p = PoolArgs{k_codes, v_codes, k_scale, v_scale, n_pages, hkv, 0, 0, 0, uses, table, uses_out, table_out, status, n_seq, max_pages, nullptr};
   int rc = check_pool(who, n_pages, n_new, "n_new");
   if (rc) return rc;
-  if ((rc = check_pages(who, A.p, page, D, n_new, "n_seq", workspace, workspace_bytes, fork_bytes(n_pages, n_new)))) return rc;
+  if ((int64_t)n_new * max_pages > INT32_MAX)   // the entries that ask are counted in 32 bits
+    return dh::fail(DH_ESHAPE, "fork: n_new * max_pages must be below 2^31 (got %d * %d)", n_new, max_pages);
+  const Span lists[3] = {{kv_len, (size_t)std::max(n_seq, 0) * 4}, {parents, (size_t)n_new * 4}, {need, (size_t)n_new * 4}};
+  if ((rc = check_pages(who, A.p, page, D, n_new, "n_seq", lists, workspace, workspace_bytes, fork_bytes(n_pages, n_new)))) return rc;
   if (!kv_len || !parents || !need) return dh::fail(DH_EINVAL, "fork: null pointer");
   if (!aligned(kv_len, 4) || !aligned(parents, 4) || !aligned(need, 4))
     return dh::fail(DH_EINVAL, "fork: kv_len, parents and need must be 4-byte aligned");
@@ -685,7 +696,7 @@ int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, flo
   const char* who = "compact";
   CompactArgs A{};
   A.p = PoolArgs{k_codes, v_codes, k_scale, v_scale, n_pages, hkv, 0, 0, 0, uses, table, uses_out, table_out, status, n_rows, max_pages, nullptr};
-  const int rc = check_pages(who, A.p, page, D, n_rows, "n_rows", workspace, workspace_bytes, compact_bytes(n_pages));
+  const int rc = check_pages(who, A.p, page, D, n_rows, "n_rows", {}, workspace, workspace_bytes, compact_bytes(n_pages));
   if (rc) return rc;
   A.src = A.p.counts + counts_bytes(n_pages) / 4;
   A.dst = A.src + moves_bytes(n_pages) / 4;

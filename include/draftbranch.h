@@ -77,11 +77,11 @@ int draft_branch_pages_workspace_bytes(int n_pages, int n_new, size_t* bytes);
  *   k_codes .. v_scale  the pool, whose free pages take the copies
  *   table      int32 [n_seq][max_pages], kv_len int32 [n_seq]
  *   parents, need  int32 [n_new]
- *   uses_out   out, int32 [n_pages];  table_out  out, int32 [n_new][max_pages];
- *              neither may overlap uses or table
+ *   uses_out   out, int32 [n_pages];  table_out  out, int32 [n_new][max_pages]
  *   status     out, int32 [2]: free pages after the call; pages that were lacking
+ *              (none of the three may overlap another, or an int32 input)
  * Limits: 1 <= n_seq, n_new <= DL_MAX_SEQS, n_pages <= DB_MAX_PAGES, D, page,
- * heads and max_pages as in draftlayer.h.
+ * heads and max_pages as in draftlayer.h, n_new * max_pages < 2^31.
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */
 int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page, int hkv,
@@ -97,10 +97,10 @@ int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float*
  * are free then.  Entries of `table` that name a moved page name its new place,
  * all others stay as they are; it has to hold every row that names a page of
  * the pool, n_rows of them with max_pages entries each.
- *   uses_out  out, int32 [n_pages];  table_out  out, int32 [n_rows][max_pages];
- *             neither may overlap uses or table
+ *   uses_out  out, int32 [n_pages];  table_out  out, int32 [n_rows][max_pages]
  *   status    out, int32 [2]: pages in use; pages moved
- * Limits: as draft_branch_fork's, n_rows in 1..DL_MAX_SEQS.
+ *             (none of the three may overlap another, or uses or table)
+ * Limits: as draft_branch_fork's, n_rows in 1..DL_MAX_SEQS of any max_pages.
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */
 int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float* v_scale, int n_pages, int page,

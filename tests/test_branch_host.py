@@ -40,9 +40,9 @@ P = 1 << 20       # stands for device addresses: nothing is read before the chec
 FAR = 1 << 24     # and this one for buffers that do not overlap those
 
 FORK = dict(kc=P, vc=P, ks=P, vs=P, n_pages=9, page=64, hkv=2, D=128, uses=P, table=P, kv_len=P, n_seq=3, parents=P, need=P, n_new=5,
-            max_pages=10, uses_out=FAR, table_out=FAR, status=FAR, workspace=P, bytes=1 << 40, stream=None)
+            max_pages=10, uses_out=FAR, table_out=2 * FAR, status=3 * FAR, workspace=P, bytes=1 << 40, stream=None)
 COMPACT = dict(kc=P, vc=P, ks=P, vs=P, n_pages=9, page=64, hkv=2, D=128, uses=P, table=P, n_rows=3, max_pages=10, uses_out=FAR,
-               table_out=FAR, status=FAR, workspace=P, bytes=1 << 40, stream=None)
+               table_out=2 * FAR, status=3 * FAR, workspace=P, bytes=1 << 40, stream=None)
 LOGPROBS = dict(x=P, type=0, ld=1000, M=3, N=1000, scale=1.0, scales=None, tokens=P, n_tok=1, top=8, logprob=P, lse=P, entropy=P, top_id=P,
                 top_logprob=P, workspace=P, bytes=1 << 40, stream=None)
 
@@ -57,7 +57,8 @@ PAGES = [(dict(D=96), B.DH_EUNSUP), (dict(hkv=0), B.DH_ESHAPE), (dict(hkv=257), 
          (dict(table=None), B.DH_EINVAL), (dict(table=P + 2), B.DH_EINVAL), (dict(uses_out=None), B.DH_EINVAL), (dict(table_out=None), B.DH_EINVAL),
          (dict(status=None), B.DH_EINVAL), (dict(status=FAR + 2), B.DH_EINVAL), (dict(uses_out=P), B.DH_EINVAL), (dict(uses_out=P + 32), B.DH_EINVAL),
          (dict(table_out=P), B.DH_EINVAL), (dict(table_out=P - 4), B.DH_EINVAL), (dict(status=P + 4), B.DH_EINVAL), (dict(workspace=None), B.DH_EINVAL),
-         (dict(workspace=P + 4), B.DH_EINVAL), (dict(bytes=10), B.DH_EINVAL)]
+         (dict(workspace=P + 4), B.DH_EINVAL), (dict(bytes=10), B.DH_EINVAL),
+         (dict(status=FAR), B.DH_EINVAL), (dict(status=2 * FAR + 116), B.DH_EINVAL), (dict(table_out=FAR + 32), B.DH_EINVAL)]
 
 
 def _refused(lib, f, args, change, want, who):
@@ -68,9 +69,18 @@ def _refused(lib, f, args, change, want, who):
 
 @pytest.mark.parametrize("change,want", PAGES + [
     (dict(n_seq=0), B.DH_ESHAPE), (dict(n_seq=4097), B.DH_ESHAPE), (dict(n_new=0), B.DH_ESHAPE), (dict(n_new=4097), B.DH_ESHAPE),
-    (dict(kv_len=None), B.DH_EINVAL), (dict(parents=None), B.DH_EINVAL), (dict(need=None), B.DH_EINVAL), (dict(need=P + 1), B.DH_EINVAL)])
+    (dict(kv_len=None), B.DH_EINVAL), (dict(parents=None), B.DH_EINVAL), (dict(need=None), B.DH_EINVAL), (dict(need=P + 1), B.DH_EINVAL),
+    (dict(kv_len=FAR), B.DH_EINVAL), (dict(parents=2 * FAR + 196), B.DH_EINVAL), (dict(need=3 * FAR - 16), B.DH_EINVAL),
+    (dict(n_new=128, max_pages=1 << 24), B.DH_ESHAPE), (dict(n_new=4096, max_pages=1 << 19), B.DH_ESHAPE)])
 def test_fork_refuses(lib, change, want):
     _refused(lib, lib.draft_branch_fork, FORK, change, want, b"fork")
+
+
+@pytest.mark.parametrize("change", [
+    dict(status=FAR), dict(status=FAR + 32), dict(status=2 * FAR + 196), dict(table_out=FAR), dict(uses_out=3 * FAR - 32), dict(uses_out=P),
+    dict(table_out=P - 196), dict(kv_len=FAR - 8), dict(parents=2 * FAR + 196), dict(need=3 * FAR + 4)])
+def test_fork_refuses_what_overlaps(lib, change):
+    _refused(lib, lib.draft_branch_fork, FORK, change, B.DH_EINVAL, b"overlap")
 
 
 @pytest.mark.parametrize("change,want", PAGES + [(dict(n_rows=0), B.DH_ESHAPE), (dict(n_rows=4097), B.DH_ESHAPE)])
@@ -149,7 +159,7 @@ def test_workspace_of_the_largest_serves_smaller_ones(lib):
     for n, r, size in sizes:
         assert all(size >= other for m, q, other in sizes if m <= n and q <= r)
         for f, args, name in ((lib.draft_branch_fork, FORK, "n_new"), (lib.draft_branch_compact, COMPACT, "n_rows")):
-            far = {k: 1 << 40 for k in ("uses_out", "table_out", "status")}
+            far = {k: i << 40 for i, k in enumerate(("uses_out", "table_out", "status"), 1)}
             _refused(lib, f, args, {"n_pages": n, name: r, "bytes": 0, **far}, B.DH_EINVAL, b"below the")
             need = int(re.search(rb"below the (\d+) needed", lib.draft_head_last_error()).group(1))
             assert 0 < need <= size
@@ -178,6 +188,8 @@ def test_binding_refuses_host_tensors():
     table = torch.zeros((1, 2), dtype=torch.int32)
     with pytest.raises(ValueError):
         R.draft_branch_fork(c, c, s, s, i, table, i[:1], i, i)
+    with pytest.raises(ValueError, match="parents"):
+        R.draft_branch_fork(c, c, s, s, i, table, i[:1], i[0], i)
     with pytest.raises(ValueError):
         R.draft_branch_compact(c, c, s, s, i, table)
     with pytest.raises(ValueError):
