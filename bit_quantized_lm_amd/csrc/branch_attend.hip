@@ -767,10 +767,10 @@ __global__ __launch_bounds__(kThreads) void branch_join_kernel(BranchArgs A, int
 }
 
 // ------------------------------------------------------------------ short ones
-// Contexts that are short by the table's width, and few rows: a tile of 16 rows a
-// workgroup, whose waves take turns at what it sees, the prefix's tokens and its own.
-// Nothing is shared but through the caches, nothing planned or joined, in one launch
-// (3 us of the host's time, and 5 of the card's).  Heads of 128, 40 on 8, one row of
+// Contexts that are short by the table's width or the window, and few rows: a tile of
+// 16 rows a workgroup, whose waves take turns at what it sees, the prefix's tokens and
+// its own.  Nothing is shared but through the caches, nothing planned or joined, in one
+// launch (3 us of the host's time, and 5 of the card's).  Heads of 128, 40 on 8, one row of
 // each of 4 sequences over 500, 1,000, 2,000 and 4,000 tokens: 8.3, 10.1, 14.0 and
 // 21.6 us so, 15.8, 16.0, 16.7 and 18.0 planned; 9 rows of each of 16: 16.3, 20.3,
 // 28.4 and 46.0, planned 30.8, 33.6, 38.4 and 44.2; 100 of each of 4, 1,032 tiles:
@@ -877,14 +877,24 @@ int launch_parts(const BranchArgs& A, hipStream_t s) {
   return launched("branch_parts_kernel");
 }
 
-// The short ones: tokens that the table has room for, and tiles, two rounds of a card's workgroups.
-int short_tokens(int D) { return D == 256 ? 1024 : 2048; }
-constexpr int kShortTiles = 1024;
+// Which are short, by the tokens that a row sees at most and the tiles; us so and
+// planned.  Heads of 64, 32 on 8: 416 tiles of 2,048 tokens 15.5 and 29.2, of 4,096
+// 24.6 and 34.2, 1,408 of 4,096 54 and 67.  Heads of 128, 40 on 8: 488 tiles of 1,024
+// tokens 19.2 and 34.1, of 2,048 26.8 and 37.8, 336 of a window of 2,048 14.0 and 29.6;
+// 1,728 of 1,024 61 and 54.  Heads of 256, 16 on 2: 176 tiles of 1,024 tokens 17.8 and
+// 34.2, of 2,048 28.2 and 39.8, of 4,000 47 and 53, 408 of 2,048 50 and 49, 672 of 1,024
+// 50 and 47; 48 of 1,024 17.0 and 21.4, of 2,048 25.5 and 21.9, 96 of 2,048 25.5 and 26.3.
+bool is_short(int D, int64_t tokens, int64_t tiles) {
+  if (D == 64) return tokens <= 4096 && tiles <= 2048;
+  if (D == 128) return tokens <= 2048 && tiles <= 1024;
+  return tokens <= (tiles < 96 ? 1024 : 2048) && tiles <= 512;
+}
 
 template <int D>
 int launch(const BranchArgs& A, hipStream_t s) {
   const int64_t short_tiles = ((int64_t)A.b.T * A.group / kStreamRows + A.b.n_seq) * A.c.hkv;   // at least as many as there are
-  if (((int64_t)A.b.max_pages << A.c.page_shift) <= short_tokens(D) && short_tiles <= kShortTiles) {
+  const int64_t room = (int64_t)A.b.max_pages << A.c.page_shift, seen = A.window > 0 ? std::min<int64_t>(room, (int64_t)A.window + A.sinks) : room;
+  if (is_short(D, seen, short_tiles)) {
     static dh::OncePerDevice once;
     const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_short_kernel<D>), kShortLds<D>);
     if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_short_kernel: %s", hipGetErrorString(e));

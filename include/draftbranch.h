@@ -117,12 +117,12 @@ int draft_branch_attend_workspace_bytes(int T, int n_seq, int hq, int hkv, int D
 
 /*
  * DEVICE.  draft_layer_attend for a batch whose sequences share prefixes, each
- * read once for all that share it (in short contexts, of a table with room for
- * 2048 tokens, through the caches).  The sequences group_start[g] ..
- * group_start[g+1] - 1 are a group and have the tokens of the positions 0 ..
- * prefix_len[g] - 1 in common: these are read from the pages that the first
- * sequence's table row names (group members' entries for whole pages of them
- * need not be there), those from prefix_len[g] on from each one's own.  A row
+ * read once for all that share it (where the table's width or the window makes
+ * all contexts short, and rows are few, through the caches).  The sequences
+ * group_start[g] .. group_start[g+1] - 1 are a group and have the tokens of the
+ * positions 0 .. prefix_len[g] - 1 in common: these are read from the pages that
+ * the first sequence's table row names (group members' entries for whole pages of
+ * them need not be there), those from prefix_len[g] on from each one's own.  A row
  * sees what it sees in draft_layer_attend, by its position, window and sinks,
  * whichever row the page is taken from; a token at a position that it does not
  * see stays unseen in a prefix too.  Sequences from group_start[n_groups] on have

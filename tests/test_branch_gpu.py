@@ -294,7 +294,7 @@ class Branches:
         self.dev, self.hq, self.hkv, self.d, self.page = dev, hq, hkv, d, page
         lens = [(n, p + t, p, i == 0) for p, m in groups for i, (n, t) in enumerate(m)] + [(n, t, 0, True) for n, t in loose]
         reach = max([t for _, t, _, _ in lens] + [p for p, _ in groups] + [1])
-        self.max_pages = max_pages or max(-(-reach // page) + 1, (2048 // page + 3) * wide)
+        self.max_pages = max_pages or max(-(-reach // page) + 1, (4096 // page + 3) * wide)
         n_pages = sum(-(-max(t, p) // page) for _, t, p, _ in lens) + 3
         order, at = rng.permutation(n_pages), 0
         self.table = np.full((len(lens), self.max_pages), -7, np.int32)
@@ -370,6 +370,22 @@ ATTENDS = [
     ([(40 + i, [(1, 3), (1, 1 + i)]) for i in range(70)], [(1, 9)], 2, 1, 64, 32, 0, 0),  # and more groups
     ([(40 + i, [(1, -30 + i), (2, 1 + i)]) for i in range(70)], [(1, 9)], 2, 2, 64, 32, 45, 2),
     ([(20000, [(1, 3)] * 3)], [], 8, 1, 64, 128, 0, 0),                                   # few rows over a long prefix: many parts
+    ([(3900, [(1, 30)] * 3)], [(2, 4000)], 8, 2, 64, 64, 0, 0),                           # the longest of the short
+    ([(1200, [(3, 60)] * 25)], [(2, 900)], 16, 2, 256, 128, 0, 0),
+    ([(3000, [(3, 60)] * 25)], [(2, 900)], 16, 2, 256, 128, 1900, 30),
+]
+SIX = [(9, 60), (1, 9), (0, 7), (1, 300), (3, 3), (2, 40)]
+WINDOWS = [   # too many tiles to be short
+    ([(130 * i + 5, SIX) for i in range(10)], [], 40, 40, 64, 32, 100, 4),
+    ([(130 * i + 5, SIX) for i in range(10)], [(1, 500)] * 4, 40, 40, 64, 32, 1, 0),
+    ([(300, SIX * 4), (64, SIX * 5)], [(2, 100)] * 3, 40, 20, 128, 64, 33, 3),
+    ([(1000, SIX * 10)], [], 40, 20, 128, 64, 200, 70),
+    ([(40, SIX * 10)], [], 20, 20, 128, 32, 50, 100),
+    ([(200, [(70, 90)] * 8), (100, SIX)], [(90, 200)] * 2, 32, 8, 128, 32, 77, 0),
+    ([(500, SIX * 5), (700, SIX * 4)], [(1, 900)], 20, 10, 256, 64, 150, 4),
+    ([(130 * i + 5, SIX) for i in range(15)], [(1, 5)], 24, 24, 64, 32, 45, 2),
+    ([(130 * i + 5, SIX) for i in range(15)], [(1, 5)], 24, 12, 128, 32, 45, 2),
+    ([(130 * i + 5, SIX) for i in range(12)], [(1, 5)], 10, 10, 256, 32, 200, 2),
 ]
 
 
@@ -377,6 +393,14 @@ ATTENDS = [
 @pytest.mark.parametrize("groups,loose,hq,hkv,d,page,window,sinks", ATTENDS)
 def test_attend(dev, groups, loose, hq, hkv, d, page, window, sinks, wide):
     Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq + len(groups), members_know=len(groups) % 2 == 0, wide=wide).check(window, sinks)
+
+
+@pytest.mark.parametrize("groups,loose,hq,hkv,d,page,window,sinks", WINDOWS)
+def test_attend_windows_of_many_tiles(dev, groups, loose, hq, hkv, d, page, window, sinks):
+    c = Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq, wide=True)
+    tiles = (c.rows * (hq // hkv) // 16 + len(c.kv_len)) * hkv
+    assert tiles > {64: 2048, 128: 1024, 256: 512}[d]
+    c.check(window, sinks)
 
 
 @pytest.mark.parametrize("wide", [False, True])
