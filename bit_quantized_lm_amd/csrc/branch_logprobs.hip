@@ -310,7 +310,9 @@ __global__ __launch_bounds__(kThreads, 8) void logprobs_kernel(LogprobArgs A) {
   fetch(v0);
   const float edge = tid < edges ? row.at(row.edge(tid)) : -INFINITY;
   Running t;
-  float bound = INFINITY;
+  // reached by nothing, +inf neither: before the first bound nothing is put down, and the
+  // counters' zeros are only there from the first barrier on, which that bound comes behind
+  float bound = __builtin_nanf("");
   auto put_down = [&](int v, const float (&e)[kPer]) {
     const int at = atomicAdd(&lds.n_list, 1);
     if (at < kList) lds.raw[at] = RowOf<T>::packed(e), lds.at[at] = v;

@@ -714,6 +714,18 @@ def test_logprobs_of_rows_that_are_no_numbers(dev, m, n):
     check_logprobs(dev, x, tokens, 4)
 
 
+@pytest.mark.parametrize("top", [0, 4, 64])
+@pytest.mark.parametrize("m,n", [(3, 700), (3, 9001), (700, 5000), (1030, 20011), (2, 124160)])
+def test_logprobs_of_infinite_elements_before_the_first_bound(dev, m, n, top):
+    """+inf in a row's first steps, in every wave, one and many: that row is NaN, its neighbours are not touched."""
+    rng = np.random.default_rng(n + top)
+    x = rows_of(rng, m, n, "plain")
+    x[0, rng.integers(0, n, 40)] = np.inf
+    x[m - 1] = np.inf
+    for dtype in (torch.bfloat16, torch.float32):
+        check_logprobs(dev, x, rng.integers(0, n, (m, 1)), top, gap=1, dtype=dtype)
+
+
 def test_logprobs_of_bits_and_shards(dev):
     """int16 rows are bf16 bits; two shards join by their lse."""
     rng = np.random.default_rng(2)
