@@ -638,8 +638,18 @@ int check_pages(const char* who, PoolArgs& A, int page, int D, int made, const c
   }
   if (!workspace || !aligned(workspace, 16)) return dh::fail(DH_EINVAL, "%s: workspace must be a 16-byte aligned pointer", who);
   if (given < need) return dh::fail(DH_EINVAL, "%s: workspace of %zu bytes is below the %zu needed", who, given, need);
-  A.n_chunks = chunks_of(A.n_pages);
   A.page_bytes = (int64_t)A.hkv * page * D;
+  // so it is with the workspace, and pages are written while all of them are read
+  const size_t codes = (size_t)A.n_pages * A.page_bytes, scales = (size_t)A.n_pages * A.hkv * 4;
+  const Span scratch{workspace, need}, pool[] = {{A.k, codes}, {A.v, codes}, {A.ks, scales}, {A.vs, scales}, scratch};
+  for (const Span& p : pool) {
+    if (&p != &pool[4] && overlap(p, scratch)) return dh::fail(DH_EINVAL, "%s: the workspace must not overlap the cache", who);
+    for (const Span& i : present)
+      if (overlap(p, i)) return dh::fail(DH_EINVAL, "%s: the counts, table and lists must not overlap the cache or the workspace", who);
+    for (const Span& o : out)
+      if (overlap(p, o)) return dh::fail(DH_EINVAL, "%s: the new counts, table and status must not overlap the cache or the workspace", who);
+  }
+  A.n_chunks = chunks_of(A.n_pages);
   A.slices = (int)std::min<int64_t>(std::max<int64_t>(2 * A.page_bytes / kSlice, 1), 128);
   A.counts = static_cast<int32_t*>(workspace);
   return DH_OK;

@@ -79,7 +79,8 @@ int draft_branch_pages_workspace_bytes(int n_pages, int n_new, size_t* bytes);
  *   parents, need  int32 [n_new]
  *   uses_out   out, int32 [n_pages];  table_out  out, int32 [n_new][max_pages]
  *   status     out, int32 [2]: free pages after the call; pages that were lacking
- *              (none of the three may overlap another, or an int32 input)
+ *              (the three, the int32 inputs, the cache and the workspace: none of
+ *              these may overlap another, but for inputs among themselves)
  * Limits: 1 <= n_seq, n_new <= DL_MAX_SEQS, n_pages <= DB_MAX_PAGES, D, page,
  * heads and max_pages as in draftlayer.h, n_new * max_pages < 2^31.
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
@@ -99,7 +100,7 @@ int draft_branch_fork(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, float*
  * the pool, n_rows of them with max_pages entries each.
  *   uses_out  out, int32 [n_pages];  table_out  out, int32 [n_rows][max_pages]
  *   status    out, int32 [2]: pages in use; pages moved
- *             (none of the three may overlap another, or uses or table)
+ *             (what may not overlap: as in draft_branch_fork)
  * Limits: as draft_branch_fork's, n_rows in 1..DL_MAX_SEQS of any max_pages.
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */

@@ -83,6 +83,36 @@ def test_fork_refuses_what_overlaps(lib, change):
     _refused(lib, lib.draft_branch_fork, FORK, change, B.DH_EINVAL, b"overlap")
 
 
+# buffers that follow each other without a gap, in units of 1 MiB: n_pages 64 of 64 KiB make a cache of 4 MiB codes twice
+APART = {name: (i + 16) << 20 for i, name in enumerate(("uses", "table", "kv_len", "parents", "need", "uses_out", "table_out", "status", "workspace", "ks", "vs"))}
+APART.update(kc=64 << 20, vc=68 << 20, n_pages=64, page=256, hkv=2, D=128)
+SIZES = dict(uses=256, table=120, kv_len=12, parents=20, need=20, uses_out=256, table_out=0, status=8, ks=512, vs=512, kc=4 << 20, vc=4 << 20)
+
+
+@pytest.mark.parametrize("f,args", [("draft_branch_fork", FORK), ("draft_branch_compact", COMPACT)])
+def test_pages_refuse_what_overlaps_the_workspace_or_the_cache(lib, f, args):
+    """The kernels write pages and workspace while they go by counts, tables and what they left in the workspace."""
+    apart = {k: v for k, v in APART.items() if k in args}
+    written = ("workspace", "kc", "vc", "ks", "vs")
+    for a in written:
+        for b in set(apart) & set(SIZES):
+            if a == b or {a, b} <= set(written[1:]):      # the cache's own four are the caller's to keep apart
+                continue
+            size = {**SIZES, "table_out": 4 * args["max_pages"] * args.get("n_new", args.get("n_rows"))}
+            for at in {apart[a], apart[a] + size.get(a, 16) - 4, apart[a] - size[b] + 4}:      # of the workspace the first bytes at least
+                change = {**apart, b: at // 16 * 16 if b in ("kc", "vc") else at}
+                if change["workspace"] % 16 == 0:
+                    _refused(lib, getattr(lib, f), args, change, B.DH_EINVAL, b"overlap")
+
+
+def test_fork_takes_buffers_that_follow_each_other(lib):
+    """Refused for the misaligned list alone, which is looked at last."""
+    for change in (dict(), dict(workspace=APART["kc"] - 4096, bytes=4096), dict(uses_out=APART["kc"] - 256), dict(table_out=APART["kc"] + (8 << 20)),
+                   dict(status=APART["uses"] + 256), dict(parents=APART["kv_len"] + 12, need=APART["kv_len"] + 33), dict(kv_len=APART["uses"])):
+        rc = lib.draft_branch_fork(*{**FORK, **APART, "need": APART["need"] + 1, **change}.values())
+        assert rc == B.DH_EINVAL and b"aligned" in lib.draft_head_last_error(), (change, lib.draft_head_last_error())
+
+
 @pytest.mark.parametrize("change,want", PAGES + [(dict(n_rows=0), B.DH_ESHAPE), (dict(n_rows=4097), B.DH_ESHAPE)])
 def test_compact_refuses(lib, change, want):
     _refused(lib, lib.draft_branch_compact, COMPACT, change, want, b"compact")
