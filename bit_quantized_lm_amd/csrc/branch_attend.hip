@@ -959,6 +959,15 @@ int draft_branch_attend(const void* q, int64_t ldq, const uint8_t* k_codes, cons
   const size_t need = workspace_bytes(rows, items, hkv, D);
   if (workspace_bytes_given < need)
     return dh::fail(DH_EINVAL, "attend: workspace of %zu bytes is below the %zu needed", workspace_bytes_given, need);
+  // a second launch finds the parts by the plan that the first one leaves in the workspace, and by the row starts
+  const Span written[] = {{workspace, need}, {out, (size_t)T * hq * D * 2}, {lse, lse ? (size_t)T * hq * 4 : 0}};
+  const Span lists[] = {{q_start, ((size_t)n_seq + 1) * 4}, {kv_len, (size_t)n_seq * 4}, {table, (size_t)n_seq * max_pages * 4},
+                        {group_start, ((size_t)n_groups + 1) * 4}, {prefix_len, (size_t)n_groups * 4}};
+  for (int w = 0; w < 3; ++w) {
+    if (overlap(written[w], written[(w + 1) % 3])) return dh::fail(DH_EINVAL, "attend: out, lse and the workspace must not overlap each other");
+    for (const Span& l : lists)
+      if (overlap(written[w], l)) return dh::fail(DH_EINVAL, "attend: out, lse and the workspace must not overlap the batch or the groups");
+  }
   A.group_start = group_start;
   A.prefix_len = prefix_len;
   A.n_groups = n_groups;

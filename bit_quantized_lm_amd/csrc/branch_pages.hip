@@ -600,15 +600,6 @@ size_t moves_bytes(int n_pages) { return rounded(((size_t)n_pages / 2 + 1) * 4);
 size_t fork_bytes(int n_pages, int n_new) { return counts_bytes(n_pages) + (size_t)n_new * 4; }
 size_t compact_bytes(int n_pages) { return counts_bytes(n_pages) + 2 * moves_bytes(n_pages) + (size_t)n_pages * 4; }
 
-struct Span {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Span& a, const Span& b) {   // none with nothing
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
-}
-
 int check_pool(const char* who, int n_pages, int rows, const char* rows_name) {
   if (n_pages < 1 || n_pages > DB_MAX_PAGES)
     return dh::fail(DH_ESHAPE, "%s: n_pages must be in 1..%d (got %d)", who, DB_MAX_PAGES, n_pages);

@@ -152,6 +152,15 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
 // ------------------------------------------------------------- host checks
 inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+struct Span {
+  const void* p;
+  size_t n;
+};
+inline bool overlap(const Span& a, const Span& b) {   // none with nothing
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return a.n > 0 && b.n > 0 && x < y + b.n && y < x + a.n;
+}
+
 inline int page_shift_of(int page) { return page == 32 ? 5 : page == 64 ? 6 : page == 128 ? 7 : page == 256 ? 8 : -1; }
 
 inline int check_heads(const char* who, int hq, int hkv, int D) {

@@ -133,7 +133,8 @@ int draft_branch_attend_workspace_bytes(int T, int n_seq, int hq, int hkv, int D
  *   group_start  device, int32 [n_groups + 1], not decreasing, 0 first, at most n_seq
  *   prefix_len   device, int32 [n_groups], any number of tokens (a negative one is 0)
  *   the other arguments, their limits, what is said of rows without a token to
- *   see, of values that are not finite, and the precision: as draft_layer_attend's
+ *   see, of values that are not finite, and the precision: as draft_layer_attend's;
+ *   out, lse and the workspace must not overlap each other or an int32 input
  * Limits: 1 <= n_groups <= n_seq.
  * Errors: DH_EINVAL, DH_ESHAPE, DH_EUNSUP, DH_EHIP.
  */

@@ -133,6 +133,19 @@ def test_attend_refuses(lib, change, want):
     _refused(lib, lib.draft_branch_attend, ATTEND, change, want, b"attend")
 
 
+def test_attend_refuses_what_overlaps(lib):
+    """A second launch goes by what the first one left in the workspace, and by the row starts."""
+    at = dict(q=1 << 30, kc=2 << 30, vc=3 << 30, ks=4 << 30, vs=5 << 30)
+    names = ("q_start", "kv_len", "table", "group_start", "prefix_len", "out", "lse", "workspace")
+    at.update({k: (6 << 30) + (i << 28) for i, k in enumerate(names)})
+    size = dict(q_start=16, kv_len=12, table=120, group_start=12, prefix_len=8, out=5 * 8 * 128 * 2, lse=5 * 8 * 4, workspace=4096)
+    for a in names[5:]:
+        for b in names:
+            for there in {at[a], at[a] + size[a] - 16, at[a] - size[b] + 16 & -16}:
+                if a != b and there < at[a] + size[a] and there + size[b] > at[a]:
+                    _refused(lib, lib.draft_branch_attend, ATTEND, {**at, b: there}, B.DH_EINVAL, b"overlap")
+
+
 @pytest.mark.parametrize("hq,hkv,d", [(40, 8, 128), (7, 7, 256), (16, 1, 64), (16, 2, 256), (200, 200, 64), (256, 1, 128)])
 def test_attend_takes_the_largest_batchs_workspace(lib, hq, hkv, d):
     """The size never falls as rows or sequences grow, and no smaller call asks for more."""
