@@ -210,7 +210,8 @@ __device__ __forceinline__ float factor_of(const LogprobArgs& A, int m) { return
 template <class T>
 __device__ __forceinline__ void finish(const LogprobArgs& A, int m, const RowOf<T>& row, Sum t, float f, const uint64_t* best) {
   const int tid = threadIdx.x;
-  const bool bad = !(f > 0.0f && f < INFINITY) || t.l != t.l, none = t.l == 0.0f;
+  // the exponents' factor has to be a number too, of rows without an element as of others
+  const bool bad = !(f > 0.0f && f * kLog2e < INFINITY) || t.l != t.l, none = t.l == 0.0f;
   const float nan = __builtin_nanf(""), log_l = logf(t.l);
   auto logprob = [&](float x) { return bad ? nan : none ? -INFINITY : (x - t.m) * f - log_l; };
   if (tid == 0) {

@@ -164,8 +164,9 @@ int draft_branch_logprobs_workspace_bytes(int M, int N, int top, size_t* bytes);
  *                 first, of equal ones the lower id first, and their log
  *                 probabilities; id -1 and -inf where the row has no more
  * A row without an element above -inf gets lse, logprob and top_logprob -inf,
- * entropy 0 and ids -1.  A row with a NaN or +inf element, or whose f is not
- * finite and > 0, gets NaN in lse, logprob, entropy and top_logprob, and ids -1.
+ * entropy 0 and ids -1.  A row with a NaN or +inf element, or whose f is not > 0
+ * or is too large (f log2(e) has to be below 2^128: f up to 2.35e38), gets NaN in
+ * lse, logprob, entropy and top_logprob, and ids -1.
  * The shards of one vocabulary join by their lse: with L = ln sum_r exp(lse_r),
  * log probabilities fall by L - lse_r, and the entropy is
  * L - sum_r exp(lse_r - L) (lse_r - entropy_r).

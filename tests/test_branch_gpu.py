@@ -726,6 +726,20 @@ def test_logprobs_of_infinite_elements_before_the_first_bound(dev, m, n, top):
         check_logprobs(dev, x, rng.integers(0, n, (m, 1)), top, gap=1, dtype=dtype)
 
 
+def test_logprobs_of_the_largest_factors(dev):
+    """Up to ln 2 times fp32's largest number a factor is one; beyond, every row is NaN, one without an element too."""
+    rng = np.random.default_rng(6)
+    x = rows_of(rng, 4, 5000, "plain") * np.float32(2.0 ** -127)
+    x[3] = -np.inf
+    tokens = rng.integers(0, 5000, (4, 2))
+    for dtype in (torch.bfloat16, torch.float32):
+        check_logprobs(dev, x, tokens, 4, scales=[1e38, 2.3e38, 2.35e38, 2.35e38], dtype=dtype)
+        given = torch.from_numpy(x).to(dtype).to(dev)
+        for f in (2.37e38, 3.0e38, 3.4028234e38):
+            got = R.draft_branch_logprobs(given, ints(tokens, dev), top=4, scales=torch.full((4,), f, device=dev))
+            assert all(bool(torch.isnan(got[i]).all()) for i in (0, 2, 3, 4)) and bool((got[1] == -1).all())
+
+
 def test_logprobs_of_bits_and_shards(dev):
     """int16 rows are bf16 bits; two shards join by their lse."""
     rng = np.random.default_rng(2)
