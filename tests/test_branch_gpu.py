@@ -726,6 +726,44 @@ def test_logprobs_of_infinite_elements_before_the_first_bound(dev, m, n, top):
         check_logprobs(dev, x, rng.integers(0, n, (m, 1)), top, gap=1, dtype=dtype)
 
 
+@pytest.mark.parametrize("n", [5, 2047, 9001, 40000, 124160])
+def test_logprobs_of_peaked_rows_are_small_and_right(dev, n):
+    """One element far above the rest.  Its weight is 1 exactly and its distance 0, so what is left
+    are the others' share W = sum e^d and D = sum e^d |d|, small numbers of their own:
+      a lane       of k = n / (256 per) vectors of `per` elements moves its reference k times at most, the
+                   lanes, waves and parts 9 times each: weights are e = (k + 18) 2^-22 + 4 u |d| off
+      sum          adding to the peak's 1 loses u at most, and no more than what is added: min((k + per + 18) u, W)
+      ln(sum)      that, e W and the logarithm's 2 u ln(sum): L
+      entropy      L, and of D: e, the additions' (k + per + 54) u, 8 u
+    A reference other than the peak leaves 2^-23 of its distance: 1e-7, where entropies here begin at 1e-12."""
+    rng = np.random.default_rng(n)
+    m = 24
+    peak = rng.integers(0, n, m)
+    peak[:2] = 0, n - 1
+    for dtype, per in ((torch.bfloat16, 8), (torch.float32, 4)):
+        x = rows_of(rng, m, n, "plain")
+        x[np.arange(m), peak] = x.max(1) + np.linspace(1.0, 40.0, m)
+        given = torch.from_numpy(x).to(dtype)
+        x = given.double().numpy()
+        d = x - x.max(1, keepdims=True)
+        assert ((d == 0).sum(1) == 1).all()
+        w = np.where(d < 0, np.exp(d), 0.0)
+        W, D, D2 = w.sum(1), (w * -d).sum(1), (w * d * d).sum(1)
+        k = n / (256 * per) + 1
+        e = (k + 18) * 2.0 ** -22
+        lnl, entropy = np.log1p(W), np.log1p(W) + D / (1 + W)
+        L = np.minimum((k + per + 18) * U, W) + e * W + 4 * U * D + 2 * U * lnl
+        lim = L + (e + (k + per + 62) * U) * D + 4 * U * D2 + (L + U) * D + U * entropy
+        tokens = np.stack([peak, rng.integers(0, n, m)], 1)
+        logprob, top_id, top_logprob, lse, got = (t.cpu().numpy() for t in R.draft_branch_logprobs(given.to(dev), ints(tokens, dev), top=3))
+        assert np.array_equal(top_id[:, 0], peak)
+        assert np.all(np.abs(got - entropy) <= lim), (np.abs(got - entropy) / lim).max()
+        assert (lim < 0.2 * entropy)[W < 0.01].all() and entropy.min() < 1e-8 * n      # nothing else is as small
+        for t in (logprob[:, 0], top_logprob[:, 0]):
+            assert np.all(np.abs(t + lnl) <= L + U * lnl)
+        assert np.all(np.abs(lse - x.max(1) - lnl) <= L + U * np.abs(lse))
+
+
 def test_logprobs_of_the_largest_factors(dev):
     """Up to ln 2 times fp32's largest number a factor is one; beyond, every row is NaN, one without an element too."""
     rng = np.random.default_rng(6)
