@@ -21,6 +21,7 @@
 
 #include "../../include/draftbranch.h"
 #include "attend_tile.h"
+#include "branch_cost.h"
 
 namespace {
 
@@ -28,7 +29,6 @@ using namespace dl;
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kNoLimit = DL_MAX_POSITIONS;
-constexpr int kStreamRows = 16, kSmallRows = 64;
 
 // Partial results of one kind of items and of tiles: row x of a head from run r at
 // place x + r * (rows of a tile).  Runs that share a tile stand that far apart, so two
@@ -79,22 +79,6 @@ struct Item {
   int of;                // the sequence's group, -1: none
   int seq, lead;         // whose table rows name the pages of the own and of the shared tokens
   int p_first, p_last;   // the rows' positions
-};
-
-// Lengths of tiles in units of about 0.1 us of a workgroup (of a wave, for the
-// stream): what a tile's beginning and end take, and what a group of 32 tokens takes.
-// Measured with heads of 128 on a full card: 0.8 us a group for 64 rows (0.9 to 1.2
-// beside tiles of 128), 1.15 for 128, 1.6 for a wave's 16; a workgroup that goes on
-// from one tile to the next loses 8 to 10 us, of which 5 pass until the first product.
-template <int D>
-struct Cost {
-  static constexpr int kRows = D == 256 ? 64 : 128;     // H
-  static constexpr bool kStreams = D != 256;
-  static __host__ __device__ constexpr int per_group(int rows) {
-    return std::max(1, (rows <= kStreamRows ? 16 : rows <= kSmallRows ? 9 : 12) * D / 128);
-  }
-  static __host__ __device__ constexpr int begin(int rows) { return rows <= kStreamRows ? 40 : 80; }
-  static __device__ __forceinline__ int of(int rows, int groups) { return groups == 0 ? 0 : begin(rows) + groups * per_group(rows); }
 };
 
 // An item's tiles: `full` ones of H rows, then one of `rest`, and their units, of
