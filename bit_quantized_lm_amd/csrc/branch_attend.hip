@@ -861,28 +861,15 @@ int launch_parts(const BranchArgs& A, hipStream_t s) {
   return launched("branch_parts_kernel");
 }
 
-// Which are short, by the tokens that a row sees at most and the tiles; us so and
-// planned.  Heads of 64, 32 on 8: 416 tiles of 2,048 tokens 15.5 and 29.2, of 4,096
-// 24.6 and 34.2, 1,408 of 4,096 54 and 67.  Heads of 128, 40 on 8: 488 tiles of 1,024
-// tokens 19.2 and 34.1, of 2,048 26.8 and 37.8, 336 of a window of 2,048 14.0 and 29.6;
-// 1,728 of 1,024 61 and 54.  Heads of 256, 16 on 2: 176 tiles of 1,024 tokens 17.8 and
-// 34.2, of 2,048 28.2 and 39.8, of 4,000 47 and 53, 408 of 2,048 50 and 49, 672 of 1,024
-// 50 and 47; 48 of 1,024 17.0 and 21.4, of 2,048 25.5 and 21.9, 96 of 2,048 25.5 and 26.3.
-bool is_short(int D, int64_t tokens, int64_t tiles) {
-  if (D == 64) return tokens <= 4096 && tiles <= 2048;
-  if (D == 128) return tokens <= 2048 && tiles <= 1024;
-  return tokens <= (tiles < 96 ? 1024 : 2048) && tiles <= 512;
-}
-
 template <int D>
 int launch(const BranchArgs& A, hipStream_t s) {
-  const int64_t short_tiles = ((int64_t)A.b.T * A.group / kStreamRows + A.b.n_seq) * A.c.hkv;   // at least as many as there are
   const int64_t room = (int64_t)A.b.max_pages << A.c.page_shift, seen = A.window > 0 ? std::min<int64_t>(room, (int64_t)A.window + A.sinks) : room;
-  if (is_short(D, seen, short_tiles)) {
+  if (seen <= short_tokens(D, short_tiles(A.b.T, A.b.n_seq, A.hq, A.c.hkv))) {
+    const int64_t tiles = ((int64_t)A.b.T * A.group / kStreamRows + A.b.n_seq) * A.c.hkv;   // at least as many as there are
     static dh::OncePerDevice once;
     const hipError_t e = allow_lds(once, reinterpret_cast<const void*>(&branch_short_kernel<D>), kShortLds<D>);
     if (e != hipSuccess) return dh::fail(DH_EHIP, "branch_short_kernel: %s", hipGetErrorString(e));
-    hipLaunchKernelGGL(branch_short_kernel<D>, dim3((unsigned)short_tiles), dim3(64 * kShortWaves<D>), kShortLds<D>, s, A);
+    hipLaunchKernelGGL(branch_short_kernel<D>, dim3((unsigned)tiles), dim3(64 * kShortWaves<D>), kShortLds<D>, s, A);
     return launched("branch_short_kernel");
   }
   const int rc = A.b.n_seq <= kSmall && A.n_groups <= kSmall ? launch_parts<D, true>(A, s) : launch_parts<D, false>(A, s);

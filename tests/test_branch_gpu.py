@@ -403,6 +403,43 @@ def test_attend_windows_of_many_tiles(dev, groups, loose, hq, hkv, d, page, wind
     c.check(window, sinks)
 
 
+@pytest.mark.parametrize("groups,loose,hq,hkv,d,page,window,sinks", [
+    ([(1000, SIX * 10)], [], 48, 24, 128, 64, 200, 70),                    # up to 64 sequences
+    ([(500, SIX * 5), (700, SIX * 4)], [], 32, 16, 256, 64, 150, 4),
+    ([(300, SIX * 8), (64, SIX * 8)], [(2, 100)] * 3, 40, 20, 128, 64, 33, 3),      # more
+    ([(40, SIX * 14)], [], 20, 20, 128, 32, 50, 100),
+    ([(130 * i + 5, SIX) for i in range(18)], [(1, 5)], 10, 10, 256, 32, 200, 2),
+])
+def test_attend_windows_planned(dev, groups, loose, hq, hkv, d, page, window, sinks):
+    """Tiles of sequences of equal rows, by which a batch with a window is too large for one launch."""
+    c = Branches(dev, groups, loose, hq, hkv, d, page, seed=d + page + hq, wide=True)
+    rows = -(-c.rows * (hq // hkv) // len(c.kv_len))
+    assert len(c.kv_len) * -(-rows // 16) * hkv > {128: 1216, 256: 800}[d]
+    c.check(window, sinks)
+
+
+@pytest.mark.parametrize("groups,hq,hkv,d,window", [
+    ([(1500, [(1, 30)] * 70), (2500, [(2, 60)] * 50)], 8, 8, 128, 0),       # 960 tiles, room for 2,592 tokens: planned
+    ([(2500, [(1, 30)] * 60)], 8, 8, 128, 0),                               # 480: one launch
+    ([(700, [(3, 60)] * 60)], 8, 8, 256, 0), ([(900, [(3, 60)] * 60)], 8, 8, 256, 0),      # 480 tiles, up to 896 tokens of room and more
+    ([(200, [(40, 60)] * 16)], 16, 8, 256, 0), ([(600, [(40, 60)] * 16)], 16, 8, 256, 0),  # 640 tiles of full rows
+    ([(2200, [(1, 60)] * 100), (2000, [(1, 60)] * 100)], 8, 8, 64, 0),      # 1,600
+    ([(4000, [(1, 60)] * 64)], 8, 8, 64, 0),                                # 512
+    ([(5000, [(5, 60)] * 30)], 40, 8, 128, 2048),                           # by the window
+])
+def test_attend_on_both_sides_of_short(dev, groups, hq, hkv, d, window):
+    """Against the layer's attention, as the large batches."""
+    groups = [(p // 32 * 32, m) for p, m in groups]
+    c = Branches(dev, groups, [], hq, hkv, d, 32, seed=hq + d, quick=True).upload()
+    c.batch[2] = ints(np.maximum(c.table, 0), dev)
+    q = c.q.to(dev)
+    got = R.draft_branch_attend(q, *c.cache, *c.batch, window=window, sinks=4)
+    want = L.draft_layer_attend(q, *c.cache, *c.batch[:3], window=window, sinks=4)
+    assert all(torch.equal(a, b) for a, b in zip(got, R.draft_branch_attend(q, *c.cache, *c.batch, window=window, sinks=4)))
+    assert float((got[1] - want[1]).abs().max()) < 1e-4
+    assert float((got[0].float() - want[0].float()).abs().max()) <= 2.0 ** -7 * float(want[0].float().abs().max())
+
+
 @pytest.mark.parametrize("wide", [False, True])
 def test_attend_is_the_layers(dev, wide):
     """Where the rows name one prefix's pages, draft_layer_attend of the same batch says the same."""
