@@ -169,7 +169,8 @@ def draft_branch_attend_workspace(rows: int, n_seq: int, hq: int, hkv: int, d: i
 
 def draft_branch_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, group_start, prefix_len, scale: float | None = None,
                         window: int = 0, sinks: int = 0, out=None, lse=None, workspace=None, stream=None):
-    """draft_layer_attend for sequences that share prefixes, each read once.
+    """draft_layer_attend for sequences that share prefixes, each read once but
+    for short contexts and groups of long members (include/draftbranch.h).
 
     group_start: CUDA int32 [groups + 1]: sequences group_start[g] ..
     group_start[g+1] - 1 share the tokens of the positions below prefix_len[g]

@@ -64,7 +64,12 @@ struct BranchArgs {
 // H a workgroup's (shared_tile), whatever the other items have.  Where the members of
 // a group have H rows each on average, sharing saves no time (such tiles are bound by
 // the matrix units) and joining costs some, so the prefix's tokens are the
-// sequences' own then (16 prompts of 112 rows over 6,000 tokens: 345 us so, 517 apart).
+// sequences' own then.  Heads of 128, 40 on 8, us so and apart: 16 prompts of 112 rows
+// over 2,048, 6,144 and 20,480 tokens 121, 273, 805 and 135, 288, 845; of 300 rows down
+// to 15, 160, 360, 1,081 and 199, 400, 1,088.  By the average, so a group of one prompt
+// and many single tokens has each of them read the prefix: 2,000 rows and 15 of one 183,
+// 335, 921 and 213, 372, 919, but 600 and 15 of one 72, 118, 315 and 70, 115, 278, and
+// 4 of 112 and 12 of one 58, 103, 256 and 56, 91, 223.
 //
 // All tiles of a line are laid end to end, each as long as it is thought to take, and
 // cut into equal runs: a workgroup's, or a wave's, which walks its own segments and

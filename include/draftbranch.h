@@ -111,25 +111,39 @@ int draft_branch_compact(uint8_t* k_codes, uint8_t* v_codes, float* k_scale, flo
 
 /*
  * Bytes of device workspace for draft_branch_attend's calls of up to T rows of
- * up to n_seq sequences with these heads.
+ * up to n_seq sequences with these heads.  It has a place for every row's fp32 sums
+ * four times: 40 heads on 8 of 128 ask for 103 MB for few rows, 443 MB for 4,096 and
+ * 1,465 MB for 16,384.
  * Errors: DH_EINVAL (null pointer), DH_ESHAPE, DH_EUNSUP.
  */
 int draft_branch_attend_workspace_bytes(int T, int n_seq, int hq, int hkv, int D, size_t* bytes);
 
 /*
- * DEVICE.  draft_layer_attend for a batch whose sequences share prefixes, each
- * read once for all that share it (where the table's width or the window makes
- * all contexts short, and rows are few, through the caches).  The sequences
- * group_start[g] .. group_start[g+1] - 1 are a group and have the tokens of the
- * positions 0 .. prefix_len[g] - 1 in common: these are read from the pages that
- * the first sequence's table row names (group members' entries for whole pages of
- * them need not be there), those from prefix_len[g] on from each one's own.  A row
+ * DEVICE.  draft_layer_attend for a batch whose sequences share prefixes.  The
+ * sequences group_start[g] .. group_start[g+1] - 1 are a group and have the tokens
+ * of the positions 0 .. prefix_len[g] - 1 in common: these are read from the pages
+ * that the first sequence's table row names (group members' entries for whole pages
+ * of them need not be there), those from prefix_len[g] on from each one's own.  A row
  * sees what it sees in draft_layer_attend, by its position, window and sinks,
  * whichever row the page is taken from; a token at a position that it does not
  * see stays unseen in a prefix too.  Sequences from group_start[n_groups] on have
  * no prefix.  Where the members' table rows name the pages of one prefix, as
  * draft_branch_fork leaves them, the result is draft_layer_attend's of the same
  * batch up to rounding.
+ * A prefix is read once for all that share it, with two exceptions, where the
+ * caches alone share it:
+ *   short contexts  the table's width or the window leaves every row few tokens,
+ *             and rows are few: one launch instead of two or three (heads of 128 up
+ *             to 2,816 tokens, of 64 4,096, of 256 2,560)
+ *   long members    a group whose members have on average 128 rows of query heads
+ *             for a kv head (heads of 256: 64): each reads the prefix for itself,
+ *             since the products bound such rows.  One long prompt among single
+ *             tokens makes its group such a one: 600 rows and 15 of one row over
+ *             20,480 tokens, 40 heads on 8 of 128, take 315 us, 278 if shared.
+ * Where there is little to share, draft_layer_attend of the same batch is the faster
+ * call: 16 prompts of 112 rows over 6,000 tokens 260 us there and 267 here, 204 and 242
+ * with 16 heads on 2 of 256, 32 single rows of those under a window of 2,048 19.5 and
+ * 26.3, 4 single rows over 1,000 tokens in a table for more than 2,816 11.0 and 15.9.
  *   group_start  device, int32 [n_groups + 1], not decreasing, 0 first, at most n_seq
  *   prefix_len   device, int32 [n_groups], any number of tokens (a negative one is 0)
  *   the other arguments, their limits, what is said of rows without a token to
