@@ -186,6 +186,11 @@ int draft_branch_logprobs_workspace_bytes(int M, int N, int top, size_t* bytes);
  * L - sum_r exp(lse_r - L) (lse_r - entropy_r).
  * Sums are fp32 under the running maximum; x is taken as it is, differences to
  * the maximum are rounded once, so rows at the type's lowest value are rows too.
+ * A difference that is past fp32's largest number is infinite, whatever f: such an
+ * element weighs nothing and its log probability is -inf.
+ * Rows in which far more elements than `top` are equal to the top-th largest or
+ * above it (constant rows) are passed over `top` times more: 72 rows of 124,160
+ * equal elements take 66 us with 8 alternatives and 408 with 64, others 17.
  *   logits    device, bf16 (type DB_BF16) or fp32 (DB_FP32), row m at logits +
  *             m*ld elements, ld >= N; aligned to its element alone
  *   scales    device, fp32 [M], or NULL

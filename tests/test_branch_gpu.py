@@ -815,6 +815,22 @@ def test_logprobs_of_the_largest_factors(dev):
             assert all(bool(torch.isnan(got[i]).all()) for i in (0, 2, 3, 4)) and bool((got[1] == -1).all())
 
 
+def test_logprobs_of_differences_past_the_largest_number(dev):
+    """They are infinite: the element weighs nothing, though f would bring it near."""
+    x = torch.full((2, 3000), -3e38)
+    x[:, 7], x[:, 2900], x[1, 5] = 3e38, 2.9e38, 0.0
+    logprob, top_id, top_logprob, lse, entropy = (t.double().cpu() for t in R.draft_branch_logprobs(
+        x.to(dev), ints([[7, 2900, 5, 0]] * 2, dev), top=4, scales=torch.full((2,), 1e-37, device=dev)))
+    z = torch.where(x > -1e38, x.double() * float(np.float32(1e-37)), -torch.inf)
+    want = torch.log_softmax(z, 1)
+    assert torch.equal(torch.isinf(logprob), torch.isinf(want[:, [7, 2900, 5, 0]])) and not torch.isnan(logprob).any()
+    fine = torch.isfinite(logprob)
+    assert float((logprob - want[:, [7, 2900, 5, 0]])[fine].abs().max()) < 2e-5      # 30 of z: u |z| and a few 2^-22
+    assert float((lse - torch.logsumexp(z, 1)).abs().max()) < 2e-5
+    assert float((entropy + torch.special.xlogy(want.exp(), want.exp()).sum(1)).abs().max()) < 2e-5
+    assert top_id[0].tolist() == [7, 2900, 0, 1] and top_id[1].tolist() == [7, 2900, 5, 0] and bool(torch.isneginf(top_logprob[0, 2:]).all())
+
+
 def test_logprobs_of_bits_and_shards(dev):
     """int16 rows are bf16 bits; two shards join by their lse."""
     rng = np.random.default_rng(2)
