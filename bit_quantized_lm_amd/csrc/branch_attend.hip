@@ -10,11 +10,11 @@
 // takes is computed on the device, from the lengths.  Short contexts take one launch
 // that shares nothing (branch_short_kernel).
 //
-// 40 heads on 8 of 128: 64 samples of a prompt of 8,192 tokens 41 us, 16 sequences of
-// 9 slots over four prefixes of up to 20,000 52, 16 prompts of 112 rows over 6,000
-// tokens 263 (843 TFLOP/s).  Of the first two's 34 and 47 us on the card before the
-// joining (8), the tiles take 16 and 36; the rest begins (plan 2.6, segment 1, queries
-// and first codes 4) and leaves (2).
+// 40 heads on 8 of 128: 64 samples of a prompt of 8,192 tokens 39 us, 16 sequences of
+// 9 slots over four prefixes of up to 20,000 53, 16 prompts of 112 rows over 6,000
+// tokens 266 (834 TFLOP/s).  Of the first two's 34 and 47 us on the card before the
+// joining (8), a workgroup's tiles take 19 and 31; the rest begins (start 0.4, plan 2.9,
+// segment and its setup 2) and leaves (2), and the last workgroups end 5 after most.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
