@@ -242,6 +242,37 @@ def _empty(shape, dtype, like):
     return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _keep_for(made, stream):
+    """Tells torch's allocator that tensors made on the current stream are used on
+    `stream` too, and lets that wait for what has been done with them and their
+    memory here (None: the current one, nothing to do)."""
+    if stream is None or not made:
+        return
+    import torch
+    dev = made[0].device
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=dev) if stream else torch.cuda.default_stream(dev)
+    here = torch.cuda.current_stream(dev)
+    if stream.cuda_stream != here.cuda_stream:
+        stream.wait_stream(here)
+        for t in made:
+            t.record_stream(stream)
+
+
+class _Made:
+    """What a call allocates: made(given, shape, dtype) is the caller's tensor, or a new one."""
+
+    def __init__(self, like):
+        self.like, self.new = like, []
+
+    def __call__(self, given, shape, dtype):
+        return self.keep(_empty(shape, dtype, self.like)) if given is None else given
+
+    def keep(self, t):
+        self.new.append(t)
+        return t
+
+
 def draft_head_workspace_bytes(M: int, K: int) -> int:
     """Device workspace bytes the coarse pass needs for M rows of length K."""
     lib = load_library()
@@ -271,12 +302,12 @@ def draft_head_coarse(x, tiled, pairs, N: int, kcand: int = 8, cand_val=None, ca
     lib = load_library()
     M, K = x.shape
     nblk = (N + BLOCK_N - 1) // BLOCK_N
-    if cand_val is None:
-        cand_val = _empty((M, nblk * kcand), torch.float32, x)
-    if cand_id is None:
-        cand_id = _empty((M, nblk * kcand), torch.int32, x)
+    made = _Made(x)
+    cand_val = made(cand_val, (M, nblk * kcand), torch.float32)
+    cand_id = made(cand_id, (M, nblk * kcand), torch.int32)
     if workspace is None:
-        workspace = workspace_for(M, K * (2 if bits == 4 else 1), x.device)
+        workspace = made.keep(workspace_for(M, K * (2 if bits == 4 else 1), x.device))
+    _keep_for(made.new, stream)
     f = lib.draft_head_coarse_int4 if bits == 4 else lib.draft_head_coarse
     _check(f(_ptr(x), M, K, N, _ptr(tiled), _ptr(pairs), kcand, _ptr(cand_val), _ptr(cand_id), _ptr(coarse_out),
              *_ws(workspace), _stream(stream)))
@@ -293,10 +324,9 @@ def draft_head_rerank(x, w, cand_val, cand_id, R: int = 32, rr_id=None, rr_val=N
     n = w.shape[0] if N is None else N
     ldw = w.stride(0)
     ncand = cand_val.shape[1]
-    if rr_id is None:
-        rr_id = _empty((M, R), torch.int32, x)
-    if rr_val is None:
-        rr_val = _empty((M, R), torch.float32, x)
+    made = _Made(x)
+    rr_id, rr_val = made(rr_id, (M, R), torch.int32), made(rr_val, (M, R), torch.float32)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_rerank(_ptr(x), _ptr(w), ldw, M, K, n, _ptr(cand_val), _ptr(cand_id), ncand,
                                  R, _ptr(rr_id), _ptr(rr_val), _stream(stream)))
     return rr_id, rr_val
@@ -311,10 +341,9 @@ def draft_head_rerank_e4m3(x, w8, wscale, cand_val, cand_id, R: int = 32, rr_id=
     M, K = x.shape
     n = w8.shape[0] if N is None else N
     ncand = cand_val.shape[1]
-    if rr_id is None:
-        rr_id = _empty((M, R), torch.int32, x)
-    if rr_val is None:
-        rr_val = _empty((M, R), torch.float32, x)
+    made = _Made(x)
+    rr_id, rr_val = made(rr_id, (M, R), torch.int32), made(rr_val, (M, R), torch.float32)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_rerank_e4m3(_ptr(x), _ptr(w8), _ptr(wscale), w8.stride(0), M, K, n, _ptr(cand_val),
                                       _ptr(cand_id), ncand, R, _ptr(rr_id), _ptr(rr_val), _stream(stream)))
     return rr_id, rr_val
@@ -330,10 +359,9 @@ def draft_head_rerank_nvfp4(x, w4, bscale, gscale, cand_val, cand_id, R: int = 3
     M, K = x.shape
     n = w4.shape[0] if N is None else N
     ncand = cand_val.shape[1]
-    if rr_id is None:
-        rr_id = _empty((M, R), torch.int32, x)
-    if rr_val is None:
-        rr_val = _empty((M, R), torch.float32, x)
+    made = _Made(x)
+    rr_id, rr_val = made(rr_id, (M, R), torch.int32), made(rr_val, (M, R), torch.float32)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_rerank_nvfp4(_ptr(x), _ptr(w4), w4.stride(0), _ptr(bscale), bscale.stride(0),
                                        _ptr(gscale), M, K, n, _ptr(cand_val), _ptr(cand_id), ncand, R, _ptr(rr_id),
                                        _ptr(rr_val), _stream(stream)))
@@ -346,8 +374,9 @@ def draft_head_logits_row(rr_id, rr_val, N: int, coarse=None, topk_only=False, o
     import torch
     lib = load_library()
     M, R = rr_id.shape
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.int16, device=rr_id.device)
+    made = _Made(rr_id)
+    out = made(out, (M, N), torch.int16)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_logits_row(_ptr(coarse), _ptr(rr_id), _ptr(rr_val), M, N, R, 1 if topk_only else 0,
                                      _ptr(out), _stream(stream)))
     return out
@@ -361,8 +390,9 @@ def draft_head_stream_read(buf, out=None, stream=None):
     returns the uint32 [DH_READ_BLOCKS] XOR folds of the workgroups' spans."""
     import torch
     lib = load_library()
-    if out is None:
-        out = torch.empty(DH_READ_BLOCKS, dtype=torch.int32, device=buf.device)
+    made = _Made(buf)
+    out = made(out, DH_READ_BLOCKS, torch.int32)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_stream_read(_ptr(buf), buf.numel() * buf.element_size(), _ptr(out), _stream(stream)))
     return out
 
@@ -372,10 +402,9 @@ def draft_head_argmax(rr_id, rr_val, out_id=None, out_val=None, stream=None):
     import torch
     lib = load_library()
     M, R = rr_id.shape
-    if out_id is None:
-        out_id = _empty((M,), torch.int32, rr_id)
-    if out_val is None:
-        out_val = _empty((M,), torch.float32, rr_id)
+    made = _Made(rr_id)
+    out_id, out_val = made(out_id, (M,), torch.int32), made(out_val, (M,), torch.float32)
+    _keep_for(made.new, stream)
     _check(lib.draft_head_argmax(_ptr(rr_id), _ptr(rr_val), M, R, _ptr(out_id), _ptr(out_val),
                                  _stream(stream)))
     return out_id, out_val
@@ -413,10 +442,13 @@ def draft_head_forward(x, tiled, pairs, w, N: int, kcand: int = 8, R: int = 32, 
     timestamps.  Returns the dict of output tensors."""
     lib = load_library()
     M, K = x.shape
+    made = _Made(x)
     if out is None:
         out = forward_buffers(M, N, kcand, R, x.device)
+        made.new += out.values()
     if workspace is None:
-        workspace = workspace_for(M, K * (2 if bits == 4 else 1), x.device)
+        workspace = made.keep(workspace_for(M, K * (2 if bits == 4 else 1), x.device))
+    _keep_for(made.new, stream)
     e0, e1 = (None, None) if coarse_events is None else (_event(coarse_events[0]), _event(coarse_events[1]))
     outs = (_ptr(out["cand_val"]), _ptr(out["cand_id"]), _ptr(out["rr_id"]), _ptr(out["rr_val"]),
             _ptr(out["out_id"]), _ptr(out["out_val"]), _ptr(coarse_out), *_ws(workspace), _stream(stream), e0, e1)
@@ -444,12 +476,14 @@ def draft_head_forward_row(x, tiled, pairs, w, N: int, kcand: int = 8, R: int = 
     import torch
     lib = load_library()
     M, K = x.shape
+    made = _Made(x)
     if out is None:
         out = forward_buffers(M, N, kcand, R, x.device)
-    if row is None:
-        row = torch.empty((M, N), dtype=torch.int16, device=x.device)
+        made.new += out.values()
+    row = made(row, (M, N), torch.int16)
     if workspace is None:
-        workspace = workspace_for(M, K, x.device)
+        workspace = made.keep(workspace_for(M, K, x.device))
+    _keep_for(made.new, stream)
     _check(lib.draft_head_forward_row(_ptr(x), M, K, N, _ptr(tiled), _ptr(pairs), _ptr(w), w.stride(0), kcand, R,
                                       _ptr(out["cand_val"]), _ptr(out["cand_id"]), _ptr(out["rr_id"]),
                                       _ptr(out["rr_val"]), _ptr(out["out_id"]), _ptr(out["out_val"]), _ptr(row),
@@ -467,6 +501,7 @@ def draft_head_forward_noalloc(x, tiled, pairs, w, N: int, kcand: int = 8, R: in
     M, K = x.shape
     if out is None:
         out = forward_buffers(M, N, kcand, R, x.device)
+        _keep_for(list(out.values()), stream)
     e0, e1 = (None, None) if coarse_events is None else (_event(coarse_events[0]), _event(coarse_events[1]))
     _check(lib.draft_head_forward_noalloc(_ptr(x), M, K, N, _ptr(tiled), _ptr(pairs), _ptr(w), w.stride(0), kcand,
                                           R, _ptr(out["cand_val"]), _ptr(out["cand_id"]), _ptr(out["rr_id"]),
@@ -544,6 +579,7 @@ class DraftHead:
         then draft_head_logits_row."""
         import torch
         coarse = torch.empty((x.shape[0], self.N), dtype=torch.float32, device=x.device)
+        _keep_for([coarse], stream)
         out = self(x, coarse_out=coarse, stream=stream)
         out["row"] = draft_head_logits_row(out["rr_id"], out["rr_val"], self.N,
                                            coarse=None if topk_only else coarse, topk_only=topk_only,

@@ -71,7 +71,7 @@ def _workspace(given, size, dev, stream):
     if given is None:
         given = torch.empty(size(), dtype=torch.uint8, device=f"cuda:{dev}")
         if stream is not None:
-            L._keep_for(given, stream)
+            B._keep_for((given,), stream)
     elif given.get_device() != dev or not given.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on GPU {dev}")
     return given.data_ptr(), given.numel() * given.element_size(), given

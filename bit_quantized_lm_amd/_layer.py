@@ -160,18 +160,8 @@ def _out(given, name, like, shape, dtype, dev, stream):
         return given
     t = like.new_empty(shape) if like.dtype is dtype else like.new_empty(shape, dtype=dtype)
     if stream is not None:
-        _keep_for(t, stream)
+        B._keep_for((t,), stream)
     return t
-
-
-def _keep_for(t, stream):
-    """Tells torch's allocator that `t`, made on the current stream, is used on `stream` too."""
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=t.device) if stream else torch.cuda.default_stream(t.device)
-    here = torch.cuda.current_stream(t.device)
-    if stream.cuda_stream != here.cuda_stream:
-        stream.wait_stream(here)   # the memory's last use there comes first
-        t.record_stream(stream)
 
 
 def draft_layer_append(q, k, v, rope, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, table, interleaved: bool = False,
@@ -268,7 +258,7 @@ def draft_layer_attend(q, k_codes, v_codes, k_scale, v_scale, q_start, kv_len, t
     if workspace is None:
         workspace = draft_layer_workspace(rows, n_seq, hq, hkv, d, dev)
         if stream is not None:
-            _keep_for(workspace, stream)
+            B._keep_for((workspace,), stream)
     if workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be a contiguous tensor on GPU {dev}")
     B._check(lib.draft_layer_attend(

@@ -888,3 +888,33 @@ def test_head_scores_its_tokens(dev):
         want = O.logprobs(first["row"].view(torch.bfloat16).double().cpu().numpy(), tokens.cpu().numpy(), 3, np.full(m, np.float32(0.8)))
         assert np.array_equal(got["top_id"].cpu().numpy(), want["top_id"])
         assert np.abs(got["logprob"].cpu().numpy() - want["logprob"]).max() < 1e-4 and np.abs(got["entropy"].cpu().numpy() - want["entropy"]).max() < 1e-4
+
+
+def test_head_on_another_stream(dev):
+    """Memory that the current stream is still reading is not written by a call on another one, and the results are those of the current one."""
+    from bit_quantized_lm_amd import workload
+    n, k, m = 4000, 1024, 5
+    head = B.DraftHead.from_weight(workload.gen_weight(n, k, seed=3), device=dev)
+    x = torch.from_numpy(workload.gen_x(m, k, seed=4).view(np.int16)).to(dev)
+    tokens = ints(np.arange(m)[:, None], dev)
+    side = torch.cuda.Stream()
+    calls = [lambda s: head(x, stream=s), lambda s: head.logits_row(x, stream=s), lambda s: head.logits_row_staged(x, stream=s),
+             lambda s: head.staged(x, stream=s), lambda s: head.logprobs(x, tokens, top=3, scale=0.8, stream=s)]
+    for call in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        for s in (side, side.cuda_stream):
+            # blocks of the sizes that the call takes, freed while a copy of them waits
+            busy = [torch.full_like(t, 7) for t in want.values()] + [torch.full((1 << 16,), 7, dtype=torch.uint8, device=dev)]
+            copies = [torch.empty_like(t) for t in busy]
+            torch.cuda.synchronize()
+            torch.cuda._sleep(4_000_000)
+            for a, b in zip(copies, busy):
+                a.copy_(b)
+            del busy, b
+            got = call(s)
+            side.synchronize()
+            for name, t in want.items():
+                assert torch.equal(got[name], t), name
+            torch.cuda.synchronize()
+            assert all(bool((t == 7).all()) for t in copies)
