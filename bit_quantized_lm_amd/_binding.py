@@ -4,6 +4,8 @@ Argument marshalling only: host functions take and return numpy arrays, device
 functions take torch CUDA tensors (torch is used for device memory and the
 current stream, nothing else) and allocate their outputs with torch.empty when
 the caller passes none.  Every step of the draft head runs in the library.
+With `stream` another one than the current, that stream first waits for the
+current one where the call allocates something for it.
 
 Error mapping: DH_EINVAL / DH_ESHAPE / DH_EUNSUP raise ValueError, DH_EHIP
 raises DraftHeadError (a RuntimeError); the message is the library's own.
